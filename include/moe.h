@@ -28,6 +28,15 @@
  *   moe_forward      the four forward calls in sequence, intermediates in the
  *                    caller's workspace
  *
+ * Around the layer, for a training or decoding step of the model that holds it:
+ *
+ *   moe_embed, moe_embed_backward            token embedding with a scale; its
+ *                    gradient by sorted tokens
+ *   moe_block_norm, moe_block_norm_backward  norm after a block, gate, scaled
+ *                    residual sum and norm before the next block in one pass
+ *   moe_distill, moe_distill_backward, moe_distill_step  distillation from a
+ *                    teacher's top logits
+ *
  * Conventions that hold for every entry point:
  *  - Pointers named as device buffers are CUDA device (or managed) memory of
  *    the current device; they must be 16-byte aligned.  Matrices are dense
@@ -516,6 +525,161 @@ int moe_backward(const moe_dims_t *d, const moe_bwd_args_t *a, void *ws, size_t 
 int moe_backward_ep(const moe_dims_t *d, int32_t e_begin, int32_t e_end, int32_t phase, const moe_bwd_args_t *a,
                     float *dxr_sorted, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer.  The conventions above hold, except that their
+ * row buffers may have a row stride (elements; 0 = dense) and need only the
+ * alignment of their element type: rows that all start on 16-byte boundaries
+ * take the wide loads, others the same kernels element by element.  In-place
+ * use is allowed where an output is said to alias an input, with the same row
+ * stride; other overlaps are not.
+ * ------------------------------------------------------------------------ */
+
+/* How the gate of moe_block_norm spreads over its rows. */
+enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2, MOE_GATE_ELEMENT = 3 };
+
+typedef struct moe_norm_args {
+  int32_t T, H;      /* rows; channels, 1 <= H <= 16384 */
+  int32_t dtype;     /* y, h, dy, dh and an element gate */
+  int32_t rdtype;    /* the residual rows r, r_out, dr_out, dr: dtype or MOE_F32 */
+  int32_t wdtype;    /* w_post, w_pre and a channel gate: dtype or MOE_F32 */
+  int32_t gate_kind; /* enum moe_gate */
+  float scale, eps, weight_offset;
+  int32_t reserved;  /* 0 */
+  /* Row strides, elements; 0 means H. */
+  int64_t ld_r, ld_y, ld_gate, ld_r_out, ld_h, ld_dr_out, ld_dh, ld_dr, ld_dy, ld_dgate;
+  const void *r;      /* [T, H] rdtype (forward) */
+  const void *y;      /* [T, H] dtype: the block's output, or NULL (forward: h alone) */
+  const void *w_post; /* [H] wdtype, or NULL: no norm after the block */
+  const void *w_pre;  /* [H] wdtype, or NULL: no norm before the next block */
+  const void *gate;   /* token: [T] float; channel: [H] wdtype; element: [T, H] dtype */
+  void *r_out;        /* [T, H] rdtype: out of the forward (may be r), in for the backward */
+  void *h;            /* [T, H] dtype out of the forward; needs w_pre */
+  /* backward */
+  const void *dr_out; /* [T, H] rdtype or NULL (zero) */
+  const void *dh;     /* [T, H] dtype; needs w_pre */
+  void *dr;           /* [T, H] rdtype out (may be dr_out) */
+  void *dy;           /* [T, H] dtype out (may be dh) */
+  float *dw_post;     /* [H] out; needs w_post */
+  float *dw_pre;      /* [H] out; needs w_pre */
+  void *dgate;        /* token: [T] float; channel: [H] float; element: [T, H] dtype; out */
+} moe_norm_args_t;
+
+/*
+ * moe_block_norm -- the join between two blocks in one pass over the rows:
+ * norm after a block, its gate, the scaled residual sum, and the norm before
+ * the next block.  With n(v; w) = v * rsqrt(mean(v^2) + eps) * (w + weight_offset):
+ *
+ *   r_out = r + scale * gate * n(y; w_post)     (n left out where w_post is NULL)
+ *   h     = n(r + scale * gate * n(y; w_post); w_pre)    (where w_pre is not NULL)
+ *
+ * y = NULL: h = n(r; w_pre) and r_out is not written (no gate, no w_post).
+ * Everything is FP32 inside, each output rounded once; h is computed from the
+ * unrounded sum.  Every sum runs in an order that depends on H only, so a
+ * row's outputs do not depend on T or on the other rows.
+ */
+int moe_block_norm(const moe_norm_args_t *a, void *stream);
+
+/*
+ * moe_block_norm_backward -- gradients of moe_block_norm.  With
+ * J(v; w)' d = rstd * (d w - v rstd * mean(d w v rstd)), rstd = rsqrt(mean(v^2) + eps),
+ * w already with its offset, all statistics recomputed from r_out and y:
+ *
+ *   dr = dr_out + J(r_out; w_pre)' dh          u  = scale * gate * dr
+ *   dy = J(y; w_post)' u                       dgate = scale * dr * n(y; w_post), summed over
+ *   dw_pre = sum_t dh * r_out rstd                     what the gate was spread over
+ *   dw_post = sum_t u * y rstd
+ *
+ * Reads r_out (as the forward stored it), not r.  dr may be NULL where w_pre
+ * is (it is then dr_out itself); y = NULL: dr and dw_pre alone.  The float
+ * gradients of weights and gates are overwritten and summed over the rows in
+ * a fixed order (set by T, H and the device's number of SMs).  Rows of a
+ * token are independent of the batch.  Workspace:
+ * moe_block_norm_workspace_size(a) bytes, 256-byte aligned.
+ */
+size_t moe_block_norm_workspace_size(const moe_norm_args_t *a);
+int moe_block_norm_backward(const moe_norm_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+typedef struct moe_embed_args {
+  int32_t T, H, V;    /* T < 2^31 tokens, H >= 1 channels, 1 <= V < 2^20 rows of the table */
+  int32_t dtype;      /* table */
+  int32_t odtype;     /* out (forward), dout (backward) */
+  int32_t ids64;      /* 1: ids are int64, 0: int32 */
+  float scale;
+  int32_t accumulate; /* backward: 1 adds to dtable, 0 overwrites it */
+  int64_t padding_id; /* backward: this token gets no gradient; -1: none */
+  int64_t ld_table, ld_out; /* row strides, elements; 0 means H (ld_out: out and dout) */
+  const void *ids;    /* [T] */
+  const void *table;  /* [V, H] dtype (forward) */
+  void *out;          /* [T, H] odtype (forward) */
+  const void *dout;   /* [T, H] odtype (backward) */
+  float *dtable;      /* [V, H] dense (backward) */
+} moe_embed_args_t;
+
+/*
+ * moe_embed -- out[t] = scale * table[ids[t]], one rounding.  An id outside
+ * [0, V) fails closed: its row is zeros and the device status word records
+ * code 5.
+ */
+int moe_embed(const moe_embed_args_t *a, void *stream);
+
+/*
+ * moe_embed_backward -- dtable[v] = scale * sum over t with ids[t] = v of
+ * dout[t] (plus dtable[v] where `accumulate`), FP32.  The tokens are sorted
+ * (stable) and the rows of one token summed in ascending t, in runs of
+ * sorted positions whose bounds depend on the ids alone, joined in order: no
+ * atomics, the same bits every time.  Ids outside [0, V) are left out
+ * and recorded (code 5); padding_id is left out.  T = 0 zeroes dtable unless
+ * `accumulate`.  Workspace: moe_embed_workspace_size(a) bytes.
+ */
+size_t moe_embed_workspace_size(const moe_embed_args_t *a);
+int moe_embed_backward(const moe_embed_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+typedef struct moe_distill_args {
+  int32_t T, V, K;   /* rows; vocabulary, V >= 1; teacher slots, 1 <= K <= 256 */
+  int32_t dtype;     /* logits, dlogits */
+  float temperature; /* > 0 */
+  float scale;       /* factor of the loss (temperature^2 keeps gradients comparable) */
+  int64_t ld_logits, ld_dlogits; /* row strides, elements; 0 means V */
+  const void *logits;     /* [T, V] dtype: the student's */
+  const int32_t *t_ids;   /* [T, K] the teacher's tokens, any order; -1: no such slot */
+  const float *t_logits;  /* [T, K] its logits (or log-probabilities) */
+  const float *t_lse;     /* [T] or NULL, see below */
+  const float *weight;    /* [T]: d(total)/d(loss_t) (backward, step) */
+  float *loss;            /* [T] out (forward, step) */
+  float *lse;             /* [T] out of the forward, in for the backward; the step may leave it NULL */
+  void *dlogits;          /* [T, V] dtype out (backward, step); may be logits */
+} moe_distill_args_t;
+
+/*
+ * moe_distill -- distillation from a teacher's top logits.  With tau the
+ * temperature, q = softmax(logits / tau) over the vocabulary and
+ *   p_k = exp(t_k / tau - c),  c = log sum_k exp(t_k / tau)  (p sums to 1), or
+ *   c = t_lse, the teacher's own log-sum-exp over its whole vocabulary (at
+ *   this temperature), where given (p sums to at most 1):
+ *
+ *   loss_t = scale * sum_k p_k (log p_k - log q[id_k])
+ *   lse_t  = log sum_v exp(logits_v / tau)
+ *
+ * Slots with id -1 or a teacher logit of -inf do not count (p log p is 0 at
+ * p = 0); an id below -1 or at V or above is left out and recorded (code 6);
+ * an id given twice counts twice.  A row with no slot has loss 0 and a zero
+ * gradient.  Student logits of -inf have q = 0 (a teacher token there makes
+ * the loss +inf); a row of nothing but -inf has lse -inf, loss +inf and a
+ * zero gradient.  FP32 inside.
+ */
+int moe_distill(const moe_distill_args_t *a, void *stream);
+
+/*
+ * moe_distill_backward -- dlogits_t = weight_t * scale / tau * (P q - p at
+ * its ids), P = sum p, from the forward's lse; one rounding.  Rows of weight
+ * 0 or without slots are zeros whatever their logits hold.
+ */
+int moe_distill_backward(const moe_distill_args_t *a, void *stream);
+
+/* moe_distill_step -- loss and dlogits in one pass: each row's logits are read
+ * once and stay on chip between the two (where they fit there). */
+int moe_distill_step(const moe_distill_args_t *a, void *stream);
+
 /*
  * moe_device_status -- read (and, if `reset`, clear) the device status word
  * of the current device.  Synchronises the device.  Returns MOE_OK when no
@@ -524,7 +688,8 @@ int moe_backward_ep(const moe_dims_t *d, int32_t e_begin, int32_t e_end, int32_t
  * MOE_ERR_CUDA.  Codes: 1 = expert id out of range in moe_permute or
  * moe_route_replay, 4 = expert id repeated within a token in moe_route_replay,
  * 2 = a pipeline wait in a tensor-core kernel timed out,
- * 3 = tensor-memory allocation failed.
+ * 3 = tensor-memory allocation failed, 5 = token id out of range in moe_embed
+ * or moe_embed_backward, 6 = teacher id out of range in moe_distill*.
  */
 int moe_device_status(int reset, int32_t *detail);
 

@@ -1,0 +1,230 @@
+"""block_norm and its gradients against the plain 64-bit form."""
+import pytest
+import torch
+
+import _step_ref as ref
+import top_routed_grouped_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+EPS = 1e-6
+
+
+def make(T, H, dtype, rdtype, wdtype, post=True, pre=True, block=True, gate="none", offset=0.0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(1000 * seed + 7 * T + H)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    c = {"r": rn(T, H).to(rdtype), "y": rn(T, H).to(dtype) if block else None,
+         "w_post": (1 - offset + 0.2 * rn(H)).to(wdtype) if post and block else None,
+         "w_pre": (1 - offset + 0.2 * rn(H)).to(wdtype) if pre else None, "gate": None}
+    if block:
+        c["gate"] = {"none": lambda: None, "token": lambda: rn(T, 1), "channel": lambda: rn(H).to(wdtype),
+                     "element": lambda: rn(T, H).to(dtype)}[gate]()
+    c["dr_out"], c["dh"] = rn(T, H).to(rdtype), rn(T, H).to(dtype) if pre else None
+    return c
+
+
+def forward_ok(c, dtype, scale, offset, **kw):
+    r_out, h = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"], scale=scale, eps=EPS,
+                              weight_offset=offset, dtype=dtype, **kw)
+    want = ref.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"], scale, EPS, offset)
+    if c["y"] is not None:
+        assert r_out.dtype == c["r"].dtype
+        ref.check(r_out, *want["r_out"], what="r_out")
+    else:
+        assert r_out is c["r"]
+    if c["w_pre"] is not None:
+        assert h.dtype == dtype
+        ref.check(h, *want["h"], what="h")
+    else:
+        assert h is None
+    return r_out, h
+
+
+def backward_ok(c, r_out, scale, offset):
+    got = moe.block_norm_backward(c["dr_out"], c["dh"], r_out, c["y"], c["w_post"], c["w_pre"], c["gate"],
+                                  scale=scale, eps=EPS, weight_offset=offset)
+    want = ref.block_norm_backward(c["dr_out"], c["dh"], r_out, c["y"], c["w_post"], c["w_pre"], c["gate"], scale,
+                                   EPS, offset)
+    T = c["r"].shape[0]
+    for name in ("dr", "dy", "dw_post", "dw_pre", "dgate"):
+        assert (got[name] is None) == (name not in want), name
+        if name in want:
+            sums = name.startswith("dw") or (name == "dgate" and c["gate"].dim() == 1)
+            tokens = name == "dgate" and c["gate"].dim() == 2 and c["gate"].shape[1] == 1
+            ref.check(got[name], *want[name], ops=ref.ROW + (T if sums else 0) + (64 if tokens else 0), what=name)
+    return got
+
+
+TYPES = [(F32, F32, F32), (BF16, BF16, BF16), (BF16, F32, F32), (BF16, F32, BF16), (BF16, BF16, F32)]
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 2), (5, 7), (2, 31), (33, 64), (9, 100), (4, 257), (37, 256), (1, 2048),
+                                 (700, 1001), (513, 2048), (6, 4104), (3, 8192), (2, 11111), (2, 16384)])
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x).split(".")[1] for x in t))
+def test_join_and_gradients(T, H, types):
+    c = make(T, H, *types, gate="none")
+    r_out, _ = forward_ok(c, types[0], 0.5, 0.0)
+    backward_ok(c, r_out, 0.5, 0.0)
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "element"])
+@pytest.mark.parametrize("post,pre,block", [(True, True, True), (False, True, True), (True, False, True),
+                                            (False, False, True), (False, True, False)])
+@pytest.mark.parametrize("T,H", [(35, 96), (12, 77), (130, 2048)])
+@pytest.mark.parametrize("types", TYPES[:3], ids=lambda t: "-".join(str(x).split(".")[1] for x in t))
+def test_forms(gate, post, pre, block, T, H, types):
+    if not block and gate != "none":
+        pytest.skip("a gate belongs to y")
+    c = make(T, H, *types, post=post, pre=pre, block=block, gate=gate, offset=1.0)
+    r_out, _ = forward_ok(c, types[0], -1.5, 1.0)
+    if block or pre:
+        backward_ok(c, r_out, -1.5, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_upstream_for_the_residual(dtype):
+    c = make(19, 320, dtype, F32, F32, gate="element")
+    c["dr_out"] = None
+    r_out, _ = forward_ok(c, dtype, 1.0, 0.0)
+    backward_ok(c, r_out, 1.0, 0.0)
+
+
+@pytest.mark.parametrize("shift,pad", [(0, 8), (1, 3), (8, 24), (3, 0)])
+@pytest.mark.parametrize("types", TYPES[:3], ids=lambda t: "-".join(str(x).split(".")[1] for x in t))
+def test_strided_and_misaligned_rows(shift, pad, types):
+    """Rows that are windows of wider ones, each tensor at its own offset."""
+    c = make(21, 264, *types, gate="element")
+
+    def window(t, s):
+        wide = torch.full((t.shape[0], t.shape[1] + shift + pad + s), float("nan"), device="cuda", dtype=t.dtype)
+        wide[:, s + shift:s + shift + t.shape[1]] = t
+        return wide[:, s + shift:s + shift + t.shape[1]]
+
+    dense = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    w = dict(c, **{n: window(c[n], 8 * i) for i, n in enumerate(("r", "y", "gate", "dr_out", "dh"))})
+    r_out, h = forward_ok(w, types[0], 1.0, 0.0)
+    if (264 + shift + pad) % 8 == 0 and shift % 8 == 0:
+        assert torch.equal(r_out, dense[0]) and torch.equal(h, dense[1])
+    backward_ok(w, window(r_out, 0), 1.0, 0.0)
+
+
+def test_transposed_and_broadcast_rows_are_taken():
+    c = make(16, 48, F32, F32, F32)
+    c["y"] = c["y"].t().contiguous().t()
+    c["dh"] = c["dh"][:1].expand(16, 48)
+    c["r"] = c["r"][:1].expand(16, 48)
+    r_out, _ = forward_ok(c, F32, 1.0, 0.0)
+    backward_ok(c, r_out, 1.0, 0.0)
+
+
+def test_in_place():
+    c = make(50, 512, BF16, F32, F32, gate="token")
+    want = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    r = c["r"].clone()
+    got = moe.block_norm(r, c["y"], c["w_post"], c["w_pre"], c["gate"], inplace=True)
+    assert got[0] is r and torch.equal(r, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_no_tokens():
+    c = make(0, 64, BF16, BF16, BF16, gate="channel")
+    r_out, h = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    assert r_out.shape == (0, 64) and h.shape == (0, 64)
+    g = moe.block_norm_backward(c["dr_out"], c["dh"], r_out, c["y"], c["w_post"], c["w_pre"], c["gate"])
+    for n in ("dw_post", "dw_pre", "dgate"):
+        assert g[n].shape == (64,) and not g[n].any()
+
+
+def test_zero_and_odd_rows():
+    """Rows of zeros (only eps under the root), huge and tiny ones, and a row
+    of NaN, which stays alone."""
+    c = make(6, 128, F32, F32, F32)
+    c["r"][0] = c["y"][0] = 0
+    c["r"][1] *= 1e12
+    c["y"][2] *= 1e-18
+    c["y"][3] *= 1e15
+    forward_ok(c, F32, 1.0, 0.0)
+    c["y"][4, 5] = float("nan")
+    c["r"][5, 7] = float("inf")
+    r_out, h = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"])
+    assert torch.isnan(h[4]).all() and torch.isfinite(h[:4]).all() and torch.isnan(h[5, 7])
+
+
+@pytest.mark.parametrize("types,H", [(TYPES[0], 1001), (TYPES[1], 2048), (TYPES[2], 64), (TYPES[1], 77)])
+def test_rows_do_not_depend_on_the_batch(types, H):
+    c = make(777, H, *types, gate="token")
+    full = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    g = moe.block_norm_backward(c["dr_out"], c["dh"], full[0], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    for rows in (slice(0, 1), slice(5, 6), slice(100, 333), slice(776, 777)):
+        part = moe.block_norm(c["r"][rows], c["y"][rows], c["w_post"], c["w_pre"], c["gate"][rows])
+        assert torch.equal(part[0], full[0][rows]) and torch.equal(part[1], full[1][rows])
+        p = moe.block_norm_backward(c["dr_out"][rows], c["dh"][rows], full[0][rows], c["y"][rows], c["w_post"],
+                                    c["w_pre"], c["gate"][rows])
+        for n in ("dr", "dy", "dgate"):
+            assert torch.equal(p[n], g[n][rows]), n
+    again = moe.block_norm_backward(c["dr_out"], c["dh"], full[0], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    assert all(torch.equal(again[n], g[n]) for n in g)
+
+
+def test_gradients_against_differences():
+    """Central differences of sum(a r_out + b h) along random directions.  The
+    loss is summed in 64 bits; with step 1e-2 the cut-off error is of order
+    1e-4 of the derivative's terms and the outputs' roundings, 2^-24 of each
+    over the step, are below that."""
+    T, H = 11, 200
+    c = make(T, H, F32, F32, F32, gate="element")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    a, b = torch.randn(T, H, generator=g, device="cuda"), torch.randn(T, H, generator=g, device="cuda")
+
+    def loss(d):
+        r_out, h = moe.block_norm(d["r"], d["y"], d["w_post"], d["w_pre"], d["gate"], scale=0.7)
+        return float((a.double() * r_out.double()).sum() + (b.double() * h.double()).sum())
+
+    r_out, _ = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"], scale=0.7)
+    grad = moe.block_norm_backward(a, b, r_out, c["y"], c["w_post"], c["w_pre"], c["gate"], scale=0.7)
+    for name, key in (("r", "dr"), ("y", "dy"), ("w_post", "dw_post"), ("w_pre", "dw_pre"), ("gate", "dgate")):
+        v = torch.randn(c[name].shape, generator=g, device="cuda")
+        step = 1e-2
+        num = (loss(dict(c, **{name: c[name] + step * v})) - loss(dict(c, **{name: c[name] - step * v}))) / (2 * step)
+        terms = (grad[key].double() * v.double())
+        assert abs(num - float(terms.sum())) <= 2e-3 * float(terms.abs().sum()), name
+
+
+def test_side_stream():
+    c = make(64, 1024, BF16, BF16, BF16)
+    want = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], stream=s)
+    g = moe.block_norm_backward(c["dr_out"], c["dh"], got[0], c["y"], c["w_post"], c["w_pre"], stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    w = moe.block_norm_backward(c["dr_out"], c["dh"], want[0], c["y"], c["w_post"], c["w_pre"])
+    assert all(g[n] is None or torch.equal(g[n], w[n]) for n in g)
+
+
+def test_refusals():
+    c = make(4, 64, BF16, F32, F32)
+    ok = lambda **k: moe.block_norm(**dict(dict(r=c["r"], y=c["y"], w_post=c["w_post"], w_pre=c["w_pre"]), **k))  # noqa: E731
+    ok()
+    for bad in (dict(y=c["y"][:3]), dict(y=c["y"].half()), dict(r=c["r"].to(BF16).half()), dict(w_post=c["w_post"][:5]),
+                dict(w_post=c["w_post"].to(BF16)), dict(gate=torch.ones(4, 2, device="cuda")),
+                dict(gate=torch.ones(4, 1, device="cuda", dtype=BF16)), dict(y=None), dict(r=c["r"].cpu()),
+                dict(y=None, w_post=None, w_pre=None)):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(moe.MoEError):
+        ok(eps=-1.0)
+    with pytest.raises(moe.MoEError):
+        ok(scale=float("nan"))
+    wide = torch.ones(2, 16392, device="cuda")
+    with pytest.raises(moe.MoEError) as e:
+        moe.block_norm(wide, None, None, wide[0])
+    assert e.value.status == -2
+    with pytest.raises(moe.MoEError) as e:
+        moe.block_norm_backward(c["dr_out"], c["dh"], c["r"], c["y"], c["w_post"], c["w_pre"],
+                                ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -3
+    with pytest.raises(ValueError):
+        moe.block_norm_backward(c["dr_out"], None, c["r"], c["y"], c["w_post"], c["w_pre"])
+    with pytest.raises(ValueError):
+        moe.block_norm_backward(None, None, None, c["y"], c["w_post"])

@@ -10,6 +10,9 @@ lower-case helpers (``route``, ``permute``, ``grouped_ffn``, ``combine``,
 There is no fallback: if the library is missing, ``lib()`` raises.  Build it
 with ``python -m top_routed_grouped_gb300.build`` (or ``__graft_entry__.build()``).
 
+The operators around the layer (``step.py``) are reached the same way:
+``embed``, ``block_norm``, ``distill`` and their gradients.
+
 ``MoELayer`` / ``MoEFunction`` (``layer.py``): the layer as a torch module
 whose autograd Function calls ``moe_forward`` and ``moe_backward``.
 """
@@ -29,7 +32,10 @@ STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3:
 EXPORTED = ("moe_workspace_size", "moe_status_string", "moe_route", "moe_permute", "moe_grouped_ffn",
             "moe_combine", "moe_forward", "moe_backward", "moe_device_status", "moe_permute_noalloc",
             "moe_route_replay", "moe_grouped_ffn_ep", "moe_combine_sorted", "moe_router_logits",
-            "moe_backward_ep", "moe_grouped_ffn_etp", "moe_etp_reduce", "moe_grouped_ffn_etp_fused")
+            "moe_backward_ep", "moe_grouped_ffn_etp", "moe_etp_reduce", "moe_grouped_ffn_etp_fused",
+            "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward", "moe_embed",
+            "moe_embed_workspace_size", "moe_embed_backward", "moe_distill", "moe_distill_backward",
+            "moe_distill_step")
 
 _vp = ctypes.c_void_p
 
@@ -103,6 +109,16 @@ def lib() -> ctypes.CDLL:
                                      _vp, ctypes.c_size_t, _vp], ctypes.c_int),
                 "moe_device_status": ([ctypes.c_int, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
                 "moe_permute_noalloc": ([D] + [_vp] * 4 + [_vp], ctypes.c_int),
+                # The operators around the layer take a packed struct (bytes; see step.py).
+                "moe_block_norm": ([ctypes.c_char_p, _vp], ctypes.c_int),
+                "moe_block_norm_workspace_size": ([ctypes.c_char_p], ctypes.c_size_t),
+                "moe_block_norm_backward": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_embed": ([ctypes.c_char_p, _vp], ctypes.c_int),
+                "moe_embed_workspace_size": ([ctypes.c_char_p], ctypes.c_size_t),
+                "moe_embed_backward": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_distill": ([ctypes.c_char_p, _vp], ctypes.c_int),
+                "moe_distill_backward": ([ctypes.c_char_p, _vp], ctypes.c_int),
+                "moe_distill_step": ([ctypes.c_char_p, _vp], ctypes.c_int),
             }
             for name, (args, res) in sigs.items():
                 fn = getattr(L, name)
@@ -420,10 +436,20 @@ def backward(fwd: dict, dy, x, w_router, w_shared_gate, w_gate_up, w_down, ws_ga
     return out
 
 
+_STEP = ("block_norm", "block_norm_backward", "embed", "embed_backward", "distill", "distill_backward", "distill_step",
+         "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward", "moe_embed",
+         "moe_embed_workspace_size", "moe_embed_backward", "moe_distill", "moe_distill_backward", "moe_distill_step")
+
+
 def __getattr__(name):
-    # The torch module lives in layer.py (imported on first use, so that this
-    # binding itself does not import torch at load time).
+    # The torch modules and the operators around the layer live in files of
+    # their own (imported on first use, so that this binding itself does not
+    # import torch at load time).
     if name in ("MoELayer", "MoEFunction"):
         from . import layer
         return getattr(layer, name)
+    if name in _STEP:
+        from . import step
+        globals().update({n: getattr(step, n) for n in _STEP})
+        return globals()[name]
     raise AttributeError(name)

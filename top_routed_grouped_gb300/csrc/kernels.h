@@ -187,4 +187,57 @@ cudaError_t launch_dgrad_tc(const BwArgs &a, void *scratch, int *status, cudaStr
 // dWdn, dWgu and the shared expert's weight gradients.
 cudaError_t launch_wgrad_tc(const BwArgs &a, int *status, cudaStream_t stream);
 
+// ---- block_norm.cu ----
+// moe_norm_args with its types as flags and its strides filled in.
+struct NormArgs {
+  int T, H;
+  bool f32, rf32, wf32;  // rows, residual rows, weights: float (else bf16)
+  int gate_kind;
+  float scale, eps, offset;
+  int64_t ld_r, ld_y, ld_gate, ld_r_out, ld_h, ld_dr_out, ld_dh, ld_dr, ld_dy, ld_dgate;
+  const void *r, *y, *w_post, *w_pre, *gate;
+  void *r_out, *h;
+  const void *dr_out, *dh;
+  void *dr, *dy;
+  float *dw_post, *dw_pre;
+  void *dgate;
+};
+constexpr int NORM_MAX_H = 16384;
+cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t stream);
+size_t block_norm_scratch_bytes(const NormArgs &a);
+cudaError_t launch_block_norm_bwd(const NormArgs &a, void *scratch, cudaStream_t stream);
+
+// ---- embed.cu ----
+struct EmbedArgs {
+  int T, H, V;
+  bool f32, of32;  // table, out / dout: float (else bf16)
+  int ids64, accumulate;
+  float scale;
+  int64_t padding_id, ld_table, ld_out;
+  const void *ids, *table;
+  void *out;
+  const void *dout;
+  float *dtable;
+};
+cudaError_t launch_embed(const EmbedArgs &a, int *status, cudaStream_t stream);
+size_t embed_scratch_bytes(const EmbedArgs &a);
+cudaError_t launch_embed_bwd(const EmbedArgs &a, void *scratch, int *status, cudaStream_t stream);
+
+// ---- distill.cu ----
+struct DistillArgs {
+  int T, V, K;
+  bool f32;  // logits, dlogits: float (else bf16)
+  float inv_tau, scale;
+  int64_t ld_logits, ld_dlogits;
+  const void *logits;
+  const int32_t *t_ids;
+  const float *t_logits, *t_lse, *weight;
+  float *loss, *lse;
+  void *dlogits;
+};
+constexpr int DISTILL_MAX_K = 256;
+enum { DISTILL_LOSS = 1, DISTILL_GRAD = 2 };
+// mode: DISTILL_LOSS (loss, lse), DISTILL_GRAD (dlogits from lse) or both.
+cudaError_t launch_distill(const DistillArgs &a, int mode, int *status, cudaStream_t stream);
+
 }  // namespace moe
