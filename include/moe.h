@@ -635,7 +635,7 @@ size_t moe_embed_workspace_size(const moe_embed_args_t *a);
 int moe_embed_backward(const moe_embed_args_t *a, void *ws, size_t ws_bytes, void *stream);
 
 typedef struct moe_distill_args {
-  int32_t T, V, K;   /* rows, T <= 2^27; vocabulary, V >= 1; teacher slots, 1 <= K <= 256 */
+  int32_t T, V, K;   /* rows, T <= 2^27; vocabulary, 1 <= V <= 2^28; teacher slots, 1 <= K <= 256 */
   int32_t dtype;     /* logits, dlogits */
   float temperature; /* > 0 */
   float scale;       /* factor of the loss (temperature^2 keeps gradients comparable) */

@@ -198,7 +198,7 @@ static int distill_run(const moe_distill_args_t *a, int mode, void *stream) {
   if (!(a->temperature > 0.f) || !isfinite(a->temperature) || !isfinite(a->scale)) return MOE_ERR_INVALID_ARG;
   if (!isfinite(1.f / a->temperature) || !stride_ok(a->ld_logits, a->V) || !stride_ok(a->ld_dlogits, a->V))
     return MOE_ERR_INVALID_ARG;
-  if (a->K > DISTILL_MAX_K || a->T > DISTILL_MAX_T) return MOE_ERR_UNSUPPORTED;
+  if (a->K > DISTILL_MAX_K || a->T > DISTILL_MAX_T || a->V > DISTILL_MAX_V) return MOE_ERR_UNSUPPORTED;
   if (a->T == 0) return MOE_OK;
   const int e = type_size(a->dtype);
   if (!there(a->logits, e) || !there(a->t_ids, 4) || !there(a->t_logits, 4) || !maybe(a->t_lse, 4) || !maybe(a->lse, 4))

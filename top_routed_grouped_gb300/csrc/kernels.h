@@ -235,7 +235,7 @@ struct DistillArgs {
   float *loss, *lse;
   void *dlogits;
 };
-constexpr int DISTILL_MAX_K = 256, DISTILL_MAX_T = 1 << 27;
+constexpr int DISTILL_MAX_K = 256, DISTILL_MAX_T = 1 << 27, DISTILL_MAX_V = 1 << 28;
 enum { DISTILL_LOSS = 1, DISTILL_GRAD = 2 };
 // mode: DISTILL_LOSS (loss, lse), DISTILL_GRAD (dlogits from lse) or both.
 cudaError_t launch_distill(const DistillArgs &a, int mode, int *status, cudaStream_t stream);

@@ -109,19 +109,20 @@ inline int device_sms() {
   return n;
 }
 
+constexpr int ENSURE_SMEM_KERNELS = 64;  // more than the library has
 // Opt `fn` in to `bytes` of dynamic shared memory once per device.
 inline cudaError_t ensure_smem(const void *fn, int bytes) {
   static std::mutex mu;
-  static const void *done[64][16] = {};
+  static const void *done[64][ENSURE_SMEM_KERNELS] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
   const void **row = done[dev & 63];
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < ENSURE_SMEM_KERNELS; ++i)
     if (row[i] == fn) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < ENSURE_SMEM_KERNELS; ++i)
     if (!row[i]) {
       row[i] = fn;
       break;

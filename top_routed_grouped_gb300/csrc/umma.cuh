@@ -51,16 +51,31 @@ __device__ inline bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same, seeing what other CTAs of the cluster wrote before they arrived.
+__device__ inline bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase of `bar` with the given parity to complete.  Gives up
 // (returns false) when another thread of the CTA raised `abort_flag`, or
 // after `timeout_ns`, in which case it raises the flag and records
 // STATUS_WAIT_TIMEOUT in the device status word.
+template <bool CLUSTER = false>
 __device__ inline bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status,
                                  uint64_t timeout_ns = WAIT_TIMEOUT_NS) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if ((it & 63) == 0) {
       if (*abort_flag) return false;
       if (globaltimer() - t0 > timeout_ns) {
@@ -70,6 +85,9 @@ __device__ inline bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *a
       }
     }
   }
+}
+__device__ inline bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status) {
+  return mbar_wait<true>(bar, parity, abort_flag, status);
 }
 
 // ---------------------------------------------------------------- TMA
