@@ -1,0 +1,759 @@
+// Distillation from a teacher's top logits: loss, gradient, and both in one
+// call (contracts with moe_distill in moe.h).
+//
+//   lse = m / tau + log s,  m = max z,  s = sum exp((z - m) / tau)
+//   dz  = w (P exp((z - m) / tau) / s - p at the teacher's ids)
+//
+// A row belongs to a cluster of CTAs (one, where it is short), every CTA to a
+// slice of it, every thread to some 16-byte units of the slice.  Clusters walk
+// over the rows; three slices stand in shared memory, one whose gradient is
+// written, one whose statistics are taken and one on its way, so that a row is
+// read from memory once and nothing waits for it.  The warps of a CTA:
+//   producer   loads the teacher's slots a row ahead, starts the bulk copies,
+//              turns the slots into p
+//   consumers  statistics of row j + 1, then gradient of row j
+//   joiner     joins the warps' statistics, hands them to the other CTAs
+//              through distributed shared memory, sums the loss, and writes
+//              the teacher's places of the gradient again, p subtracted,
+//              behind the dense pass
+// They meet at mbarriers alone; no barrier stops a whole CTA.
+// The maximum is taken before the exponentials, in a thread's own units first;
+// the (max, sum) pairs of threads, warps and CTAs are joined in a fixed order.
+// The shape goes by the vocabulary alone, so a row's results do not depend on
+// the batch, and a thread's units do not depend on where the row starts.
+// Rows too long for the shared memory of a cluster take a plainer kernel that
+// reads them twice.
+//
+// Exponents are differences of logits before they are scaled, so that rows at
+// the type's lowest value do not overflow.
+#pragma once
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_host.h"
+#include "umma.cuh"
+
+namespace moe {
+
+constexpr float DS_LOG2E = 1.4426950408889634f;
+
+__device__ inline float ds_neg_inf() { return __int_as_float(0xff800000); }
+
+// 2^x in hardware (two units in the last place; results below 2^-126 are 0).
+__device__ inline float ds_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two FP32 lanes in one instruction.
+struct DsPair {
+  uint64_t v;
+  __device__ inline DsPair() {}
+  __device__ inline DsPair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ inline void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ inline DsPair ds_add2(DsPair a, DsPair b) {
+  DsPair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ inline DsPair ds_mul2(DsPair a, DsPair b) {
+  DsPair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ inline DsPair ds_fma2(DsPair a, DsPair b, DsPair c) {
+  DsPair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// Keeps the compiler from holding what was unpacked from `v` beside it.
+__device__ inline void ds_opaque(uint4 &v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+
+__device__ inline float ds_warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, d));
+  return v;
+}
+__device__ inline float ds_warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+  return v;
+}
+
+// Max of logits and sum of 2^(k (. - max)); (-inf, 0) is empty.
+struct DsStat {
+  float m, s;
+};
+// The pairs of a warp's lanes as one.
+__device__ inline DsStat ds_warp_join(DsStat a, float k) {
+  const float m = ds_warp_max(a.m);
+  const float base = m == ds_neg_inf() ? 0.f : m;
+  return {m, ds_warp_sum(a.s * exp2f((a.m - base) * k))};
+}
+
+// Elements n.. of the 2 N elements of (lo, hi), sh = n sizeof(T) bytes.
+__device__ inline uint4 ds_funnel(const uint4 &lo, const uint4 &hi, int sh) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (sh & 8)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (sh & 4)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if (sh & 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Units of a row: unit u holds elements u N .. u N + N - 1.  A row may start
+// `off` elements past a 16-byte boundary; its units are then put together from
+// the two aligned pieces that they lie in, so that what a thread holds does
+// not depend on where the row stands.
+template <typename T>
+struct DsUnit {
+  static constexpr int N = 16 / sizeof(T);
+  // Whether the aligned piece c (elements c N - off ...) lies in the row.
+  static __device__ inline bool piece_in(int off, int c, int V) {
+    const int i = c * N - off;
+    return i >= 0 && i + N <= V;
+  }
+  // Unit u element by element; what is not of the row reads as -inf.
+  static __device__ __noinline__ uint4 edge(const T *row, int u, int V) {
+    uint4 v;
+    T *e = (T *)&v;
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = u * N + j < V ? row[u * N + j] : Elem<T>::from_f32(ds_neg_inf());
+    return v;
+  }
+  // Unit u, from its aligned pieces (`pieces` is where piece u stands, in
+  // shared memory or in the row itself) where they are of the row.
+  template <bool ALIGNED>
+  static __device__ inline uint4 load(const uint4 *pieces, const T *row, int off, int u, int V) {
+    if (ALIGNED || off == 0) {
+      if ((u + 1) * N <= V) return *pieces;
+    } else if (piece_in(off, u, V) && piece_in(off, u + 1, V)) {
+      return ds_funnel(pieces[0], pieces[1], off * (int)sizeof(T));
+    }
+    return edge(row, u, V);
+  }
+  static __device__ __noinline__ void edge_store(T *row, int u, int V, uint4 v, int from, int to) {
+    const T *e = (const T *)&v;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j >= from && j < to && u * N + j < V) row[u * N + j] = e[j];
+  }
+  // The whole warp: lane l holds unit u of consecutive ones.
+  template <bool ALIGNED>
+  static __device__ inline void store(T *row, int off, int u, int V, const uint4 &v) {
+    const int i = u * N, lane = threadIdx.x & 31;
+    int from = 0, to = N;  // what is left to write element by element
+    if (ALIGNED || off == 0) {
+      if (i + N <= V) {
+        __stcs((uint4 *)(row + i), v);
+        return;
+      }
+    } else {
+      // The aligned piece that ends in this unit: the tail of the unit before
+      // it and N - off of its own elements.
+      uint4 b;
+      b.x = __shfl_up_sync(FULL_MASK, v.x, 1);
+      b.y = __shfl_up_sync(FULL_MASK, v.y, 1);
+      b.z = __shfl_up_sync(FULL_MASK, v.z, 1);
+      b.w = __shfl_up_sync(FULL_MASK, v.w, 1);
+      if (lane > 0 && i - off + N <= V) {
+        __stcs((uint4 *)(row + i - off), ds_funnel(b, v, (N - off) * (int)sizeof(T)));
+        from = N - off;
+      }
+      // The next lane writes the rest, where there is one that does.
+      if (lane < 31 && i + 2 * N - off <= V) to = N - off;
+    }
+    if (from < to && i + from < V) edge_store(row, u, V, v, from, to);
+  }
+};
+
+// The largest element of a unit (NaN aside).
+template <typename T>
+__device__ inline float ds_unit_max(const uint4 &v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    const __nv_bfloat162 *h = (const __nv_bfloat162 *)&v;
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+}
+
+// Writes a pair to another CTA's shared memory.
+__device__ inline void ds_st_cluster(uint32_t addr, DsStat v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.m), "f"(v.s) : "memory");
+}
+
+constexpr int DS_MAX_CTAS = 8, DS_RING = 3, DS_STATS = 4;
+
+template <typename T>
+__device__ inline int ds_offset(const T *p) {
+  return (int)(((uintptr_t)p / sizeof(T)) & (DsUnit<T>::N - 1));
+}
+
+// (max, sum) of U units, joined to what the thread has.
+template <typename T, int U>
+__device__ inline DsStat ds_units_stat(uint4 (&raw)[U], DsStat mine, float k) {
+  constexpr int N = DsUnit<T>::N;
+  float m = mine.m;
+#pragma unroll
+  for (int j = 0; j < U; ++j) m = fmaxf(m, ds_unit_max<T>(raw[j]));
+  const float base = m == ds_neg_inf() ? 0.f : m;
+  const DsPair nbase(-base, -base), kk(k, k);
+  DsPair sum[2] = {DsPair(mine.s * ds_exp2((mine.m - base) * k), 0.f), DsPair(0.f, 0.f)};
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    float v[N];
+    ds_opaque(raw[j]);
+    Vec16<T>::unpack(raw[j], v);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float x, y;
+      ds_mul2(ds_add2(DsPair(v[i], v[i + 1]), nbase), kk).get(x, y);
+      sum[(i >> 1) & 1] = ds_add2(sum[(i >> 1) & 1], DsPair(ds_exp2(x), ds_exp2(y)));
+    }
+  }
+  float s0, s1;
+  ds_add2(sum[0], sum[1]).get(s0, s1);
+  return {m, s0 + s1};
+}
+
+// The gradient's dense part: w P q of two logits at a time, by
+// exp((z - m) / tau) * mul with the loss's own m (mul holds 1 / s), or by
+// exp(z / tau - lse) * mul where only lse is known.
+template <bool LOSS>
+struct DsGrad {
+  DsPair a, b, mul;
+  __device__ inline DsGrad(float m_or_lse, float k, float inv_tau, float mul_)
+      : a(-m_or_lse, -m_or_lse), b(LOSS ? k : inv_tau, LOSS ? k : inv_tau), mul(mul_, mul_) {}
+  __device__ inline void operator()(float &u, float &v) const {
+    DsPair x(u, v);
+    if (LOSS) x = ds_mul2(ds_add2(x, a), b);
+    else x = ds_mul2(ds_fma2(x, b, a), DsPair(DS_LOG2E, DS_LOG2E));
+    x.get(u, v);
+    ds_mul2(DsPair(ds_exp2(u), ds_exp2(v)), mul).get(u, v);
+  }
+};
+
+// What a row's teacher is to a CTA.
+struct __align__(16) DsSlots {
+  int id[DISTILL_MAX_K];   // -1 where there is no slot
+  float x[DISTILL_MAX_K];  // t / tau
+  float p[DISTILL_MAX_K];
+  float z[DISTILL_MAX_K];  // the student's logit there
+  float c, total, w, lse;  // p = exp(x - c), their sum; the row's weight; its lse where that is given
+  int any, read;           // whether there is a slot; whether the row's logits are loaded
+  float sub, mul;          // what DsGrad takes; mul 0 where there is no gradient
+};
+
+// One warp: the teacher's distribution from its slots.
+__device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl) {
+  const int lane = threadIdx.x & 31;
+  float c, total = 0.f;
+  if (a.t_lse) {
+    c = a.t_lse[t];
+  } else {
+    float m = ds_neg_inf(), e = 0.f;
+    for (int s = lane; s < a.K; s += 32)
+      if (sl.id[s] >= 0) m = fmaxf(m, sl.x[s]);
+    m = ds_warp_max(m);
+    for (int s = lane; s < a.K; s += 32)
+      if (sl.id[s] >= 0) e += expf(sl.x[s] - m);
+    c = m + logf(ds_warp_sum(e));
+  }
+  for (int s = lane; s < a.K; s += 32) {
+    const float p = sl.id[s] >= 0 ? expf(sl.x[s] - c) : 0.f;
+    total += p;
+    sl.p[s] = p;
+  }
+  total = ds_warp_sum(total);
+  if (lane == 0) {
+    sl.c = c;
+    sl.total = total;
+  }
+  for (int s = a.K + lane; s < (int)round_up(a.K, 4); s += 32) sl.id[s] = -1;
+}
+
+// Nothing but -inf (NaN is something).
+__device__ inline bool ds_none(DsStat st) { return st.m == ds_neg_inf() && !(st.s != st.s); }
+
+// One warp: a row's loss and lse from its statistics.
+__device__ inline void ds_loss(const DistillArgs &a, int64_t t, const DsSlots &sl, DsStat st) {
+  const int lane = threadIdx.x & 31;
+  const float logs = logf(st.s);
+  float l = 0.f;
+  for (int s = lane; s < a.K; s += 32) {
+    const float p = sl.p[s];
+    if (p != 0.f) l += p * (sl.x[s] - sl.c - fmaf(sl.z[s] - st.m, a.inv_tau, -logs));
+  }
+  l = ds_warp_sum(l);
+  if (ds_none(st)) l = -ds_neg_inf();
+  if (lane == 0) {
+    a.loss[t] = sl.any ? a.scale * l : 0.f;
+    if (a.lse) a.lse[t] = ds_none(st) ? ds_neg_inf() : fmaf(st.m, a.inv_tau, logs);
+  }
+}
+
+// The gradient at the teacher's places in [lo, hi), by `n` threads of which this is number `i`.
+template <typename T, bool LOSS>
+__device__ inline void ds_places(const DistillArgs &a, const DsSlots &sl, T *dz, int lo, int hi, float w,
+                                 const DsGrad<LOSS> &grad, int i, int n) {
+  for (int s = i; s < a.K; s += n) {
+    const int id = sl.id[s];
+    if (id < 0 || id < lo || id >= hi) continue;
+    float p = 0.f;
+    bool once = true;  // the first slot of an id writes for all of them
+    for (int j = 0; j < a.K; j += 4) {
+      const int4 q = *(const int4 *)&sl.id[j];
+      const int e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (e[r] == id) {
+          once = once && j + r >= s;
+          p += sl.p[j + r];
+        }
+    }
+    if (once) {
+      float u = sl.z[s], v = 0.f;
+      grad(u, v);
+      dz[id] = Elem<T>::from_f32(fmaf(-w, p, u));
+    }
+  }
+}
+
+// The dense part of the gradient of U units a thread.
+template <typename T, bool ALIGNED, bool LOSS, int U, typename Load>
+__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, const DsGrad<LOSS> &grad, Load load) {
+  constexpr int N = DsUnit<T>::N;
+  const int off = ALIGNED ? 0 : ds_offset(dz);
+  if (zero) {
+#pragma unroll 1
+    for (int j = 0; j < U; ++j) DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, uint4{});
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    float v[N];
+    Vec16<T>::unpack(load(j), v);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) grad(v[i], v[i + 1]);
+    uint4 o;
+    Vec16<T>::store((T *)&o, v);
+    DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, o);
+  }
+}
+
+struct DsShared {
+  DsSlots slots[DS_RING];
+  DsStat warp[DS_RING][16];
+  DsStat cta[DS_STATS][DS_MAX_CTAS];
+  uint64_t full[DS_RING], empty[DS_RING];         // a slice has arrived; the consumers are done with it
+  uint64_t ready[DS_RING], freed[DS_RING];        // a teacher is there; the joiner is done with it
+  uint64_t taken[DS_RING], stats[DS_STATS];       // the warps' pairs are there; all CTAs' pairs are there
+  uint64_t go[DS_RING];                           // the row's gradient can be written
+  int abort_flag;
+};
+
+// W: consumer warps; U: units a thread; 1 << shift: CTAs of a cluster.
+// ALIGNED: all rows start on 16-byte boundaries.
+template <typename T, bool ALIGNED, int MODE, int W, int U>
+__global__ void __launch_bounds__(32 * (W + 2), W == 16 ? 1 : W == 8 ? 2 : 4)
+distill_kernel(const DistillArgs a, int shift, int *status) {
+  using namespace umma;
+  constexpr int N = DsUnit<T>::N, SPAN = U * W * 32;
+  constexpr bool LOSS = (MODE & DISTILL_LOSS) != 0, GRAD = (MODE & DISTILL_GRAD) != 0;
+  extern __shared__ __align__(128) uint4 slices[];  // DS_RING x (SPAN + 1) aligned pieces
+  __shared__ DsShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = 1 << shift;
+  const int rank = blockIdx.x & (ctas - 1), stride = gridDim.x >> shift;
+  const float k = a.inv_tau * DS_LOG2E;
+  const int u_first = rank * SPAN, lo = u_first * N, hi = lo + SPAN * N;  // units, elements of this CTA
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < DS_RING; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], W);
+      mbar_init(&sh.ready[i], 1);
+      mbar_init(&sh.freed[i], 1);
+      mbar_init(&sh.taken[i], W);
+      mbar_init(&sh.go[i], 1);
+    }
+    for (int i = 0; i < DS_STATS; ++i) mbar_init(&sh.stats[i], ctas);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // The barriers of the whole cluster are there before anyone arrives at them.
+  if (LOSS && ctas > 1) cluster_sync();
+  griddep_launch();
+  griddep_wait();
+
+  const int64_t t0 = blockIdx.x >> shift;
+  const int rows = t0 < a.T ? (int)((a.T - 1 - t0) / stride) + 1 : 0;  // of this cluster
+  auto row_of = [&](int j) { return (const T *)a.logits + (t0 + (int64_t)j * stride) * a.ld_logits; };
+  auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, phase & 1, &sh.abort_flag, status); };
+
+  if (warp == W) {
+    // ------------------------------------------------------------ producer
+    constexpr int SL = DISTILL_MAX_K / 32;
+    int id[SL];
+    float x[SL], w = 0.f, lse = 0.f;
+    auto fetch = [&](int j) {
+      const int64_t t = t0 + (int64_t)j * stride;
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        const int s = lane + 32 * i;
+        id[i] = -1;
+        if (s < a.K) {
+          id[i] = a.t_ids[t * a.K + s];
+          x[i] = a.t_logits[t * a.K + s];
+        }
+      }
+      if (GRAD) w = a.weight[t];
+      if (!LOSS) lse = a.lse[t];
+    };
+    if (rows > 0) fetch(0);
+    for (int j = 0; j < rows; ++j) {
+      const int r = j % DS_RING, round = j / DS_RING;
+      const int64_t t = t0 + (int64_t)j * stride;
+      const T *z = row_of(j);
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        if (id[i] < -1 || id[i] >= a.V) {
+          record_status(status, STATUS_BAD_TEACHER_ID);
+          id[i] = -1;
+        }
+        x[i] *= a.inv_tau;
+        if (x[i] == ds_neg_inf()) id[i] = -1;
+        found |= id[i] >= 0;
+      }
+      const bool any = __any_sync(FULL_MASK, found);
+      // Rows that have no gradient and whose loss is 0 or not asked for are not read.
+      const bool read = (LOSS && (!GRAD || a.lse)) || (any && (LOSS || w != 0.f));
+      if (!wait(&sh.empty[r], round + 1)) break;
+      if (lane == 0) {
+        // The aligned pieces that lie in the row (none of a row that is not read).
+        const int off = ds_offset(z);
+        const int from = u_first + (off && u_first == 0 ? 1 : 0);
+        const int to = min(u_first + SPAN + (off ? 1 : 0), (a.V + off) / N);
+        const uint32_t bytes = read && to > from ? (uint32_t)(to - from) * 16 : 0;
+        if (bytes) {
+          mbar_arrive_expect_tx(&sh.full[r], bytes);
+          bulk_load(slices + r * (SPAN + 1) + (from - u_first), z - off + (int64_t)from * N, bytes, &sh.full[r]);
+        } else {
+          mbar_arrive(&sh.full[r]);
+        }
+      }
+      float zk[SL];
+#pragma unroll
+      for (int i = 0; i < SL; ++i)  // without a loss, only this CTA's places matter (others may have been written)
+        zk[i] = id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi)) ? Elem<T>::load(z + id[i]) : 0.f;
+      if (!wait(&sh.freed[r], round + 1)) break;
+      DsSlots &sl = sh.slots[r];
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        const int s = lane + 32 * i;
+        if (s < a.K) {
+          sl.id[s] = id[i];
+          sl.x[s] = x[i];
+          sl.z[s] = zk[i];
+        }
+      }
+      if (lane == 0) {
+        sl.w = w * a.scale * a.inv_tau;
+        sl.lse = lse;
+        sl.any = any;
+        sl.read = read;
+      }
+      if (j + 1 < rows) fetch(j + 1);
+      __syncwarp();
+      ds_teacher(a, t, sl);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ready[r]);
+    }
+  } else if (warp == W + 1) {
+    // ------------------------------------------------------------ joiner
+    // The teacher's places of row j, behind the dense pass.
+    auto places = [&](int j) {
+      const int r = j % DS_RING;
+      DsSlots &sl = sh.slots[r];
+      if (GRAD) {
+        if (!wait(&sh.empty[r], j / DS_RING)) return false;
+        if (sl.mul != 0.f)
+          ds_places<T, LOSS>(a, sl, (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits, lo, hi, sl.w,
+                             DsGrad<LOSS>(sl.sub, k, a.inv_tau, sl.mul), lane, 32);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.freed[r]);
+      return true;
+    };
+    bool ok = true;
+    for (int j = 0; j < rows && ok; ++j) {
+      const int r = j % DS_RING, q = j % DS_STATS;
+      DsSlots &sl = sh.slots[r];
+      if (!wait(&sh.ready[r], j / DS_RING)) break;
+      DsStat st = {sl.lse, 1.f};
+      if (LOSS) {
+        if (!wait(&sh.taken[r], j / DS_RING)) break;
+        st = {ds_neg_inf(), 0.f};
+        if (lane < W) st = sh.warp[r][lane];
+        st = ds_warp_join(st, k);
+        if (ctas > 1) {
+          if (lane < ctas) {
+            ds_st_cluster(mapa_shared(&sh.cta[q][rank], lane), st);
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             mapa_shared(&sh.stats[q], lane))
+                         : "memory");
+          }
+          __syncwarp();
+          if (!mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status)) break;
+          st = ds_warp_join(lane < ctas ? sh.cta[q][lane] : DsStat{ds_neg_inf(), 0.f}, k);
+        }
+      }
+      if (GRAD) {
+        const bool none = LOSS ? ds_none(st) : st.m == ds_neg_inf();
+        if (lane == 0) {
+          sl.sub = st.m;
+          sl.mul = !sl.any || sl.w == 0.f || none ? 0.f : sl.w * sl.total / st.s;
+          mbar_arrive(&sh.go[r]);
+        }
+        __syncwarp();
+      }
+      if (LOSS && rank == 0) ds_loss(a, t0 + (int64_t)j * stride, sl, st);
+      if (j > 0) ok = places(j - 1);
+    }
+    if (ok && rows > 0) places(rows - 1);
+  } else {
+    // ------------------------------------------------------------ consumers
+    constexpr int STEP = W * 32;
+    const int u0 = u_first + threadIdx.x;
+    // Statistics of row j.
+    auto statistics = [&](int j) {
+      const int r = j % DS_RING;
+      if (!wait(&sh.ready[r], j / DS_RING)) return false;
+      DsStat mine = {ds_neg_inf(), 0.f};
+      if (sh.slots[r].read) {
+        if (!wait(&sh.full[r], j / DS_RING)) return false;
+        const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
+        const T *z = row_of(j);
+        const int off = ALIGNED ? 0 : ds_offset(z);
+        uint4 raw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+        mine = ds_warp_join(ds_units_stat<T, U>(raw, mine, k), k);
+      }
+      if (lane == 0) {
+        sh.warp[r][warp] = mine;
+        mbar_arrive(&sh.taken[r]);
+        if (!GRAD) mbar_arrive(&sh.empty[r]);
+      }
+      return true;
+    };
+    // Gradient of row j.
+    auto gradient = [&](int j) {
+      const int r = j % DS_RING;
+      const DsSlots &sl = sh.slots[r];
+      if (!wait(&sh.go[r], j / DS_RING)) return false;
+      if (!LOSS && sl.read && !wait(&sh.full[r], j / DS_RING)) return false;
+      const T *z = row_of(j);
+      const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
+      const int off = ALIGNED ? 0 : ds_offset(z);
+      T *dz = (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits;
+      ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, DsGrad<LOSS>(sl.sub, k, a.inv_tau, sl.mul), [&](int i) {
+        return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+      });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[r]);
+      return true;
+    };
+    if (LOSS && rows > 0 && !statistics(0)) return;
+    for (int j = 0; j < rows; ++j) {
+      if (LOSS && j + 1 < rows && !statistics(j + 1)) return;
+      if (GRAD && !gradient(j)) return;
+    }
+  }
+}
+
+// Rows of any length: a cluster a row, U units a thread at a time straight from
+// memory, a second time for the gradient.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, int shift, int groups, int *status) {
+  using namespace umma;
+  constexpr int N = DsUnit<T>::N, U = 4, THREADS = 512;
+  constexpr bool LOSS = (MODE & DISTILL_LOSS) != 0, GRAD = (MODE & DISTILL_GRAD) != 0;
+  __shared__ DsSlots sl;
+  __shared__ DsStat wstat[THREADS / 32], cstat[DS_MAX_CTAS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = 1 << shift;
+  const int64_t t = blockIdx.x >> shift;
+  const int rank = blockIdx.x & (ctas - 1);
+  const float k = a.inv_tau * DS_LOG2E;
+  griddep_launch();
+  griddep_wait();
+  if (LOSS && ctas > 1) cluster_sync();  // all CTAs run
+  const T *z = (const T *)a.logits + t * a.ld_logits;
+  const int off = ds_offset(z), u_first = rank * groups * U * THREADS;
+  const int lo = u_first * N, hi = lo + groups * U * THREADS * N;
+  auto piece = [&](int u) { return (const uint4 *)(z - off) + u; };
+  if (warp == 0) {
+    bool found = false;
+    for (int s = lane; s < a.K; s += 32) {
+      int id = a.t_ids[t * a.K + s];
+      const float x = a.t_logits[t * a.K + s] * a.inv_tau;
+      if (id < -1 || id >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
+      if (id >= a.V || x == ds_neg_inf()) id = -1;
+      sl.id[s] = id = id < 0 ? -1 : id;
+      sl.x[s] = x;
+      sl.z[s] = id >= 0 && (LOSS || (id >= lo && id < hi)) ? Elem<T>::load(z + id) : 0.f;
+      found |= id >= 0;
+    }
+    found = __any_sync(FULL_MASK, found);
+    if (lane == 0) {
+      sl.any = found;
+      sl.w = GRAD ? a.weight[t] * a.scale * a.inv_tau : 0.f;
+      sl.lse = LOSS ? 0.f : a.lse[t];
+    }
+    __syncwarp();
+    ds_teacher(a, t, sl);
+  }
+  DsStat st = {ds_neg_inf(), 0.f};
+  if (LOSS) {
+    for (int g = 0; g < groups; ++g) {
+      uint4 raw[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int u = u_first + (g * U + i) * THREADS + threadIdx.x;
+        raw[i] = DsUnit<T>::template load<false>(piece(u), z, off, u, a.V);
+      }
+      st = ds_units_stat<T, U>(raw, st, k);
+    }
+    st = ds_warp_join(st, k);
+    if (lane == 0) wstat[warp] = st;
+  }
+  __syncthreads();
+  if (LOSS) {
+    if (warp == 0) {
+      st = ds_warp_join(lane < THREADS / 32 ? wstat[lane] : DsStat{ds_neg_inf(), 0.f}, k);
+      if (ctas == 1) cstat[0] = st;
+      else if (lane < ctas) ds_st_cluster(mapa_shared(&cstat[rank], lane), st);
+    }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    st = ds_warp_join(lane < ctas ? cstat[lane] : DsStat{ds_neg_inf(), 0.f}, k);
+    if (rank == 0 && warp == 0) ds_loss(a, t, sl, st);
+  } else {
+    st = {sl.lse, 1.f};
+  }
+  if (!GRAD) return;
+  T *dz = (T *)a.dlogits + t * a.ld_dlogits;
+  const bool zero = !sl.any || sl.w == 0.f || (LOSS ? ds_none(st) : sl.lse == ds_neg_inf());
+  const DsGrad<LOSS> grad(st.m, k, a.inv_tau, sl.w * sl.total / st.s);
+  for (int g = 0; g < groups; ++g) {
+    const int u0 = u_first + g * U * THREADS + threadIdx.x;
+    uint4 raw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) raw[i] = zero ? uint4{} : DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
+    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, grad, [&](int i) { return raw[i]; });
+  }
+  __syncthreads();
+  if (!zero) ds_places<T, LOSS>(a, sl, dz, lo, hi, sl.w, grad, threadIdx.x, THREADS);
+}
+
+// ---------------------------------------------------------------- host
+template <typename T, int MODE>
+static cudaError_t ds_launch_long(const DistillArgs &a, int *status, cudaStream_t stream) {
+  const int shift = 3;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.T << shift);
+  cfg.blockDim = dim3(512);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1u << shift;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  const int groups = (int)ceil_div(ceil_div(a.V, 16 / (int)sizeof(T)), (int64_t)(512 * 4) << shift);
+  return cudaLaunchKernelEx(&cfg, distill_long_kernel<T, MODE>, a, shift, groups, status);
+}
+
+template <typename T, bool ALIGNED, int MODE, int W, int U>
+static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaStream_t stream) {
+  const auto kernel = distill_kernel<T, ALIGNED, MODE, W, U>;
+  const int smem = DS_RING * (U * W * 32 + 1) * 16;
+  cudaError_t e = ensure_smem((const void *)kernel, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1u << shift);
+  cfg.blockDim = dim3(32 * (W + 2));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1u << shift;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  // Clusters that run at once, asked for once for each shape and device.
+  static std::mutex mu;
+  static int known[64][4];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int clusters;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    int &n = known[dev & 63][shift];
+    if (!n) {
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+    }
+    clusters = n;
+  }
+  cfg.gridDim = dim3((unsigned)std::min(a.T, clusters) << shift);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a, shift, status);
+}
+
+// The shape of a launch, by the row's 16-byte units alone.
+template <typename T, bool ALIGNED, int MODE>
+static cudaError_t ds_shape(const DistillArgs &a, int *status, cudaStream_t stream) {
+  const int64_t n = ceil_div(a.V, 16 / (int)sizeof(T));
+  if (n <= 256) return ds_launch<T, ALIGNED, MODE, 4, 2>(a, 0, status, stream);
+  if (n <= 1024) return ds_launch<T, ALIGNED, MODE, 4, 8>(a, 0, status, stream);
+  if (n <= 2048) return ds_launch<T, ALIGNED, MODE, 8, 8>(a, 0, status, stream);
+  for (int shift = 0; 1 << shift <= DS_MAX_CTAS; ++shift)
+    if (n <= (int64_t)4096 << shift) return ds_launch<T, ALIGNED, MODE, 16, 8>(a, shift, status, stream);
+  return ds_launch_long<T, MODE>(a, status, stream);
+}
+
+template <typename T, bool ALIGNED>
+static cudaError_t ds_mode(const DistillArgs &a, int mode, int *status, cudaStream_t stream) {
+  if (mode == DISTILL_LOSS) return ds_shape<T, ALIGNED, DISTILL_LOSS>(a, status, stream);
+  if (mode == DISTILL_GRAD) return ds_shape<T, ALIGNED, DISTILL_GRAD>(a, status, stream);
+  return ds_shape<T, ALIGNED, DISTILL_LOSS | DISTILL_GRAD>(a, status, stream);
+}
+
+template <typename T>
+cudaError_t distill_launch(const DistillArgs &a, int mode, int *status, cudaStream_t stream) {
+  constexpr int N = 16 / (int)sizeof(T);
+  bool aligned = (uintptr_t)a.logits % 16 == 0 && a.ld_logits % N == 0;
+  if (mode & DISTILL_GRAD) aligned = aligned && (uintptr_t)a.dlogits % 16 == 0 && a.ld_dlogits % N == 0;
+  return aligned ? ds_mode<T, true>(a, mode, status, stream) : ds_mode<T, false>(a, mode, status, stream);
+}
+
+}  // namespace moe
