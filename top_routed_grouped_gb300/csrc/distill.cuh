@@ -9,8 +9,9 @@
 // over the rows; three slices stand in shared memory, one whose gradient is
 // written, one whose statistics are taken and one on its way, so that a row is
 // read from memory once and nothing waits for it.  The warps of a CTA:
-//   producer   loads the teacher's slots a row ahead, starts the bulk copies,
-//              turns the slots into p
+//   loader     starts the bulk copies, half a slice at a time, as soon as the
+//              consumers are done with what stood there
+//   teacher    loads the teacher's slots a row ahead and turns them into p
 //   consumers  statistics of row j + 1, then gradient of row j
 //   joiner     joins the warps' statistics, hands them to the other CTAs
 //              through distributed shared memory, sums the loss, and writes
@@ -329,14 +330,16 @@ __device__ inline void ds_places(const DistillArgs &a, const DsSlots &sl, T *dz,
   }
 }
 
-// The dense part of the gradient of U units a thread.
-template <typename T, bool ALIGNED, bool LOSS, int U, typename Load>
-__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, const DsGrad<LOSS> &grad, Load load) {
+// The dense part of the gradient of U units a thread; half() is called between
+// the halves of them.
+template <typename T, bool ALIGNED, bool LOSS, int U, typename Load, typename Half>
+__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, const DsGrad<LOSS> &grad, Load load, Half half) {
   constexpr int N = DsUnit<T>::N;
   const int off = ALIGNED ? 0 : ds_offset(dz);
   if (zero) {
 #pragma unroll 1
     for (int j = 0; j < U; ++j) DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, uint4{});
+    half();
     return;
   }
 #pragma unroll
@@ -348,6 +351,7 @@ __device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, const
     uint4 o;
     Vec16<T>::store((T *)&o, v);
     DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, o);
+    if (j == U / 2 - 1) half();
   }
 }
 
@@ -355,7 +359,7 @@ struct DsShared {
   DsSlots slots[DS_RING];
   DsStat warp[DS_RING][16];
   DsStat cta[DS_STATS][DS_MAX_CTAS];
-  uint64_t full[DS_RING], empty[DS_RING];         // a slice has arrived; the consumers are done with it
+  uint64_t full[DS_RING], empty[DS_RING][2];      // a slice has arrived; the consumers are done with its halves
   uint64_t ready[DS_RING], freed[DS_RING];        // a teacher is there; the joiner is done with it
   uint64_t taken[DS_RING], stats[DS_STATS];       // the warps' pairs are there; all CTAs' pairs are there
   uint64_t go[DS_RING];                           // the row's gradient can be written
@@ -365,7 +369,7 @@ struct DsShared {
 // W: consumer warps; U: units a thread; 1 << shift: CTAs of a cluster.
 // ALIGNED: all rows start on 16-byte boundaries.
 template <typename T, bool ALIGNED, int MODE, int W, int U>
-__global__ void __launch_bounds__(32 * (W + 2), W == 16 ? 1 : W == 8 ? 2 : 4)
+__global__ void __launch_bounds__(32 * (W + 3), W == 16 ? 1 : W == 8 ? 2 : 4)
 distill_kernel(const DistillArgs a, int shift, int *status) {
   using namespace umma;
   constexpr int N = DsUnit<T>::N, SPAN = U * W * 32;
@@ -379,8 +383,9 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < DS_RING; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], W);
+      mbar_init(&sh.full[i], 2);
+      mbar_init(&sh.empty[i][0], W);
+      mbar_init(&sh.empty[i][1], W);
       mbar_init(&sh.ready[i], 1);
       mbar_init(&sh.freed[i], 1);
       mbar_init(&sh.taken[i], W);
@@ -401,70 +406,92 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
   auto row_of = [&](int j) { return (const T *)a.logits + (t0 + (int64_t)j * stride) * a.ld_logits; };
   auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, phase & 1, &sh.abort_flag, status); };
 
+  // Rows that have no gradient and whose loss is 0 or not asked for are not read.
+  auto needed = [&](bool any, float w) { return (LOSS && (!GRAD || a.lse)) || (any && (LOSS || w != 0.f)); };
+  constexpr int SL = DISTILL_MAX_K / 32;
+  auto slot_id = [&](int64_t t, int i) { return lane + 32 * i < a.K ? __ldg(a.t_ids + t * a.K + lane + 32 * i) : -1; };
+  auto slot_x = [&](int64_t t, int i) { return lane + 32 * i < a.K ? __ldg(a.t_logits + t * a.K + lane + 32 * i) : 0.f; };
+  auto counts = [&](int id, float x) { return id >= 0 && id < a.V && x * a.inv_tau != ds_neg_inf(); };
+
   if (warp == W) {
-    // ------------------------------------------------------------ producer
-    constexpr int SL = DISTILL_MAX_K / 32;
+    // ------------------------------------------------------------ loader
+    int id[SL];
+    float x[SL], w = 0.f;
+    auto fetch = [&](int j) {
+      const int64_t t = t0 + (int64_t)j * stride;
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        id[i] = slot_id(t, i);
+        x[i] = slot_x(t, i);
+      }
+      if (GRAD) w = a.weight[t];
+    };
+    if (rows > 0) fetch(0);
+    for (int j = 0; j < rows; ++j) {
+      const int r = j % DS_RING;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < SL; ++i) found |= counts(id[i], x[i]);
+      const bool read = needed(__any_sync(FULL_MASK, found), w);
+      if (j + 1 < rows) fetch(j + 1);
+      // The aligned pieces that lie in the row (none of a row that is not read).
+      const T *z = row_of(j);
+      const int off = ALIGNED ? 0 : ds_offset(z);
+      const int last = read ? (a.V + off) / N : 0;
+      uint4 *slice = slices + r * (SPAN + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!wait(&sh.empty[r][h], j / DS_RING + 1)) return;
+        if (lane == 0) {
+          const int from = u_first + (h ? SPAN / 2 : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
+          const int to = min(u_first + (h ? SPAN + (off ? 1 : 0) : SPAN / 2), last);
+          if (to > from) {
+            mbar_arrive_expect_tx(&sh.full[r], (uint32_t)(to - from) * 16);
+            bulk_load(slice + (from - u_first), z - off + (int64_t)from * N, (uint32_t)(to - from) * 16, &sh.full[r]);
+          } else {
+            mbar_arrive(&sh.full[r]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == W + 1) {
+    // ------------------------------------------------------------ teacher
     int id[SL];
     float x[SL], w = 0.f, lse = 0.f;
     auto fetch = [&](int j) {
       const int64_t t = t0 + (int64_t)j * stride;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
-        const int s = lane + 32 * i;
-        id[i] = -1;
-        if (s < a.K) {
-          id[i] = a.t_ids[t * a.K + s];
-          x[i] = a.t_logits[t * a.K + s];
-        }
+        id[i] = slot_id(t, i);
+        x[i] = slot_x(t, i);
       }
       if (GRAD) w = a.weight[t];
       if (!LOSS) lse = a.lse[t];
     };
     if (rows > 0) fetch(0);
     for (int j = 0; j < rows; ++j) {
-      const int r = j % DS_RING, round = j / DS_RING;
-      const int64_t t = t0 + (int64_t)j * stride;
+      const int r = j % DS_RING;
       const T *z = row_of(j);
       bool found = false;
-#pragma unroll
-      for (int i = 0; i < SL; ++i) {
-        if (id[i] < -1 || id[i] >= a.V) {
-          record_status(status, STATUS_BAD_TEACHER_ID);
-          id[i] = -1;
-        }
-        x[i] *= a.inv_tau;
-        if (x[i] == ds_neg_inf()) id[i] = -1;
-        found |= id[i] >= 0;
-      }
-      const bool any = __any_sync(FULL_MASK, found);
-      // Rows that have no gradient and whose loss is 0 or not asked for are not read.
-      const bool read = (LOSS && (!GRAD || a.lse)) || (any && (LOSS || w != 0.f));
-      if (!wait(&sh.empty[r], round + 1)) break;
-      if (lane == 0) {
-        // The aligned pieces that lie in the row (none of a row that is not read).
-        const int off = ds_offset(z);
-        const int from = u_first + (off && u_first == 0 ? 1 : 0);
-        const int to = min(u_first + SPAN + (off ? 1 : 0), (a.V + off) / N);
-        const uint32_t bytes = read && to > from ? (uint32_t)(to - from) * 16 : 0;
-        if (bytes) {
-          mbar_arrive_expect_tx(&sh.full[r], bytes);
-          bulk_load(slices + r * (SPAN + 1) + (from - u_first), z - off + (int64_t)from * N, bytes, &sh.full[r]);
-        } else {
-          mbar_arrive(&sh.full[r]);
-        }
-      }
       float zk[SL];
 #pragma unroll
-      for (int i = 0; i < SL; ++i)  // without a loss, only this CTA's places matter (others may have been written)
+      for (int i = 0; i < SL; ++i) {
+        if (id[i] < -1 || id[i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
+        if (!counts(id[i], x[i])) id[i] = -1;
+        found |= id[i] >= 0;
+        // without a loss, only this CTA's places matter (others may have been written)
         zk[i] = id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi)) ? Elem<T>::load(z + id[i]) : 0.f;
-      if (!wait(&sh.freed[r], round + 1)) break;
+      }
+      const bool any = __any_sync(FULL_MASK, found);
+      if (!wait(&sh.freed[r], j / DS_RING + 1)) return;
       DsSlots &sl = sh.slots[r];
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         const int s = lane + 32 * i;
         if (s < a.K) {
           sl.id[s] = id[i];
-          sl.x[s] = x[i];
+          sl.x[s] = x[i] * a.inv_tau;
           sl.z[s] = zk[i];
         }
       }
@@ -472,22 +499,22 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         sl.w = w * a.scale * a.inv_tau;
         sl.lse = lse;
         sl.any = any;
-        sl.read = read;
+        sl.read = needed(any, w);
       }
       if (j + 1 < rows) fetch(j + 1);
       __syncwarp();
-      ds_teacher(a, t, sl);
+      ds_teacher(a, t0 + (int64_t)j * stride, sl);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[r]);
     }
-  } else if (warp == W + 1) {
+  } else if (warp == W + 2) {
     // ------------------------------------------------------------ joiner
     // The teacher's places of row j, behind the dense pass.
     auto places = [&](int j) {
       const int r = j % DS_RING;
       DsSlots &sl = sh.slots[r];
       if (GRAD) {
-        if (!wait(&sh.empty[r], j / DS_RING)) return false;
+        if (!wait(&sh.empty[r][1], j / DS_RING)) return false;
         if (sl.mul != 0.f)
           ds_places<T, LOSS>(a, sl, (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits, lo, hi, sl.w,
                              DsGrad<LOSS>(sl.sub, k, a.inv_tau, sl.mul), lane, 32);
@@ -554,7 +581,10 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       if (lane == 0) {
         sh.warp[r][warp] = mine;
         mbar_arrive(&sh.taken[r]);
-        if (!GRAD) mbar_arrive(&sh.empty[r]);
+        if (!GRAD) {
+          mbar_arrive(&sh.empty[r][0]);
+          mbar_arrive(&sh.empty[r][1]);
+        }
       }
       return true;
     };
@@ -570,9 +600,12 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       T *dz = (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits;
       ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, DsGrad<LOSS>(sl.sub, k, a.inv_tau, sl.mul), [&](int i) {
         return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+      }, [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[r][0]);
       });
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[r]);
+      if (lane == 0) mbar_arrive(&sh.empty[r][1]);
       return true;
     };
     if (LOSS && rows > 0 && !statistics(0)) return;
@@ -661,7 +694,7 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
     uint4 raw[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) raw[i] = zero ? uint4{} : DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
-    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, grad, [&](int i) { return raw[i]; });
+    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, grad, [&](int i) { return raw[i]; }, [] {});
   }
   __syncthreads();
   if (!zero) ds_places<T, LOSS>(a, sl, dz, lo, hi, sl.w, grad, threadIdx.x, THREADS);
@@ -696,7 +729,7 @@ static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaS
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1u << shift);
-  cfg.blockDim = dim3(32 * (W + 2));
+  cfg.blockDim = dim3(32 * (W + 3));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
