@@ -10,8 +10,9 @@
 // written, one whose statistics are taken and one on its way, so that a row is
 // read from memory once and nothing waits for it.  The warps of a CTA:
 //   loader     starts the bulk copies, half a slice at a time, as soon as the
-//              consumers are done with what stood there
-//   teacher    loads the teacher's slots a row ahead and turns them into p
+//              consumers are done with what stood there, and brings the
+//              teacher's slots, with the student's logits at their places
+//   teacher    turns the slots into p
 //   consumers  statistics of row j + 1, then gradient of row j
 //   joiner     joins the warps' statistics, hands them to the other CTAs
 //              through distributed shared memory, sums the loss, and writes
@@ -92,7 +93,19 @@ struct DsStat {
 __device__ inline DsStat ds_warp_join(DsStat a, float k) {
   const float m = ds_warp_max(a.m);
   const float base = m == ds_neg_inf() ? 0.f : m;
-  return {m, ds_warp_sum(a.s * exp2f((a.m - base) * k))};
+  return {m, ds_warp_sum(a.s * ds_exp2((a.m - base) * k))};
+}
+
+// M pairs in shared memory as one, by every thread that calls it.
+template <int M>
+__device__ inline DsStat ds_join(const DsStat *p, float k) {
+  float m = ds_neg_inf(), s = 0.f;
+#pragma unroll
+  for (int i = 0; i < M; ++i) m = fmaxf(m, p[i].m);
+  const float base = m == ds_neg_inf() ? 0.f : m;
+#pragma unroll
+  for (int i = 0; i < M; ++i) s = fmaf(p[i].s, ds_exp2((p[i].m - base) * k), s);
+  return {m, s};
 }
 
 // Elements n.. of the 2 N elements of (lo, hi), sh = n sizeof(T) bytes.
@@ -245,42 +258,66 @@ struct DsGrad {
 };
 
 // What a row's teacher is to a CTA.
+constexpr int DS_MARKS = 2048;
 struct __align__(16) DsSlots {
   int id[DISTILL_MAX_K];   // -1 where there is no slot
   float x[DISTILL_MAX_K];  // t / tau
   float p[DISTILL_MAX_K];
   float z[DISTILL_MAX_K];  // the student's logit there
   float c, total, w, lse;  // p = exp(x - c), their sum; the row's weight; its lse where that is given
-  int any, read;           // whether there is a slot; whether the row's logits are loaded
+  int any, twice;          // whether there is a slot; whether an id may be there twice
   float sub, mul;          // what DsGrad takes; mul 0 where there is no gradient
 };
 
-// One warp: the teacher's distribution from its slots.
-__device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl) {
+// One warp: the teacher's distribution from its slots; `marks` finds ids given
+// twice: every slot leaves its number at a place that its id hashes to.  One
+// that reads another number there is a copy of that slot, or looks for itself
+// among all of them.
+__device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl, uint8_t *marks) {
   const int lane = threadIdx.x & 31;
-  float c, total = 0.f;
+  auto mark = [&](int id) { return ((uint32_t)id * 2654435761u) >> 21; };
+  float c, total = 1.f, m = ds_neg_inf(), e = 0.f;
+  for (int s = lane; s < a.K; s += 32) {
+    const int id = sl.id[s];
+    if (id >= 0) {
+      m = fmaxf(m, sl.x[s]);
+      marks[mark(id)] = (uint8_t)s;
+    }
+  }
+  for (int s = a.K + lane; s < (int)round_up(a.K, 4); s += 32) sl.id[s] = -1;
   if (a.t_lse) {
     c = a.t_lse[t];
   } else {
-    float m = ds_neg_inf(), e = 0.f;
-    for (int s = lane; s < a.K; s += 32)
-      if (sl.id[s] >= 0) m = fmaxf(m, sl.x[s]);
     m = ds_warp_max(m);
     for (int s = lane; s < a.K; s += 32)
-      if (sl.id[s] >= 0) e += expf(sl.x[s] - m);
+      if (sl.id[s] >= 0) e += ds_exp2((sl.x[s] - m) * DS_LOG2E);
     c = m + logf(ds_warp_sum(e));
   }
+  __syncwarp();
+  float sum = 0.f;
+  bool twice = false;
   for (int s = lane; s < a.K; s += 32) {
-    const float p = sl.id[s] >= 0 ? expf(sl.x[s] - c) : 0.f;
-    total += p;
+    const int id = sl.id[s];
+    float p = 0.f;
+    if (id >= 0) {
+      p = expf(sl.x[s] - c);
+      const int other = marks[mark(id)];
+      if (other != s) {
+        if (sl.id[other] == id) twice = true;
+        else
+          for (int i = 0; i < a.K; ++i) twice |= i != s && sl.id[i] == id;
+      }
+    }
+    sum += p;
     sl.p[s] = p;
   }
-  total = ds_warp_sum(total);
+  if (a.t_lse) total = ds_warp_sum(sum);
+  twice = __any_sync(FULL_MASK, twice);
   if (lane == 0) {
     sl.c = c;
     sl.total = total;
+    sl.twice = twice;
   }
-  for (int s = a.K + lane; s < (int)round_up(a.K, 4); s += 32) sl.id[s] = -1;
 }
 
 // Nothing but -inf (NaN is something).
@@ -310,16 +347,14 @@ __device__ inline void ds_places(const DistillArgs &a, const DsSlots &sl, T *dz,
   for (int s = i; s < a.K; s += n) {
     const int id = sl.id[s];
     if (id < 0 || id < lo || id >= hi) continue;
-    float p = 0.f;
-    bool once = true;  // the first slot of an id writes for all of them
-    for (int j = 0; j < a.K; j += 4) {
-      const int4 q = *(const int4 *)&sl.id[j];
-      const int e[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (e[r] == id) {
-          once = once && j + r >= s;
-          p += sl.p[j + r];
+    float p = sl.p[s];
+    bool once = true;
+    if (sl.twice) {  // the first slot of an id writes for all of them
+      p = 0.f;
+      for (int j = 0; j < a.K; ++j)
+        if (sl.id[j] == id) {
+          once = once && j >= s;
+          p += sl.p[j];
         }
     }
     if (once) {
@@ -357,12 +392,15 @@ __device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, const
 
 struct DsShared {
   DsSlots slots[DS_RING];
-  DsStat warp[DS_RING][16];
-  DsStat cta[DS_STATS][DS_MAX_CTAS];
+  __align__(16) DsStat warp[DS_RING][16];
+  __align__(16) DsStat cta[DS_STATS][DS_MAX_CTAS];
+  uint8_t marks[DS_MARKS];
+  uint64_t raw[DS_RING];                          // a teacher's slots are there
   uint64_t full[DS_RING], empty[DS_RING][2];      // a slice has arrived; the consumers are done with its halves
   uint64_t ready[DS_RING], freed[DS_RING];        // a teacher is there; the joiner is done with it
   uint64_t taken[DS_RING], stats[DS_STATS];       // the warps' pairs are there; all CTAs' pairs are there
   uint64_t go[DS_RING];                           // the row's gradient can be written
+  int read[DS_RING];                              // whether a slice was loaded (written by the loader before `full`)
   int abort_flag;
 };
 
@@ -390,11 +428,13 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       mbar_init(&sh.freed[i], 1);
       mbar_init(&sh.taken[i], W);
       mbar_init(&sh.go[i], 1);
+      mbar_init(&sh.raw[i], 1);
     }
     for (int i = 0; i < DS_STATS; ++i) mbar_init(&sh.stats[i], ctas);
     sh.abort_flag = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x < DS_STATS * DS_MAX_CTAS) sh.cta[0][threadIdx.x] = {ds_neg_inf(), 0.f};  // CTAs that the cluster lacks
   __syncthreads();
   // The barriers of the whole cluster are there before anyone arrives at them.
   if (LOSS && ctas > 1) cluster_sync();
@@ -409,54 +449,12 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
   // Rows that have no gradient and whose loss is 0 or not asked for are not read.
   auto needed = [&](bool any, float w) { return (LOSS && (!GRAD || a.lse)) || (any && (LOSS || w != 0.f)); };
   constexpr int SL = DISTILL_MAX_K / 32;
-  auto slot_id = [&](int64_t t, int i) { return lane + 32 * i < a.K ? __ldg(a.t_ids + t * a.K + lane + 32 * i) : -1; };
-  auto slot_x = [&](int64_t t, int i) { return lane + 32 * i < a.K ? __ldg(a.t_logits + t * a.K + lane + 32 * i) : 0.f; };
+  auto slot_id = [&](int64_t t, int i) { return lane + 32 * i < a.K ? a.t_ids[t * a.K + lane + 32 * i] : -1; };
+  auto slot_x = [&](int64_t t, int i) { return lane + 32 * i < a.K ? a.t_logits[t * a.K + lane + 32 * i] : 0.f; };
   auto counts = [&](int id, float x) { return id >= 0 && id < a.V && x * a.inv_tau != ds_neg_inf(); };
 
   if (warp == W) {
     // ------------------------------------------------------------ loader
-    int id[SL];
-    float x[SL], w = 0.f;
-    auto fetch = [&](int j) {
-      const int64_t t = t0 + (int64_t)j * stride;
-#pragma unroll
-      for (int i = 0; i < SL; ++i) {
-        id[i] = slot_id(t, i);
-        x[i] = slot_x(t, i);
-      }
-      if (GRAD) w = a.weight[t];
-    };
-    if (rows > 0) fetch(0);
-    for (int j = 0; j < rows; ++j) {
-      const int r = j % DS_RING;
-      bool found = false;
-#pragma unroll
-      for (int i = 0; i < SL; ++i) found |= counts(id[i], x[i]);
-      const bool read = needed(__any_sync(FULL_MASK, found), w);
-      if (j + 1 < rows) fetch(j + 1);
-      // The aligned pieces that lie in the row (none of a row that is not read).
-      const T *z = row_of(j);
-      const int off = ALIGNED ? 0 : ds_offset(z);
-      const int last = read ? (a.V + off) / N : 0;
-      uint4 *slice = slices + r * (SPAN + 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!wait(&sh.empty[r][h], j / DS_RING + 1)) return;
-        if (lane == 0) {
-          const int from = u_first + (h ? SPAN / 2 : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
-          const int to = min(u_first + (h ? SPAN + (off ? 1 : 0) : SPAN / 2), last);
-          if (to > from) {
-            mbar_arrive_expect_tx(&sh.full[r], (uint32_t)(to - from) * 16);
-            bulk_load(slice + (from - u_first), z - off + (int64_t)from * N, (uint32_t)(to - from) * 16, &sh.full[r]);
-          } else {
-            mbar_arrive(&sh.full[r]);
-          }
-        }
-        __syncwarp();
-      }
-    }
-  } else if (warp == W + 1) {
-    // ------------------------------------------------------------ teacher
     int id[SL];
     float x[SL], w = 0.f, lse = 0.f;
     auto fetch = [&](int j) {
@@ -474,16 +472,39 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const int r = j % DS_RING;
       const T *z = row_of(j);
       bool found = false;
-      float zk[SL];
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         if (id[i] < -1 || id[i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
         if (!counts(id[i], x[i])) id[i] = -1;
         found |= id[i] >= 0;
-        // without a loss, only this CTA's places matter (others may have been written)
-        zk[i] = id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi)) ? Elem<T>::load(z + id[i]) : 0.f;
       }
-      const bool any = __any_sync(FULL_MASK, found);
+      const bool any = __any_sync(FULL_MASK, found), read = needed(any, w);
+      // The aligned pieces that lie in the row (none of a row that is not read).
+      const int off = ALIGNED ? 0 : ds_offset(z);
+      const int last = read ? (a.V + off) / N : 0;
+      uint4 *slice = slices + r * (SPAN + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!wait(&sh.empty[r][h], j / DS_RING + 1)) return;
+        // (with a gradient the consumers cannot be done before the joiner is)
+        if (!GRAD && !wait(&sh.freed[r], j / DS_RING + 1)) return;
+        if (lane == 0) {
+          if (h == 1) sh.read[r] = read;
+          const int from = u_first + (h ? SPAN / 2 : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
+          const int to = min(u_first + (h ? SPAN + (off ? 1 : 0) : SPAN / 2), last);
+          if (to > from) {
+            mbar_arrive_expect_tx(&sh.full[r], (uint32_t)(to - from) * 16);
+            bulk_load(slice + (from - u_first), z - off + (int64_t)from * N, (uint32_t)(to - from) * 16, &sh.full[r]);
+          } else {
+            mbar_arrive(&sh.full[r]);
+          }
+        }
+        __syncwarp();
+      }
+      float zk[SL];
+#pragma unroll
+      for (int i = 0; i < SL; ++i)  // without a loss, only this CTA's places matter (others may have been written)
+        zk[i] = id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi)) ? Elem<T>::load(z + id[i]) : 0.f;
       if (!wait(&sh.freed[r], j / DS_RING + 1)) return;
       DsSlots &sl = sh.slots[r];
 #pragma unroll
@@ -492,18 +513,26 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         if (s < a.K) {
           sl.id[s] = id[i];
           sl.x[s] = x[i] * a.inv_tau;
-          sl.z[s] = zk[i];
         }
       }
       if (lane == 0) {
         sl.w = w * a.scale * a.inv_tau;
         sl.lse = lse;
         sl.any = any;
-        sl.read = needed(any, w);
       }
       if (j + 1 < rows) fetch(j + 1);
+#pragma unroll
+      for (int i = 0; i < SL; ++i)
+        if (lane + 32 * i < a.K) sl.z[lane + 32 * i] = zk[i];
       __syncwarp();
-      ds_teacher(a, t0 + (int64_t)j * stride, sl);
+      if (lane == 0) mbar_arrive(&sh.raw[r]);
+    }
+  } else if (warp == W + 1) {
+    // ------------------------------------------------------------ teacher
+    for (int j = 0; j < rows; ++j) {
+      const int r = j % DS_RING;
+      if (!wait(&sh.raw[r], j / DS_RING)) return;
+      ds_teacher(a, t0 + (int64_t)j * stride, sh.slots[r], sh.marks);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[r]);
     }
@@ -531,9 +560,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       DsStat st = {sl.lse, 1.f};
       if (LOSS) {
         if (!wait(&sh.taken[r], j / DS_RING)) break;
-        st = {ds_neg_inf(), 0.f};
-        if (lane < W) st = sh.warp[r][lane];
-        st = ds_warp_join(st, k);
+        st = ds_join<W>(sh.warp[r], k);
         if (ctas > 1) {
           if (lane < ctas) {
             ds_st_cluster(mapa_shared(&sh.cta[q][rank], lane), st);
@@ -543,7 +570,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
           }
           __syncwarp();
           if (!mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status)) break;
-          st = ds_warp_join(lane < ctas ? sh.cta[q][lane] : DsStat{ds_neg_inf(), 0.f}, k);
+          st = ds_join<DS_MAX_CTAS>(sh.cta[q], k);
         }
       }
       if (GRAD) {
@@ -566,10 +593,9 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
     // Statistics of row j.
     auto statistics = [&](int j) {
       const int r = j % DS_RING;
-      if (!wait(&sh.ready[r], j / DS_RING)) return false;
+      if (!wait(&sh.full[r], j / DS_RING)) return false;
       DsStat mine = {ds_neg_inf(), 0.f};
-      if (sh.slots[r].read) {
-        if (!wait(&sh.full[r], j / DS_RING)) return false;
+      if (sh.read[r]) {
         const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
         const T *z = row_of(j);
         const int off = ALIGNED ? 0 : ds_offset(z);
@@ -593,7 +619,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const int r = j % DS_RING;
       const DsSlots &sl = sh.slots[r];
       if (!wait(&sh.go[r], j / DS_RING)) return false;
-      if (!LOSS && sl.read && !wait(&sh.full[r], j / DS_RING)) return false;
+      if (!LOSS && !wait(&sh.full[r], j / DS_RING)) return false;
       const T *z = row_of(j);
       const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
       const int off = ALIGNED ? 0 : ds_offset(z);
@@ -624,6 +650,7 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
   constexpr int N = DsUnit<T>::N, U = 4, THREADS = 512;
   constexpr bool LOSS = (MODE & DISTILL_LOSS) != 0, GRAD = (MODE & DISTILL_GRAD) != 0;
   __shared__ DsSlots sl;
+  __shared__ uint8_t marks[DS_MARKS];
   __shared__ DsStat wstat[THREADS / 32], cstat[DS_MAX_CTAS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = 1 << shift;
   const int64_t t = blockIdx.x >> shift;
@@ -655,7 +682,7 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
       sl.lse = LOSS ? 0.f : a.lse[t];
     }
     __syncwarp();
-    ds_teacher(a, t, sl);
+    ds_teacher(a, t, sl, marks);
   }
   DsStat st = {ds_neg_inf(), 0.f};
   if (LOSS) {
