@@ -14,10 +14,11 @@
 //              teacher's slots, with the student's logits at their places
 //   teacher    turns the slots into p
 //   consumers  statistics of row j + 1, then gradient of row j
-//   joiner     joins the warps' statistics, hands them to the other CTAs
-//              through distributed shared memory, sums the loss, and writes
-//              the teacher's places of the gradient again, p subtracted,
-//              behind the dense pass
+//   joiner     joins the warps' statistics and hands them to the other CTAs
+//              through distributed shared memory
+//   finisher   sums the loss, and writes the teacher's places of the gradient
+//              again, p subtracted, behind the dense pass (apart from the
+//              joiner: its stores to memory would hold up every hand-over)
 // They meet at mbarriers alone; no barrier stops a whole CTA.
 // The maximum is taken before the exponentials, in a thread's own units first;
 // the (max, sum) pairs of threads, warps and CTAs are joined in a fixed order.
@@ -75,9 +76,9 @@ __device__ inline DsPair ds_fma2(DsPair a, DsPair b, DsPair c) {
 __device__ inline void ds_opaque(uint4 &v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
 
 __device__ inline float ds_warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, d));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ inline float ds_warp_sum(float v) {
 #pragma unroll
@@ -266,7 +267,8 @@ struct __align__(16) DsSlots {
   float z[DISTILL_MAX_K];  // the student's logit there
   float c, total, w, lse;  // p = exp(x - c), their sum; the row's weight; its lse where that is given
   int any, twice;          // whether there is a slot; whether an id may be there twice
-  float sub, mul;          // what DsGrad takes; mul 0 where there is no gradient
+  float m, s;              // the student's statistics (m: lse where that is given)
+  float mul;               // what DsGrad takes; 0 where there is no gradient
 };
 
 // One warp: the teacher's distribution from its slots; `marks` finds ids given
@@ -274,48 +276,54 @@ struct __align__(16) DsSlots {
 // that reads another number there is a copy of that slot, or looks for itself
 // among all of them.
 __device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl, uint8_t *marks) {
+  constexpr int SL = DISTILL_MAX_K / 32;
   const int lane = threadIdx.x & 31;
   auto mark = [&](int id) { return ((uint32_t)id * 2654435761u) >> 21; };
-  float c, total = 1.f, m = ds_neg_inf(), e = 0.f;
-  for (int s = lane; s < a.K; s += 32) {
-    const int id = sl.id[s];
-    if (id >= 0) {
-      m = fmaxf(m, sl.x[s]);
-      marks[mark(id)] = (uint8_t)s;
+  int id[SL];
+  float x[SL], m = ds_neg_inf(), sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    if (32 * i >= a.K) break;
+    const int s = lane + 32 * i;
+    id[i] = s < a.K ? sl.id[s] : -1;
+    x[i] = s < a.K ? sl.x[s] : 0.f;
+    if (id[i] >= 0) {
+      m = fmaxf(m, x[i]);
+      marks[mark(id[i])] = (uint8_t)s;
     }
-  }
-  for (int s = a.K + lane; s < (int)round_up(a.K, 4); s += 32) sl.id[s] = -1;
-  if (a.t_lse) {
-    c = a.t_lse[t];
-  } else {
-    m = ds_warp_max(m);
-    for (int s = lane; s < a.K; s += 32)
-      if (sl.id[s] >= 0) e += ds_exp2((sl.x[s] - m) * DS_LOG2E);
-    c = m + logf(ds_warp_sum(e));
   }
   __syncwarp();
-  float sum = 0.f;
+  float c = 0.f;
+  if (a.t_lse) m = c = a.t_lse[t];
+  else m = ds_warp_max(m);
+  float e[SL];
   bool twice = false;
-  for (int s = lane; s < a.K; s += 32) {
-    const int id = sl.id[s];
-    float p = 0.f;
-    if (id >= 0) {
-      p = expf(sl.x[s] - c);
-      const int other = marks[mark(id)];
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    if (32 * i >= a.K) break;
+    e[i] = 0.f;
+    if (id[i] >= 0) {
+      e[i] = expf(x[i] - m);
+      const int s = lane + 32 * i, other = marks[mark(id[i])];
       if (other != s) {
-        if (sl.id[other] == id) twice = true;
+        if (sl.id[other] == id[i]) twice = true;
         else
-          for (int i = 0; i < a.K; ++i) twice |= i != s && sl.id[i] == id;
+          for (int q = 0; q < a.K; ++q) twice |= q != s && sl.id[q] == id[i];
       }
     }
-    sum += p;
-    sl.p[s] = p;
+    sum += e[i];
   }
-  if (a.t_lse) total = ds_warp_sum(sum);
+  sum = ds_warp_sum(sum);
+  const float inv = a.t_lse ? 1.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    if (32 * i >= a.K) break;
+    if (lane + 32 * i < a.K) sl.p[lane + 32 * i] = e[i] * inv;
+  }
   twice = __any_sync(FULL_MASK, twice);
   if (lane == 0) {
-    sl.c = c;
-    sl.total = total;
+    sl.c = a.t_lse ? c : m + logf(sum);
+    sl.total = a.t_lse ? sum : 1.f;
     sl.twice = twice;
   }
 }
@@ -407,7 +415,7 @@ struct DsShared {
 // W: consumer warps; U: units a thread; 1 << shift: CTAs of a cluster.
 // ALIGNED: all rows start on 16-byte boundaries.
 template <typename T, bool ALIGNED, int MODE, int W, int U>
-__global__ void __launch_bounds__(32 * (W + 3), W == 16 ? 1 : W == 8 ? 2 : 4)
+__global__ void __launch_bounds__(32 * (W + 4), W == 16 ? 1 : W == 8 ? 2 : 4)
 distill_kernel(const DistillArgs a, int shift, int *status) {
   using namespace umma;
   constexpr int N = DsUnit<T>::N, SPAN = U * W * 32;
@@ -538,28 +546,13 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
     }
   } else if (warp == W + 2) {
     // ------------------------------------------------------------ joiner
-    // The teacher's places of row j, behind the dense pass.
-    auto places = [&](int j) {
-      const int r = j % DS_RING;
-      DsSlots &sl = sh.slots[r];
-      if (GRAD) {
-        if (!wait(&sh.empty[r][1], j / DS_RING)) return false;
-        if (sl.mul != 0.f)
-          ds_places<T, LOSS>(a, sl, (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits, lo, hi, sl.w,
-                             DsGrad<LOSS>(sl.sub, k, a.inv_tau, sl.mul), lane, 32);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.freed[r]);
-      return true;
-    };
-    bool ok = true;
-    for (int j = 0; j < rows && ok; ++j) {
+    for (int j = 0; j < rows; ++j) {
       const int r = j % DS_RING, q = j % DS_STATS;
       DsSlots &sl = sh.slots[r];
-      if (!wait(&sh.ready[r], j / DS_RING)) break;
+      if (LOSS && !wait(&sh.taken[r], j / DS_RING)) return;
+      if (!wait(&sh.ready[r], j / DS_RING)) return;
       DsStat st = {sl.lse, 1.f};
       if (LOSS) {
-        if (!wait(&sh.taken[r], j / DS_RING)) break;
         st = ds_join<W>(sh.warp[r], k);
         if (ctas > 1) {
           if (lane < ctas) {
@@ -569,23 +562,36 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
                          : "memory");
           }
           __syncwarp();
-          if (!mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status)) break;
+          if (!mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status)) return;
           st = ds_join<DS_MAX_CTAS>(sh.cta[q], k);
         }
       }
-      if (GRAD) {
+      if (lane == 0) {
         const bool none = LOSS ? ds_none(st) : st.m == ds_neg_inf();
-        if (lane == 0) {
-          sl.sub = st.m;
-          sl.mul = !sl.any || sl.w == 0.f || none ? 0.f : sl.w * sl.total / st.s;
-          mbar_arrive(&sh.go[r]);
-        }
-        __syncwarp();
+        sl.m = st.m;
+        sl.s = st.s;
+        sl.mul = !sl.any || sl.w == 0.f || none ? 0.f : sl.w * sl.total / st.s;
+        mbar_arrive(&sh.go[r]);
       }
-      if (LOSS && rank == 0) ds_loss(a, t0 + (int64_t)j * stride, sl, st);
-      if (j > 0) ok = places(j - 1);
+      __syncwarp();
     }
-    if (ok && rows > 0) places(rows - 1);
+  } else if (warp == W + 3) {
+    // ------------------------------------------------------------ finisher
+    for (int j = 0; j < rows; ++j) {
+      const int r = j % DS_RING;
+      const int64_t t = t0 + (int64_t)j * stride;
+      DsSlots &sl = sh.slots[r];
+      if (!wait(&sh.go[r], j / DS_RING)) return;
+      if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s});
+      if (GRAD) {
+        if (!wait(&sh.empty[r][1], j / DS_RING)) return;
+        if (sl.mul != 0.f)
+          ds_places<T, LOSS>(a, sl, (T *)a.dlogits + t * a.ld_dlogits, lo, hi, sl.w,
+                             DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), lane, 32);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.freed[r]);
+    }
   } else {
     // ------------------------------------------------------------ consumers
     constexpr int STEP = W * 32;
@@ -624,7 +630,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
       const int off = ALIGNED ? 0 : ds_offset(z);
       T *dz = (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits;
-      ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, DsGrad<LOSS>(sl.sub, k, a.inv_tau, sl.mul), [&](int i) {
+      ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), [&](int i) {
         return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
       }, [&] {
         __syncwarp();
@@ -756,7 +762,7 @@ static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaS
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1u << shift);
-  cfg.blockDim = dim3(32 * (W + 3));
+  cfg.blockDim = dim3(32 * (W + 4));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
