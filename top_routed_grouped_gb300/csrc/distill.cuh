@@ -20,15 +20,19 @@
 //              again, p subtracted, behind the dense pass (apart from the
 //              joiner: its stores to memory would hold up every hand-over)
 // They meet at mbarriers alone; no barrier stops a whole CTA.
-// The maximum is taken before the exponentials, in a thread's own units first;
-// the (max, sum) pairs of threads, warps and CTAs are joined in a fixed order.
+// Sums of exponentials stand beside the logit that they are relative to: a
+// thread takes the largest of its first unit, and the largest of all it has
+// only where that turns out too small (a sum above 2^40) or is -inf.  The
+// (reference, sum) pairs of threads, warps and CTAs are joined in a fixed
+// order.
 // The shape goes by the vocabulary alone, so a row's results do not depend on
 // the batch, and a thread's units do not depend on where the row starts.
 // Rows too long for the shared memory of a cluster take a plainer kernel that
 // reads them twice.
 //
-// Exponents are differences of logits before they are scaled, so that rows at
-// the type's lowest value do not overflow.
+// An exponent is one fused multiply-add, z k - m k with k = log2(e) / tau, and m k
+// rounded alike wherever it is used; where m k would overflow (rows at the
+// type's lowest value) the difference is taken first.
 #pragma once
 
 #include <algorithm>
@@ -40,7 +44,7 @@
 
 namespace moe {
 
-constexpr float DS_LOG2E = 1.4426950408889634f;
+constexpr float DS_LOG2E = 1.4426950408889634f, DS_LN2 = 0.6931471805599453f;
 
 __device__ inline float ds_neg_inf() { return __int_as_float(0xff800000); }
 
@@ -86,15 +90,39 @@ __device__ inline float ds_warp_sum(float v) {
   return v;
 }
 
-// Max of logits and sum of 2^(k (. - max)); (-inf, 0) is empty.
+// 2^((z - m) k) for many z: z b + a, or (z + a) b where m k is out of range.
+struct DsPower {
+  DsPair a, b;
+  bool far;
+  __device__ inline DsPower(float m, float k) {
+    const float base = m == ds_neg_inf() ? 0.f : m, mk = __fmul_rn(base, k);
+    far = !(fabsf(mk) < 1e37f);
+    const float x = far ? -base : -mk;
+    a = DsPair(x, x);
+    b = DsPair(k, k);
+  }
+  __device__ inline DsPair two(DsPair z) const {
+    float x, y;
+    (far ? ds_mul2(ds_add2(z, a), b) : ds_fma2(z, b, a)).get(x, y);
+    return DsPair(ds_exp2(x), ds_exp2(y));
+  }
+  // 2^((m' - m) k) for another reference m'.
+  __device__ inline float of(float m) const {
+    float x, k, y;
+    a.get(x, y);
+    b.get(k, y);
+    return ds_exp2(far ? (m + x) * k : __fadd_rn(__fmul_rn(m, k), x));
+  }
+};
+
+// A logit and the sum of 2^(k (. - it)); (-inf, 0) is empty.
 struct DsStat {
   float m, s;
 };
 // The pairs of a warp's lanes as one.
 __device__ inline DsStat ds_warp_join(DsStat a, float k) {
   const float m = ds_warp_max(a.m);
-  const float base = m == ds_neg_inf() ? 0.f : m;
-  return {m, ds_warp_sum(a.s * ds_exp2((a.m - base) * k))};
+  return {m, ds_warp_sum(a.s * DsPower(m, k).of(a.m))};
 }
 
 // M pairs in shared memory as one, by every thread that calls it.
@@ -103,9 +131,9 @@ __device__ inline DsStat ds_join(const DsStat *p, float k) {
   float m = ds_neg_inf(), s = 0.f;
 #pragma unroll
   for (int i = 0; i < M; ++i) m = fmaxf(m, p[i].m);
-  const float base = m == ds_neg_inf() ? 0.f : m;
+  const DsPower power(m, k);
 #pragma unroll
-  for (int i = 0; i < M; ++i) s = fmaf(p[i].s, ds_exp2((p[i].m - base) * k), s);
+  for (int i = 0; i < M; ++i) s = fmaf(p[i].s, power.of(p[i].m), s);
   return {m, s};
 }
 
@@ -143,6 +171,19 @@ struct DsUnit {
 #pragma unroll
     for (int j = 0; j < N; ++j) e[j] = u * N + j < V ? row[u * N + j] : Elem<T>::from_f32(ds_neg_inf());
     return v;
+  }
+  // Whether all units u, u + step, ... u + (n - 1) step of every lane of the
+  // warp lie in the row with their pieces.
+  template <bool ALIGNED>
+  static __device__ inline bool inner(int off, int u, int step, int n, int V) {
+    const int last = u + (n - 1) * step;
+    const bool in = ALIGNED || off == 0 ? (int64_t)(last + 1) * N <= V : piece_in(off, u, V) && piece_in(off, last + 1, V);
+    return __all_sync(FULL_MASK, in);
+  }
+  template <bool ALIGNED>
+  static __device__ inline uint4 load_inner(const uint4 *pieces, int off) {
+    if (ALIGNED || off == 0) return *pieces;
+    return ds_funnel(pieces[0], pieces[1], off * (int)sizeof(T));
   }
   // Unit u, from its aligned pieces (`pieces` is where piece u stands, in
   // shared memory or in the row itself) where they are of the row.
@@ -202,9 +243,16 @@ __device__ inline float ds_unit_max(const uint4 &v) {
   }
 }
 
-// Writes a pair to another CTA's shared memory.
+// Writes a pair to the shared memory of a CTA of the cluster.
 __device__ inline void ds_st_cluster(uint32_t addr, DsStat v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.m), "f"(v.s) : "memory");
+}
+// The same, counted on a barrier there: it needs no fence, which would wait
+// for every store to memory that the SM has under way.
+__device__ inline void ds_st_async(uint32_t addr, DsStat v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+               "f"(v.m), "f"(v.s), "r"(bar)
+               : "memory");
 }
 
 constexpr int DS_MAX_CTAS = 8, DS_RING = 3, DS_STATS = 4;
@@ -214,47 +262,59 @@ __device__ inline int ds_offset(const T *p) {
   return (int)(((uintptr_t)p / sizeof(T)) & (DsUnit<T>::N - 1));
 }
 
-// (max, sum) of U units, joined to what the thread has.
+// The pair of U units.
 template <typename T, int U>
-__device__ inline DsStat ds_units_stat(uint4 (&raw)[U], DsStat mine, float k) {
+__device__ inline DsStat ds_units_stat(uint4 (&raw)[U], float k) {
   constexpr int N = DsUnit<T>::N;
-  float m = mine.m;
+  float m = ds_unit_max<T>(raw[0]), s;
+  for (bool all = m == ds_neg_inf();; all = true) {
+    if (all)
 #pragma unroll
-  for (int j = 0; j < U; ++j) m = fmaxf(m, ds_unit_max<T>(raw[j]));
-  const float base = m == ds_neg_inf() ? 0.f : m;
-  const DsPair nbase(-base, -base), kk(k, k);
-  DsPair sum[2] = {DsPair(mine.s * ds_exp2((mine.m - base) * k), 0.f), DsPair(0.f, 0.f)};
+      for (int j = 0; j < U; ++j) m = fmaxf(m, ds_unit_max<T>(raw[j]));
+    const DsPower power(m, k);
+    DsPair sum[2] = {DsPair(0.f, 0.f), DsPair(0.f, 0.f)};
+    auto add = [&](bool far) {
+      DsPower p = power;
+      p.far = far;
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    float v[N];
-    ds_opaque(raw[j]);
-    Vec16<T>::unpack(raw[j], v);
+      for (int j = 0; j < U; ++j) {
+        float v[N];
+        ds_opaque(raw[j]);
+        Vec16<T>::unpack(raw[j], v);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float x, y;
-      ds_mul2(ds_add2(DsPair(v[i], v[i + 1]), nbase), kk).get(x, y);
-      sum[(i >> 1) & 1] = ds_add2(sum[(i >> 1) & 1], DsPair(ds_exp2(x), ds_exp2(y)));
-    }
+        for (int i = 0; i < N; i += 2) sum[(i >> 1) & 1] = ds_add2(sum[(i >> 1) & 1], p.two(DsPair(v[i], v[i + 1])));
+      }
+    };
+    if (power.far) add(true);
+    else add(false);
+    float s0, s1;
+    ds_add2(sum[0], sum[1]).get(s0, s1);
+    s = s0 + s1;
+    if (all || s <= 1099511627776.f) break;  // (NaN goes on, once)
   }
-  float s0, s1;
-  ds_add2(sum[0], sum[1]).get(s0, s1);
-  return {m, s0 + s1};
+  return {m, s};
 }
 
 // The gradient's dense part: w P q of two logits at a time, by
-// exp((z - m) / tau) * mul with the loss's own m (mul holds 1 / s), or by
+// 2^((z - m) k) * mul with the loss's own pair (mul holds 1 / s), or by
 // exp(z / tau - lse) * mul where only lse is known.
 template <bool LOSS>
 struct DsGrad {
-  DsPair a, b, mul;
+  DsPower power;
+  DsPair tau, mul;
   __device__ inline DsGrad(float m_or_lse, float k, float inv_tau, float mul_)
-      : a(-m_or_lse, -m_or_lse), b(LOSS ? k : inv_tau, LOSS ? k : inv_tau), mul(mul_, mul_) {}
+      : power(m_or_lse, k), tau(inv_tau, inv_tau), mul(mul_, mul_) {
+    if (!LOSS) power.a = DsPair(-m_or_lse, -m_or_lse);
+  }
   __device__ inline void operator()(float &u, float &v) const {
     DsPair x(u, v);
-    if (LOSS) x = ds_mul2(ds_add2(x, a), b);
-    else x = ds_mul2(ds_fma2(x, b, a), DsPair(DS_LOG2E, DS_LOG2E));
-    x.get(u, v);
-    ds_mul2(DsPair(ds_exp2(u), ds_exp2(v)), mul).get(u, v);
+    if (LOSS) {
+      x = power.two(x);
+    } else {
+      ds_mul2(ds_fma2(x, tau, power.a), DsPair(DS_LOG2E, DS_LOG2E)).get(u, v);
+      x = DsPair(ds_exp2(u), ds_exp2(v));
+    }
+    ds_mul2(x, mul).get(u, v);
   }
 };
 
@@ -332,19 +392,22 @@ __device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl, 
 __device__ inline bool ds_none(DsStat st) { return st.m == ds_neg_inf() && !(st.s != st.s); }
 
 // One warp: a row's loss and lse from its statistics.
-__device__ inline void ds_loss(const DistillArgs &a, int64_t t, const DsSlots &sl, DsStat st) {
+__device__ inline void ds_loss(const DistillArgs &a, int64_t t, const DsSlots &sl, DsStat st, float k) {
   const int lane = threadIdx.x & 31;
-  const float logs = logf(st.s);
+  const float logs = logf(st.s), mk = __fmul_rn(st.m, k);
+  const bool far = !(fabsf(mk) < 1e37f);
   float l = 0.f;
   for (int s = lane; s < a.K; s += 32) {
     const float p = sl.p[s];
-    if (p != 0.f) l += p * (sl.x[s] - sl.c - fmaf(sl.z[s] - st.m, a.inv_tau, -logs));
+    const float z = sl.z[s];
+    const float d = far || !(fabsf(z * k) < 1e37f) ? (z - st.m) * a.inv_tau : fmaf(z, k, -mk) * DS_LN2;
+    if (p != 0.f) l += p * (sl.x[s] - sl.c - (d - logs));
   }
   l = ds_warp_sum(l);
   if (ds_none(st)) l = -ds_neg_inf();
   if (lane == 0) {
     a.loss[t] = sl.any ? a.scale * l : 0.f;
-    if (a.lse) a.lse[t] = ds_none(st) ? ds_neg_inf() : fmaf(st.m, a.inv_tau, logs);
+    if (a.lse) a.lse[t] = ds_none(st) ? ds_neg_inf() : far ? fmaf(st.m, a.inv_tau, logs) : fmaf(mk, DS_LN2, logs);
   }
 }
 
@@ -373,28 +436,38 @@ __device__ inline void ds_places(const DistillArgs &a, const DsSlots &sl, T *dz,
   }
 }
 
-// The dense part of the gradient of U units a thread; half() is called between
-// the halves of them.
+// The dense part of the gradient of U units a thread: load(j, inner) gives
+// unit j, half() is called between the halves of them.  Units inside the row
+// run without a branch between them, so that one's exponentials overlap the
+// next one's loads; the others one after the other.
 template <typename T, bool ALIGNED, bool LOSS, int U, typename Load, typename Half>
-__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, const DsGrad<LOSS> &grad, Load load, Half half) {
+__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, bool inner, DsGrad<LOSS> grad, Load load, Half half) {
   constexpr int N = DsUnit<T>::N;
   const int off = ALIGNED ? 0 : ds_offset(dz);
-  if (zero) {
-#pragma unroll 1
-    for (int j = 0; j < U; ++j) DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, uint4{});
-    half();
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
+  auto unit = [&](const uint4 &raw) {
     float v[N];
-    Vec16<T>::unpack(load(j), v);
+    Vec16<T>::unpack(raw, v);
 #pragma unroll
     for (int i = 0; i < N; i += 2) grad(v[i], v[i + 1]);
     uint4 o;
     Vec16<T>::store((T *)&o, v);
-    DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, o);
-    if (j == U / 2 - 1) half();
+    return o;
+  };
+  if (!zero && inner && !(LOSS && grad.power.far)) {
+    grad.power.far = false;  // known to the compiler
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint4 o = unit(load(j, true));
+      if (ALIGNED) __stcs((uint4 *)dz + u0 + j * step, o);
+      else DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, o);
+      if (j == U / 2 - 1) half();
+    }
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < U; ++j) {
+      DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, zero ? uint4{} : unit(load(j, false)));
+      if (j == U / 2 - 1) half();
+    }
   }
 }
 
@@ -438,7 +511,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       mbar_init(&sh.go[i], 1);
       mbar_init(&sh.raw[i], 1);
     }
-    for (int i = 0; i < DS_STATS; ++i) mbar_init(&sh.stats[i], ctas);
+    for (int i = 0; i < DS_STATS; ++i) mbar_init(&sh.stats[i], 1);
     sh.abort_flag = 0;
     fence_mbar_init();
   }
@@ -463,39 +536,51 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
 
   if (warp == W) {
     // ------------------------------------------------------------ loader
-    int id[SL];
-    float x[SL], w = 0.f, lse = 0.f;
-    auto fetch = [&](int j) {
+    // Slots two rows ahead (memory under load answers late).
+    int id[2][SL];
+    float x[2][SL], w[2] = {0.f, 0.f}, lse[2] = {0.f, 0.f};
+    T zk[SL];  // as loaded: turned into floats only when they have arrived
+    auto fetch = [&](int j, int b) {
+      if (j >= rows) return;
       const int64_t t = t0 + (int64_t)j * stride;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
-        id[i] = slot_id(t, i);
-        x[i] = slot_x(t, i);
+        id[b][i] = slot_id(t, i);
+        x[b][i] = slot_x(t, i);
       }
-      if (GRAD) w = a.weight[t];
-      if (!LOSS) lse = a.lse[t];
+      if (GRAD) w[b] = a.weight[t];
+      if (!LOSS) lse[b] = a.lse[t];
     };
-    if (rows > 0) fetch(0);
-    for (int j = 0; j < rows; ++j) {
+    // The student's logits of row j have been on their way for a row's time.
+    auto hand_over = [&](int j) {
+      DsSlots &sl = sh.slots[j % DS_RING];
+#pragma unroll
+      for (int i = 0; i < SL; ++i)
+        if (lane + 32 * i < a.K) sl.z[lane + 32 * i] = Elem<T>::to_f32(zk[i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.raw[j % DS_RING]);
+    };
+    auto turn = [&](int j, int b) {
       const int r = j % DS_RING;
       const T *z = row_of(j);
       bool found = false;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
-        if (id[i] < -1 || id[i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
-        if (!counts(id[i], x[i])) id[i] = -1;
-        found |= id[i] >= 0;
+        if (id[b][i] < -1 || id[b][i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
+        if (!counts(id[b][i], x[b][i])) id[b][i] = -1;
+        found |= id[b][i] >= 0;
       }
-      const bool any = __any_sync(FULL_MASK, found), read = needed(any, w);
+      const bool any = __any_sync(FULL_MASK, found), read = needed(any, w[b]);
+      if (j > 0) hand_over(j - 1);
       // The aligned pieces that lie in the row (none of a row that is not read).
       const int off = ALIGNED ? 0 : ds_offset(z);
       const int last = read ? (a.V + off) / N : 0;
       uint4 *slice = slices + r * (SPAN + 1);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!wait(&sh.empty[r][h], j / DS_RING + 1)) return;
+        if (!wait(&sh.empty[r][h], j / DS_RING + 1)) return false;
         // (with a gradient the consumers cannot be done before the joiner is)
-        if (!GRAD && !wait(&sh.freed[r], j / DS_RING + 1)) return;
+        if (!GRAD && !wait(&sh.freed[r], j / DS_RING + 1)) return false;
         if (lane == 0) {
           if (h == 1) sh.read[r] = read;
           const int from = u_first + (h ? SPAN / 2 : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
@@ -509,32 +594,35 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         }
         __syncwarp();
       }
-      float zk[SL];
 #pragma unroll
       for (int i = 0; i < SL; ++i)  // without a loss, only this CTA's places matter (others may have been written)
-        zk[i] = id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi)) ? Elem<T>::load(z + id[i]) : 0.f;
-      if (!wait(&sh.freed[r], j / DS_RING + 1)) return;
+        if (id[b][i] >= 0 && (LOSS || (id[b][i] >= lo && id[b][i] < hi))) zk[i] = z[id[b][i]];
+        else zk[i] = T(0.f);
+      if (!wait(&sh.freed[r], j / DS_RING + 1)) return false;
       DsSlots &sl = sh.slots[r];
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         const int s = lane + 32 * i;
         if (s < a.K) {
-          sl.id[s] = id[i];
-          sl.x[s] = x[i] * a.inv_tau;
+          sl.id[s] = id[b][i];
+          sl.x[s] = x[b][i] * a.inv_tau;
         }
       }
       if (lane == 0) {
-        sl.w = w * a.scale * a.inv_tau;
-        sl.lse = lse;
+        sl.w = w[b] * a.scale * a.inv_tau;
+        sl.lse = lse[b];
         sl.any = any;
       }
-      if (j + 1 < rows) fetch(j + 1);
-#pragma unroll
-      for (int i = 0; i < SL; ++i)
-        if (lane + 32 * i < a.K) sl.z[lane + 32 * i] = zk[i];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.raw[r]);
+      fetch(j + 2, b);
+      return true;
+    };
+    fetch(0, 0);
+    fetch(1, 1);
+    for (int j = 0; j < rows; j += 2) {
+      if (!turn(j, 0)) return;
+      if (j + 1 < rows && !turn(j + 1, 1)) return;
     }
+    if (rows > 0) hand_over(rows - 1);
   } else if (warp == W + 1) {
     // ------------------------------------------------------------ teacher
     for (int j = 0; j < rows; ++j) {
@@ -555,12 +643,8 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       if (LOSS) {
         st = ds_join<W>(sh.warp[r], k);
         if (ctas > 1) {
-          if (lane < ctas) {
-            ds_st_cluster(mapa_shared(&sh.cta[q][rank], lane), st);
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                             mapa_shared(&sh.stats[q], lane))
-                         : "memory");
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&sh.stats[q], ctas * (uint32_t)sizeof(DsStat));
+          if (lane < ctas) ds_st_async(mapa_shared(&sh.cta[q][rank], lane), st, mapa_shared(&sh.stats[q], lane));
           __syncwarp();
           if (!mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status)) return;
           st = ds_join<DS_MAX_CTAS>(sh.cta[q], k);
@@ -582,7 +666,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const int64_t t = t0 + (int64_t)j * stride;
       DsSlots &sl = sh.slots[r];
       if (!wait(&sh.go[r], j / DS_RING)) return;
-      if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s});
+      if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s}, k);
       if (GRAD) {
         if (!wait(&sh.empty[r][1], j / DS_RING)) return;
         if (sl.mul != 0.f)
@@ -606,9 +690,14 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         const T *z = row_of(j);
         const int off = ALIGNED ? 0 : ds_offset(z);
         uint4 raw[U];
+        if (DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V)) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
-        mine = ds_warp_join(ds_units_stat<T, U>(raw, mine, k), k);
+          for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load_inner<ALIGNED>(slice + i * STEP, off);
+        } else {
+#pragma unroll
+          for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+        }
+        mine = ds_warp_join(ds_units_stat<T, U>(raw, k), k);
       }
       if (lane == 0) {
         sh.warp[r][warp] = mine;
@@ -630,7 +719,9 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
       const int off = ALIGNED ? 0 : ds_offset(z);
       T *dz = (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits;
-      ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), [&](int i) {
+      const bool inner = DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V);
+      ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, inner, DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), [&](int i, bool in) {
+        if (in) return DsUnit<T>::template load_inner<ALIGNED>(slice + i * STEP, off);
         return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
       }, [&] {
         __syncwarp();
@@ -699,7 +790,9 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
         const int u = u_first + (g * U + i) * THREADS + threadIdx.x;
         raw[i] = DsUnit<T>::template load<false>(piece(u), z, off, u, a.V);
       }
-      st = ds_units_stat<T, U>(raw, st, k);
+      const DsStat one = ds_units_stat<T, U>(raw, k);
+      const DsPower power(fmaxf(st.m, one.m), k);
+      st = {fmaxf(st.m, one.m), st.s * power.of(st.m) + one.s * power.of(one.m)};
     }
     st = ds_warp_join(st, k);
     if (lane == 0) wstat[warp] = st;
@@ -714,7 +807,7 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
     if (ctas > 1) cluster_sync();
     else __syncthreads();
     st = ds_warp_join(lane < ctas ? cstat[lane] : DsStat{ds_neg_inf(), 0.f}, k);
-    if (rank == 0 && warp == 0) ds_loss(a, t, sl, st);
+    if (rank == 0 && warp == 0) ds_loss(a, t, sl, st, k);
   } else {
     st = {sl.lse, 1.f};
   }
@@ -724,10 +817,11 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
   const DsGrad<LOSS> grad(st.m, k, a.inv_tau, sl.w * sl.total / st.s);
   for (int g = 0; g < groups; ++g) {
     const int u0 = u_first + g * U * THREADS + threadIdx.x;
-    uint4 raw[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) raw[i] = zero ? uint4{} : DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
-    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, grad, [&](int i) { return raw[i]; }, [] {});
+    const bool inner = DsUnit<T>::template inner<false>(off, u0, THREADS, U, a.V);
+    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, inner, grad, [&](int i, bool in) {
+      if (in) return DsUnit<T>::template load_inner<false>(piece(u0 + i * THREADS), off);
+      return DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
+    }, [] {});
   }
   __syncthreads();
   if (!zero) ds_places<T, LOSS>(a, sl, dz, lo, hi, sl.w, grad, threadIdx.x, THREADS);
