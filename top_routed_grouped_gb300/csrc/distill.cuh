@@ -545,6 +545,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const int64_t t = t0 + (int64_t)j * stride;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
         id[b][i] = slot_id(t, i);
         x[b][i] = slot_x(t, i);
       }
@@ -555,8 +556,10 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
     auto hand_over = [&](int j) {
       DsSlots &sl = sh.slots[j % DS_RING];
 #pragma unroll
-      for (int i = 0; i < SL; ++i)
+      for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
         if (lane + 32 * i < a.K) sl.z[lane + 32 * i] = Elem<T>::to_f32(zk[i]);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.raw[j % DS_RING]);
     };
@@ -566,6 +569,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       bool found = false;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
         if (id[b][i] < -1 || id[b][i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
         if (!counts(id[b][i], x[b][i])) id[b][i] = -1;
         found |= id[b][i] >= 0;
@@ -595,13 +599,16 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         __syncwarp();
       }
 #pragma unroll
-      for (int i = 0; i < SL; ++i)  // without a loss, only this CTA's places matter (others may have been written)
+      for (int i = 0; i < SL; ++i) {  // without a loss, only this CTA's places matter (others may have been written)
+        if (32 * i >= a.K) break;
         if (id[b][i] >= 0 && (LOSS || (id[b][i] >= lo && id[b][i] < hi))) zk[i] = z[id[b][i]];
         else zk[i] = T(0.f);
+      }
       if (!wait(&sh.freed[r], j / DS_RING + 1)) return false;
       DsSlots &sl = sh.slots[r];
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
         const int s = lane + 32 * i;
         if (s < a.K) {
           sl.id[s] = id[b][i];
