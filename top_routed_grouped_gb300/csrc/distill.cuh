@@ -10,15 +10,14 @@
 // written, one whose statistics are taken and one on its way, so that a row is
 // read from memory once and nothing waits for it.  The warps of a CTA:
 //   loader     starts the bulk copies, half a slice at a time, as soon as the
-//              consumers are done with what stood there, and brings the
-//              teacher's slots, with the student's logits at their places
-//   teacher    turns the slots into p
+//              consumers are done with what stood there
 //   consumers  statistics of row j + 1, then gradient of row j
 //   joiner     joins the warps' statistics and hands them to the other CTAs
 //              through distributed shared memory
-//   finisher   sums the loss, and writes the teacher's places of the gradient
-//              again, p subtracted, behind the dense pass (apart from the
-//              joiner: its stores to memory would hold up every hand-over)
+//   three row warps, a row each in turn: the teacher's slots and their softmax,
+//              then the loss, then the teacher's places of the gradient again,
+//              p subtracted, behind the dense pass (apart from the joiner: its
+//              stores to memory would hold up the hand-over)
 // They meet at mbarriers alone; no barrier stops a whole CTA.
 // Sums of exponentials stand beside the logit that they are relative to: a
 // thread takes the largest of its first unit, and the largest of all it has
@@ -27,8 +26,9 @@
 // order.
 // The shape goes by the vocabulary alone, so a row's results do not depend on
 // the batch, and a thread's units do not depend on where the row starts.
-// Rows too long for the shared memory of a cluster take a plainer kernel that
-// reads them twice.
+// Short rows, where those hand-overs cost more than they hide, and rows too
+// long for the shared memory of a cluster take a plainer kernel: a cluster
+// (one CTA, for the short ones) for every row, many at once on an SM.
 //
 // An exponent is one fused multiply-add, z k - m k with k = log2(e) / tau, and m k
 // rounded alike wherever it is used; where m k would overflow (rows at the
@@ -331,46 +331,31 @@ struct __align__(16) DsSlots {
   float mul;               // what DsGrad takes; 0 where there is no gradient
 };
 
-// One warp: the teacher's distribution from its slots; `marks` finds ids given
-// twice: every slot leaves its number at a place that its id hashes to.  One
-// that reads another number there is a copy of that slot, or looks for itself
-// among all of them.
+// One warp: the teacher's distribution from its slots, and whether an id is
+// there twice.  For that every slot leaves its number at a place of `marks`
+// that its id hashes to: one that reads its own number there is alone or the
+// one that its copies read; one that reads another's is a copy, or tries again
+// with another hash (its copies, if any, do the same).
 __device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl, uint8_t *marks) {
   constexpr int SL = DISTILL_MAX_K / 32;
   const int lane = threadIdx.x & 31;
-  auto mark = [&](int id) { return ((uint32_t)id * 2654435761u) >> 21; };
   int id[SL];
-  float x[SL], m = ds_neg_inf(), sum = 0.f;
+  float x[SL], e[SL], m = ds_neg_inf(), sum = 0.f;
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
     if (32 * i >= a.K) break;
     const int s = lane + 32 * i;
     id[i] = s < a.K ? sl.id[s] : -1;
     x[i] = s < a.K ? sl.x[s] : 0.f;
-    if (id[i] >= 0) {
-      m = fmaxf(m, x[i]);
-      marks[mark(id[i])] = (uint8_t)s;
-    }
+    if (id[i] >= 0) m = fmaxf(m, x[i]);
   }
-  __syncwarp();
   float c = 0.f;
   if (a.t_lse) m = c = a.t_lse[t];
   else m = ds_warp_max(m);
-  float e[SL];
-  bool twice = false;
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
     if (32 * i >= a.K) break;
-    e[i] = 0.f;
-    if (id[i] >= 0) {
-      e[i] = expf(x[i] - m);
-      const int s = lane + 32 * i, other = marks[mark(id[i])];
-      if (other != s) {
-        if (sl.id[other] == id[i]) twice = true;
-        else
-          for (int q = 0; q < a.K; ++q) twice |= q != s && sl.id[q] == id[i];
-      }
-    }
+    e[i] = id[i] >= 0 ? expf(x[i] - m) : 0.f;
     sum += e[i];
   }
   sum = ds_warp_sum(sum);
@@ -379,6 +364,38 @@ __device__ inline void ds_teacher(const DistillArgs &a, int64_t t, DsSlots &sl, 
   for (int i = 0; i < SL; ++i) {
     if (32 * i >= a.K) break;
     if (lane + 32 * i < a.K) sl.p[lane + 32 * i] = e[i] * inv;
+  }
+  bool twice = false, again = a.K > 1;
+  uint32_t mix = 2654435761u;
+  for (int round = 0; again; ++round) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      if (32 * i >= a.K) break;
+      if (id[i] >= 0) marks[(uint32_t)(id[i] + 1) * mix >> 21] = (uint8_t)(lane + 32 * i);
+    }
+    __syncwarp();
+    bool open = false;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      if (32 * i >= a.K) break;
+      if (id[i] < 0) continue;
+      const int other = marks[(uint32_t)(id[i] + 1) * mix >> 21];
+      if (other != lane + 32 * i) {
+        if (sl.id[other] == id[i]) twice = true;
+        else {
+          open = true;
+          continue;
+        }
+      }
+      id[i] = -1;  // settled
+    }
+    again = __any_sync(FULL_MASK, open);
+    if (again && round == 7) {  // an odd set of ids: take it that there are copies
+      twice = true;
+      break;
+    }
+    mix = mix * 747796405u + 2891336453u | 1u;
   }
   twice = __any_sync(FULL_MASK, twice);
   if (lane == 0) {
@@ -475,10 +492,9 @@ struct DsShared {
   DsSlots slots[DS_RING];
   __align__(16) DsStat warp[DS_RING][16];
   __align__(16) DsStat cta[DS_STATS][DS_MAX_CTAS];
-  uint8_t marks[DS_MARKS];
-  uint64_t raw[DS_RING];                          // a teacher's slots are there
+  uint8_t marks[DS_RING][DS_MARKS];
   uint64_t full[DS_RING], empty[DS_RING][2];      // a slice has arrived; the consumers are done with its halves
-  uint64_t ready[DS_RING], freed[DS_RING];        // a teacher is there; the joiner is done with it
+  uint64_t ready[DS_RING];                        // a teacher is there
   uint64_t taken[DS_RING], stats[DS_STATS];       // the warps' pairs are there; all CTAs' pairs are there
   uint64_t go[DS_RING];                           // the row's gradient can be written
   int read[DS_RING];                              // whether a slice was loaded (written by the loader before `full`)
@@ -488,7 +504,7 @@ struct DsShared {
 // W: consumer warps; U: units a thread; 1 << shift: CTAs of a cluster.
 // ALIGNED: all rows start on 16-byte boundaries.
 template <typename T, bool ALIGNED, int MODE, int W, int U>
-__global__ void __launch_bounds__(32 * (W + 4), W == 16 ? 1 : W == 8 ? 2 : 4)
+__global__ void __launch_bounds__(32 * (W + 2 + DS_RING), 1)
 distill_kernel(const DistillArgs a, int shift, int *status) {
   using namespace umma;
   constexpr int N = DsUnit<T>::N, SPAN = U * W * 32;
@@ -506,10 +522,8 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       mbar_init(&sh.empty[i][0], W);
       mbar_init(&sh.empty[i][1], W);
       mbar_init(&sh.ready[i], 1);
-      mbar_init(&sh.freed[i], 1);
       mbar_init(&sh.taken[i], W);
       mbar_init(&sh.go[i], 1);
-      mbar_init(&sh.raw[i], 1);
     }
     for (int i = 0; i < DS_STATS; ++i) mbar_init(&sh.stats[i], 1);
     sh.abort_flag = 0;
@@ -538,8 +552,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
     // ------------------------------------------------------------ loader
     // Slots two rows ahead (memory under load answers late).
     int id[2][SL];
-    float x[2][SL], w[2] = {0.f, 0.f}, lse[2] = {0.f, 0.f};
-    T zk[SL];  // as loaded: turned into floats only when they have arrived
+    float x[2][SL], w[2] = {0.f, 0.f};
     auto fetch = [&](int j, int b) {
       if (j >= rows) return;
       const int64_t t = t0 + (int64_t)j * stride;
@@ -550,41 +563,27 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         x[b][i] = slot_x(t, i);
       }
       if (GRAD) w[b] = a.weight[t];
-      if (!LOSS) lse[b] = a.lse[t];
-    };
-    // The student's logits of row j have been on their way for a row's time.
-    auto hand_over = [&](int j) {
-      DsSlots &sl = sh.slots[j % DS_RING];
-#pragma unroll
-      for (int i = 0; i < SL; ++i) {
-        if (32 * i >= a.K) break;
-        if (lane + 32 * i < a.K) sl.z[lane + 32 * i] = Elem<T>::to_f32(zk[i]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.raw[j % DS_RING]);
     };
     auto turn = [&](int j, int b) {
-      const int r = j % DS_RING;
+      const int r = j % DS_RING, round = j / DS_RING;
       const T *z = row_of(j);
       bool found = false;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         if (32 * i >= a.K) break;
-        if (id[b][i] < -1 || id[b][i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
-        if (!counts(id[b][i], x[b][i])) id[b][i] = -1;
-        found |= id[b][i] >= 0;
+        found |= counts(id[b][i], x[b][i]);
       }
-      const bool any = __any_sync(FULL_MASK, found), read = needed(any, w[b]);
-      if (j > 0) hand_over(j - 1);
+      const bool read = needed(__any_sync(FULL_MASK, found), w[b]);
+      fetch(j + 2, b);
       // The aligned pieces that lie in the row (none of a row that is not read).
       const int off = ALIGNED ? 0 : ds_offset(z);
       const int last = read ? (a.V + off) / N : 0;
       uint4 *slice = slices + r * (SPAN + 1);
+      // (with a gradient the consumers cannot be done before the joiner is)
+      if (!GRAD && round > 0 && !wait(&sh.go[r], round - 1)) return false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!wait(&sh.empty[r][h], j / DS_RING + 1)) return false;
-        // (with a gradient the consumers cannot be done before the joiner is)
-        if (!GRAD && !wait(&sh.freed[r], j / DS_RING + 1)) return false;
+        if (!wait(&sh.empty[r][h], round + 1)) return false;
         if (lane == 0) {
           if (h == 1) sh.read[r] = read;
           const int from = u_first + (h ? SPAN / 2 : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
@@ -598,29 +597,6 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         }
         __syncwarp();
       }
-#pragma unroll
-      for (int i = 0; i < SL; ++i) {  // without a loss, only this CTA's places matter (others may have been written)
-        if (32 * i >= a.K) break;
-        if (id[b][i] >= 0 && (LOSS || (id[b][i] >= lo && id[b][i] < hi))) zk[i] = z[id[b][i]];
-        else zk[i] = T(0.f);
-      }
-      if (!wait(&sh.freed[r], j / DS_RING + 1)) return false;
-      DsSlots &sl = sh.slots[r];
-#pragma unroll
-      for (int i = 0; i < SL; ++i) {
-        if (32 * i >= a.K) break;
-        const int s = lane + 32 * i;
-        if (s < a.K) {
-          sl.id[s] = id[b][i];
-          sl.x[s] = x[b][i] * a.inv_tau;
-        }
-      }
-      if (lane == 0) {
-        sl.w = w[b] * a.scale * a.inv_tau;
-        sl.lse = lse[b];
-        sl.any = any;
-      }
-      fetch(j + 2, b);
       return true;
     };
     fetch(0, 0);
@@ -629,17 +605,73 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       if (!turn(j, 0)) return;
       if (j + 1 < rows && !turn(j + 1, 1)) return;
     }
-    if (rows > 0) hand_over(rows - 1);
-  } else if (warp == W + 1) {
-    // ------------------------------------------------------------ teacher
-    for (int j = 0; j < rows; ++j) {
-      const int r = j % DS_RING;
-      if (!wait(&sh.raw[r], j / DS_RING)) return;
-      ds_teacher(a, t0 + (int64_t)j * stride, sh.slots[r], sh.marks);
+  } else if (warp > W + 1) {
+    // ------------------------------------------------------------ row warps
+    const int r = warp - (W + 2);
+    DsSlots &sl = sh.slots[r];
+    int id[SL];
+    float x[SL], w = 0.f, lse = 0.f;
+    auto fetch = [&](int j) {
+      if (j >= rows) return;
+      const int64_t t = t0 + (int64_t)j * stride;
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
+        id[i] = slot_id(t, i);
+        x[i] = slot_x(t, i);
+      }
+      if (GRAD) w = a.weight[t];
+      if (!LOSS) lse = a.lse[t];
+    };
+    fetch(r);
+    for (int j = r; j < rows; j += DS_RING) {
+      const int round = j / DS_RING;
+      const int64_t t = t0 + (int64_t)j * stride;
+      const T *z = row_of(j);
+      bool found = false;
+      T zk[SL];
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
+        if (id[i] < -1 || id[i] >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
+        if (!counts(id[i], x[i])) id[i] = -1;
+        found |= id[i] >= 0;
+        // without a loss, only this CTA's places matter (others may have been written)
+        if (id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi))) zk[i] = z[id[i]];
+        else zk[i] = T(0.f);
+      }
+      const bool any = __any_sync(FULL_MASK, found);
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        if (32 * i >= a.K) break;
+        const int s = lane + 32 * i;
+        if (s < a.K) {
+          sl.id[s] = id[i];
+          sl.x[s] = x[i] * a.inv_tau;
+          sl.z[s] = Elem<T>::to_f32(zk[i]);
+        }
+      }
+      if (lane == 0) {
+        sl.w = w * a.scale * a.inv_tau;
+        sl.lse = lse;
+        sl.any = any;
+      }
+      __syncwarp();
+      fetch(j + DS_RING);
+      ds_teacher(a, t, sl, sh.marks[r]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[r]);
+      if (!wait(&sh.go[r], round)) return;
+      if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s}, k);
+      if (GRAD) {
+        if (!wait(&sh.empty[r][1], round)) return;
+        if (sl.mul != 0.f)
+          ds_places<T, LOSS>(a, sl, (T *)a.dlogits + t * a.ld_dlogits, lo, hi, sl.w,
+                             DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), lane, 32);
+      }
+      __syncwarp();
     }
-  } else if (warp == W + 2) {
+  } else if (warp == W + 1) {
     // ------------------------------------------------------------ joiner
     for (int j = 0; j < rows; ++j) {
       const int r = j % DS_RING, q = j % DS_STATS;
@@ -665,23 +697,6 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         mbar_arrive(&sh.go[r]);
       }
       __syncwarp();
-    }
-  } else if (warp == W + 3) {
-    // ------------------------------------------------------------ finisher
-    for (int j = 0; j < rows; ++j) {
-      const int r = j % DS_RING;
-      const int64_t t = t0 + (int64_t)j * stride;
-      DsSlots &sl = sh.slots[r];
-      if (!wait(&sh.go[r], j / DS_RING)) return;
-      if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s}, k);
-      if (GRAD) {
-        if (!wait(&sh.empty[r][1], j / DS_RING)) return;
-        if (sl.mul != 0.f)
-          ds_places<T, LOSS>(a, sl, (T *)a.dlogits + t * a.ld_dlogits, lo, hi, sl.w,
-                             DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), lane, 32);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.freed[r]);
     }
   } else {
     // ------------------------------------------------------------ consumers
@@ -746,12 +761,14 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
   }
 }
 
-// Rows of any length: a cluster a row, U units a thread at a time straight from
-// memory, a second time for the gradient.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, int shift, int groups, int *status) {
+// Rows of any length: a cluster for each row, U units a thread at a time
+// straight from memory, for the gradient a second time where there are several
+// groups of them.
+template <typename T, int MODE, int THREADS, int U>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 10 : 1024 / THREADS)
+distill_plain_kernel(const DistillArgs a, int shift, int groups, int *status) {
   using namespace umma;
-  constexpr int N = DsUnit<T>::N, U = 4, THREADS = 512;
+  constexpr int N = DsUnit<T>::N;
   constexpr bool LOSS = (MODE & DISTILL_LOSS) != 0, GRAD = (MODE & DISTILL_GRAD) != 0;
   __shared__ DsSlots sl;
   __shared__ uint8_t marks[DS_MARKS];
@@ -767,14 +784,30 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
   const int off = ds_offset(z), u_first = rank * groups * U * THREADS;
   const int lo = u_first * N, hi = lo + groups * U * THREADS * N;
   auto piece = [&](int u) { return (const uint4 *)(z - off) + u; };
+  // The first group's units are on their way while the teacher is worked out.
+  uint4 raw[U];
+  bool inner = false;
+  auto load = [&](int g) {
+    const int u0 = u_first + g * U * THREADS + threadIdx.x;
+    inner = DsUnit<T>::template inner<false>(off, u0, THREADS, U, a.V);
+    if (inner) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load_inner<false>(piece(u0 + i * THREADS), off);
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        raw[i] = DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
+    }
+  };
+  if (LOSS) load(0);
   if (warp == 0) {
     bool found = false;
     for (int s = lane; s < a.K; s += 32) {
       int id = a.t_ids[t * a.K + s];
       const float x = a.t_logits[t * a.K + s] * a.inv_tau;
       if (id < -1 || id >= a.V) record_status(status, STATUS_BAD_TEACHER_ID);
-      if (id >= a.V || x == ds_neg_inf()) id = -1;
-      sl.id[s] = id = id < 0 ? -1 : id;
+      if (id < 0 || id >= a.V || x == ds_neg_inf()) id = -1;
+      sl.id[s] = id;
       sl.x[s] = x;
       sl.z[s] = id >= 0 && (LOSS || (id >= lo && id < hi)) ? Elem<T>::load(z + id) : 0.f;
       found |= id >= 0;
@@ -791,12 +824,7 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
   DsStat st = {ds_neg_inf(), 0.f};
   if (LOSS) {
     for (int g = 0; g < groups; ++g) {
-      uint4 raw[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int u = u_first + (g * U + i) * THREADS + threadIdx.x;
-        raw[i] = DsUnit<T>::template load<false>(piece(u), z, off, u, a.V);
-      }
+      if (g) load(g);
       const DsStat one = ds_units_stat<T, U>(raw, k);
       const DsPower power(fmaxf(st.m, one.m), k);
       st = {fmaxf(st.m, one.m), st.s * power.of(st.m) + one.s * power.of(one.m)};
@@ -806,14 +834,12 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
   }
   __syncthreads();
   if (LOSS) {
-    if (warp == 0) {
-      st = ds_warp_join(lane < THREADS / 32 ? wstat[lane] : DsStat{ds_neg_inf(), 0.f}, k);
-      if (ctas == 1) cstat[0] = st;
-      else if (lane < ctas) ds_st_cluster(mapa_shared(&cstat[rank], lane), st);
+    st = ds_join<THREADS / 32>(wstat, k);
+    if (ctas > 1) {
+      if (warp == 0 && lane < ctas) ds_st_cluster(mapa_shared(&cstat[rank], lane), st);
+      cluster_sync();
+      st = ds_warp_join(lane < ctas ? cstat[lane] : DsStat{ds_neg_inf(), 0.f}, k);
     }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
-    st = ds_warp_join(lane < ctas ? cstat[lane] : DsStat{ds_neg_inf(), 0.f}, k);
     if (rank == 0 && warp == 0) ds_loss(a, t, sl, st, k);
   } else {
     st = {sl.lse, 1.f};
@@ -824,9 +850,9 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
   const DsGrad<LOSS> grad(st.m, k, a.inv_tau, sl.w * sl.total / st.s);
   for (int g = 0; g < groups; ++g) {
     const int u0 = u_first + g * U * THREADS + threadIdx.x;
-    const bool inner = DsUnit<T>::template inner<false>(off, u0, THREADS, U, a.V);
+    if (!zero && (!LOSS || groups > 1)) load(g);
     ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, inner, grad, [&](int i, bool in) {
-      if (in) return DsUnit<T>::template load_inner<false>(piece(u0 + i * THREADS), off);
+      if (in) return raw[i];
       return DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
     }, [] {});
   }
@@ -835,24 +861,23 @@ __global__ void __launch_bounds__(512) distill_long_kernel(const DistillArgs a, 
 }
 
 // ---------------------------------------------------------------- host
-template <typename T, int MODE>
-static cudaError_t ds_launch_long(const DistillArgs &a, int *status, cudaStream_t stream) {
-  const int shift = 3;
+template <typename T, int MODE, int THREADS, int U>
+static cudaError_t ds_launch_plain(const DistillArgs &a, int shift, int *status, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T << shift);
-  cfg.blockDim = dim3(512);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1u << shift;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 1u << shift;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  const int groups = (int)ceil_div(ceil_div(a.V, 16 / (int)sizeof(T)), (int64_t)(512 * 4) << shift);
-  return cudaLaunchKernelEx(&cfg, distill_long_kernel<T, MODE>, a, shift, groups, status);
+  cfg.numAttrs = shift ? 2 : 1;
+  const int groups = (int)ceil_div(ceil_div(a.V, 16 / (int)sizeof(T)), (int64_t)(THREADS * U) << shift);
+  return cudaLaunchKernelEx(&cfg, distill_plain_kernel<T, MODE, THREADS, U>, a, shift, groups, status);
 }
 
 template <typename T, bool ALIGNED, int MODE, int W, int U>
@@ -863,7 +888,7 @@ static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaS
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1u << shift);
-  cfg.blockDim = dim3(32 * (W + 4));
+  cfg.blockDim = dim3(32 * (W + 2 + DS_RING));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
@@ -900,12 +925,11 @@ static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaS
 template <typename T, bool ALIGNED, int MODE>
 static cudaError_t ds_shape(const DistillArgs &a, int *status, cudaStream_t stream) {
   const int64_t n = ceil_div(a.V, 16 / (int)sizeof(T));
-  if (n <= 256) return ds_launch<T, ALIGNED, MODE, 4, 2>(a, 0, status, stream);
-  if (n <= 1024) return ds_launch<T, ALIGNED, MODE, 4, 8>(a, 0, status, stream);
-  if (n <= 2048) return ds_launch<T, ALIGNED, MODE, 8, 8>(a, 0, status, stream);
+  if (n <= 1024) return ds_launch_plain<T, MODE, 128, 4>(a, 0, status, stream);
+  if (n <= 2048) return ds_launch_plain<T, MODE, 256, 8>(a, 0, status, stream);
   for (int shift = 0; 1 << shift <= DS_MAX_CTAS; ++shift)
     if (n <= (int64_t)4096 << shift) return ds_launch<T, ALIGNED, MODE, 16, 8>(a, shift, status, stream);
-  return ds_launch_long<T, MODE>(a, status, stream);
+  return ds_launch_plain<T, MODE, 512, 4>(a, 3, status, stream);
 }
 
 template <typename T, bool ALIGNED>
