@@ -9,7 +9,8 @@
 //      token's bits each: one launch on a cluster of sixteen CTAs, whose
 //      counts meet in distributed shared memory (for more tokens than that is
 //      good for, the kernels of the route permutation, twice);
-//   2. meanwhile, on the other SMs, the table is zeroed;
+//   2. meanwhile, on the other SMs, the rows of the table that no token hits
+//      are zeroed;
 //   3. tiles of consecutive sorted positions sum their rows, token by token.
 //      A token that lies in one tile is written at once, one that spans tiles
 //      leaves a partial row in each;
@@ -28,7 +29,8 @@ namespace moe {
 constexpr int EM_THREADS = 256, EM_ROWS = 4;
 constexpr int ES_CTAS = 16, ES_THREADS = 1024, ES_WARPS = 32;
 constexpr int EM_DIGIT = 1024;                   // of the permutation's kernels
-constexpr int64_t ES_MAX_T = int64_t(1) << 17;   // tokens of the one-launch sort
+constexpr int ES_STEPS = 8;                      // of 32 positions a warp
+constexpr int64_t ES_MAX_T = ES_CTAS * ES_WARPS * 32 * ES_STEPS;  // tokens of the one-launch sort
 
 __device__ inline int64_t em_id(const EmbedArgs &a, int64_t t) {
   return a.ids64 ? ((const int64_t *)a.ids)[t] : (int64_t)((const int32_t *)a.ids)[t];
@@ -41,71 +43,88 @@ __device__ inline int32_t em_key(const EmbedArgs &a, int64_t t, int *status) {
   return ok && id != a.padding_id ? (int32_t)id : a.V;
 }
 
-// VEC neighbouring elements as floats.
+// What a thread holds of a row: VEC neighbouring elements, or, where rows do
+// not all start on 16-byte boundaries (VEC = 0), four elements `stride` apart.
+template <int VEC>
+constexpr int em_n() {
+  return VEC ? VEC : 4;
+}
 template <typename T, int VEC>
-__device__ inline void em_load(const T *p, float (&o)[VEC]) {
-  if constexpr (VEC == 1) {
-    o[0] = Elem<T>::load(p);
+__device__ inline void em_load(const T *row, int i, int stride, int H, float (&o)[em_n<VEC>()]) {
+  if constexpr (VEC == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = i + k * stride < H ? Elem<T>::load(row + i + k * stride) : 0.f;
   } else {
     constexpr int N = Vec16<T>::N;
 #pragma unroll
     for (int b = 0; b < VEC / N; ++b) {
       float v[N];
-      Vec16<T>::load(p + b * N, v);
+      Vec16<T>::load(row + i + b * N, v);
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[b * N + i] = v[i];
+      for (int k = 0; k < N; ++k) o[b * N + k] = v[k];
     }
   }
 }
 template <typename T, int VEC>
-__device__ inline void em_store(T *p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    p[0] = Elem<T>::from_f32(v[0]);
+__device__ inline void em_store(T *row, int i, int stride, int H, const float (&v)[em_n<VEC>()]) {
+  if constexpr (VEC == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * stride < H) row[i + k * stride] = Elem<T>::from_f32(v[k]);
   } else {
     constexpr int N = Vec16<T>::N;
 #pragma unroll
     for (int b = 0; b < VEC / N; ++b) {
       float o[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = v[b * N + i];
-      Vec16<T>::store(p + b * N, o);
+      for (int k = 0; k < N; ++k) o[k] = v[b * N + k];
+      Vec16<T>::store(row + i + b * N, o);
     }
   }
 }
 
 // ---------------------------------------------------------------- lookup
 template <typename TE, typename TO, int VEC>
-__global__ void __launch_bounds__(EM_THREADS) embed_kernel(const EmbedArgs a, int group, int rows, int *status) {
+__global__ void __launch_bounds__(EM_THREADS, 4) embed_kernel(const EmbedArgs a, int group, int rows, int *status) {
+  constexpr int N = em_n<VEC>();
   griddep_launch();
   griddep_wait();
-  const int sub = threadIdx.x / group, lane = threadIdx.x % group;
-  const int64_t t0 = ((int64_t)blockIdx.x * (EM_THREADS / group) + sub) * rows;
-  if (sub >= EM_THREADS / group) return;
-  const TE *src[EM_ROWS];
+  const int per_cta = EM_THREADS / group, sub = threadIdx.x / group, lane = threadIdx.x % group;
+  const int64_t step = (int64_t)gridDim.x * per_cta * rows;
+  int64_t t0 = ((int64_t)blockIdx.x * per_cta + sub) * rows;
+  int64_t next[EM_ROWS];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
-  for (int r = 0; r < EM_ROWS; ++r) {
-    src[r] = nullptr;
-    if (r < rows && t0 + r < a.T) {
-      const int64_t id = em_id(a, t0 + r);
-      if (id >= 0 && id < a.V) src[r] = (const TE *)a.table + id * a.ld_table;
-      else if (lane == 0) record_status(status, STATUS_BAD_TOKEN_ID);
-    }
-  }
-  for (int i = lane * VEC; i < a.H; i += group * VEC) {
-    float v[EM_ROWS][VEC];
+    for (int r = 0; r < EM_ROWS; ++r) next[r] = r < rows && t + r < a.T ? em_id(a, t + r) : 0;
+  };
+  fetch(t0);
+  for (; t0 < a.T; t0 += step) {
+    const TE *src[EM_ROWS];
 #pragma unroll
     for (int r = 0; r < EM_ROWS; ++r) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[r][k] = 0.f;
-      if (src[r]) em_load<TE, VEC>(src[r] + i, v[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < EM_ROWS; ++r)
+      src[r] = nullptr;
       if (r < rows && t0 + r < a.T) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) v[r][k] *= a.scale;
-        em_store<TO, VEC>((TO *)a.out + (t0 + r) * a.ld_out + i, v[r]);
+        if (next[r] >= 0 && next[r] < a.V) src[r] = (const TE *)a.table + next[r] * a.ld_table;
+        else if (lane == 0) record_status(status, STATUS_BAD_TOKEN_ID);
       }
+    }
+    fetch(t0 + step);
+    for (int i = VEC ? lane * VEC : lane; i < a.H; i += group * N) {
+      float v[EM_ROWS][N];
+#pragma unroll
+      for (int r = 0; r < EM_ROWS; ++r) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[r][k] = 0.f;
+        if (src[r]) em_load<TE, VEC>(src[r], i, group, a.H, v[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < EM_ROWS; ++r)
+        if (r < rows && t0 + r < a.T) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) v[r][k] *= a.scale;
+          em_store<TO, VEC>((TO *)a.out + (t0 + r) * a.ld_out, i, group, a.H, v[r]);
+        }
+    }
   }
 }
 
@@ -121,7 +140,8 @@ __device__ inline int32_t es_ld_cluster(uint32_t addr) {
 // are prefixed over warps, CTAs and digits, then its positions are handed out
 // in order, 32 at a time.  Buffers hold T entries.
 __global__ void __launch_bounds__(ES_THREADS)
-embed_sort_kernel(const EmbedArgs a, int bits, int32_t *key1, int32_t *pos1, int32_t *key2, int32_t *pos2, int *status) {
+embed_sort_kernel(const EmbedArgs a, int bits, int32_t *mark, int32_t *key1, int32_t *pos1, int32_t *key2, int32_t *pos2,
+                  int32_t *spans, int *status) {
   using namespace umma;
   extern __shared__ int32_t es_smem[];
   const int D = 1 << bits;
@@ -129,16 +149,32 @@ embed_sort_kernel(const EmbedArgs a, int bits, int32_t *key1, int32_t *pos1, int
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   griddep_wait();
-  griddep_launch();  // the zeroing may start: what came before has finished
   const int T = a.T;
   const int per_warp = (int)round_up(ceil_div(T, ES_CTAS * ES_WARPS), 32);
   const int begin = (rank * ES_WARPS + warp) * per_warp, end = min(begin + per_warp, T);
   int32_t *mine = hist + warp * D;
   for (int pass = 0; pass < 2; ++pass) {
-    auto key_at = [&](int j) { return pass ? __ldcg(key1 + j) : em_key(a, j, status); };
+    // The warp's positions, 32 at a time.
+    int32_t keys[ES_STEPS], tokens[ES_STEPS];
+#pragma unroll
+    for (int q = 0; q < ES_STEPS; ++q) {
+      const int j = begin + 32 * q + lane;
+      keys[q] = tokens[q] = -1;
+      if (j < end) {
+        keys[q] = pass ? __ldcg(key1 + j) : em_key(a, j, status);
+        tokens[q] = pass ? __ldcg(pos1 + j) : j;
+      }
+    }
     for (int d = threadIdx.x; d < ES_WARPS * D; d += ES_THREADS) hist[d] = 0;
     __syncthreads();
-    for (int j = begin + lane; j < end; j += 32) atomicAdd(mine + ((key_at(j) >> (pass * bits)) & (D - 1)), 1);
+#pragma unroll
+    for (int q = 0; q < ES_STEPS; ++q)
+      if (keys[q] >= 0) {
+        atomicAdd(mine + ((keys[q] >> (pass * bits)) & (D - 1)), 1);
+        if (pass == 0 && keys[q] < a.V) mark[keys[q]] = tokens[q];
+      }
+    if (pass == 0 && rank == 0 && threadIdx.x == 0) *spans = 0;
+    if (pass == 0) griddep_launch();  // the zeroing may start: what came before this kernel has finished
     __syncthreads();
     // Before this warp in the CTA.
     const int d = threadIdx.x;
@@ -185,11 +221,11 @@ embed_sort_kernel(const EmbedArgs a, int bits, int32_t *key1, int32_t *pos1, int
     __syncthreads();
     if (d < D) total[d] = wsum[warp] + inc - all + before;
     __syncthreads();
-    for (int j0 = begin; j0 < end; j0 += 32) {
-      const int j = j0 + lane;
-      const bool in = j < end;
-      const int32_t key = in ? key_at(j) : -1;
-      const int digit = in ? (key >> (pass * bits)) & (D - 1) : -1 - lane;
+#pragma unroll
+    for (int q = 0; q < ES_STEPS; ++q) {
+      if (begin + 32 * q >= end) break;
+      const bool in = keys[q] >= 0;
+      const int digit = in ? (keys[q] >> (pass * bits)) & (D - 1) : -1 - lane;
       const unsigned same = __match_any_sync(FULL_MASK, digit);
       const int ahead = __popc(same & lanemask_lt());
       int32_t base = 0;
@@ -198,8 +234,8 @@ embed_sort_kernel(const EmbedArgs a, int bits, int32_t *key1, int32_t *pos1, int
       if (in && ahead == 0) mine[digit] += __popc(same);
       __syncwarp();
       if (in) {
-        (pass ? key2 : key1)[base + ahead] = key;
-        (pass ? pos2 : pos1)[base + ahead] = pass ? __ldcg(pos1 + j) : j;
+        (pass ? key2 : key1)[base + ahead] = keys[q];
+        (pass ? pos2 : pos1)[base + ahead] = tokens[q];
       }
     }
     if (pass == 0) {
@@ -210,9 +246,10 @@ embed_sort_kernel(const EmbedArgs a, int bits, int32_t *key1, int32_t *pos1, int
 }
 
 // The same by the permutation's kernels: low digits, then high digits.
-__global__ void __launch_bounds__(256) embed_key_kernel(const EmbedArgs a, int32_t *key, int32_t *lo, int *status) {
+__global__ void __launch_bounds__(256) embed_key_kernel(const EmbedArgs a, int32_t *key, int32_t *lo, int32_t *spans, int *status) {
   griddep_launch();
   griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *spans = 0;
   for (int64_t t = blockIdx.x * 256ll + threadIdx.x; t < a.T; t += gridDim.x * 256ll) {
     const int32_t k = em_key(a, t, status);
     key[t] = k;
@@ -237,18 +274,36 @@ __global__ void __launch_bounds__(256) embed_order_kernel(int64_t T, const int32
 }
 
 // ---------------------------------------------------------------- zeroing
-// `beside`: runs beside the one-launch sort, which lets it start once it knows
-// that what came before has finished, and waits for it at its end only, so
-// that what follows waits for both.
-__global__ void __launch_bounds__(512) embed_zero_kernel(float *p, int64_t n, int beside) {
-  if (!beside) griddep_wait();
-  const int64_t head = min(n, (int64_t)((16 - ((uintptr_t)p & 15)) & 15) / 4), vecs = (n - head) / 4;
-  float4 *v = (float4 *)(p + head);
-  const int64_t i0 = blockIdx.x * 512ll + threadIdx.x, step = gridDim.x * 512ll;
-  for (int64_t i = i0; i < vecs; i += step) __stcs(v + i, make_float4(0.f, 0.f, 0.f, 0.f));
-  if (i0 < head) p[i0] = 0.f;
-  if (i0 < n - head - 4 * vecs) p[head + 4 * vecs + i0] = 0.f;
-  if (beside) griddep_wait();
+// Zeroes dtable.  With `mark` it runs beside the one-launch sort, which lets it
+// start once what came before has finished; it waits for the sort at its end
+// only, so that what follows waits for both.  mark[v] is a token of row v or
+// not written: a row whose mark is such a token is written by the sums and
+// left alone here (one that were zeroed all the same would only be written
+// twice).  A warp takes `rows` rows at a time, at most 32.
+__global__ void __launch_bounds__(512) embed_zero_kernel(const EmbedArgs a, const int32_t *mark, int rows) {
+  if (!mark) griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const bool wide = a.H % 4 == 0 && ((uintptr_t)a.dtable & 15) == 0;
+  const int64_t step = (int64_t)gridDim.x * 16 * rows;
+  for (int64_t v0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 5)) * rows; v0 < a.V; v0 += step) {
+    bool hit = lane >= rows || v0 + lane >= a.V;
+    if (mark && !hit) {
+      const int32_t t = __ldcg(mark + v0 + lane);
+      if (t >= 0 && t < a.T) {
+        const int64_t id = em_id(a, t);
+        hit = id == v0 + lane && id != a.padding_id;
+      }
+    }
+    for (unsigned left = ~__ballot_sync(FULL_MASK, hit); left; left &= left - 1) {
+      float *row = a.dtable + (v0 + __ffs(left) - 1) * a.H;
+      if (wide) {
+        for (int i = lane; i < a.H / 4; i += 32) __stcs((float4 *)row + i, make_float4(0.f, 0.f, 0.f, 0.f));
+      } else {
+        for (int i = lane; i < a.H; i += 32) __stcs(row + i, 0.f);
+      }
+    }
+  }
+  if (mark) griddep_wait();
 }
 
 // ---------------------------------------------------------------- sums
@@ -256,100 +311,128 @@ __global__ void __launch_bounds__(512) embed_zero_kernel(float *p, int64_t n, in
 // token that was there before it (0) and of the one that goes on behind it (1).
 template <typename TO, int VEC>
 __global__ void __launch_bounds__(EM_THREADS)
-embed_sum_kernel(const EmbedArgs a, int tile, int group, const int32_t *key, const int32_t *order, float *part) {
-  constexpr int AHEAD = VEC == 1 ? 8 : 4;
+embed_sum_kernel(const EmbedArgs a, int tile, int group, const int32_t *key, const int32_t *order, float *part,
+                 int32_t *spans, int32_t *span_tiles) {
+  constexpr int AHEAD = 8, N = em_n<VEC>();
+  // Keys and tokens of the CTA's tiles.
+  __shared__ int32_t skey[EM_THREADS], sorder[EM_THREADS];
   griddep_launch();
   griddep_wait();
-  const int per_cta = EM_THREADS / group, sub = threadIdx.x / group;
-  if (sub >= per_cta) return;
+  const int per_cta = EM_THREADS / group, sub = threadIdx.x / group, lane = threadIdx.x % group;
   const int64_t b = (int64_t)blockIdx.x * per_cta + sub;
+  const int64_t start = (int64_t)blockIdx.x * per_cta * tile;
   const int p0 = (int)min(b * tile, (int64_t)a.T), p1 = min(p0 + tile, a.T);
-  if (p0 >= p1) return;
-  const int first = key[p0];
-  if (first >= a.V) return;
-  const bool from_before = p0 > 0 && key[p0 - 1] == first;
-  const int after = p1 < a.T ? key[p1] : a.V;
-  const int i = (blockIdx.y * group + threadIdx.x % group) * VEC;
-  if (i >= a.H) return;
-  float s[VEC];
+  const int i = blockIdx.y * group * N + (VEC ? lane * VEC : lane);
+  const bool live = p0 < p1 && i < a.H;
+  const int first = live ? key[p0] : a.V;
+  const int after = live && p1 < a.T ? key[p1] : a.V;
+  bool before = live && p0 > 0 && key[p0 - 1] == first;  // whether the token was there before this tile
+  float s[N];
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) s[k] = 0.f;
+  for (int k = 0; k < N; ++k) s[k] = 0.f;
   int now = first;
-  bool spans = from_before;
   auto flush = [&](bool goes_on) {
-    if (spans || goes_on) {
-      float *o = part + (b * 2 + (spans ? 0 : 1)) * a.H + i;
-      if constexpr (VEC == 1) o[0] = s[0];
-      else em_store<float, VEC>(o, s);
+    if (before || goes_on) {
+      em_store<float, VEC>(part + (b * 2 + (before ? 0 : 1)) * a.H, i, group, a.H, s);
+      if (!before && lane == 0 && blockIdx.y == 0) span_tiles[atomicAdd(spans, 1)] = (int32_t)b;
     } else {
-      float *o = a.dtable + (int64_t)now * a.H + i;
-      float v[VEC];
+      float *o = a.dtable + (int64_t)now * a.H;
+      float v[N];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) v[k] = 0.f;
-      if (a.accumulate) em_load<float, VEC>(o, v);
+      for (int k = 0; k < N; ++k) v[k] = 0.f;
+      if (a.accumulate) em_load<float, VEC>(o, i, group, a.H, v);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) v[k] = a.accumulate ? fmaf(a.scale, s[k], v[k]) : a.scale * s[k];
-      em_store<float, VEC>(o, v);
+      for (int k = 0; k < N; ++k) v[k] = a.accumulate ? fmaf(a.scale, s[k], v[k]) : a.scale * s[k];
+      em_store<float, VEC>(o, i, group, a.H, v);
     }
   };
-  for (int p = p0; p < p1; p += AHEAD) {
-    float v[AHEAD][VEC];
-    int k_at[AHEAD];
-#pragma unroll
-    for (int r = 0; r < AHEAD; ++r) {
-      k_at[r] = p + r < p1 ? key[p + r] : a.V;
-      if (k_at[r] < a.V) em_load<TO, VEC>((const TO *)a.dout + (int64_t)order[p + r] * a.ld_out + i, v[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < AHEAD; ++r) {
-      if (p + r >= p1 || now >= a.V) break;
-      if (k_at[r] != now) {
-        flush(false);
-        spans = false;
-        now = k_at[r];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) s[k] = 0.f;
-        if (now >= a.V) break;
+  // Rounds of n positions of each tile, so many that all tiles' fit.
+  const int n = min(tile, EM_THREADS / per_cta);
+  for (int q = 0; q < tile; q += n) {
+    __syncthreads();
+    {
+      const int64_t at = start + (int64_t)(threadIdx.x / n) * tile + q + threadIdx.x % n;
+      if ((int)threadIdx.x < n * per_cta && at < a.T) {
+        skey[threadIdx.x] = key[at];
+        sorder[threadIdx.x] = order[at];
       }
+    }
+    __syncthreads();
+    const int m = min(n, p1 - p0 - q), at = sub * n;
+    for (int p = 0; p < m && now < a.V; p += AHEAD) {
+      uint4 raw[VEC ? AHEAD : 1];
+      TO loose[VEC ? 1 : AHEAD][4];
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) s[k] += v[r][k];
+      for (int r = 0; r < AHEAD; ++r)
+        if (p + r < m && skey[at + p + r] < a.V) {
+          const TO *row = (const TO *)a.dout + (int64_t)sorder[at + p + r] * a.ld_out;
+          if constexpr (VEC != 0) {
+            static_assert(VEC == Vec16<TO>::N, "one 16-byte load");
+            raw[r] = __ldcs((const uint4 *)(row + i));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (i + k * group < a.H) loose[r][k] = row[i + k * group];
+          }
+        }
+#pragma unroll
+      for (int r = 0; r < AHEAD; ++r) {
+        if (p + r >= m || now >= a.V) break;
+        const int k_at = skey[at + p + r];
+        if (k_at != now) {
+          flush(false);
+          before = false;
+          now = k_at;
+#pragma unroll
+          for (int k = 0; k < N; ++k) s[k] = 0.f;
+          if (now >= a.V) break;
+        }
+        float v[N];
+        if constexpr (VEC != 0) {
+          Vec16<TO>::unpack(raw[r], v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = i + k * group < a.H ? Elem<TO>::to_f32(loose[r][k]) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] += v[k];
+      }
     }
   }
   if (now < a.V) flush(after == now);
 }
 
-// A token that spans tiles: the tile that it starts in adds the partial rows
-// up, in order.
-__global__ void __launch_bounds__(EM_THREADS) embed_join_kernel(const EmbedArgs a, int tile, const int32_t *key,
-                                                                const float *part) {
+// Tokens that span tiles, listed by the tile that each starts in: a warp adds
+// the partial rows of one up, in order, 32 channels at a time.
+__global__ void __launch_bounds__(EM_THREADS, 4) embed_join_kernel(const EmbedArgs a, int tile, const int32_t *key,
+                                                                   const float *part, const int32_t *spans,
+                                                                   const int32_t *span_tiles) {
+  constexpr int AHEAD = 16;  // a join is a chain of loads: many at a time
   griddep_launch();
   griddep_wait();
-  const int64_t tiles = ceil_div(a.T, tile), b = blockIdx.x;
-  const int p0 = (int)(b * tile), p1 = p0 + tile;
-  if (p1 >= a.T) return;
-  const int now = key[p1 - 1];
-  if (now >= a.V || key[p1] != now) return;
-  if (key[p0] == now && p0 > 0 && key[p0 - 1] == now) return;  // it started before
-  // Tiles behind this one that it reaches.
-  int64_t n = 0;
-  for (;;) {
-    const int64_t c = b + 1 + n + threadIdx.x;
-    const int got = __syncthreads_count(c < tiles && key[c * tile] == now);
-    n += got;
-    if (got < EM_THREADS) break;
-  }
-  for (int i = blockIdx.y * EM_THREADS + threadIdx.x; i < a.H; i += gridDim.y * EM_THREADS) {
+  const int lane = threadIdx.x & 31, slices = (a.H + 31) / 32;
+  const int64_t tiles = ceil_div(a.T, tile), items = (int64_t)*spans * slices, warps = (int64_t)gridDim.x * (EM_THREADS / 32);
+  for (int64_t w = (int64_t)blockIdx.x * (EM_THREADS / 32) + (threadIdx.x >> 5); w < items; w += warps) {
+    const int64_t b = span_tiles[w / slices];
+    const int i = (int)(w % slices) * 32 + lane;
+    const int32_t now = key[(b + 1) * tile];
+    int64_t n = 1;  // tiles behind that one which it reaches
+    for (;;) {
+      const int64_t c = b + 1 + n + lane;
+      const int got = __popc(__ballot_sync(FULL_MASK, c < tiles && key[c * tile] == now));
+      n += got;
+      if (got < 32) break;
+    }
+    if (i >= a.H) continue;
     float s = part[(b * 2 + 1) * a.H + i];
     const float *q = part + (b + 1) * 2 * (int64_t)a.H + i;
-    int64_t c = 0;
-    for (; c + 8 <= n; c += 8) {
-      float v[8];
+    for (int64_t c = 0; c < n; c += AHEAD) {
+      float v[AHEAD];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) v[r] = q[(c + r) * 2 * a.H];
+      for (int r = 0; r < AHEAD; ++r) v[r] = c + r < n ? q[(c + r) * 2 * a.H] : 0.f;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) s += v[r];
+      for (int r = 0; r < AHEAD; ++r) s += v[r];
     }
-    for (; c < n; ++c) s += q[c * 2 * a.H];
     float *o = a.dtable + (int64_t)now * a.H + i;
     *o = a.accumulate ? fmaf(a.scale, s, *o) : a.scale * s;
   }
@@ -370,12 +453,13 @@ template <typename TE, typename TO>
 static cudaError_t embed_types(const EmbedArgs &a, int *status, cudaStream_t stream) {
   constexpr int VEC = Vec16<TE>::N;
   const bool wide = em_wide(a.table, a.ld_table, sizeof(TE), a.H, VEC) && em_wide(a.out, a.ld_out, sizeof(TO), a.H, VEC);
-  const int group = em_group(a.H, wide ? VEC : 1);
+  const int group = em_group(a.H, wide ? VEC : 4);
   // Four rows a group where there are enough of them to fill the SMs.
   const int rows = ceil_div(a.T, EM_THREADS / group) >= (int64_t)device_sms() * 2 * EM_ROWS ? EM_ROWS : 1;
-  const dim3 grid((unsigned)ceil_div(a.T, (int64_t)(EM_THREADS / group) * rows)), block(EM_THREADS);
+  const int64_t ctas = ceil_div(a.T, (int64_t)(EM_THREADS / group) * rows);
+  const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)device_sms() * 4)), block(EM_THREADS);
   if (wide) return launch_pdl(embed_kernel<TE, TO, VEC>, grid, block, 0, stream, a, group, rows, status);
-  return launch_pdl(embed_kernel<TE, TO, 1>, grid, block, 0, stream, a, group, rows, status);
+  return launch_pdl(embed_kernel<TE, TO, 0>, grid, block, 0, stream, a, group, rows, status);
 }
 
 cudaError_t launch_embed(const EmbedArgs &a, int *status, cudaStream_t stream) {
@@ -422,7 +506,7 @@ static bool es_fits() {
 static bool es_used(const EmbedArgs &a) { return a.T <= ES_MAX_T && es_fits(); }
 
 struct EmbedScratch {
-  int32_t *key, *order, *key1, *pos1, *lo, *second, *digits;
+  int32_t *key, *order, *key1, *pos1, *mark, *spans, *span_tiles, *lo, *second, *digits;
   float *part;
   void *sort;
 };
@@ -440,6 +524,9 @@ static EmbedScratch embed_carve(const EmbedArgs &a, char *base, size_t *bytes) {
   s.key1 = (int32_t *)take(t);
   s.pos1 = (int32_t *)take(t);
   s.part = (float *)take((size_t)ceil_div(a.T, em_tile(a.T)) * 2 * a.H * 4);
+  s.mark = (int32_t *)take((size_t)a.V * 4);
+  s.spans = (int32_t *)take(4);
+  s.span_tiles = (int32_t *)take((size_t)ceil_div(a.T, em_tile(a.T)) * 4);
   s.lo = (int32_t *)take(t);
   s.second = (int32_t *)take(t);
   s.digits = (int32_t *)take((EM_DIGIT + 1) * 4);
@@ -472,11 +559,11 @@ static cudaError_t embed_sort(const EmbedArgs &a, const EmbedScratch &s, int *st
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, bits, s.key1, s.pos1, s.key, s.order, status);
+    return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, bits, s.mark, s.key1, s.pos1, s.key, s.order, s.spans, status);
   }
   const int64_t T = a.T;
   const dim3 grid((unsigned)ceil_div(T, 256)), block(256);
-  cudaError_t e = launch_pdl(embed_key_kernel, grid, block, 0, stream, a, s.key1, s.lo, status);
+  cudaError_t e = launch_pdl(embed_key_kernel, grid, block, 0, stream, a, s.key1, s.lo, s.spans, status);
   if (e == cudaSuccess) e = launch_permute(T, EM_DIGIT, s.lo, s.digits, s.pos1, s.key, s.sort, status, stream);
   if (e == cudaSuccess)
     e = launch_pdl(embed_high_kernel, grid, block, 0, stream, T, (const int32_t *)s.key1, (const int32_t *)s.pos1, s.lo);
@@ -491,15 +578,17 @@ template <typename TO>
 static cudaError_t embed_sum(const EmbedArgs &a, const EmbedScratch &s, cudaStream_t stream) {
   constexpr int VEC = Vec16<TO>::N;
   const bool wide = em_wide(a.dout, a.ld_out, sizeof(TO), a.H, VEC) && em_wide(a.dtable, a.H, 4, a.H, VEC);
-  const int vec = wide ? VEC : 1, group = em_group(a.H, vec), tile = em_tile(a.T);
+  const int vec = wide ? VEC : 4, group = em_group(a.H, vec), tile = em_tile(a.T);
   const int64_t tiles = ceil_div(a.T, tile);
   const dim3 grid((unsigned)ceil_div(tiles, EM_THREADS / group), (unsigned)ceil_div(a.H, group * vec));
   const int32_t *key = s.key, *order = s.order;
-  cudaError_t e = wide ? launch_pdl(embed_sum_kernel<TO, VEC>, grid, dim3(EM_THREADS), 0, stream, a, tile, group, key, order, s.part)
-                       : launch_pdl(embed_sum_kernel<TO, 1>, grid, dim3(EM_THREADS), 0, stream, a, tile, group, key, order, s.part);
+  cudaError_t e = wide ? launch_pdl(embed_sum_kernel<TO, VEC>, grid, dim3(EM_THREADS), 0, stream, a, tile, group, key, order, s.part, s.spans, s.span_tiles)
+                       : launch_pdl(embed_sum_kernel<TO, 0>, grid, dim3(EM_THREADS), 0, stream, a, tile, group, key, order, s.part, s.spans, s.span_tiles);
   if (e != cudaSuccess || tiles < 2) return e;
-  return launch_pdl(embed_join_kernel, dim3((unsigned)tiles, (unsigned)std::min<int64_t>(ceil_div(a.H, EM_THREADS), 64)), dim3(EM_THREADS), 0, stream, a,
-                    tile, key, (const float *)s.part);
+  const int64_t warps = tiles * ceil_div(a.H, 32);  // at most
+  return launch_pdl(embed_join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(warps, EM_THREADS / 32), (int64_t)device_sms() * 4)),
+                    dim3(EM_THREADS), 0, stream, a, tile, key, (const float *)s.part, (const int32_t *)s.spans,
+                    (const int32_t *)s.span_tiles);
 }
 
 cudaError_t launch_embed_bwd(const EmbedArgs &a, void *scratch, int *status, cudaStream_t stream) {
@@ -509,8 +598,9 @@ cudaError_t launch_embed_bwd(const EmbedArgs &a, void *scratch, int *status, cud
   const EmbedScratch s = embed_carve(a, (char *)scratch, &bytes);
   cudaError_t e = embed_sort(a, s, status, stream);
   if (e == cudaSuccess && !a.accumulate) {
-    const int64_t ctas = std::min<int64_t>(ceil_div(n, 512 * 16), (int64_t)device_sms() * 4);
-    e = launch_pdl(embed_zero_kernel, dim3((unsigned)ctas), dim3(512), 0, stream, a.dtable, n, es_used(a) ? 1 : 0);
+    const int rows = std::max(1, std::min(32, 4096 / a.H));
+    const int64_t ctas = std::min<int64_t>(ceil_div(a.V, 16 * rows), (int64_t)device_sms() * 4);
+    e = launch_pdl(embed_zero_kernel, dim3((unsigned)ctas), dim3(512), 0, stream, a, (const int32_t *)(es_used(a) ? s.mark : nullptr), rows);
   }
   if (e != cudaSuccess) return e;
   return a.of32 ? embed_sum<float>(a, s, stream) : embed_sum<__nv_bfloat16>(a, s, stream);
