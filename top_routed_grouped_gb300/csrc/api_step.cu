@@ -107,7 +107,9 @@ MOE_API int moe_block_norm(const moe_norm_args_t *a, void *stream) {
   if ((rc = norm_inputs(a)) != MOE_OK) return rc;
   const int e = type_size(a->dtype), r = type_size(a->rdtype);
   if (!there(a->r, r) || (a->y && !there(a->r_out, r)) || (a->w_pre && !there(a->h, e))) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_block_norm(norm_fwd_args(a), (cudaStream_t)stream));
+  int *status = device_status_ptr();
+  if (!status) return MOE_ERR_CUDA;
+  return cuda_status(launch_block_norm(norm_fwd_args(a), status, (cudaStream_t)stream));
 }
 
 MOE_API size_t moe_block_norm_workspace_size(const moe_norm_args_t *a) {
@@ -131,7 +133,9 @@ MOE_API int moe_block_norm_backward(const moe_norm_args_t *a, void *ws, size_t w
   }
   const NormArgs n = norm_bwd_args(a);
   if ((rc = workspace_status(ws, ws_bytes, (size_t)round_up((int64_t)block_norm_scratch_bytes(n), 256))) != MOE_OK) return rc;
-  return cuda_status(launch_block_norm_bwd(n, ws, (cudaStream_t)stream));
+  int *status = device_status_ptr();
+  if (!status) return MOE_ERR_CUDA;
+  return cuda_status(launch_block_norm_bwd(n, ws, status, (cudaStream_t)stream));
 }
 
 // ---------------------------------------------------------------- embed

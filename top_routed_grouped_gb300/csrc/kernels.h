@@ -203,9 +203,9 @@ struct NormArgs {
   void *dgate;
 };
 constexpr int NORM_MAX_H = 16384;
-cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t stream);
+cudaError_t launch_block_norm(const NormArgs &a, int *status, cudaStream_t stream);
 size_t block_norm_scratch_bytes(const NormArgs &a);
-cudaError_t launch_block_norm_bwd(const NormArgs &a, void *scratch, cudaStream_t stream);
+cudaError_t launch_block_norm_bwd(const NormArgs &a, void *scratch, int *status, cudaStream_t stream);
 
 // ---- embed.cu ----
 struct EmbedArgs {
