@@ -1,0 +1,662 @@
+// The join between two blocks: norm after a block, gate, scaled residual sum
+// and norm before the next block, forward and backward (contracts with
+// moe_block_norm in moe.h).
+//
+// A row belongs to a group of threads, 4 to 32 lanes of a warp for short
+// rows and a whole CTA for others, and stays in registers between its loads
+// and its stores: every input is read once.  CTAs walk over the rows; the
+// inputs of the next few blocks of rows are on their way to shared memory by
+// bulk copies meanwhile.  A row that starts between 16-byte boundaries is
+// copied with the bytes around it, so odd widths move as fast.  A group takes
+// two rows at a time where they are short, so that the rounds of a sum over a row, which are
+// latency, are shared.  Rows too long for two such stages are loaded straight
+// from memory.  A row's statistics
+// are summed in an order set by H and the load width alone, so its outputs do
+// not depend on the other rows.
+//
+// Backward: with v = r_out, x = v rstd the normed row and g = dh w,
+//   dr = dr_out + rstd g - v c,   c = rstd^3 mean(g v)
+// (the derivative of v -> v rsqrt(mean v^2 + eps)), and the same once more for
+// y with u = scale gate dr in place of dh.  The row's first round of sums
+// (v^2, g v, y^2) gives dr, the second (u w y) gives dy.  The gradients of
+// the weights are sums over rows: each group keeps those of its own rows in
+// registers, writes them once, and a second kernel adds the groups in order.
+#pragma once
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_host.h"
+#include "umma.cuh"
+
+namespace moe {
+
+constexpr int BN_MAX_THREADS = 512, BN_MAX_STAGES = 6, BN_MAX_INPUTS = 5;
+
+// The row inputs of a launch and where their blocks of rows stand in a stage.
+struct BnStages {
+  int n, stages, bytes;  // inputs, stages, bytes of a stage
+  int rows;              // of a block
+  int runs;              // runs of bytes that it is: 1 (rows behind one another), or its rows
+  int off[BN_MAX_INPUTS], es[BN_MAX_INPUTS], pitch[BN_MAX_INPUTS];  // pitch: bytes from run to run in a stage
+  int64_t ld[BN_MAX_INPUTS];
+  const void *base[BN_MAX_INPUTS];
+};
+
+struct BnBars {
+  uint64_t full[BN_MAX_STAGES];
+  int abort_flag;
+};
+
+// The bytes that run `q` of input k of block `t0` copies: the 16-byte pieces
+// that its rows touch, none outside the buffer; and its rows' own bytes.
+struct BnPiece {
+  uintptr_t from, to, lo, hi;  // [from, to) is copied; the rows are [lo, hi)
+};
+__device__ inline BnPiece bn_piece(const BnStages &st, int k, int q, int64_t t0, int T, int H) {
+  const int64_t first_row = t0 + q, rows = st.runs > 1 ? 1 : min((int64_t)st.rows, T - t0);
+  BnPiece p = {0, 0, 0, 0};
+  if (first_row >= T) return p;
+  p.lo = (uintptr_t)st.base[k] + first_row * st.ld[k] * st.es[k];
+  p.hi = p.lo + ((rows - 1) * st.ld[k] + H) * st.es[k];
+  const uintptr_t first = ((uintptr_t)st.base[k] + 15) & ~(uintptr_t)15;
+  const uintptr_t last = ((uintptr_t)st.base[k] + ((T - 1) * st.ld[k] + H) * st.es[k]) & ~(uintptr_t)15;
+  p.from = max(p.lo & ~(uintptr_t)15, first);
+  p.to = min((p.hi + 15) & ~(uintptr_t)15, last);
+  if (p.to < p.from) p.from = p.to = p.hi;
+  return p;
+}
+// Starts the copies of a block (one warp; at most 32 of them).
+__device__ inline void bn_start(const BnStages &st, uint8_t *stage, uint64_t *bar, int64_t t0, int T, int H) {
+  const int lane = threadIdx.x & 31, k = lane / st.runs, q = lane % st.runs;
+  BnPiece p = {0, 0, 0, 0};
+  if (k < st.n) p = bn_piece(st, k, q, t0, T, H);
+  const uint32_t bytes = (uint32_t)(p.to - p.from);
+  const uint32_t all = __reduce_add_sync(FULL_MASK, bytes);
+  if (lane == 0) {
+    if (all) umma::mbar_arrive_expect_tx(bar, all);
+    else umma::mbar_arrive(bar);
+  }
+  __syncwarp();
+  if (bytes)
+    umma::bulk_load(stage + st.off[k] + q * st.pitch[k] + (p.from - (p.lo & ~(uintptr_t)15)), (const void *)p.from, bytes, bar);
+}
+// What the copies of the first and the last block may have missed (the whole
+// CTA; the caller's barrier follows).
+__device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, int T, int H) {
+  if (t0 > 0 && t0 + st.rows < T) return false;
+  bool missed = false;
+  for (int k = 0; k < st.n; ++k)
+    for (int q = 0; q < st.runs; ++q) {
+      const BnPiece p = bn_piece(st, k, q, t0, T, H);
+      if (p.from <= p.lo && p.to >= p.hi) continue;
+      missed = true;
+      uint8_t *dst = stage + st.off[k] + q * st.pitch[k] - (p.lo & ~(uintptr_t)15);
+      for (uintptr_t b = p.lo + threadIdx.x; b < p.hi; b += blockDim.x)
+        if (b < p.from || b >= p.to) dst[b] = *(const uint8_t *)b;
+    }
+  return missed;
+}
+
+// ---- what a thread holds of a row: NP pairs of floats ----
+// Wide: CH runs of VEC neighbouring elements, at (c group + lane) VEC.  Scalar
+// (VEC = 1): elements lane, lane + group, ...  Past the row it holds zeros.
+template <int VEC, int CH>
+struct BnRow {
+  static constexpr int NP = VEC * CH / 2;
+  int lane, group, H;
+
+  template <typename T>
+  __device__ inline void load(const T *row, F2 (&o)[NP]) const {
+    if constexpr (VEC == 1) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int i = 2 * p * group + lane;
+        o[p] = F2(i < H ? Elem<T>::load(row + i) : 0.f, i + group < H ? Elem<T>::load(row + i + group) : 0.f);
+      }
+    } else {
+      constexpr int N = Vec16<T>::N;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * group + lane) * VEC;
+#pragma unroll
+        for (int b = 0; b < VEC / N; ++b) {
+          float v[N];
+#pragma unroll
+          for (int k = 0; k < N; ++k) v[k] = 0.f;
+          if (i < H) Vec16<T>::load(row + i + b * N, v);
+#pragma unroll
+          for (int k = 0; k < N; k += 2) o[(c * VEC + b * N + k) / 2] = F2(v[k], v[k + 1]);
+        }
+      }
+    }
+  }
+  template <typename T>
+  __device__ inline void store(T *row, const F2 (&x)[NP]) const {
+    if constexpr (VEC == 1) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int i = 2 * p * group + lane;
+        float a, b;
+        x[p].get(a, b);
+        if (i < H) row[i] = Elem<T>::from_f32(a);
+        if (i + group < H) row[i + group] = Elem<T>::from_f32(b);
+      }
+    } else {
+      constexpr int N = Vec16<T>::N;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * group + lane) * VEC;
+#pragma unroll
+        for (int b = 0; b < VEC / N; ++b) {
+          float v[N];
+#pragma unroll
+          for (int k = 0; k < N; k += 2) x[(c * VEC + b * N + k) / 2].get(v[k], v[k + 1]);
+          if (i < H) Vec16<T>::store(row + i + b * N, v);
+        }
+      }
+    }
+  }
+  // Weights and channel gates: float or the rows' type.
+  template <typename T>
+  __device__ inline void weights(const void *p, bool f32, float add, F2 (&o)[NP]) const {
+    if (f32) load((const float *)p, o);
+    else load((const T *)p, o);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) o[k] = add2(o[k], F2(add));
+  }
+};
+
+// Sums of N values over the threads of a row, in a fixed order; all get them.
+// Consecutive calls alternate between two buffers: the barrier of one call
+// tells that the buffer of the call before it has been read.
+template <int N>
+__device__ inline void bn_row_sum(float (&v)[N], int group, float (*buf)[16]) {
+  const int top = group < 32 ? group : 32;
+  for (int d = top >> 1; d; d >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(FULL_MASK, v[n], d);
+  if (group > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = group >> 5;
+    if (lane == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) buf[n][warp] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = 0.f;
+    for (int w = 0; w < warps; w += 4)  // (slots past the last warp hold zeros)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float4 f = *(const float4 *)&buf[n][w];
+        v[n] += f.x;
+        v[n] += f.y;
+        v[n] += f.z;
+        v[n] += f.w;
+      }
+  }
+}
+
+// A CTA's walk over its blocks of rows, with stages (BULK) or without.
+template <bool BULK, int R>
+struct BnWalk {
+  const BnStages &st;
+  const int T, H, per_cta;
+  const int64_t step;
+  uint8_t *stages, *stage;
+  BnBars &bars;
+  int64_t t0;
+  int slot = 0;
+  uint32_t phase = 0;
+  bool first = true;
+
+  __device__ inline BnWalk(const BnStages &s, int T_, int H_, int per_cta_, uint8_t *stages_, BnBars &b)
+      : st(s), T(T_), H(H_), per_cta(per_cta_), step((int64_t)gridDim.x * per_cta_ * R), stages(stages_), stage(stages_),
+        bars(b), t0((int64_t)blockIdx.x * per_cta_ * R) {
+    if (BULK) {
+      if (threadIdx.x == 0) {
+        for (int i = 0; i < st.stages; ++i) umma::mbar_init(&bars.full[i], 1);
+        umma::fence_mbar_init();
+        bars.abort_flag = 0;
+      }
+      __syncthreads();
+    }
+    griddep_launch();
+    griddep_wait();
+    if (BULK && threadIdx.x < 32)
+      for (int i = 0; i < st.stages; ++i)
+        if (t0 + i * step < T) bn_start(st, stages + i * st.bytes, &bars.full[i], t0 + i * step, T, H);
+  }
+  // Waits for the block's stage.
+  __device__ inline bool arrive(int *status) {
+    if (!BULK) return true;
+    stage = stages + slot * st.bytes;
+    if (!umma::mbar_wait(&bars.full[slot], phase, &bars.abort_flag, status)) return false;
+    if (bn_mend(st, stage, t0, T, H)) __syncthreads();
+    return true;
+  }
+  // Row t (the j-th of the block) of staged input k, or of `p` in memory.
+  template <typename E>
+  __device__ inline const E *row(int k, const void *p, int64_t ld, int64_t t, int j) const {
+    if (!BULK) return (const E *)p + t * ld;
+    if (st.runs > 1) {
+      const uintptr_t at = (uintptr_t)p + t * ld * sizeof(E);
+      return (const E *)(stage + st.off[k] + j * st.pitch[k] + (at & 15));
+    }
+    const uintptr_t at = (uintptr_t)p + t0 * ld * sizeof(E);
+    return (const E *)(stage + st.off[k] + (at & 15)) + (t - t0) * ld;
+  }
+  // Behind a barrier of this block: the last block's stage has been read by
+  // all, its copies for a later block start.
+  __device__ inline void refill() {
+    if (BULK && !first && threadIdx.x < 32) {
+      const int old = slot ? slot - 1 : st.stages - 1;
+      const int64_t later = t0 - step + st.stages * step;
+      if (later < T) bn_start(st, stages + old * st.bytes, &bars.full[old], later, T, H);
+    }
+    first = false;
+  }
+  __device__ inline void next() {
+    t0 += step;
+    if (++slot == st.stages) slot = 0, phase ^= 1;
+  }
+};
+
+// Threads of an SM that the kernels' registers allow.
+constexpr int bn_resident(bool backward, int np) { return !backward && np <= 4 ? 1024 : 512; }
+
+// The rows of a block that a group takes: number, place in the block, whether
+// there is such a row (a row of the block stands in where there is none).
+template <int R>
+struct BnRows {
+  int64_t t[R];
+  int at[R];
+  bool there[R];
+  __device__ inline BnRows(int64_t t0, int per_cta, int sub, int T) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      there[j] = t0 + j * per_cta + sub < T;
+      at[j] = there[j] ? j * per_cta + sub : 0;
+      t[j] = t0 + at[j];
+    }
+  }
+};
+
+template <typename TE, typename TR, int VEC, int CH, int R, bool BULK>
+__global__ void __launch_bounds__(BN_MAX_THREADS, bn_resident(false, VEC * CH / 2) / BN_MAX_THREADS)
+block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
+  constexpr int NP = VEC * CH / 2;
+  constexpr bool HELD = NP <= 4;  // weights stay in registers
+  extern __shared__ __align__(128) uint8_t bn_smem[];
+  __shared__ BnBars bars;
+  __shared__ __align__(16) float buf[2][R][16];
+  const int per_cta = blockDim.x / group, sub = threadIdx.x / group, lane = threadIdx.x % group;
+  const float inv_h = 1.f / a.H;
+  const BnRow<VEC, CH> io = {lane, group, a.H};
+  if (threadIdx.x < 2 * R * 16) buf[0][0][threadIdx.x] = 0.f;
+  if (!BULK) __syncthreads();
+  BnWalk<BULK, R> walk(st, a.T, a.H, per_cta, bn_smem, bars);
+  F2 w_post[NP], w_pre[NP];
+  if (HELD && a.w_post) io.template weights<TE>(a.w_post, a.wf32, a.offset, w_post);
+  if (HELD && a.w_pre) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
+  int round = 0;
+  for (; walk.t0 < a.T; walk.next()) {
+    if (!walk.arrive(status)) return;
+    const BnRows<R> rows(walk.t0, per_cta, sub, a.T);
+    float s[R], rstd[R];
+    F2 v[R][NP], y[NP];
+#pragma unroll
+    for (int j = 0; j < R; ++j) rstd[j] = 1.f;
+    if (a.w_post) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        io.load(walk.template row<TE>(1, a.y, a.ld_y, rows.t[j], rows.at[j]), y);
+        F2 sum(0.f);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) sum = fma2(y[p], y[p], sum);
+        s[j] = sum.sum();
+      }
+      bn_row_sum(s, group, buf[round++ & 1]);
+#pragma unroll
+      for (int j = 0; j < R; ++j) rstd[j] = rsqrtf(fmaf(s[j], inv_h, a.eps));
+    }
+    if (BULK && (!a.w_post || group <= 32)) __syncthreads();
+    walk.refill();
+    if (!HELD && a.w_post) io.template weights<TE>(a.w_post, a.wf32, a.offset, w_post);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t t = rows.t[j];
+      io.load(walk.template row<TR>(0, a.r, a.ld_r, t, rows.at[j]), v[j]);
+      if (a.y) {
+        io.load(walk.template row<TE>(1, a.y, a.ld_y, t, rows.at[j]), y);
+        const F2 f(a.w_post ? a.scale * rstd[j] : a.scale);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) y[p] = mul2(y[p], f);
+        if (a.w_post) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p) y[p] = mul2(y[p], w_post[p]);
+        }
+        F2 g[NP];
+        if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<TE>(2, a.gate, a.ld_gate, t, rows.at[j]), g);
+        else if (a.gate_kind == MOE_GATE_CHANNEL) io.template weights<TE>(a.gate, a.wf32, 0.f, g);
+        else {
+          const F2 one(a.gate_kind == MOE_GATE_TOKEN ? ((const float *)a.gate)[t] : 1.f);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) g[p] = one;
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) v[j][p] = fma2(g[p], y[p], v[j][p]);
+        if (rows.there[j]) io.store((TR *)a.r_out + t * a.ld_r_out, v[j]);
+      }
+      F2 sum(0.f);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) sum = fma2(v[j][p], v[j][p], sum);
+      s[j] = sum.sum();
+    }
+    if (a.w_pre) {
+      bn_row_sum(s, group, buf[round++ & 1]);
+      if (!HELD) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const F2 rs(rsqrtf(fmaf(s[j], inv_h, a.eps)));
+#pragma unroll
+        for (int p = 0; p < NP; ++p) v[j][p] = mul2(mul2(v[j][p], rs), w_pre[p]);
+        if (rows.there[j]) io.store((TE *)a.h + rows.t[j] * a.ld_h, v[j]);
+      }
+    }
+  }
+}
+
+// part: [3][groups][H] sums over a group's rows of what dw_pre, dw_post and a
+// channel gate's gradient are made of (only those that the call asks for).
+template <typename TE, typename TR, int VEC, int CH, int R, bool BULK>
+__global__ void __launch_bounds__(BN_MAX_THREADS)
+block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *part, int *status) {
+  constexpr int NP = VEC * CH / 2;
+  constexpr bool HELD = NP <= 4;
+  extern __shared__ __align__(128) uint8_t bn_smem[];
+  __shared__ BnBars bars;
+  __shared__ __align__(16) float buf[2][3 * R][16];
+  const int per_cta = blockDim.x / group, sub = threadIdx.x / group, lane = threadIdx.x % group;
+  const float inv_h = 1.f / a.H;
+  const BnRow<VEC, CH> io = {lane, group, a.H};
+  for (int i = threadIdx.x; i < 2 * 3 * R * 16; i += blockDim.x) buf[0][0][i] = 0.f;
+  if (!BULK) __syncthreads();
+  // Inputs are staged in the order of their use.
+  const int in_r = a.dr_out ? 1 : 0, in_d = in_r + 1, in_y = in_r + (a.w_pre ? 2 : 0), in_g = in_y + 1;
+  BnWalk<BULK, R> walk(st, a.T, a.H, per_cta, bn_smem, bars);
+  F2 w_post[NP], w_pre[NP], dw_post[NP], dw_pre[NP], dgate[NP];
+  if (HELD && a.w_post) io.template weights<TE>(a.w_post, a.wf32, a.offset, w_post);
+  if (HELD && a.w_pre) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) dw_post[p] = dw_pre[p] = dgate[p] = F2(0.f);
+  int round = 0;
+  for (; walk.t0 < a.T; walk.next()) {
+    if (!walk.arrive(status)) return;
+    const BnRows<R> rows(walk.t0, per_cta, sub, a.T);
+    float s[3 * R];  // v^2, dh w v, y^2 of each row
+    if (!HELD && a.w_pre) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      F2 vv(0.f), dv(0.f), yy(0.f), x[NP], d[NP];
+      if (a.w_pre) {
+        io.load(walk.template row<TR>(in_r, a.r_out, a.ld_r_out, rows.t[j], rows.at[j]), x);
+        io.load(walk.template row<TE>(in_d, a.dh, a.ld_dh, rows.t[j], rows.at[j]), d);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          vv = fma2(x[p], x[p], vv);
+          dv = fma2(mul2(d[p], w_pre[p]), x[p], dv);
+        }
+      }
+      if (a.w_post) {
+        io.load(walk.template row<TE>(in_y, a.y, a.ld_y, rows.t[j], rows.at[j]), x);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) yy = fma2(x[p], x[p], yy);
+      }
+      s[3 * j] = vv.sum();
+      s[3 * j + 1] = dv.sum();
+      s[3 * j + 2] = yy.sum();
+    }
+    bn_row_sum(s, group, buf[round++ & 1]);
+    if (BULK && group <= 32) __syncthreads();
+    walk.refill();
+    if (!HELD && a.w_post) io.template weights<TE>(a.w_post, a.wf32, a.offset, w_post);
+    float ry[R], q[2 * R];  // q: u w y, scale dr w y
+    F2 e[R][NP];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t t = rows.t[j];
+      const float one = rows.there[j] ? 1.f : 0.f;  // a row that stands in adds nothing
+      const float rv = rsqrtf(fmaf(s[3 * j], inv_h, a.eps));
+      ry[j] = a.w_post ? rsqrtf(fmaf(s[3 * j + 2], inv_h, a.eps)) : 1.f;
+      if (a.dr_out) {
+        io.load(walk.template row<TR>(0, a.dr_out, a.ld_dr_out, t, rows.at[j]), e[j]);
+      } else {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) e[j][p] = F2(0.f);
+      }
+      if (a.w_pre) {
+        F2 x[NP], d[NP];
+        io.load(walk.template row<TR>(in_r, a.r_out, a.ld_r_out, t, rows.at[j]), x);
+        io.load(walk.template row<TE>(in_d, a.dh, a.ld_dh, t, rows.at[j]), d);
+        const F2 rr(rv), r1(rv * one), cr(-(s[3 * j + 1] * inv_h * rv * rv * rv));
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          dw_pre[p] = fma2(d[p], mul2(x[p], r1), dw_pre[p]);
+          e[j][p] = add2(e[j][p], fma2(mul2(d[p], w_pre[p]), rr, mul2(x[p], cr)));
+        }
+        if (rows.there[j]) io.store((TR *)a.dr + t * a.ld_dr, e[j]);
+      }
+      q[2 * j] = q[2 * j + 1] = 0.f;
+      if (a.y) {
+        F2 y[NP], g[NP], q0(0.f), q1(0.f);
+        io.load(walk.template row<TE>(in_y, a.y, a.ld_y, t, rows.at[j]), y);
+        const F2 sc(a.scale * one), rr(ry[j]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) e[j][p] = mul2(e[j][p], sc);
+        if (a.gate_kind != MOE_GATE_NONE) {
+          if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<TE>(in_g, a.gate, a.ld_gate, t, rows.at[j]), g);
+          else if (a.gate_kind == MOE_GATE_CHANNEL) io.template weights<TE>(a.gate, a.wf32, 0.f, g);
+          else {
+            const F2 gt(((const float *)a.gate)[t]);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) g[p] = gt;
+          }
+          // the gate's gradient, and u in the place of scale dr
+          F2 dg[NP];
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            dg[p] = mul2(e[j][p], mul2(y[p], rr));
+            if (a.w_post) dg[p] = mul2(dg[p], w_post[p]);
+            q1 = add2(q1, dg[p]);
+            e[j][p] = mul2(e[j][p], g[p]);
+          }
+          if (a.gate_kind == MOE_GATE_CHANNEL) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) dgate[p] = add2(dgate[p], dg[p]);
+          }
+          if (a.gate_kind == MOE_GATE_ELEMENT && rows.there[j]) io.store((TE *)a.dgate + t * a.ld_dgate, dg);
+        }
+        if (a.w_post) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const F2 x = mul2(y[p], rr);
+            dw_post[p] = fma2(e[j][p], x, dw_post[p]);
+            e[j][p] = mul2(e[j][p], w_post[p]);
+            q0 = fma2(e[j][p], y[p], q0);
+            e[j][p] = mul2(e[j][p], rr);  // dy but for its last term
+          }
+        }
+        q[2 * j] = q0.sum();
+        q[2 * j + 1] = q1.sum();
+      }
+    }
+    if (a.y) {
+      if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) bn_row_sum(q, group, buf[round++ & 1]);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (a.gate_kind == MOE_GATE_TOKEN && lane == 0 && rows.there[j]) ((float *)a.dgate)[rows.t[j]] = q[2 * j + 1];
+        if (a.w_post) {
+          const F2 cy(-(q[2 * j] * inv_h * ry[j] * ry[j] * ry[j]));
+          F2 y[NP];
+          io.load(walk.template row<TE>(in_y, a.y, a.ld_y, rows.t[j], rows.at[j]), y);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) e[j][p] = fma2(y[p], cy, e[j][p]);
+        }
+        if (rows.there[j]) io.store((TE *)a.dy + rows.t[j] * a.ld_dy, e[j]);
+      }
+    }
+  }
+  const int64_t groups = (int64_t)gridDim.x * per_cta;
+  float *p = part + ((int64_t)blockIdx.x * per_cta + sub) * a.H;
+  if (a.dw_pre) io.store(p, dw_pre);
+  if (a.dw_post) io.store(p + groups * a.H, dw_post);
+  if (a.gate_kind == MOE_GATE_CHANNEL) io.store(p + 2 * groups * a.H, dgate);
+}
+
+// ---------------------------------------------------------------- host
+// Load width; pairs of elements a thread; threads of a row (a power of two up to
+// 32, or a multiple of 32); threads of a CTA.
+struct BnShape {
+  int vec, pairs, group, threads;
+};
+
+inline bool bn_wide(const NormArgs &a, int vec) {
+  auto row = [&](const void *p, int64_t ld, int es) { return !p || (((uintptr_t)p & 15) == 0 && ld * es % 16 == 0); };
+  const int e = a.f32 ? 4 : 2, r = a.rf32 ? 4 : 2;
+  bool ok = a.H % vec == 0 && row(a.r, a.ld_r, r) && row(a.y, a.ld_y, e) && row(a.r_out, a.ld_r_out, r) &&
+            row(a.h, a.ld_h, e) && row(a.dr_out, a.ld_dr_out, r) && row(a.dh, a.ld_dh, e) && row(a.dr, a.ld_dr, r) &&
+            row(a.dy, a.ld_dy, e) && row(a.w_post, 0, 1) && row(a.w_pre, 0, 1);
+  if (a.gate_kind == MOE_GATE_CHANNEL) ok = ok && row(a.gate, 0, 1);
+  if (a.gate_kind == MOE_GATE_ELEMENT) ok = ok && row(a.gate, a.ld_gate, e) && row(a.dgate, a.ld_dgate, e);
+  return ok;
+}
+
+// dense: the rows of every input stand behind one another.
+inline BnShape bn_shape(const NormArgs &a, bool dense) {
+  BnShape s;
+  s.vec = a.f32 ? 4 : 8;
+  if (!bn_wide(a, s.vec)) s.vec = 1;
+  s.pairs = 4;
+  while (s.pairs < 16 && ceil_div(a.H, 2 * s.pairs) > BN_MAX_THREADS) s.pairs *= 2;
+  const int need = (int)ceil_div(a.H, 2 * s.pairs);
+  if (need <= 32) {
+    s.group = 4;
+    while (s.group < need) s.group *= 2;
+    s.threads = 256;
+    if (!dense) s.threads = s.group = 32;  // one row a CTA: its inputs are copied row by row
+  } else {
+    s.group = (int)round_up(need, 32);
+    s.threads = s.group;
+  }
+  return s;
+}
+
+// The inputs that rows come from, in the order in which the kernels name them.
+inline BnStages bn_inputs(const NormArgs &a, bool backward) {
+  BnStages st = {};
+  const int e = a.f32 ? 4 : 2, r = a.rf32 ? 4 : 2;
+  auto add = [&](const void *p, int64_t ld, int es) {
+    if (!p) return;
+    st.base[st.n] = p;
+    st.ld[st.n] = ld;
+    st.es[st.n++] = es;
+  };
+  const void *gate = a.gate_kind == MOE_GATE_ELEMENT ? a.gate : nullptr;
+  if (backward) {
+    add(a.dr_out, a.ld_dr_out, r);
+    add(a.r_out, a.ld_r_out, r);
+    add(a.dh, a.ld_dh, e);
+    add(a.y, a.ld_y, e);
+    add(gate, a.ld_gate, e);
+  } else {
+    add(a.r, a.ld_r, r);
+    add(a.y, a.ld_y, e);
+    add(gate, a.ld_gate, e);
+  }
+  return st;
+}
+
+constexpr int BN_SMEM = 220 * 1024;  // of an SM, for the stages of its CTAs
+
+// Fills in the stages for `ctas` CTAs on an SM that take R rows a group; false
+// where two stages do not fit, or short rows are not behind one another.
+inline bool bn_stages(const NormArgs &a, const BnShape &s, int ctas, int R, BnStages &st) {
+  const int per_cta = s.threads / s.group;
+  st.rows = per_cta * R;
+  st.runs = 1;
+  st.bytes = 0;
+  for (int k = 0; k < st.n; ++k)
+    if (st.rows > 1 && st.ld[k] != a.H) st.runs = st.rows;
+  if (st.runs > 1 && (per_cta > 1 || st.runs * st.n > 32)) return false;
+  for (int k = 0; k < st.n; ++k) {
+    st.off[k] = st.bytes;
+    st.pitch[k] = (int)round_up((int64_t)(st.runs > 1 ? 1 : st.rows) * a.H * st.es[k], 16) + 16;
+    st.bytes += st.runs * st.pitch[k];
+  }
+  st.bytes = (int)round_up(st.bytes, 128);
+  st.stages = std::min(BN_MAX_STAGES, BN_SMEM / ctas / st.bytes);
+  return st.stages >= 2;
+}
+
+struct BnLaunch {
+  const NormArgs &a;
+  bool backward;
+  float *part;
+  int *status;
+  cudaStream_t stream;
+  int *groups;  // out: groups that leave partial sums
+  bool dry;     // only `groups` is wanted
+};
+
+template <typename TE, typename TR, int VEC, int CH, int R, bool BULK>
+static cudaError_t bn_go(const BnLaunch &l, const BnShape &s, int ctas, const BnStages &st) {
+  const NormArgs &a = l.a;
+  const int per_cta = s.threads / s.group;
+  const int grid = (int)std::min<int64_t>(ceil_div(a.T, per_cta * R), (int64_t)device_sms() * ctas);
+  if (l.groups) *l.groups = grid * per_cta;
+  if (l.dry) return cudaSuccess;
+  const int smem = BULK ? st.bytes * st.stages : 0;
+  auto go = [&](auto kernel, auto... args) {
+    cudaError_t e = smem > 40 * 1024 ? ensure_smem((const void *)kernel, BN_SMEM) : cudaSuccess;
+    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(s.threads), smem, l.stream, a, s.group, st, args...);
+  };
+  if (l.backward) return go(block_norm_bwd_kernel<TE, TR, VEC, CH, R, BULK>, l.part, l.status);
+  return go(block_norm_kernel<TE, TR, VEC, CH, R, BULK>, l.status);
+}
+
+template <typename TE, typename TR, int VEC, int NP>
+static cudaError_t bn_launch(const BnLaunch &l, const BnShape &s) {
+  constexpr int CH = 2 * NP / VEC;
+  BnStages st = bn_inputs(l.a, l.backward);
+  const int ctas = std::max(1, bn_resident(l.backward, NP) / s.threads);
+  if constexpr (NP <= 4) {
+    // Two rows a group where shared memory holds them and all CTAs still get two blocks.
+    if (l.a.T >= (int64_t)device_sms() * ctas * (s.threads / s.group) * 4 && bn_stages(l.a, s, ctas, 2, st))
+      return bn_go<TE, TR, VEC, CH, 2, true>(l, s, ctas, st);
+    if (!bn_stages(l.a, s, ctas, 1, st)) return cudaErrorInvalidConfiguration;  // (at most 4096 elements: they fit)
+    return bn_go<TE, TR, VEC, CH, 1, true>(l, s, ctas, st);
+  } else {
+    if (bn_stages(l.a, s, ctas, 1, st)) return bn_go<TE, TR, VEC, CH, 1, true>(l, s, ctas, st);
+    return bn_go<TE, TR, VEC, CH, 1, false>(l, s, ctas, st);
+  }
+}
+
+template <typename TE, typename TR>
+cudaError_t bn_dispatch(const BnLaunch &l) {
+  constexpr int W = Vec16<TE>::N;
+  bool dense = true;
+  const BnStages st = bn_inputs(l.a, l.backward);
+  for (int k = 0; k < st.n; ++k) dense = dense && st.ld[k] == l.a.H;
+  const BnShape s = bn_shape(l.a, dense);
+  if (s.vec == 1) {
+    if (s.pairs == 4) return bn_launch<TE, TR, 1, 4>(l, s);
+    if (s.pairs == 8) return bn_launch<TE, TR, 1, 8>(l, s);
+    return bn_launch<TE, TR, 1, 16>(l, s);
+  }
+  if (s.pairs == 4) return bn_launch<TE, TR, W, 4>(l, s);
+  if (s.pairs == 8) return bn_launch<TE, TR, W, 8>(l, s);
+  return bn_launch<TE, TR, W, 16>(l, s);
+}
+
+}  // namespace moe

@@ -75,6 +75,35 @@ template <> struct Vec16<__nv_bfloat16> {
   }
 };
 
+// ---- two FP32 lanes in one instruction ----
+struct F2 {
+  uint64_t v;
+  __device__ inline F2() {}
+  __device__ inline F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ inline explicit F2(float a) : F2(a, a) {}
+  __device__ inline void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+  __device__ inline float sum() const {
+    float a, b;
+    get(a, b);
+    return a + b;
+  }
+};
+__device__ inline F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ inline F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ inline F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 // ---- programmatic dependent launch ----
 // Kernels of the layer are launched with programmatic stream serialization:
 // a kernel may be scheduled while its predecessor on the stream is still

@@ -54,28 +54,6 @@ __device__ inline float ds_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two FP32 lanes in one instruction.
-struct DsPair {
-  uint64_t v;
-  __device__ inline DsPair() {}
-  __device__ inline DsPair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ inline void get(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ inline DsPair ds_add2(DsPair a, DsPair b) {
-  DsPair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ inline DsPair ds_mul2(DsPair a, DsPair b) {
-  DsPair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ inline DsPair ds_fma2(DsPair a, DsPair b, DsPair c) {
-  DsPair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 // Keeps the compiler from holding what was unpacked from `v` beside it.
 __device__ inline void ds_opaque(uint4 &v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
 
@@ -92,19 +70,19 @@ __device__ inline float ds_warp_sum(float v) {
 
 // 2^((z - m) k) for many z: z b + a, or (z + a) b where m k is out of range.
 struct DsPower {
-  DsPair a, b;
+  F2 a, b;
   bool far;
   __device__ inline DsPower(float m, float k) {
     const float base = m == ds_neg_inf() ? 0.f : m, mk = __fmul_rn(base, k);
     far = !(fabsf(mk) < 1e37f);
     const float x = far ? -base : -mk;
-    a = DsPair(x, x);
-    b = DsPair(k, k);
+    a = F2(x, x);
+    b = F2(k, k);
   }
-  __device__ inline DsPair two(DsPair z) const {
+  __device__ inline F2 two(F2 z) const {
     float x, y;
-    (far ? ds_mul2(ds_add2(z, a), b) : ds_fma2(z, b, a)).get(x, y);
-    return DsPair(ds_exp2(x), ds_exp2(y));
+    (far ? mul2(add2(z, a), b) : fma2(z, b, a)).get(x, y);
+    return F2(ds_exp2(x), ds_exp2(y));
   }
   // 2^((m' - m) k) for another reference m'.
   __device__ inline float of(float m) const {
@@ -272,7 +250,7 @@ __device__ inline DsStat ds_units_stat(uint4 (&raw)[U], float k) {
 #pragma unroll
       for (int j = 0; j < U; ++j) m = fmaxf(m, ds_unit_max<T>(raw[j]));
     const DsPower power(m, k);
-    DsPair sum[2] = {DsPair(0.f, 0.f), DsPair(0.f, 0.f)};
+    F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
     auto add = [&](bool far) {
       DsPower p = power;
       p.far = far;
@@ -282,13 +260,13 @@ __device__ inline DsStat ds_units_stat(uint4 (&raw)[U], float k) {
         ds_opaque(raw[j]);
         Vec16<T>::unpack(raw[j], v);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) sum[(i >> 1) & 1] = ds_add2(sum[(i >> 1) & 1], p.two(DsPair(v[i], v[i + 1])));
+        for (int i = 0; i < N; i += 2) sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], p.two(F2(v[i], v[i + 1])));
       }
     };
     if (power.far) add(true);
     else add(false);
     float s0, s1;
-    ds_add2(sum[0], sum[1]).get(s0, s1);
+    add2(sum[0], sum[1]).get(s0, s1);
     s = s0 + s1;
     if (all || s <= 1099511627776.f) break;  // (NaN goes on, once)
   }
@@ -301,20 +279,20 @@ __device__ inline DsStat ds_units_stat(uint4 (&raw)[U], float k) {
 template <bool LOSS>
 struct DsGrad {
   DsPower power;
-  DsPair tau, mul;
+  F2 tau, mul;
   __device__ inline DsGrad(float m_or_lse, float k, float inv_tau, float mul_)
       : power(m_or_lse, k), tau(inv_tau, inv_tau), mul(mul_, mul_) {
-    if (!LOSS) power.a = DsPair(-m_or_lse, -m_or_lse);
+    if (!LOSS) power.a = F2(-m_or_lse, -m_or_lse);
   }
   __device__ inline void operator()(float &u, float &v) const {
-    DsPair x(u, v);
+    F2 x(u, v);
     if (LOSS) {
       x = power.two(x);
     } else {
-      ds_mul2(ds_fma2(x, tau, power.a), DsPair(DS_LOG2E, DS_LOG2E)).get(u, v);
-      x = DsPair(ds_exp2(u), ds_exp2(v));
+      mul2(fma2(x, tau, power.a), F2(DS_LOG2E, DS_LOG2E)).get(u, v);
+      x = F2(ds_exp2(u), ds_exp2(v));
     }
-    ds_mul2(x, mul).get(u, v);
+    mul2(x, mul).get(u, v);
   }
 };
 
