@@ -34,12 +34,16 @@ namespace moe {
 
 constexpr int BN_MAX_THREADS = 512, BN_MAX_STAGES = 6, BN_MAX_INPUTS = 5;
 
-// The row inputs of a launch and where their blocks of rows stand in a stage.
+// The row inputs of a launch (NULL: not there) and where their blocks of rows
+// stand in a stage.  Forward: r, y, element gate; backward: dr_out, r_out, dh,
+// y, element gate.
 struct BnStages {
   int n, stages, bytes;  // inputs, stages, bytes of a stage
   int rows;              // of a block
   int runs;              // runs of bytes that it is: 1 (rows behind one another), or its rows
-  int off[BN_MAX_INPUTS], es[BN_MAX_INPUTS], pitch[BN_MAX_INPUTS];  // pitch: bytes from run to run in a stage
+  int off[BN_MAX_INPUTS], es[BN_MAX_INPUTS];
+  uint32_t row[BN_MAX_INPUTS];    // bytes from row to row in a stage
+  uint32_t apart[BN_MAX_INPUTS];  // and in memory (modulo 2^32)
   int64_t ld[BN_MAX_INPUTS];
   const void *base[BN_MAX_INPUTS];
 };
@@ -57,7 +61,7 @@ struct BnPiece {
 __device__ inline BnPiece bn_piece(const BnStages &st, int k, int q, int64_t t0, int T, int H) {
   const int64_t first_row = t0 + q, rows = st.runs > 1 ? 1 : min((int64_t)st.rows, T - t0);
   BnPiece p = {0, 0, 0, 0};
-  if (first_row >= T) return p;
+  if (first_row >= T || !st.base[k]) return p;
   p.lo = (uintptr_t)st.base[k] + first_row * st.ld[k] * st.es[k];
   p.hi = p.lo + ((rows - 1) * st.ld[k] + H) * st.es[k];
   const uintptr_t first = ((uintptr_t)st.base[k] + 15) & ~(uintptr_t)15;
@@ -80,7 +84,7 @@ __device__ inline void bn_start(const BnStages &st, uint8_t *stage, uint64_t *ba
   }
   __syncwarp();
   if (bytes)
-    umma::bulk_load(stage + st.off[k] + q * st.pitch[k] + (p.from - (p.lo & ~(uintptr_t)15)), (const void *)p.from, bytes, bar);
+    umma::bulk_load(stage + st.off[k] + q * st.row[k] + (p.from - (p.lo & ~(uintptr_t)15)), (const void *)p.from, bytes, bar);
 }
 // What the copies of the first and the last block may have missed (the whole
 // CTA; the caller's barrier follows).
@@ -92,7 +96,7 @@ __device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, i
       const BnPiece p = bn_piece(st, k, q, t0, T, H);
       if (p.from <= p.lo && p.to >= p.hi) continue;
       missed = true;
-      uint8_t *dst = stage + st.off[k] + q * st.pitch[k] - (p.lo & ~(uintptr_t)15);
+      uint8_t *dst = stage + st.off[k] + q * st.row[k] - (p.lo & ~(uintptr_t)15);
       for (uintptr_t b = p.lo + threadIdx.x; b < p.hi; b += blockDim.x)
         if (b < p.from || b >= p.to) dst[b] = *(const uint8_t *)b;
     }
@@ -101,8 +105,9 @@ __device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, i
 
 // ---- what a thread holds of a row: NP pairs of floats ----
 // Wide: CH runs of VEC neighbouring elements, at (c group + lane) VEC.  Scalar
-// (VEC = 1): elements lane, lane + group, ...  Past the row it holds zeros.
-template <int VEC, int CH>
+// (VEC = 1): elements lane, lane + group, ...  Past the row it holds zeros;
+// FULL: no thread reaches past the row.
+template <int VEC, int CH, bool FULL>
 struct BnRow {
   static constexpr int NP = VEC * CH / 2;
   int lane, group, H;
@@ -123,9 +128,9 @@ struct BnRow {
 #pragma unroll
         for (int b = 0; b < VEC / N; ++b) {
           float v[N];
-#pragma unroll
-          for (int k = 0; k < N; ++k) v[k] = 0.f;
-          if (i < H) Vec16<T>::load(row + i + b * N, v);
+          uint4 raw = {0, 0, 0, 0};
+          if (FULL || i < H) raw = *(const uint4 *)(row + i + b * N);
+          Vec16<T>::unpack(raw, v);
 #pragma unroll
           for (int k = 0; k < N; k += 2) o[(c * VEC + b * N + k) / 2] = F2(v[k], v[k + 1]);
         }
@@ -153,7 +158,7 @@ struct BnRow {
           float v[N];
 #pragma unroll
           for (int k = 0; k < N; k += 2) x[(c * VEC + b * N + k) / 2].get(v[k], v[k + 1]);
-          if (i < H) Vec16<T>::store(row + i + b * N, v);
+          if (FULL || i < H) Vec16<T>::store(row + i + b * N, v);
         }
       }
     }
@@ -235,16 +240,14 @@ struct BnWalk {
     if (bn_mend(st, stage, t0, T, H)) __syncthreads();
     return true;
   }
-  // Row t (the j-th of the block) of staged input k, or of `p` in memory.
-  template <typename E>
-  __device__ inline const E *row(int k, const void *p, int64_t ld, int64_t t, int j) const {
+  // Row `at` of the block (row t in memory, of `p`) of input K.
+  template <int K, bool WIDE, typename E>
+  __device__ inline const E *row(const void *p, int64_t ld, int64_t t, int at) const {
     if (!BULK) return (const E *)p + t * ld;
-    if (st.runs > 1) {
-      const uintptr_t at = (uintptr_t)p + t * ld * sizeof(E);
-      return (const E *)(stage + st.off[k] + j * st.pitch[k] + (at & 15));
-    }
-    const uintptr_t at = (uintptr_t)p + t0 * ld * sizeof(E);
-    return (const E *)(stage + st.off[k] + (at & 15)) + (t - t0) * ld;
+    uint32_t o = st.off[K] + at * st.row[K];
+    // where the run starts between 16-byte boundaries
+    if (!WIDE) o += ((uint32_t)(uintptr_t)st.base[K] + (uint32_t)(st.runs > 1 ? t : t0) * st.apart[K]) & 15;
+    return (const E *)(stage + o);
   }
   // Behind a barrier of this block: the last block's stage has been read by
   // all, its copies for a later block start.
@@ -263,7 +266,18 @@ struct BnWalk {
 };
 
 // Threads of an SM that the kernels' registers allow.
-constexpr int bn_resident(bool backward, int np) { return !backward && np <= 4 ? 1024 : 512; }
+constexpr int bn_resident(bool backward, int np, int r) { return !backward && np <= 4 && r == 1 ? 1024 : 512; }
+
+// An output's rows: row j of a group in a block, by a pointer that moves on.
+template <typename E>
+struct BnOut {
+  E *p;
+  int64_t next, step;  // elements from row j to j + 1, and to the next block
+  __device__ inline BnOut(void *base, int64_t ld, int64_t t, int per_cta, int64_t step_rows)
+      : p((E *)base + t * ld), next(per_cta * ld), step(step_rows * ld) {}
+  __device__ inline E *row(int j) const { return p + j * next; }
+  __device__ inline void move() { p += step; }
+};
 
 // The rows of a block that a group takes: number, place in the block, whether
 // there is such a row (a row of the block stands in where there is none).
@@ -282,20 +296,22 @@ struct BnRows {
   }
 };
 
-template <typename TE, typename TR, int VEC, int CH, int R, bool BULK>
-__global__ void __launch_bounds__(BN_MAX_THREADS, bn_resident(false, VEC * CH / 2) / BN_MAX_THREADS)
+template <typename TE, typename TR, int VEC, int CH, int R, bool BULK, bool FULL>
+__global__ void __launch_bounds__(BN_MAX_THREADS, bn_resident(false, VEC * CH / 2, R) / BN_MAX_THREADS)
 block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
   constexpr int NP = VEC * CH / 2;
-  constexpr bool HELD = NP <= 4;  // weights stay in registers
+  constexpr bool WIDE = VEC > 1, HELD = NP <= 4;  // weights stay in registers
   extern __shared__ __align__(128) uint8_t bn_smem[];
   __shared__ BnBars bars;
   __shared__ __align__(16) float buf[2][R][16];
   const int per_cta = blockDim.x / group, sub = threadIdx.x / group, lane = threadIdx.x % group;
   const float inv_h = 1.f / a.H;
-  const BnRow<VEC, CH> io = {lane, group, a.H};
+  const BnRow<VEC, CH, FULL> io = {lane, group, a.H};
   if (threadIdx.x < 2 * R * 16) buf[0][0][threadIdx.x] = 0.f;
   if (!BULK) __syncthreads();
   BnWalk<BULK, R> walk(st, a.T, a.H, per_cta, bn_smem, bars);
+  BnOut<TR> r_out(a.r_out, a.ld_r_out, walk.t0 + sub, per_cta, walk.step);
+  BnOut<TE> h_out(a.h, a.ld_h, walk.t0 + sub, per_cta, walk.step);
   F2 w_post[NP], w_pre[NP];
   if (HELD && a.w_post) io.template weights<TE>(a.w_post, a.wf32, a.offset, w_post);
   if (HELD && a.w_pre) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
@@ -310,7 +326,7 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
     if (a.w_post) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        io.load(walk.template row<TE>(1, a.y, a.ld_y, rows.t[j], rows.at[j]), y);
+        io.load(walk.template row<1, WIDE, TE>(a.y, a.ld_y, rows.t[j], rows.at[j]), y);
         F2 sum(0.f);
 #pragma unroll
         for (int p = 0; p < NP; ++p) sum = fma2(y[p], y[p], sum);
@@ -326,9 +342,9 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int64_t t = rows.t[j];
-      io.load(walk.template row<TR>(0, a.r, a.ld_r, t, rows.at[j]), v[j]);
+      io.load(walk.template row<0, WIDE, TR>(a.r, a.ld_r, t, rows.at[j]), v[j]);
       if (a.y) {
-        io.load(walk.template row<TE>(1, a.y, a.ld_y, t, rows.at[j]), y);
+        io.load(walk.template row<1, WIDE, TE>(a.y, a.ld_y, t, rows.at[j]), y);
         const F2 f(a.w_post ? a.scale * rstd[j] : a.scale);
 #pragma unroll
         for (int p = 0; p < NP; ++p) y[p] = mul2(y[p], f);
@@ -337,7 +353,7 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
           for (int p = 0; p < NP; ++p) y[p] = mul2(y[p], w_post[p]);
         }
         F2 g[NP];
-        if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<TE>(2, a.gate, a.ld_gate, t, rows.at[j]), g);
+        if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<2, WIDE, TE>(a.gate, a.ld_gate, t, rows.at[j]), g);
         else if (a.gate_kind == MOE_GATE_CHANNEL) io.template weights<TE>(a.gate, a.wf32, 0.f, g);
         else {
           const F2 one(a.gate_kind == MOE_GATE_TOKEN ? ((const float *)a.gate)[t] : 1.f);
@@ -346,7 +362,7 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) v[j][p] = fma2(g[p], y[p], v[j][p]);
-        if (rows.there[j]) io.store((TR *)a.r_out + t * a.ld_r_out, v[j]);
+        if (rows.there[j]) io.store(r_out.row(j), v[j]);
       }
       F2 sum(0.f);
 #pragma unroll
@@ -361,30 +377,32 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
         const F2 rs(rsqrtf(fmaf(s[j], inv_h, a.eps)));
 #pragma unroll
         for (int p = 0; p < NP; ++p) v[j][p] = mul2(mul2(v[j][p], rs), w_pre[p]);
-        if (rows.there[j]) io.store((TE *)a.h + rows.t[j] * a.ld_h, v[j]);
+        if (rows.there[j]) io.store(h_out.row(j), v[j]);
       }
     }
+    r_out.move();
+    h_out.move();
   }
 }
 
 // part: [3][groups][H] sums over a group's rows of what dw_pre, dw_post and a
 // channel gate's gradient are made of (only those that the call asks for).
-template <typename TE, typename TR, int VEC, int CH, int R, bool BULK>
+template <typename TE, typename TR, int VEC, int CH, int R, bool BULK, bool FULL>
 __global__ void __launch_bounds__(BN_MAX_THREADS)
 block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *part, int *status) {
   constexpr int NP = VEC * CH / 2;
-  constexpr bool HELD = NP <= 4;
+  constexpr bool WIDE = VEC > 1, HELD = NP <= 4;
   extern __shared__ __align__(128) uint8_t bn_smem[];
   __shared__ BnBars bars;
   __shared__ __align__(16) float buf[2][3 * R][16];
   const int per_cta = blockDim.x / group, sub = threadIdx.x / group, lane = threadIdx.x % group;
   const float inv_h = 1.f / a.H;
-  const BnRow<VEC, CH> io = {lane, group, a.H};
+  const BnRow<VEC, CH, FULL> io = {lane, group, a.H};
   for (int i = threadIdx.x; i < 2 * 3 * R * 16; i += blockDim.x) buf[0][0][i] = 0.f;
   if (!BULK) __syncthreads();
-  // Inputs are staged in the order of their use.
-  const int in_r = a.dr_out ? 1 : 0, in_d = in_r + 1, in_y = in_r + (a.w_pre ? 2 : 0), in_g = in_y + 1;
   BnWalk<BULK, R> walk(st, a.T, a.H, per_cta, bn_smem, bars);
+  BnOut<TR> dr_out(a.dr, a.ld_dr, walk.t0 + sub, per_cta, walk.step);
+  BnOut<TE> dy_out(a.dy, a.ld_dy, walk.t0 + sub, per_cta, walk.step), dg_out(a.dgate, a.ld_dgate, walk.t0 + sub, per_cta, walk.step);
   F2 w_post[NP], w_pre[NP], dw_post[NP], dw_pre[NP], dgate[NP];
   if (HELD && a.w_post) io.template weights<TE>(a.w_post, a.wf32, a.offset, w_post);
   if (HELD && a.w_pre) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
@@ -400,8 +418,8 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
     for (int j = 0; j < R; ++j) {
       F2 vv(0.f), dv(0.f), yy(0.f), x[NP], d[NP];
       if (a.w_pre) {
-        io.load(walk.template row<TR>(in_r, a.r_out, a.ld_r_out, rows.t[j], rows.at[j]), x);
-        io.load(walk.template row<TE>(in_d, a.dh, a.ld_dh, rows.t[j], rows.at[j]), d);
+        io.load(walk.template row<1, WIDE, TR>( a.r_out, a.ld_r_out, rows.t[j], rows.at[j]), x);
+        io.load(walk.template row<2, WIDE, TE>( a.dh, a.ld_dh, rows.t[j], rows.at[j]), d);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           vv = fma2(x[p], x[p], vv);
@@ -409,7 +427,7 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
         }
       }
       if (a.w_post) {
-        io.load(walk.template row<TE>(in_y, a.y, a.ld_y, rows.t[j], rows.at[j]), x);
+        io.load(walk.template row<3, WIDE, TE>( a.y, a.ld_y, rows.t[j], rows.at[j]), x);
 #pragma unroll
         for (int p = 0; p < NP; ++p) yy = fma2(x[p], x[p], yy);
       }
@@ -430,32 +448,32 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
       const float rv = rsqrtf(fmaf(s[3 * j], inv_h, a.eps));
       ry[j] = a.w_post ? rsqrtf(fmaf(s[3 * j + 2], inv_h, a.eps)) : 1.f;
       if (a.dr_out) {
-        io.load(walk.template row<TR>(0, a.dr_out, a.ld_dr_out, t, rows.at[j]), e[j]);
+        io.load(walk.template row<0, WIDE, TR>(a.dr_out, a.ld_dr_out, t, rows.at[j]), e[j]);
       } else {
 #pragma unroll
         for (int p = 0; p < NP; ++p) e[j][p] = F2(0.f);
       }
       if (a.w_pre) {
         F2 x[NP], d[NP];
-        io.load(walk.template row<TR>(in_r, a.r_out, a.ld_r_out, t, rows.at[j]), x);
-        io.load(walk.template row<TE>(in_d, a.dh, a.ld_dh, t, rows.at[j]), d);
+        io.load(walk.template row<1, WIDE, TR>( a.r_out, a.ld_r_out, t, rows.at[j]), x);
+        io.load(walk.template row<2, WIDE, TE>( a.dh, a.ld_dh, t, rows.at[j]), d);
         const F2 rr(rv), r1(rv * one), cr(-(s[3 * j + 1] * inv_h * rv * rv * rv));
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           dw_pre[p] = fma2(d[p], mul2(x[p], r1), dw_pre[p]);
           e[j][p] = add2(e[j][p], fma2(mul2(d[p], w_pre[p]), rr, mul2(x[p], cr)));
         }
-        if (rows.there[j]) io.store((TR *)a.dr + t * a.ld_dr, e[j]);
+        if (rows.there[j]) io.store(dr_out.row(j), e[j]);
       }
       q[2 * j] = q[2 * j + 1] = 0.f;
       if (a.y) {
         F2 y[NP], g[NP], q0(0.f), q1(0.f);
-        io.load(walk.template row<TE>(in_y, a.y, a.ld_y, t, rows.at[j]), y);
+        io.load(walk.template row<3, WIDE, TE>( a.y, a.ld_y, t, rows.at[j]), y);
         const F2 sc(a.scale * one), rr(ry[j]);
 #pragma unroll
         for (int p = 0; p < NP; ++p) e[j][p] = mul2(e[j][p], sc);
         if (a.gate_kind != MOE_GATE_NONE) {
-          if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<TE>(in_g, a.gate, a.ld_gate, t, rows.at[j]), g);
+          if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<4, WIDE, TE>( a.gate, a.ld_gate, t, rows.at[j]), g);
           else if (a.gate_kind == MOE_GATE_CHANNEL) io.template weights<TE>(a.gate, a.wf32, 0.f, g);
           else {
             const F2 gt(((const float *)a.gate)[t]);
@@ -475,7 +493,7 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
 #pragma unroll
             for (int p = 0; p < NP; ++p) dgate[p] = add2(dgate[p], dg[p]);
           }
-          if (a.gate_kind == MOE_GATE_ELEMENT && rows.there[j]) io.store((TE *)a.dgate + t * a.ld_dgate, dg);
+          if (a.gate_kind == MOE_GATE_ELEMENT && rows.there[j]) io.store(dg_out.row(j), dg);
         }
         if (a.w_post) {
 #pragma unroll
@@ -499,13 +517,16 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
         if (a.w_post) {
           const F2 cy(-(q[2 * j] * inv_h * ry[j] * ry[j] * ry[j]));
           F2 y[NP];
-          io.load(walk.template row<TE>(in_y, a.y, a.ld_y, rows.t[j], rows.at[j]), y);
+          io.load(walk.template row<3, WIDE, TE>( a.y, a.ld_y, rows.t[j], rows.at[j]), y);
 #pragma unroll
           for (int p = 0; p < NP; ++p) e[j][p] = fma2(y[p], cy, e[j][p]);
         }
-        if (rows.there[j]) io.store((TE *)a.dy + rows.t[j] * a.ld_dy, e[j]);
+        if (rows.there[j]) io.store(dy_out.row(j), e[j]);
       }
     }
+    dr_out.move();
+    dy_out.move();
+    dg_out.move();
   }
   const int64_t groups = (int64_t)gridDim.x * per_cta;
   float *p = part + ((int64_t)blockIdx.x * per_cta + sub) * a.H;
@@ -557,7 +578,6 @@ inline BnStages bn_inputs(const NormArgs &a, bool backward) {
   BnStages st = {};
   const int e = a.f32 ? 4 : 2, r = a.rf32 ? 4 : 2;
   auto add = [&](const void *p, int64_t ld, int es) {
-    if (!p) return;
     st.base[st.n] = p;
     st.ld[st.n] = ld;
     st.es[st.n++] = es;
@@ -587,12 +607,15 @@ inline bool bn_stages(const NormArgs &a, const BnShape &s, int ctas, int R, BnSt
   st.runs = 1;
   st.bytes = 0;
   for (int k = 0; k < st.n; ++k)
-    if (st.rows > 1 && st.ld[k] != a.H) st.runs = st.rows;
+    if (st.base[k] && st.rows > 1 && st.ld[k] != a.H) st.runs = st.rows;
   if (st.runs > 1 && (per_cta > 1 || st.runs * st.n > 32)) return false;
   for (int k = 0; k < st.n; ++k) {
+    if (!st.base[k]) continue;
+    const int run = (int)round_up((int64_t)(st.runs > 1 ? 1 : st.rows) * a.H * st.es[k], 16) + 16;
     st.off[k] = st.bytes;
-    st.pitch[k] = (int)round_up((int64_t)(st.runs > 1 ? 1 : st.rows) * a.H * st.es[k], 16) + 16;
-    st.bytes += st.runs * st.pitch[k];
+    st.row[k] = st.runs > 1 ? run : a.H * st.es[k];
+    st.apart[k] = (uint32_t)(st.ld[k] * st.es[k]);
+    st.bytes += st.runs * run;
   }
   st.bytes = (int)round_up(st.bytes, 128);
   st.stages = std::min(BN_MAX_STAGES, BN_SMEM / ctas / st.bytes);
@@ -609,7 +632,7 @@ struct BnLaunch {
   bool dry;     // only `groups` is wanted
 };
 
-template <typename TE, typename TR, int VEC, int CH, int R, bool BULK>
+template <typename TE, typename TR, int VEC, int CH, int R, bool BULK, bool FULL = false>
 static cudaError_t bn_go(const BnLaunch &l, const BnShape &s, int ctas, const BnStages &st) {
   const NormArgs &a = l.a;
   const int per_cta = s.threads / s.group;
@@ -621,20 +644,27 @@ static cudaError_t bn_go(const BnLaunch &l, const BnShape &s, int ctas, const Bn
     cudaError_t e = smem > 40 * 1024 ? ensure_smem((const void *)kernel, BN_SMEM) : cudaSuccess;
     return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(s.threads), smem, l.stream, a, s.group, st, args...);
   };
-  if (l.backward) return go(block_norm_bwd_kernel<TE, TR, VEC, CH, R, BULK>, l.part, l.status);
-  return go(block_norm_kernel<TE, TR, VEC, CH, R, BULK>, l.status);
+  if (l.backward) return go(block_norm_bwd_kernel<TE, TR, VEC, CH, R, BULK, FULL>, l.part, l.status);
+  return go(block_norm_kernel<TE, TR, VEC, CH, R, BULK, FULL>, l.status);
 }
 
 template <typename TE, typename TR, int VEC, int NP>
 static cudaError_t bn_launch(const BnLaunch &l, const BnShape &s) {
   constexpr int CH = 2 * NP / VEC;
   BnStages st = bn_inputs(l.a, l.backward);
-  const int ctas = std::max(1, bn_resident(l.backward, NP) / s.threads);
+  int ctas = std::max(1, bn_resident(l.backward, NP, 2) / s.threads);
   if constexpr (NP <= 4) {
+    const bool full = VEC > 1 && l.a.H == s.group * VEC * CH;
     // Two rows a group where shared memory holds them and all CTAs still get two blocks.
-    if (l.a.T >= (int64_t)device_sms() * ctas * (s.threads / s.group) * 4 && bn_stages(l.a, s, ctas, 2, st))
+    if (l.a.T >= (int64_t)device_sms() * ctas * (s.threads / s.group) * 4 && bn_stages(l.a, s, ctas, 2, st)) {
+      if constexpr (VEC > 1)
+        if (full) return bn_go<TE, TR, VEC, CH, 2, true, true>(l, s, ctas, st);
       return bn_go<TE, TR, VEC, CH, 2, true>(l, s, ctas, st);
+    }
+    ctas = std::max(1, bn_resident(l.backward, NP, 1) / s.threads);
     if (!bn_stages(l.a, s, ctas, 1, st)) return cudaErrorInvalidConfiguration;  // (at most 4096 elements: they fit)
+    if constexpr (VEC > 1)
+      if (full) return bn_go<TE, TR, VEC, CH, 1, true, true>(l, s, ctas, st);
     return bn_go<TE, TR, VEC, CH, 1, true>(l, s, ctas, st);
   } else {
     if (bn_stages(l.a, s, ctas, 1, st)) return bn_go<TE, TR, VEC, CH, 1, true>(l, s, ctas, st);
@@ -647,7 +677,7 @@ cudaError_t bn_dispatch(const BnLaunch &l) {
   constexpr int W = Vec16<TE>::N;
   bool dense = true;
   const BnStages st = bn_inputs(l.a, l.backward);
-  for (int k = 0; k < st.n; ++k) dense = dense && st.ld[k] == l.a.H;
+  for (int k = 0; k < st.n; ++k) dense = dense && (!st.base[k] || st.ld[k] == l.a.H);
   const BnShape s = bn_shape(l.a, dense);
   if (s.vec == 1) {
     if (s.pairs == 4) return bn_launch<TE, TR, 1, 4>(l, s);

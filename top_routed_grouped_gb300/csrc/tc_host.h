@@ -109,7 +109,7 @@ inline int device_sms() {
   return n;
 }
 
-constexpr int ENSURE_SMEM_KERNELS = 96;  // more than the library has
+constexpr int ENSURE_SMEM_KERNELS = 192;  // more than the library has
 // Opt `fn` in to `bytes` of dynamic shared memory once per device.
 inline cudaError_t ensure_smem(const void *fn, int bytes) {
   static std::mutex mu;
