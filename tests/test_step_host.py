@@ -1,0 +1,134 @@
+"""Host-side checks of the operators around the layer (no GPU work): packed
+structs match the header, bad arguments return an error and launch nothing."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import top_routed_grouped_gb300 as moe
+from top_routed_grouped_gb300 import build, step
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PTR = 256  # never read: the calls fail, or have no rows
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return moe.lib()
+
+
+def fields(name):
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "moe.h")).read(), flags=re.S)
+    body = re.search(r"typedef struct %s \{(.*?)\} %s_t;" % (name, name), src, flags=re.S).group(1)
+    out = []
+    for line in body.split(";"):
+        line = line.strip()
+        if line:
+            kind, names = re.match(r"((?:const )?\w+ ?)\s*(.*)", line, flags=re.S).groups()
+            for n in names.split(","):
+                out.append((n.strip().lstrip("*"), "Q" if "*" in n else {"int32_t": "i", "float": "f", "int64_t": "q"}[kind.strip()]))
+    return out
+
+
+@pytest.mark.parametrize("name,packed", [("moe_norm_args", step._NORM), ("moe_embed_args", step._EMBED),
+                                         ("moe_distill_args", step._DISTILL)])
+def test_structs_match_the_header(name, packed):
+    f = fields(name)
+    letters = re.sub(r"(\d+)(\w)", lambda m: int(m.group(1)) * m.group(2), packed.format)
+    assert "".join(k for _, k in f) == letters
+    cls = type("S", (ctypes.Structure,), {"_fields_": [
+        (n, {"i": ctypes.c_int32, "f": ctypes.c_float, "q": ctypes.c_int64, "Q": ctypes.c_void_p}[k]) for n, k in f]})
+    assert ctypes.sizeof(cls) == packed.size
+
+
+def packed(name, spec, **kw):
+    base = {n: (PTR if k == "Q" else 0) for n, k in fields(name)}
+    base.update(kw)
+    return spec.pack(*[base[n] for n, _ in fields(name)])
+
+
+def norm(**kw):
+    return packed("moe_norm_args", step._NORM, **dict(dict(T=4, H=64, dtype=1, rdtype=1, wdtype=1, scale=1.0, eps=1e-6), **kw))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), -1), (dict(H=0), -1), (dict(H=16385), -2), (dict(dtype=2), -1), (dict(rdtype=5), -1),
+    (dict(dtype=0, rdtype=1), -1), (dict(dtype=0, rdtype=0, wdtype=1), -1), (dict(gate_kind=4), -1),
+    (dict(scale=float("nan")), -1), (dict(eps=-1.0), -1), (dict(eps=float("inf")), -1), (dict(reserved=1), -1),
+    (dict(ld_r=63), -1), (dict(ld_y=-64), -1), (dict(r=0), -1), (dict(r=PTR + 1), -1), (dict(h=0), -1),
+    (dict(r_out=0), -1), (dict(y=0), -1), (dict(y=0, w_post=0, w_pre=0), -1), (dict(gate_kind=1, gate=0), -1),
+    (dict(w_pre=PTR + 1), -1), (dict(T=0), 0), (dict(T=0, r=0, y=0, h=0), 0),
+])
+def test_norm_refusals(L, kw, want):
+    assert L.moe_block_norm(norm(**kw), None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dr=0), -1), (dict(dy=0), -1), (dict(dw_post=0), -1), (dict(dw_pre=0), -1), (dict(dh=0), -1),
+    (dict(r_out=0), -1), (dict(dr_out=0, w_pre=0), -1), (dict(gate_kind=3, dgate=0), -1), (dict(H=1 << 20), -2),
+])
+def test_norm_backward_refusals(L, kw, want):
+    assert L.moe_block_norm_backward(norm(**kw), PTR, 1 << 40, None) == want
+
+
+def test_missing_arguments(L):
+    assert L.moe_block_norm(None, None) == -1 and L.moe_block_norm_backward(None, None, 0, None) == -1
+    assert L.moe_embed(None, None) == -1 and L.moe_embed_backward(None, None, 0, None) == -1
+    assert L.moe_distill(None, None) == -1 and L.moe_block_norm_workspace_size(None) == 0
+    assert L.moe_embed_workspace_size(None) == 0
+
+
+def embed(**kw):
+    return packed("moe_embed_args", step._EMBED, **dict(dict(T=4, H=64, V=100, dtype=1, odtype=1, scale=1.0, padding_id=-1), **kw))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), -1), (dict(H=0), -1), (dict(V=0), -1), (dict(V=1 << 20), -2), (dict(dtype=3), -1),
+    (dict(dtype=0, odtype=1), -1), (dict(ids=0), -1), (dict(ids=PTR + 2), -1), (dict(ids64=1, ids=PTR + 4), -1),
+    (dict(ids64=2), -1), (dict(scale=float("inf")), -1), (dict(table=0), -1), (dict(out=PTR + 1), -1),
+    (dict(ld_table=10), -1), (dict(T=0, ids=0, table=0, out=0), 0),
+])
+def test_embed_refusals(L, kw, want):
+    assert L.moe_embed(embed(**kw), None) == want
+
+
+def test_embed_backward_refusals(L):
+    n = L.moe_embed_workspace_size(embed())
+    assert n > 0 and n % 256 == 0
+    for kw, ws, size, want in ((dict(dtable=0), PTR, n, -1), (dict(dout=0), PTR, n, -1), (dict(accumulate=2), PTR, n, -1),
+                               ({}, PTR, n - 1, -3), ({}, 0, n, -1), ({}, PTR + 16, n, -1)):
+        assert L.moe_embed_backward(embed(**kw), ws, size, None) == want
+
+
+def distill(**kw):
+    return packed("moe_distill_args", step._DISTILL, **dict(dict(T=4, V=100, K=3, dtype=1, temperature=1.0, scale=1.0), **kw))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), -1), (dict(V=0), -1), (dict(K=0), -1), (dict(K=257), -2), (dict(T=(1 << 27) + 1), -2),
+    (dict(V=(1 << 28) + 1), -2), (dict(dtype=2), -1), (dict(temperature=0.0), -1), (dict(temperature=-2.0), -1),
+    (dict(temperature=float("inf")), -1), (dict(temperature=1e-39), -1), (dict(scale=float("nan")), -1),
+    (dict(ld_logits=99), -1), (dict(logits=0), -1), (dict(logits=PTR + 1), -1), (dict(t_ids=0), -1),
+    (dict(t_logits=0), -1), (dict(t_lse=PTR + 2), -1), (dict(T=0), 0), (dict(T=0, logits=0), 0),
+])
+def test_distill_refusals(L, kw, want):
+    for f in (L.moe_distill, L.moe_distill_backward, L.moe_distill_step):
+        assert f(distill(**kw), None) == want
+
+
+def test_distill_outputs(L):
+    assert L.moe_distill(distill(loss=0), None) == -1 and L.moe_distill(distill(lse=0), None) == -1
+    assert L.moe_distill_backward(distill(lse=0), None) == -1 and L.moe_distill_backward(distill(weight=0), None) == -1
+    assert L.moe_distill_step(distill(dlogits=0), None) == -1
+    assert L.moe_distill_step(distill(ld_logits=128, ld_dlogits=100), None) == -1  # in place, another stride
+
+
+def test_cpu_tensors_are_refused():
+    t = torch.ones(4, 8)
+    for f in (lambda: moe.block_norm(t, None, None, t[0]), lambda: moe.embed(t, torch.zeros(2, dtype=torch.int64)),
+              lambda: moe.distill(t, torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1))):
+        with pytest.raises(ValueError):
+            f()

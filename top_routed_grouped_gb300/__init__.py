@@ -11,7 +11,8 @@ There is no fallback: if the library is missing, ``lib()`` raises.  Build it
 with ``python -m top_routed_grouped_gb300.build`` (or ``__graft_entry__.build()``).
 
 The operators around the layer (``step.py``) are reached the same way:
-``embed``, ``block_norm``, ``distill`` and their gradients.
+``embed``, ``block_norm``, ``distill`` and their gradients, and under autograd
+(``step_layer.py``) ``TokenEmbedding``, ``BlockNorm``, ``distillation_loss``.
 
 ``MoELayer`` / ``MoEFunction`` (``layer.py``): the layer as a torch module
 whose autograd Function calls ``moe_forward`` and ``moe_backward``.
@@ -448,6 +449,9 @@ def __getattr__(name):
     if name in ("MoELayer", "MoEFunction"):
         from . import layer
         return getattr(layer, name)
+    if name in ("TokenEmbedding", "BlockNorm", "distillation_loss"):
+        from . import step_layer
+        return getattr(step_layer, name)
     if name in _STEP:
         from . import step
         globals().update({n: getattr(step, n) for n in _STEP})

@@ -83,7 +83,7 @@ def _on(t: torch.Tensor, stream, call, *args):
 
 def _rows(t, T: int, N: int, dtype, dev, name: str):
     """``t`` as [T, N] rows of ``dtype`` with neighbouring channels, and its
-    row stride (0 where the rows are dense)."""
+    row stride (0 where the rows are dense).  An ``empty_like`` of it is dense."""
     if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != T or t.shape[1] != N:
         raise ValueError(f"{name}: {dtype} [{T}, {N}] on device {dev} expected, got {t.dtype} {list(t.shape)} "
                          f"on device {t.get_device()}")
@@ -182,9 +182,9 @@ def _block_norm(stream, r, y, w_post, w_pre, gate, scale, eps, offset, dtype, in
                 raise ValueError("r: rows that cannot be written in place")
             ld_out = ld_r
         else:
-            r_out = r.new_empty((T, H))
+            r_out = torch.empty_like(r)
     if w_pre is not None:
-        h = torch.empty((T, H), dtype=dtype, device=r.device)
+        h = torch.empty_like(r if dtype is r.dtype else y) if y is not None else torch.empty_like(r, dtype=dtype)
     moe_block_norm(_NORM.pack(T, H, code, rcode, wcode, kind, scale, eps, offset, 0, ld_r, ld_y, ld_gate, ld_out, 0, 0, 0,
                               0, 0, 0, r.data_ptr(), _ptr(y), _ptr(w_post), _ptr(w_pre), _ptr(gate), _ptr(r_out),
                               _ptr(h), 0, 0, 0, 0, 0, 0, 0), stream)
@@ -234,17 +234,17 @@ def _block_norm_backward(stream, dr_out, dh, r_out, y, w_post, w_pre, gate, scal
     if w_pre is not None:
         r_out, ld_r = _rows(r_out, T, H, like.dtype, dev, "r_out")
         dh, ld_dh = _rows(dh, T, H, dtype, dev, "dh")
-        dr = r_out.new_empty((T, H))
+        dr = torch.empty_like(r_out)
         dw_pre = torch.empty(H, dtype=torch.float32, device=device)
     else:
         r_out = None
     if y is not None:
         y, ld_y = _rows(y, T, H, dtype, dev, "y")
-        dy = y.new_empty((T, H))
+        dy = torch.empty_like(y)
         if w_post is not None:
             dw_post = torch.empty(H, dtype=torch.float32, device=device)
         if kind == 3:
-            dgate = y.new_empty((T, H))
+            dgate = torch.empty_like(y)
         elif kind:
             dgate = torch.empty((T, 1) if kind == 1 else (H,), dtype=torch.float32, device=device)
     args = _NORM.pack(T, H, code, rcode, wcode, kind, scale, eps, offset, 0, 0, ld_y, ld_gate, ld_r, 0, ld_dr, ld_dh,
@@ -359,7 +359,7 @@ def _distill(stream, logits, t_ids, t_logits, temperature, scale, t_lse, weight,
     if mode & 2:
         weight = _vec(weight, T, (torch.float32,), dev, "weight")
         if out is None:
-            out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+            out = torch.empty_like(logits)
         else:
             o, ld_out = _rows(out, T, V, logits.dtype, dev, "out")
             if o is not out or (out is given and logits is not given):
