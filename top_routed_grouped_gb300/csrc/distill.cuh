@@ -36,6 +36,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -115,19 +116,39 @@ __device__ inline DsStat ds_join(const DsStat *p, float k) {
   return {m, s};
 }
 
-// Elements n.. of the 2 N elements of (lo, hi), sh = n sizeof(T) bytes.
+// Bytes 2 H .. 2 H + 15 of the 32 bytes of (lo, hi).
+template <int H>
+__device__ inline uint4 ds_funnel(const uint4 &lo, const uint4 &hi) {
+  constexpr int W = H / 2;
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = H % 2 ? __funnelshift_r(w[W + i], w[W + i + 1], 16) : w[W + i];
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// f<H>() for a shift of 2 H bytes below 16 that is the same for all.
+template <typename T, typename F>
+__device__ inline void ds_by_shift(int off, F f) {
+  switch (off * (int)sizeof(T) / 2) {
+    case 0: f(std::integral_constant<int, 0>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 4: f(std::integral_constant<int, 4>()); break;
+    case 6: f(std::integral_constant<int, 6>()); break;
+    default:
+      if constexpr (sizeof(T) == 2) {
+        switch (off) {
+          case 1: f(std::integral_constant<int, 1>()); break;
+          case 3: f(std::integral_constant<int, 3>()); break;
+          case 5: f(std::integral_constant<int, 5>()); break;
+          default: f(std::integral_constant<int, 7>()); break;
+        }
+      }
+  }
+}
 __device__ inline uint4 ds_funnel(const uint4 &lo, const uint4 &hi, int sh) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (sh & 8)
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  if (sh & 4)
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  if (sh & 2)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  uint4 r = lo;
+  ds_by_shift<uint16_t>(sh / 2, [&](auto h) { r = ds_funnel<h.value>(lo, hi); });
+  return r;
 }
 
 // Units of a row: unit u holds elements u N .. u N + N - 1.  A row may start
@@ -466,6 +487,54 @@ __device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, bool 
   }
 }
 
+// The same by aligned pieces of the row, where the gradient's row starts like
+// the logits' between 16-byte boundaries (`off` elements past one): piece c of
+// the one is written from piece c of the other, nothing is shifted.  load(j)
+// gives piece c0 + j step.
+template <typename T, bool LOSS, int U, typename Load, typename Half>
+__device__ inline void ds_dense_pieces(const T *z, T *dz, int off, int V, int c0, int step, bool zero, DsGrad<LOSS> grad,
+                                       Load load, Half half) {
+  constexpr int N = DsUnit<T>::N;
+  auto unit = [&](const uint4 &raw) {
+    float v[N];
+    Vec16<T>::unpack(raw, v);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) grad(v[i], v[i + 1]);
+    uint4 o;
+    Vec16<T>::store((T *)&o, v);
+    return o;
+  };
+  uint4 *out = (uint4 *)(dz - off) + c0;
+  const bool inner = __all_sync(FULL_MASK, DsUnit<T>::piece_in(off, c0, V) && DsUnit<T>::piece_in(off, c0 + (U - 1) * step, V));
+  if (!zero && inner && !(LOSS && grad.power.far)) {
+    grad.power.far = false;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      __stcs(out + j * step, unit(load(j)));
+      if (j == U / 2 - 1) half();
+    }
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < U; ++j) {
+      const int c = c0 + j * step;
+      if (DsUnit<T>::piece_in(off, c, V)) {
+        __stcs(out + j * step, zero ? uint4{} : unit(load(j)));
+      } else {
+#pragma unroll 1
+        for (int e = max(c * N - off, 0); e < min((c + 1) * N - off, V); ++e) {
+          float u = 0.f, v = 0.f;
+          if (!zero) {
+            u = Elem<T>::load(z + e);
+            grad(u, v);
+          }
+          dz[e] = Elem<T>::from_f32(u);
+        }
+      }
+      if (j == U / 2 - 1) half();
+    }
+  }
+}
+
 struct DsShared {
   DsSlots slots[DS_RING];
   __align__(16) DsStat warp[DS_RING][16];
@@ -492,7 +561,10 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = 1 << shift;
   const int rank = blockIdx.x & (ctas - 1), stride = gridDim.x >> shift;
   const float k = a.inv_tau * DS_LOG2E;
-  const int u_first = rank * SPAN, lo = u_first * N, hi = lo + SPAN * N;  // units, elements of this CTA
+  const int u_first = rank * SPAN;  // units, or aligned pieces, of this CTA
+  // Where the gradient's row starts like the logits', a CTA writes pieces, else units.
+  auto by_pieces = [&](const T *z, const T *dz) { return !ALIGNED && ds_offset(z) == ds_offset(dz); };
+  auto first_of = [&](const T *z, const T *dz) { return u_first * N - (by_pieces(z, dz) ? ds_offset(z) : 0); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < DS_RING; ++i) {
@@ -517,6 +589,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
   const int64_t t0 = blockIdx.x >> shift;
   const int rows = t0 < a.T ? (int)((a.T - 1 - t0) / stride) + 1 : 0;  // of this cluster
   auto row_of = [&](int j) { return (const T *)a.logits + (t0 + (int64_t)j * stride) * a.ld_logits; };
+  auto out_of = [&](int j) { return (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits; };
   auto wait = [&](uint64_t *bar, int phase) { return mbar_wait(bar, phase & 1, &sh.abort_flag, status); };
 
   // Rows that have no gradient and whose loss is 0 or not asked for are not read.
@@ -606,6 +679,8 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const int round = j / DS_RING;
       const int64_t t = t0 + (int64_t)j * stride;
       const T *z = row_of(j);
+      T *dz = out_of(j);
+      const int lo = first_of(z, dz), hi = lo + SPAN * N;  // elements of this CTA
       bool found = false;
       T zk[SL];
 #pragma unroll
@@ -644,7 +719,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       if (GRAD) {
         if (!wait(&sh.empty[r][1], round)) return;
         if (sl.mul != 0.f)
-          ds_places<T, LOSS>(a, sl, (T *)a.dlogits + t * a.ld_dlogits, lo, hi, sl.w,
+          ds_places<T, LOSS>(a, sl, dz, lo, hi, sl.w,
                              DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), lane, 32);
       }
       __syncwarp();
@@ -680,6 +755,13 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
     // ------------------------------------------------------------ consumers
     constexpr int STEP = W * 32;
     const int u0 = u_first + threadIdx.x;
+    auto release = [&](int r) {
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.empty[r][0]);
+        mbar_arrive(&sh.empty[r][1]);
+      }
+    };
     // Statistics of row j.
     auto statistics = [&](int j) {
       const int r = j % DS_RING;
@@ -691,21 +773,27 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         const int off = ALIGNED ? 0 : ds_offset(z);
         uint4 raw[U];
         if (DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V)) {
+          if (ALIGNED) {
 #pragma unroll
-          for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load_inner<ALIGNED>(slice + i * STEP, off);
+            for (int i = 0; i < U; ++i) raw[i] = slice[i * STEP];
+          } else {
+            ds_by_shift<T>(off, [&](auto h) {
+#pragma unroll
+              for (int i = 0; i < U; ++i) raw[i] = ds_funnel<h.value>(slice[i * STEP], slice[i * STEP + (h.value ? 1 : 0)]);
+            });
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
         }
+        if (!GRAD) release(r);  // the slice is in registers
         mine = ds_warp_join(ds_units_stat<T, U>(raw, k), k);
+      } else if (!GRAD) {
+        release(r);
       }
       if (lane == 0) {
         sh.warp[r][warp] = mine;
         mbar_arrive(&sh.taken[r]);
-        if (!GRAD) {
-          mbar_arrive(&sh.empty[r][0]);
-          mbar_arrive(&sh.empty[r][1]);
-        }
       }
       return true;
     };
@@ -718,15 +806,23 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const T *z = row_of(j);
       const uint4 *slice = slices + r * (SPAN + 1) + threadIdx.x;
       const int off = ALIGNED ? 0 : ds_offset(z);
-      T *dz = (T *)a.dlogits + (t0 + (int64_t)j * stride) * a.ld_dlogits;
-      const bool inner = DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V);
-      ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, sl.mul == 0.f, inner, DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), [&](int i, bool in) {
-        if (in) return DsUnit<T>::template load_inner<ALIGNED>(slice + i * STEP, off);
-        return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
-      }, [&] {
+      T *dz = out_of(j);
+      const DsGrad<LOSS> grad(sl.m, k, a.inv_tau, sl.mul);
+      const bool zero = sl.mul == 0.f;
+      auto half = [&] {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[r][0]);
-      });
+      };
+      if (by_pieces(z, dz)) {
+        ds_dense_pieces<T, LOSS, U>(z, dz, off, a.V, u0, STEP, zero, grad, [&](int i) { return slice[i * STEP]; }, half);
+      } else {
+        // (rows that start differently go unit by unit)
+        const bool inner = ALIGNED && DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V);
+        ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, zero, inner, grad, [&](int i, bool in) {
+          if (in) return DsUnit<T>::template load_inner<ALIGNED>(slice + i * STEP, off);
+          return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+        }, half);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[r][1]);
       return true;
@@ -759,8 +855,10 @@ distill_plain_kernel(const DistillArgs a, int shift, int groups, int *status) {
   griddep_wait();
   if (LOSS && ctas > 1) cluster_sync();  // all CTAs run
   const T *z = (const T *)a.logits + t * a.ld_logits;
+  T *dz = (T *)a.dlogits + t * a.ld_dlogits;
   const int off = ds_offset(z), u_first = rank * groups * U * THREADS;
-  const int lo = u_first * N, hi = lo + groups * U * THREADS * N;
+  const bool by_pieces = off != 0 && off == ds_offset(dz);
+  const int lo = u_first * N - (by_pieces ? off : 0), hi = lo + groups * U * THREADS * N;
   auto piece = [&](int u) { return (const uint4 *)(z - off) + u; };
   // The first group's units are on their way while the teacher is worked out.
   uint4 raw[U];
@@ -823,11 +921,14 @@ distill_plain_kernel(const DistillArgs a, int shift, int groups, int *status) {
     st = {sl.lse, 1.f};
   }
   if (!GRAD) return;
-  T *dz = (T *)a.dlogits + t * a.ld_dlogits;
   const bool zero = !sl.any || sl.w == 0.f || (LOSS ? ds_none(st) : sl.lse == ds_neg_inf());
   const DsGrad<LOSS> grad(st.m, k, a.inv_tau, sl.w * sl.total / st.s);
   for (int g = 0; g < groups; ++g) {
     const int u0 = u_first + g * U * THREADS + threadIdx.x;
+    if (by_pieces) {
+      ds_dense_pieces<T, LOSS, U>(z, dz, off, a.V, u0, THREADS, zero, grad, [&](int i) { return *piece(u0 + i * THREADS); }, [] {});
+      continue;
+    }
     if (!zero && (!LOSS || groups > 1)) load(g);
     ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, inner, grad, [&](int i, bool in) {
       if (in) return raw[i];
@@ -839,7 +940,7 @@ distill_plain_kernel(const DistillArgs a, int shift, int groups, int *status) {
 }
 
 // ---------------------------------------------------------------- host
-template <typename T, int MODE, int THREADS, int U>
+template <typename T, bool ALIGNED, int MODE, int THREADS, int U>
 static cudaError_t ds_launch_plain(const DistillArgs &a, int shift, int *status, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T << shift);
@@ -854,7 +955,8 @@ static cudaError_t ds_launch_plain(const DistillArgs &a, int shift, int *status,
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = shift ? 2 : 1;
-  const int groups = (int)ceil_div(ceil_div(a.V, 16 / (int)sizeof(T)), (int64_t)(THREADS * U) << shift);
+  // (a row that starts between boundaries has one piece more than units)
+  const int groups = (int)ceil_div(ceil_div(a.V, 16 / (int)sizeof(T)) + (ALIGNED ? 0 : 1), (int64_t)(THREADS * U) << shift);
   return cudaLaunchKernelEx(&cfg, distill_plain_kernel<T, MODE, THREADS, U>, a, shift, groups, status);
 }
 
@@ -899,15 +1001,16 @@ static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaS
   return cudaLaunchKernelEx(&cfg, kernel, a, shift, status);
 }
 
-// The shape of a launch, by the row's 16-byte units alone.
+// The shape of a launch, by the row's 16-byte units (or pieces: one more where
+// rows start between boundaries) alone.
 template <typename T, bool ALIGNED, int MODE>
 static cudaError_t ds_shape(const DistillArgs &a, int *status, cudaStream_t stream) {
-  const int64_t n = ceil_div(a.V, 16 / (int)sizeof(T));
-  if (n <= 1024) return ds_launch_plain<T, MODE, 128, 4>(a, 0, status, stream);
-  if (n <= 2048) return ds_launch_plain<T, MODE, 256, 8>(a, 0, status, stream);
+  const int64_t n = ceil_div(a.V, 16 / (int)sizeof(T)) + (ALIGNED ? 0 : 1);
+  if (n <= 1024) return ds_launch_plain<T, ALIGNED, MODE, 128, 4>(a, 0, status, stream);
+  if (n <= 2048) return ds_launch_plain<T, ALIGNED, MODE, 256, 8>(a, 0, status, stream);
   for (int shift = 0; 1 << shift <= DS_MAX_CTAS; ++shift)
     if (n <= (int64_t)4096 << shift) return ds_launch<T, ALIGNED, MODE, 16, 8>(a, shift, status, stream);
-  return ds_launch_plain<T, MODE, 512, 4>(a, 3, status, stream);
+  return ds_launch_plain<T, ALIGNED, MODE, 512, 4>(a, 3, status, stream);
 }
 
 template <typename T, bool ALIGNED>
