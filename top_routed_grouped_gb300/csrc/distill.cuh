@@ -453,11 +453,12 @@ __device__ inline void ds_places(const DistillArgs &a, const DsSlots &sl, T *dz,
 }
 
 // The dense part of the gradient of U units a thread: load(j, inner) gives
-// unit j, half() is called between the halves of them.  Units inside the row
-// run without a branch between them, so that one's exponentials overlap the
-// next one's loads; the others one after the other.
+// unit j, half() is called between the halves of them.  The first `inner` (U,
+// U - 1 or none) lie in the row for the whole warp and run without a branch
+// between them, so that one's exponentials overlap the next one's loads; the
+// others one after the other.
 template <typename T, bool ALIGNED, bool LOSS, int U, typename Load, typename Half>
-__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, bool inner, DsGrad<LOSS> grad, Load load, Half half) {
+__device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, int inner, DsGrad<LOSS> grad, Load load, Half half) {
   constexpr int N = DsUnit<T>::N;
   const int off = ALIGNED ? 0 : ds_offset(dz);
   auto unit = [&](const uint4 &raw) {
@@ -469,18 +470,26 @@ __device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, bool 
     Vec16<T>::store((T *)&o, v);
     return o;
   };
+  int done = 0;
   if (!zero && inner && !(LOSS && grad.power.far)) {
     grad.power.far = false;  // known to the compiler
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
+    auto fast = [&](int j) {
       const uint4 o = unit(load(j, true));
       if (ALIGNED) __stcs((uint4 *)dz + u0 + j * step, o);
       else DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, o);
       if (j == U / 2 - 1) half();
+    };
+#pragma unroll
+    for (int j = 0; j < U - 1; ++j) fast(j);
+    if (inner == U) {
+      fast(U - 1);
+      return;
     }
-  } else {
+    done = U - 1;
+  }
+  {
 #pragma unroll 1
-    for (int j = 0; j < U; ++j) {
+    for (int j = done; j < U; ++j) {
       DsUnit<T>::template store<ALIGNED>(dz, off, u0 + j * step, V, zero ? uint4{} : unit(load(j, false)));
       if (j == U / 2 - 1) half();
     }
@@ -490,10 +499,10 @@ __device__ inline void ds_dense(T *dz, int V, int u0, int step, bool zero, bool 
 // The same by aligned pieces of the row, where the gradient's row starts like
 // the logits' between 16-byte boundaries (`off` elements past one): piece c of
 // the one is written from piece c of the other, nothing is shifted.  load(j)
-// gives piece c0 + j step.
+// gives piece c0 + j step; pieces from `end` on are not this CTA's.
 template <typename T, bool LOSS, int U, typename Load, typename Half>
-__device__ inline void ds_dense_pieces(const T *z, T *dz, int off, int V, int c0, int step, bool zero, DsGrad<LOSS> grad,
-                                       Load load, Half half) {
+__device__ inline void ds_dense_pieces(const T *z, T *dz, int off, int V, int c0, int step, int end, bool zero,
+                                       DsGrad<LOSS> grad, Load load, Half half) {
   constexpr int N = DsUnit<T>::N;
   auto unit = [&](const uint4 &raw) {
     float v[N];
@@ -505,33 +514,40 @@ __device__ inline void ds_dense_pieces(const T *z, T *dz, int off, int V, int c0
     return o;
   };
   uint4 *out = (uint4 *)(dz - off) + c0;
-  const bool inner = __all_sync(FULL_MASK, DsUnit<T>::piece_in(off, c0, V) && DsUnit<T>::piece_in(off, c0 + (U - 1) * step, V));
-  if (!zero && inner && !(LOSS && grad.power.far)) {
+  auto in = [&](int c) { return DsUnit<T>::piece_in(off, c, V) && c < end; };
+  const bool most = __all_sync(FULL_MASK, in(c0) && in(c0 + (U - 2) * step)), all = __all_sync(FULL_MASK, in(c0 + (U - 1) * step));
+  int done = 0;
+  if (!zero && most && !(LOSS && grad.power.far)) {
     grad.power.far = false;
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
+    auto fast = [&](int j) {
       __stcs(out + j * step, unit(load(j)));
       if (j == U / 2 - 1) half();
+    };
+#pragma unroll
+    for (int j = 0; j < U - 1; ++j) fast(j);
+    if (all) {
+      fast(U - 1);
+      return;
     }
-  } else {
+    done = U - 1;
+  }
 #pragma unroll 1
-    for (int j = 0; j < U; ++j) {
-      const int c = c0 + j * step;
-      if (DsUnit<T>::piece_in(off, c, V)) {
-        __stcs(out + j * step, zero ? uint4{} : unit(load(j)));
-      } else {
+  for (int j = done; j < U; ++j) {
+    const int c = c0 + j * step;
+    if (in(c)) {
+      __stcs(out + j * step, zero ? uint4{} : unit(load(j)));
+    } else if (c < end) {
 #pragma unroll 1
-        for (int e = max(c * N - off, 0); e < min((c + 1) * N - off, V); ++e) {
-          float u = 0.f, v = 0.f;
-          if (!zero) {
-            u = Elem<T>::load(z + e);
-            grad(u, v);
-          }
-          dz[e] = Elem<T>::from_f32(u);
+      for (int e = max(c * N - off, 0); e < min((c + 1) * N - off, V); ++e) {
+        float u = 0.f, v = 0.f;
+        if (!zero) {
+          u = Elem<T>::load(z + e);
+          grad(u, v);
         }
+        dz[e] = Elem<T>::from_f32(u);
       }
-      if (j == U / 2 - 1) half();
     }
+    if (j == U / 2 - 1) half();
   }
 }
 
@@ -548,20 +564,23 @@ struct DsShared {
   int abort_flag;
 };
 
-// W: consumer warps; U: units a thread; 1 << shift: CTAs of a cluster.
+// U: units a thread; 1 << shift: CTAs of a cluster; span: units of a CTA, above
+// (U - 1) 32 DS_WARPS and up to U 32 DS_WARPS.
 // ALIGNED: all rows start on 16-byte boundaries.
-template <typename T, bool ALIGNED, int MODE, int W, int U>
-__global__ void __launch_bounds__(32 * (W + 2 + DS_RING), 1)
-distill_kernel(const DistillArgs a, int shift, int *status) {
+constexpr int DS_WARPS = 16;  // consumers
+template <typename T, bool ALIGNED, int MODE, int U>
+__global__ void __launch_bounds__(32 * (DS_WARPS + 2 + DS_RING), 1)
+distill_kernel(const DistillArgs a, int shift, int span, int *status) {
   using namespace umma;
-  constexpr int N = DsUnit<T>::N, SPAN = U * W * 32;
+  constexpr int N = DsUnit<T>::N, W = DS_WARPS, SPAN = U * W * 32;
   constexpr bool LOSS = (MODE & DISTILL_LOSS) != 0, GRAD = (MODE & DISTILL_GRAD) != 0;
   extern __shared__ __align__(128) uint4 slices[];  // DS_RING x (SPAN + 1) aligned pieces
   __shared__ DsShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = 1 << shift;
   const int rank = blockIdx.x & (ctas - 1), stride = gridDim.x >> shift;
   const float k = a.inv_tau * DS_LOG2E;
-  const int u_first = rank * SPAN;  // units, or aligned pieces, of this CTA
+  const int u_first = rank * span;  // units, or aligned pieces, of this CTA: span from here
+  const int V = min(a.V, (u_first + span) * N);  // where its units end
   // Where the gradient's row starts like the logits', a CTA writes pieces, else units.
   auto by_pieces = [&](const T *z, const T *dz) { return !ALIGNED && ds_offset(z) == ds_offset(dz); };
   auto first_of = [&](const T *z, const T *dz) { return u_first * N - (by_pieces(z, dz) ? ds_offset(z) : 0); };
@@ -637,8 +656,9 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         if (!wait(&sh.empty[r][h], round + 1)) return false;
         if (lane == 0) {
           if (h == 1) sh.read[r] = read;
-          const int from = u_first + (h ? SPAN / 2 : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
-          const int to = min(u_first + (h ? SPAN + (off ? 1 : 0) : SPAN / 2), last);
+          constexpr int HALF = U / 2 * W * 32;
+          const int from = u_first + (h ? HALF : 0) + (off && u_first == 0 && h == 0 ? 1 : 0);
+          const int to = min(u_first + (h ? span + (off ? 1 : 0) : HALF), last);
           if (to > from) {
             mbar_arrive_expect_tx(&sh.full[r], (uint32_t)(to - from) * 16);
             bulk_load(slice + (from - u_first), z - off + (int64_t)from * N, (uint32_t)(to - from) * 16, &sh.full[r]);
@@ -680,7 +700,7 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
       const int64_t t = t0 + (int64_t)j * stride;
       const T *z = row_of(j);
       T *dz = out_of(j);
-      const int lo = first_of(z, dz), hi = lo + SPAN * N;  // elements of this CTA
+      const int lo = first_of(z, dz), hi = lo + span * N;  // elements of this CTA
       bool found = false;
       T zk[SL];
 #pragma unroll
@@ -772,19 +792,25 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         const T *z = row_of(j);
         const int off = ALIGNED ? 0 : ds_offset(z);
         uint4 raw[U];
-        if (DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V)) {
+        if (DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U - 1, V)) {
+          // (the last unit may be past the CTA's end; its pieces are in the slice all the same)
+          const bool all = (int64_t)(u0 + (U - 1) * STEP + 1) * N <= V && (ALIGNED || DsUnit<T>::piece_in(off, u0 + (U - 1) * STEP + 1, a.V));
           if (ALIGNED) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) raw[i] = slice[i * STEP];
+            for (int i = 0; i < U - 1; ++i) raw[i] = slice[i * STEP];
+            if (all) raw[U - 1] = slice[(U - 1) * STEP];
           } else {
             ds_by_shift<T>(off, [&](auto h) {
+              auto get = [&](int i) { return ds_funnel<h.value>(slice[i * STEP], slice[i * STEP + (h.value ? 1 : 0)]); };
 #pragma unroll
-              for (int i = 0; i < U; ++i) raw[i] = ds_funnel<h.value>(slice[i * STEP], slice[i * STEP + (h.value ? 1 : 0)]);
+              for (int i = 0; i < U - 1; ++i) raw[i] = get(i);
+              if (all) raw[U - 1] = get(U - 1);
             });
           }
+          if (!all) raw[U - 1] = DsUnit<T>::template load<ALIGNED>(slice + (U - 1) * STEP, z, off, u0 + (U - 1) * STEP, V);
         } else {
 #pragma unroll
-          for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+          for (int i = 0; i < U; ++i) raw[i] = DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, V);
         }
         if (!GRAD) release(r);  // the slice is in registers
         mine = ds_warp_join(ds_units_stat<T, U>(raw, k), k);
@@ -814,13 +840,15 @@ distill_kernel(const DistillArgs a, int shift, int *status) {
         if (lane == 0) mbar_arrive(&sh.empty[r][0]);
       };
       if (by_pieces(z, dz)) {
-        ds_dense_pieces<T, LOSS, U>(z, dz, off, a.V, u0, STEP, zero, grad, [&](int i) { return slice[i * STEP]; }, half);
+        ds_dense_pieces<T, LOSS, U>(z, dz, off, a.V, u0, STEP, u_first + span, zero, grad, [&](int i) { return slice[i * STEP]; }, half);
       } else {
         // (rows that start differently go unit by unit)
-        const bool inner = ALIGNED && DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, a.V);
-        ds_dense<T, ALIGNED, LOSS, U>(dz, a.V, u0, STEP, zero, inner, grad, [&](int i, bool in) {
+        int inner = 0;
+        if (ALIGNED && DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U - 1, V))
+          inner = DsUnit<T>::template inner<ALIGNED>(off, u0, STEP, U, V) ? U : U - 1;
+        ds_dense<T, ALIGNED, LOSS, U>(dz, V, u0, STEP, zero, inner, grad, [&](int i, bool in) {
           if (in) return DsUnit<T>::template load_inner<ALIGNED>(slice + i * STEP, off);
-          return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, a.V);
+          return DsUnit<T>::template load<ALIGNED>(slice + i * STEP, z, off, u0 + i * STEP, V);
         }, half);
       }
       __syncwarp();
@@ -926,11 +954,11 @@ distill_plain_kernel(const DistillArgs a, int shift, int groups, int *status) {
   for (int g = 0; g < groups; ++g) {
     const int u0 = u_first + g * U * THREADS + threadIdx.x;
     if (by_pieces) {
-      ds_dense_pieces<T, LOSS, U>(z, dz, off, a.V, u0, THREADS, zero, grad, [&](int i) { return *piece(u0 + i * THREADS); }, [] {});
+      ds_dense_pieces<T, LOSS, U>(z, dz, off, a.V, u0, THREADS, u_first + groups * U * THREADS, zero, grad, [&](int i) { return *piece(u0 + i * THREADS); }, [] {});
       continue;
     }
     if (!zero && (!LOSS || groups > 1)) load(g);
-    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, inner, grad, [&](int i, bool in) {
+    ds_dense<T, false, LOSS, U>(dz, a.V, u0, THREADS, zero, inner ? U : 0, grad, [&](int i, bool in) {
       if (in) return raw[i];
       return DsUnit<T>::template load<false>(piece(u0 + i * THREADS), z, off, u0 + i * THREADS, a.V);
     }, [] {});
@@ -960,9 +988,10 @@ static cudaError_t ds_launch_plain(const DistillArgs &a, int shift, int *status,
   return cudaLaunchKernelEx(&cfg, distill_plain_kernel<T, MODE, THREADS, U>, a, shift, groups, status);
 }
 
-template <typename T, bool ALIGNED, int MODE, int W, int U>
-static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaStream_t stream) {
-  const auto kernel = distill_kernel<T, ALIGNED, MODE, W, U>;
+template <typename T, bool ALIGNED, int MODE, int U>
+static cudaError_t ds_launch(const DistillArgs &a, int shift, int span, int *status, cudaStream_t stream) {
+  constexpr int W = DS_WARPS;
+  const auto kernel = distill_kernel<T, ALIGNED, MODE, U>;
   const int smem = DS_RING * (U * W * 32 + 1) * 16;
   cudaError_t e = ensure_smem((const void *)kernel, smem);
   if (e != cudaSuccess) return e;
@@ -998,7 +1027,7 @@ static cudaError_t ds_launch(const DistillArgs &a, int shift, int *status, cudaS
   }
   cfg.gridDim = dim3((unsigned)std::min(a.T, clusters) << shift);
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, shift, status);
+  return cudaLaunchKernelEx(&cfg, kernel, a, shift, span, status);
 }
 
 // The shape of a launch, by the row's 16-byte units (or pieces: one more where
@@ -1008,24 +1037,26 @@ static cudaError_t ds_shape(const DistillArgs &a, int *status, cudaStream_t stre
   const int64_t n = ceil_div(a.V, 16 / (int)sizeof(T)) + (ALIGNED ? 0 : 1);
   if (n <= 1024) return ds_launch_plain<T, ALIGNED, MODE, 128, 4>(a, 0, status, stream);
   if (n <= 2048) return ds_launch_plain<T, ALIGNED, MODE, 256, 8>(a, 0, status, stream);
+  // As few CTAs as hold the row in slices of 4096 units, alike in size.
   for (int shift = 0; 1 << shift <= DS_MAX_CTAS; ++shift)
-    if (n <= (int64_t)4096 << shift) return ds_launch<T, ALIGNED, MODE, 16, 8>(a, shift, status, stream);
+    if (n <= (int64_t)4096 << shift) {
+      const int span = (int)ceil_div(n, 1 << shift);
+      switch (ceil_div(span, DS_WARPS * 32)) {
+        case 8: return ds_launch<T, ALIGNED, MODE, 8>(a, shift, span, status, stream);
+        case 7: return ds_launch<T, ALIGNED, MODE, 7>(a, shift, span, status, stream);
+        case 6: return ds_launch<T, ALIGNED, MODE, 6>(a, shift, span, status, stream);
+        default: return ds_launch<T, ALIGNED, MODE, 5>(a, shift, span, status, stream);
+      }
+    }
   return ds_launch_plain<T, ALIGNED, MODE, 512, 4>(a, 3, status, stream);
 }
 
 template <typename T, bool ALIGNED>
-static cudaError_t ds_mode(const DistillArgs &a, int mode, int *status, cudaStream_t stream) {
+cudaError_t ds_mode(const DistillArgs &a, int mode, int *status, cudaStream_t stream) {
   if (mode == DISTILL_LOSS) return ds_shape<T, ALIGNED, DISTILL_LOSS>(a, status, stream);
   if (mode == DISTILL_GRAD) return ds_shape<T, ALIGNED, DISTILL_GRAD>(a, status, stream);
   return ds_shape<T, ALIGNED, DISTILL_LOSS | DISTILL_GRAD>(a, status, stream);
 }
 
-template <typename T>
-cudaError_t distill_launch(const DistillArgs &a, int mode, int *status, cudaStream_t stream) {
-  constexpr int N = 16 / (int)sizeof(T);
-  bool aligned = (uintptr_t)a.logits % 16 == 0 && a.ld_logits % N == 0;
-  if (mode & DISTILL_GRAD) aligned = aligned && (uintptr_t)a.dlogits % 16 == 0 && a.ld_dlogits % N == 0;
-  return aligned ? ds_mode<T, true>(a, mode, status, stream) : ds_mode<T, false>(a, mode, status, stream);
-}
 
 }  // namespace moe

@@ -3,6 +3,6 @@
 
 namespace moe {
 
-template cudaError_t distill_launch<float>(const DistillArgs &, int, int *, cudaStream_t);
+template cudaError_t ds_mode<float, true>(const DistillArgs &, int, int *, cudaStream_t);
 
 }  // namespace moe
