@@ -694,15 +694,14 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       if (GRAD) w = a.weight[t];
       if (!LOSS) lse = a.lse[t];
     };
-    fetch(r);
-    for (int j = r; j < rows; j += DS_RING) {
-      const int round = j / DS_RING;
-      const int64_t t = t0 + (int64_t)j * stride;
+    // The student's logits at the slots of row j go on their way as well.
+    bool any = false;
+    T zk[SL];
+    auto gather = [&](int j) {
+      if (j >= rows) return;
       const T *z = row_of(j);
-      T *dz = out_of(j);
-      const int lo = first_of(z, dz), hi = lo + span * N;  // elements of this CTA
+      const int lo = first_of(z, out_of(j)), hi = lo + span * N;
       bool found = false;
-      T zk[SL];
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         if (32 * i >= a.K) break;
@@ -713,7 +712,16 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
         if (id[i] >= 0 && (LOSS || (id[i] >= lo && id[i] < hi))) zk[i] = z[id[i]];
         else zk[i] = T(0.f);
       }
-      const bool any = __any_sync(FULL_MASK, found);
+      any = __any_sync(FULL_MASK, found);
+    };
+    fetch(r);
+    gather(r);
+    for (int j = r; j < rows; j += DS_RING) {
+      const int round = j / DS_RING;
+      const int64_t t = t0 + (int64_t)j * stride;
+      const T *z = row_of(j);
+      T *dz = out_of(j);
+      const int lo = first_of(z, dz), hi = lo + span * N;  // elements of this CTA
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
         if (32 * i >= a.K) break;
@@ -734,6 +742,7 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       ds_teacher(a, t, sl, sh.marks[r]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[r]);
+      gather(j + DS_RING);
       if (!wait(&sh.go[r], round)) return;
       if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s}, k);
       if (GRAD) {
@@ -1036,7 +1045,11 @@ template <typename T, bool ALIGNED, int MODE>
 static cudaError_t ds_shape(const DistillArgs &a, int *status, cudaStream_t stream) {
   const int64_t n = ceil_div(a.V, 16 / (int)sizeof(T)) + (ALIGNED ? 0 : 1);
   if (n <= 1024) return ds_launch_plain<T, ALIGNED, MODE, 128, 4>(a, 0, status, stream);
-  if (n <= 2048) return ds_launch_plain<T, ALIGNED, MODE, 256, 8>(a, 0, status, stream);
+  // Up to 2048 units the two kernels are near one another (us, this one / the
+  // plain one, 16384 rows: step at V = 16000 248 / 239 and at 12000 236 / 260,
+  // gradient 156 / 281, loss 125 / 195; between boundaries, V = 16001: step
+  // 418 / 381, loss 262 / 227, gradient 188 / 260).
+  if (!ALIGNED && n <= 2048 && (MODE & DISTILL_LOSS)) return ds_launch_plain<T, ALIGNED, MODE, 256, 8>(a, 0, status, stream);
   // As few CTAs as hold the row in slices of 4096 units, alike in size.
   for (int shift = 0; 1 << shift <= DS_MAX_CTAS; ++shift)
     if (n <= (int64_t)4096 << shift) {
@@ -1045,7 +1058,9 @@ static cudaError_t ds_shape(const DistillArgs &a, int *status, cudaStream_t stre
         case 8: return ds_launch<T, ALIGNED, MODE, 8>(a, shift, span, status, stream);
         case 7: return ds_launch<T, ALIGNED, MODE, 7>(a, shift, span, status, stream);
         case 6: return ds_launch<T, ALIGNED, MODE, 6>(a, shift, span, status, stream);
-        default: return ds_launch<T, ALIGNED, MODE, 5>(a, shift, span, status, stream);
+        case 5: return ds_launch<T, ALIGNED, MODE, 5>(a, shift, span, status, stream);
+        case 4: return ds_launch<T, ALIGNED, MODE, 4>(a, shift, span, status, stream);
+        default: return ds_launch<T, ALIGNED, MODE, 3>(a, shift, span, status, stream);
       }
     }
   return ds_launch_plain<T, ALIGNED, MODE, 512, 4>(a, 3, status, stream);
