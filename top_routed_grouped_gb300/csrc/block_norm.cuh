@@ -24,6 +24,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -173,33 +174,72 @@ struct BnRow {
   }
 };
 
-// Sums of N values over the threads of a row, in a fixed order; all get them.
-// Consecutive calls alternate between two buffers: the barrier of one call
-// tells that the buffer of the call before it has been read.
+// Sums of N values (at most 8) over the threads of a row, in a fixed order; all
+// get them.  A warp halves the number of values that a lane holds as it halves
+// the lanes that a value is spread over; the sums of several warps meet in
+// `buf`, where a quarter of a value's slots goes to each of four lanes (slots
+// past the last warp hold zeros).  Consecutive calls alternate between two
+// buffers: the barrier of one call tells that the buffer of the call before it
+// has been read.
 template <int N>
 __device__ inline void bn_row_sum(float (&v)[N], int group, float (*buf)[16]) {
-  const int top = group < 32 ? group : 32;
-  for (int d = top >> 1; d; d >>= 1)
+  static_assert(N <= 8, "a value's quarter for each lane");
+  const int lane = threadIdx.x & 31;
+  if (group < 32) {
+    for (int d = group >> 1; d; d >>= 1)
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(FULL_MASK, v[n], d);
-  if (group > 32) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = group >> 5;
-    if (lane == 0)
-#pragma unroll
-      for (int n = 0; n < N; ++n) buf[n][warp] = v[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = 0.f;
-    for (int w = 0; w < warps; w += 4)  // (slots past the last warp hold zeros)
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float4 f = *(const float4 *)&buf[n][w];
-        v[n] += f.x;
-        v[n] += f.y;
-        v[n] += f.z;
-        v[n] += f.w;
-      }
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(FULL_MASK, v[n], d);
+    return;
   }
+  constexpr int H1 = (N + 1) / 2, H2 = (H1 + 1) / 2, H3 = (H2 + 1) / 2;
+  float x[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) x[n] = v[n];
+  auto halve = [&](auto count, auto half, int d) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int i = 0; i < half.value; ++i) {
+      if (i + half.value < count.value) {
+        const float send = upper ? x[i] : x[i + half.value], keep = upper ? x[i + half.value] : x[i];
+        x[i] = keep + __shfl_xor_sync(FULL_MASK, send, d);
+      } else {  // no partner: a plain sum, which both sides hold
+        x[i] += __shfl_xor_sync(FULL_MASK, x[i], d);
+      }
+    }
+  };
+  halve(std::integral_constant<int, N>(), std::integral_constant<int, H1>(), 16);
+  halve(std::integral_constant<int, H1>(), std::integral_constant<int, H2>(), 8);
+  halve(std::integral_constant<int, H2>(), std::integral_constant<int, H3>(), 4);
+  x[0] += __shfl_xor_sync(FULL_MASK, x[0], 2);
+  x[0] += __shfl_xor_sync(FULL_MASK, x[0], 1);
+  // The lane that holds value n.
+  auto holder = [](int n) {
+    int l = 0;
+    if (N > 1 && n >= H1) n -= H1, l |= 16;
+    if (H1 > 1 && n >= H2) n -= H2, l |= 8;
+    if (H2 > 1 && n >= H3) n -= H3, l |= 4;
+    return l;
+  };
+  if (group == 32) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = __shfl_sync(FULL_MASK, x[0], holder(n));
+    return;
+  }
+  // (a lane without a value of its own holds a copy of another one's)
+  const int warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (lane == holder(n)) buf[n][warp] = x[0];
+  __syncthreads();
+  float s = 0.f;
+  if (lane < 4 * N) {
+    const float4 f = *(const float4 *)&buf[lane >> 2][4 * (lane & 3)];
+    s = (f.x + f.y) + (f.z + f.w);
+  }
+  s += __shfl_xor_sync(FULL_MASK, s, 1);
+  s += __shfl_xor_sync(FULL_MASK, s, 2);
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = __shfl_sync(FULL_MASK, s, 4 * n);
 }
 
 // A CTA's walk over its blocks of rows, with stages (BULK) or without.
