@@ -8,8 +8,8 @@ namespace moe {
 extern template cudaError_t bn_dispatch<float, float>(const BnLaunch &);
 extern template cudaError_t bn_dispatch<__nv_bfloat16, float>(const BnLaunch &);
 
-// out[i] = sum over the groups of part[.][i], in a fixed order: 32 threads of
-// a column take every 32nd group, then a tree.
+// out[i] = sum over the CTAs (`groups`) of part[.][i], in a fixed order: 32
+// threads of a column take every 32nd, then a tree.
 __global__ void __launch_bounds__(1024) block_norm_join_kernel(const float *part, int64_t groups, int H, float *o0,
                                                                float *o1, float *o2) {
   __shared__ float buf[32][33];

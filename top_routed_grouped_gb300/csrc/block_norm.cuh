@@ -20,7 +20,8 @@
 // y with u = scale gate dr in place of dh.  The row's first round of sums
 // (v^2, g v, y^2) gives dr, the second (u w y) gives dy.  The gradients of
 // the weights are sums over rows: each group keeps those of its own rows in
-// registers, writes them once, and a second kernel adds the groups in order.
+// registers, a CTA writes those of its groups once, and a second kernel adds the
+// CTAs in order.
 #pragma once
 
 #include <algorithm>
@@ -425,8 +426,8 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
   }
 }
 
-// part: [3][groups][H] sums over a group's rows of what dw_pre, dw_post and a
-// channel gate's gradient are made of (only those that the call asks for).
+// part: [3][CTAs][H] sums over a CTA's rows of what dw_pre, dw_post and a channel
+// gate's gradient are made of (only those that the call asks for).
 template <typename TE, typename TR, int VEC, int CH, int R, bool BULK, bool FULL>
 __global__ void __launch_bounds__(BN_MAX_THREADS)
 block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *part, int *status) {
@@ -568,11 +569,47 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
     dy_out.move();
     dg_out.move();
   }
-  const int64_t groups = (int64_t)gridDim.x * per_cta;
-  float *p = part + ((int64_t)blockIdx.x * per_cta + sub) * a.H;
-  if (a.dw_pre) io.store(p, dw_pre);
-  if (a.dw_post) io.store(p + groups * a.H, dw_post);
-  if (a.gate_kind == MOE_GATE_CHANNEL) io.store(p + 2 * groups * a.H, dgate);
+  // The groups of a CTA as one: lanes, then warps, in a fixed order.
+  float *p = part + (int64_t)blockIdx.x * a.H;
+  const int64_t apart = (int64_t)gridDim.x * a.H;
+  auto leave = [&](F2 (&x)[NP], float *out) {
+    if (NP <= 4 && per_cta > 1) {
+      const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+      float *red = (float *)bn_smem;  // [warps][H]: the stages are done with
+      for (int d = group; d < 32; d <<= 1) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          float u, v;
+          x[q].get(u, v);
+          u += __shfl_xor_sync(FULL_MASK, u, d);
+          v += __shfl_xor_sync(FULL_MASK, v, d);
+          x[q] = F2(u, v);
+        }
+      }
+      __syncthreads();
+      if ((threadIdx.x & 31) < group) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          float u, v;
+          x[q].get(u, v);
+          const int i = ((2 * q) / VEC * group + lane) * VEC + (2 * q) % VEC, k = VEC == 1 ? i + group : i + 1;
+          if (i < a.H) red[warp * a.H + i] = u;
+          if (k < a.H) red[warp * a.H + k] = v;
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
+        float sum = 0.f;
+        for (int w = 0; w < warps; ++w) sum += red[w * a.H + i];
+        out[i] = sum;
+      }
+    } else {
+      io.store(out, x);
+    }
+  };
+  if (a.dw_pre) leave(dw_pre, p);
+  if (a.dw_post) leave(dw_post, p + apart);
+  if (a.gate_kind == MOE_GATE_CHANNEL) leave(dgate, p + 2 * apart);
 }
 
 // ---------------------------------------------------------------- host
@@ -668,7 +705,7 @@ struct BnLaunch {
   float *part;
   int *status;
   cudaStream_t stream;
-  int *groups;  // out: groups that leave partial sums
+  int *groups;  // out: CTAs, each of which leaves partial sums
   bool dry;     // only `groups` is wanted
 };
 
@@ -677,7 +714,7 @@ static cudaError_t bn_go(const BnLaunch &l, const BnShape &s, int ctas, const Bn
   const NormArgs &a = l.a;
   const int per_cta = s.threads / s.group;
   const int grid = (int)std::min<int64_t>(ceil_div(a.T, per_cta * R), (int64_t)device_sms() * ctas);
-  if (l.groups) *l.groups = grid * per_cta;
+  if (l.groups) *l.groups = grid;
   if (l.dry) return cudaSuccess;
   const int smem = BULK ? st.bytes * st.stages : 0;
   auto go = [&](auto kernel, auto... args) {
