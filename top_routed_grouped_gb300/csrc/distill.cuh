@@ -624,7 +624,7 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
     int id[2][SL];
     float x[2][SL], w[2] = {0.f, 0.f};
     auto fetch = [&](int j, int b) {
-      if (j >= rows) return;
+      if (!GRAD || j >= rows) return;  // (without a gradient every row is read)
       const int64_t t = t0 + (int64_t)j * stride;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
@@ -632,7 +632,7 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
         id[b][i] = slot_id(t, i);
         x[b][i] = slot_x(t, i);
       }
-      if (GRAD) w[b] = a.weight[t];
+      w[b] = a.weight[t];
     };
     auto turn = [&](int j, int b) {
       const int r = j % DS_RING, round = j / DS_RING;
@@ -640,7 +640,7 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       bool found = false;
 #pragma unroll
       for (int i = 0; i < SL; ++i) {
-        if (32 * i >= a.K) break;
+        if (!GRAD || 32 * i >= a.K) break;
         found |= counts(id[b][i], x[b][i]);
       }
       const bool read = needed(__any_sync(FULL_MASK, found), w[b]);
@@ -649,8 +649,6 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       const int off = ALIGNED ? 0 : ds_offset(z);
       const int last = read ? (a.V + off) / N : 0;
       uint4 *slice = slices + r * (SPAN + 1);
-      // (with a gradient the consumers cannot be done before the joiner is)
-      if (!GRAD && round > 0 && !wait(&sh.go[r], round - 1)) return false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!wait(&sh.empty[r][h], round + 1)) return false;
@@ -826,6 +824,8 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       } else if (!GRAD) {
         release(r);
       }
+      // (with a gradient the joiner has been done with row j - DS_RING since that was written)
+      if (!GRAD && j >= DS_RING && !wait(&sh.go[r], j / DS_RING - 1)) return false;
       if (lane == 0) {
         sh.warp[r][warp] = mine;
         mbar_arrive(&sh.taken[r]);
