@@ -165,6 +165,20 @@ def test_rows_do_not_depend_on_the_batch(types, H):
     assert all(torch.equal(again[n], g[n]) for n in g)
 
 
+@pytest.mark.parametrize("types,H", [(TYPES[1], 2048), (TYPES[2], 256), (TYPES[0], 333)])
+def test_rows_of_a_large_batch_are_those_of_a_small_one(types, H):
+    """Large batches take several rows at a time: the same bits all the same."""
+    c = make(20001, H, *types, gate="element")
+    full = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    g = moe.block_norm_backward(c["dr_out"], c["dh"], full[0], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    for rows in (slice(0, 3), slice(7777, 7790), slice(20000, 20001)):
+        part = moe.block_norm(c["r"][rows], c["y"][rows], c["w_post"], c["w_pre"], c["gate"][rows])
+        assert torch.equal(part[0], full[0][rows]) and torch.equal(part[1], full[1][rows])
+        p = moe.block_norm_backward(c["dr_out"][rows], c["dh"][rows], full[0][rows], c["y"][rows], c["w_post"],
+                                    c["w_pre"], c["gate"][rows])
+        assert all(torch.equal(p[n], g[n][rows]) for n in ("dr", "dy", "dgate"))
+
+
 def test_gradients_against_differences():
     """Central differences of sum(a r_out + b h) along random directions.  The
     loss is summed in 64 bits; with step 1e-2 the cut-off error is of order

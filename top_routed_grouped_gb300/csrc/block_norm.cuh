@@ -7,12 +7,23 @@
 // and its stores: every input is read once.  CTAs walk over the rows; the
 // inputs of the next few blocks of rows are on their way to shared memory by
 // bulk copies meanwhile.  A row that starts between 16-byte boundaries is
-// copied with the bytes around it, so odd widths move as fast.  A group takes
-// two rows at a time where they are short, so that the rounds of a sum over a row, which are
-// latency, are shared.  Rows too long for two such stages are loaded straight
-// from memory.  A row's statistics
-// are summed in an order set by H and the load width alone, so its outputs do
-// not depend on the other rows.
+// copied with the bytes around it, so odd widths need no loads of their own.
+// A group takes two rows at a time where there are enough of them, so that the
+// rounds of a sum over a row, which are latency, are shared.  Rows too long
+// for two stages are loaded straight from memory.  A row's statistics are
+// summed in an order set by H and the load width alone, so its outputs do not
+// depend on the other rows.
+//
+// What it moves is the floor: 29.6 us for the join of 8192 rows of 2048
+// (bfloat16 beside a float residual) at the measured copy rate, 158 us for the
+// gradient of 32768 rows with an element gate.  Measured: 38.5 us (77 %) and
+// 247 us (64 %).  The join loses its start and its last wave; the gradient is
+// bound by its instructions, some 70 for an element (unpacking, arithmetic in
+// pairs, sums over the row), not by waiting: a block of two rows takes 8600
+// cycles, of which 300 pass at its stage's barrier.  Measured on the way for
+// that gradient: row loads without stages 435 us, stages with one row a group
+// 367, two 308, weights held and pairs 274, no test a load 244; one row a group
+// and five stages 289, three CTAs an SM with fewer registers 307.
 //
 // Backward: with v = r_out, x = v rstd the normed row and g = dh w,
 //   dr = dr_out + rstd g - v c,   c = rstd^3 mean(g v)

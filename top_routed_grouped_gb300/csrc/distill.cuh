@@ -33,6 +33,20 @@
 // An exponent is one fused multiply-add, z k - m k with k = log2(e) / tau, and m k
 // rounded alike wherever it is used; where m k would overflow (rows at the
 // type's lowest value) the difference is taken first.
+//
+// The floor is the logits read once and the gradient written once: 593 us for
+// the step at 8192 x 131072 (bfloat16, an eighth of the rows without teacher)
+// at the measured copy rate, 72 us for the gradient at 4096 x 32000, 9.9 us for
+// the loss at 333 x 50257 in float.  Measured: 597 us (99 %), 81 us (89 %) and
+// 25.6 us (38 %).  Reached for the step from 3528 us (a CTA a row, two passes
+// through L2): rows in the registers of a cluster 1147, roles and a ring of
+// slices 986, teacher and joins in warps of their own 752, statistics handed
+// over by st.async instead of a released arrival 643, a row warp for each row
+// under way 602.  The loss in float on rows of 16 bytes' multiples runs at
+// 91 % (5000 x 50256, 162 us); between boundaries the shifts and the few
+// elements at a row's ends cost twice the time (324 us at 50257).  Ends taken
+// from the copied pieces instead of from memory made every shape slower
+// (414 us there, 627 us for the step): more code in the hot loops.
 #pragma once
 
 #include <algorithm>

@@ -17,6 +17,16 @@
 //   4. the partial rows of such a token are added in order.
 // Tokens left out (outside the table, or the padding token) sort behind the
 // table as token V.  A tile's bounds depend on the number of tokens alone.
+//
+// The gradient's floor is its rows read once and the table written once: 198 us
+// for 65536 tokens into 131072 x 2048, 43.5 us for 4096 float rows into
+// 32000 x 2048.  Measured: 271 us (73 %) and 59 us (73 %), of which the zeroing,
+// at the rate of memory, takes 144 and 40, the sums 80 and 13, the joins 28 and
+// 9; the sort (27 and 13) hides behind the zeroing.  Reached from 5445 us (the
+// permutation's sort twice, a CTA a row of the table): tiles and joins 339,
+// only rows without a token zeroed and longer loads in the sums 314, spans
+// listed and joined by warps 273.  The lookup of 16384 rows of 2048 takes
+// 19 us of which 14 are its floor.
 #include <algorithm>
 
 #include "common.cuh"
