@@ -626,7 +626,7 @@ int moe_embed(const moe_embed_args_t *a, void *stream);
  * moe_embed_backward -- dtable[v] = scale * sum over t with ids[t] = v of
  * dout[t] (plus dtable[v] where `accumulate`), FP32.  The tokens are sorted
  * (stable) and the rows of one token summed in ascending t, in runs of
- * sorted positions whose bounds depend on the ids alone, joined in order: no
+ * sorted positions whose bounds T and the ids alone set, joined in order: no
  * atomics, the same bits every time.  Ids outside [0, V) are left out
  * and recorded (code 5); padding_id is left out.  T = 0 zeroes dtable unless
  * `accumulate`.  Workspace: moe_embed_workspace_size(a) bytes.
