@@ -108,6 +108,32 @@ def test_strided_and_misaligned_rows(shift, pad, types):
     backward_ok(w, window(r_out, 0), 1.0, 0.0)
 
 
+def windows(c, ld, at):
+    """The rows of ``c`` as windows of buffers of NaN: row stride ``ld``, from
+    element ``at`` on, each tensor's buffer ending with its last row."""
+    def window(t):
+        T, H = t.shape
+        buf = torch.full((at + (T - 1) * ld + H,), float("nan"), device="cuda", dtype=t.dtype)
+        w = buf.as_strided((T, H), (ld, 1), at)
+        w.copy_(t)
+        return w
+
+    return dict(c, **{n: window(c[n]) for n in ("r", "y", "gate", "dr_out", "dh")}), window
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 6, 7, 9, 12])
+@pytest.mark.parametrize("types", TYPES[:3], ids=lambda t: "-".join(str(x).split(".")[1] for x in t))
+def test_narrow_rows_at_any_place(types, H):
+    """Rows of a few bytes: several lie in the first and in the last 16 bytes of
+    their buffer, dense at every offset from a 16-byte boundary or strided."""
+    for T in (3, 5, 10, 12, 65, 66, 129, 130, 193):
+        c = make(T, H, *types, gate="element", seed=T)
+        for ld, at in [(H, n) for n in range(8)] + [(H + 1, 0), (H + 1, 1), (H + 2, 3), (H + 5, 0), (H + 5, 7)]:
+            w, window = windows(c, ld, at)
+            r_out, _ = forward_ok(w, types[0], 1.0, 0.0)
+            backward_ok(w, window(r_out), 1.0, 0.0)
+
+
 def test_transposed_and_broadcast_rows_are_taken():
     c = make(16, 48, F32, F32, F32)
     c["y"] = c["y"].t().contiguous().t()

@@ -54,6 +54,7 @@ struct BnStages {
   int n, stages, bytes;  // inputs, stages, bytes of a stage
   int rows;              // of a block
   int runs;              // runs of bytes that it is: 1 (rows behind one another), or its rows
+  int near;              // rows that may start within 16 bytes of an input's start, or end within 16 of its end
   int off[BN_MAX_INPUTS], es[BN_MAX_INPUTS];
   uint32_t row[BN_MAX_INPUTS];    // bytes from row to row in a stage
   uint32_t apart[BN_MAX_INPUTS];  // and in memory (modulo 2^32)
@@ -99,10 +100,11 @@ __device__ inline void bn_start(const BnStages &st, uint8_t *stage, uint64_t *ba
   if (bytes)
     umma::bulk_load(stage + st.off[k] + q * st.row[k] + (p.from - (p.lo & ~(uintptr_t)15)), (const void *)p.from, bytes, bar);
 }
-// What the copies of the first and the last block may have missed (the whole
-// CTA; the caller's barrier follows).
+// What the copies of a block may have missed (the whole CTA; the caller's
+// barrier follows): bytes of the pieces that an input starts or ends in, in
+// which only the first and the last `near` rows lie.
 __device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, int T, int H) {
-  if (t0 > 0 && t0 + st.rows < T) return false;
+  if (t0 >= st.near && t0 + st.rows + st.near <= T) return false;
   bool missed = false;
   for (int k = 0; k < st.n; ++k)
     for (int q = 0; q < st.runs; ++q) {
@@ -692,7 +694,7 @@ constexpr int BN_SMEM = 220 * 1024;  // of an SM, for the stages of its CTAs
 inline bool bn_stages(const NormArgs &a, const BnShape &s, int ctas, int R, BnStages &st) {
   const int per_cta = s.threads / s.group;
   st.rows = per_cta * R;
-  st.runs = 1;
+  st.runs = st.near = 1;
   st.bytes = 0;
   for (int k = 0; k < st.n; ++k)
     if (st.base[k] && st.rows > 1 && st.ld[k] != a.H) st.runs = st.rows;
@@ -703,6 +705,7 @@ inline bool bn_stages(const NormArgs &a, const BnShape &s, int ctas, int R, BnSt
     st.off[k] = st.bytes;
     st.row[k] = st.runs > 1 ? run : a.H * st.es[k];
     st.apart[k] = (uint32_t)(st.ld[k] * st.es[k]);
+    st.near = std::max(st.near, (int)ceil_div(16, st.ld[k] * st.es[k]));
     st.bytes += st.runs * run;
   }
   st.bytes = (int)round_up(st.bytes, 128);
