@@ -134,6 +134,16 @@ def test_narrow_rows_at_any_place(types, H):
             backward_ok(w, window(r_out), 1.0, 0.0)
 
 
+@pytest.mark.parametrize("types,T,H", [(TYPES[0], 9001, 333), (TYPES[1], 9001, 1001), (TYPES[2], 40001, 77)])
+def test_long_walks_from_a_misaligned_start(types, T, H):
+    """The stage of the first block, whose start is filled in by hand, is
+    copied to many times after it."""
+    c = make(T, H, *types, gate="element")
+    w, window = windows(c, H, 1)
+    r_out, _ = forward_ok(w, types[0], 1.0, 0.0)
+    backward_ok(w, window(r_out), 1.0, 0.0)
+
+
 def test_transposed_and_broadcast_rows_are_taken():
     c = make(16, 48, F32, F32, F32)
     c["y"] = c["y"].t().contiguous().t()

@@ -115,6 +115,8 @@ __device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, i
       for (uintptr_t b = p.lo + threadIdx.x; b < p.hi; b += blockDim.x)
         if (b < p.from || b >= p.to) dst[b] = *(const uint8_t *)b;
     }
+  // The stage is copied to again later; without this a copy may pass these writes.
+  if (missed) umma::fence_proxy_async_smem();
   return missed;
 }
 
