@@ -258,6 +258,16 @@ __device__ inline void bn_row_sum(float (&v)[N], int group, float (*buf)[16]) {
   for (int n = 0; n < N; ++n) v[n] = __shfl_sync(FULL_MASK, s, 4 * n);
 }
 
+// A wait ran out and the CTA ends: its copies in flight land first, those of
+// the block in `slot` and of the blocks behind it (or a limit passes for each
+// stage that has none).
+static __device__ __noinline__ void bn_drain(BnBars &bars, int stages, int slot, uint32_t phase) {
+  for (int i = 0; i < stages; ++i) {
+    umma::mbar_drain(&bars.full[slot], phase);
+    if (++slot == stages) slot = 0, phase ^= 1;
+  }
+}
+
 // A CTA's walk over its blocks of rows, with stages (BULK) or without.
 template <bool BULK, int R>
 struct BnWalk {
@@ -288,11 +298,14 @@ struct BnWalk {
       for (int i = 0; i < st.stages; ++i)
         if (t0 + i * step < T) bn_start(st, stages + i * st.bytes, &bars.full[i], t0 + i * step, T, H);
   }
-  // Waits for the block's stage.
+  // Waits for the block's stage; a warp's lanes agree on whether it came.
   __device__ inline bool arrive(int *status) {
     if (!BULK) return true;
     stage = stages + slot * st.bytes;
-    if (!umma::mbar_wait(&bars.full[slot], phase, &bars.abort_flag, status)) return false;
+    if (!__all_sync(FULL_MASK, umma::mbar_wait(&bars.full[slot], phase, &bars.abort_flag, status))) {
+      bn_drain(bars, st.stages, slot, phase);
+      return false;
+    }
     if (bn_mend(st, stage, t0, T, H)) __syncthreads();
     return true;
   }

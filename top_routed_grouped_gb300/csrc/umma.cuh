@@ -90,6 +90,13 @@ __device__ inline bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatil
   return mbar_wait<true>(bar, parity, abort_flag, status);
 }
 
+// Wait for a copy that counts on `bar` to land before the CTA exits, with a
+// limit of its own: after a wait that ran out, too.
+__device__ inline void mbar_drain(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < 100000000ull) {}
+}
+
 // ---------------------------------------------------------------- TMA
 // L2 eviction policies for TMA loads: streamed-once data (weights) is
 // evicted first, data read again by other CTAs (activations) is kept.
