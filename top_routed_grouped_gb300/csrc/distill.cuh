@@ -648,7 +648,9 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       }
       w[b] = a.weight[t];
     };
+    int started = 0;  // rows
     auto turn = [&](int j, int b) {
+      started = j + 1;
       const int r = j % DS_RING, round = j / DS_RING;
       const T *z = row_of(j);
       bool found = false;
@@ -685,9 +687,11 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
     fetch(0, 0);
     fetch(1, 1);
     for (int j = 0; j < rows; j += 2) {
-      if (!turn(j, 0)) return;
-      if (j + 1 < rows && !turn(j + 1, 1)) return;
+      if (!turn(j, 0)) break;
+      if (j + 1 < rows && !turn(j + 1, 1)) break;
     }
+    // The copies land before the CTA ends, even where the others have given up.
+    for (int j = max(started - DS_RING, 0); j < started; ++j) mbar_drain(&sh.full[j % DS_RING], (j / DS_RING) & 1);
   } else if (warp > W + 1) {
     // ------------------------------------------------------------ row warps
     const int r = warp - (W + 2);
@@ -755,10 +759,10 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[r]);
       gather(j + DS_RING);
-      if (!wait(&sh.go[r], round)) return;
+      if (!wait(&sh.go[r], round)) break;
       if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s}, k);
       if (GRAD) {
-        if (!wait(&sh.empty[r][1], round)) return;
+        if (!wait(&sh.empty[r][1], round)) break;
         if (sl.mul != 0.f)
           ds_places<T, LOSS>(a, sl, dz, lo, hi, sl.w,
                              DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), lane, 32);
@@ -767,11 +771,14 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
     }
   } else if (warp == W + 1) {
     // ------------------------------------------------------------ joiner
+    // (its lanes agree on whether a wait ran out)
+    auto came = [&](bool ok) { return __all_sync(FULL_MASK, ok) != 0; };
+    bool on = true;
     for (int j = 0; j < rows; ++j) {
       const int r = j % DS_RING, q = j % DS_STATS;
       DsSlots &sl = sh.slots[r];
-      if (LOSS && !wait(&sh.taken[r], j / DS_RING)) return;
-      if (!wait(&sh.ready[r], j / DS_RING)) return;
+      on = came((!LOSS || wait(&sh.taken[r], j / DS_RING)) && wait(&sh.ready[r], j / DS_RING));
+      if (!on) break;
       DsStat st = {sl.lse, 1.f};
       if (LOSS) {
         st = ds_join<W>(sh.warp[r], k);
@@ -779,7 +786,8 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
           if (lane == 0) mbar_arrive_expect_tx(&sh.stats[q], ctas * (uint32_t)sizeof(DsStat));
           if (lane < ctas) ds_st_async(mapa_shared(&sh.cta[q][rank], lane), st, mapa_shared(&sh.stats[q], lane));
           __syncwarp();
-          if (!mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status)) return;
+          on = came(mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status));
+          if (!on) break;
           st = ds_join<DS_MAX_CTAS>(sh.cta[q], k);
         }
       }
@@ -792,6 +800,9 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       }
       __syncwarp();
     }
+    // Where a wait ran out the CTA stays until all of its cluster have ended or
+    // given up too: until then they may write to it.
+    if (LOSS && ctas > 1 && !on) cluster_sync();
   } else {
     // ------------------------------------------------------------ consumers
     constexpr int STEP = W * 32;
@@ -878,10 +889,10 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       if (lane == 0) mbar_arrive(&sh.empty[r][1]);
       return true;
     };
-    if (LOSS && rows > 0 && !statistics(0)) return;
-    for (int j = 0; j < rows; ++j) {
-      if (LOSS && j + 1 < rows && !statistics(j + 1)) return;
-      if (GRAD && !gradient(j)) return;
+    bool on = !LOSS || rows == 0 || statistics(0);
+    for (int j = 0; on && j < rows; ++j) {
+      if (LOSS && j + 1 < rows) on = statistics(j + 1);
+      if (GRAD && on) on = gradient(j);
     }
   }
 }
