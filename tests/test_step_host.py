@@ -3,6 +3,7 @@ structs match the header, bad arguments return an error and launch nothing."""
 import ctypes
 import os
 import re
+import types
 
 import pytest
 import torch
@@ -132,3 +133,13 @@ def test_cpu_tensors_are_refused():
               lambda: moe.distill(t, torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1))):
         with pytest.raises(ValueError):
             f()
+
+
+def test_a_workspace_has_the_bytes_it_names():
+    """A broadcast tensor names more elements than it holds."""
+    cpu = types.SimpleNamespace(index=-1)  # as a CPU tensor's get_device() says
+    one = torch.empty(1, dtype=torch.uint8)
+    assert step._ws(0, one, cpu) == (one, 1) and step._ws(0, torch.empty(6), cpu)[1] == 24
+    for ws in (one.expand(1 << 20), torch.empty(64, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            step._ws(0, ws, cpu)

@@ -119,6 +119,8 @@ def _ws(n: int, ws, dev):
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
     elif ws.get_device() != dev.index:
         raise ValueError("ws: on another device than the rows")
+    elif not ws.is_contiguous():  # the bytes that it names need not all be there
+        raise ValueError("ws: contiguous memory expected")
     return ws, ws.numel() * ws.element_size()
 
 
