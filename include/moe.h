@@ -594,7 +594,8 @@ int moe_block_norm(const moe_norm_args_t *a, void *stream);
  * gradients of weights and gates are overwritten and summed over the rows in
  * a fixed order (set by T, H and the device's number of SMs).  Rows of a
  * token are independent of the batch.  Workspace:
- * moe_block_norm_workspace_size(a) bytes, 256-byte aligned.
+ * moe_block_norm_workspace_size(a) bytes, 256-byte aligned; it goes by T, H
+ * and the strides of dr_out, r_out, dh, y and gate (buffers need not be set).
  */
 size_t moe_block_norm_workspace_size(const moe_norm_args_t *a);
 int moe_block_norm_backward(const moe_norm_args_t *a, void *ws, size_t ws_bytes, void *stream);

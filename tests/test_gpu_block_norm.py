@@ -252,6 +252,21 @@ def test_side_stream():
     assert all(g[n] is None or torch.equal(g[n], w[n]) for n in g)
 
 
+@pytest.mark.parametrize("T,H,ld", [(4, 64, 64), (3000, 77, 77), (3000, 77, 80), (20000, 3, 4), (20, 4104, 4104), (700, 2048, 2056)])
+def test_a_workspace_asked_for_without_buffers(T, H, ld):
+    """Its size is that of the call, and the call takes it."""
+    from top_routed_grouped_gb300 import step
+    size = step.moe_block_norm_workspace_size(step._NORM.pack(T, H, 1, 1, 1, 3, 1.0, EPS, 0.0, 0, *[ld] * 10, *[0] * 14))
+    assert size >= 3 * H * 4 and size % 256 == 0
+    c = make(T, H, BF16, BF16, BF16, gate="element")
+    w, window = windows(c, ld, 0)
+    r_out = window(forward_ok(w, BF16, 1.0, 0.0)[0])
+    args = (w["dr_out"], w["dh"], r_out, w["y"], w["w_post"], w["w_pre"], w["gate"])
+    want = moe.block_norm_backward(*args)
+    got = moe.block_norm_backward(*args, ws=torch.empty(size, dtype=torch.uint8, device="cuda"))
+    assert all(torch.equal(got[n], want[n]) for n in want)
+
+
 def test_refusals():
     c = make(4, 64, BF16, F32, F32)
     ok = lambda **k: moe.block_norm(**dict(dict(r=c["r"], y=c["y"], w_post=c["w_post"], w_pre=c["w_pre"]), **k))  # noqa: E731

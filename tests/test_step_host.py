@@ -3,6 +3,8 @@ structs match the header, bad arguments return an error and launch nothing."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 import types
 
 import pytest
@@ -73,6 +75,29 @@ def test_norm_refusals(L, kw, want):
 ])
 def test_norm_backward_refusals(L, kw, want):
     assert L.moe_block_norm_backward(norm(**kw), PTR, 1 << 40, None) == want
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (4, 64), (1000, 77), (5000, 256), (9, 4104), (70000, 2048), (33, 16384)])
+def test_norm_workspace_goes_by_sizes(L, T, H):
+    """One size, whether the buffers are there or not (run in a process of its
+    own: a query that divides by zero takes the process with it), enough for
+    any launch with the strides that it is asked for."""
+    code = """if 1:
+        import sys
+        sys.path[:0] = [%r, %r]
+        import top_routed_grouped_gb300 as moe, test_step_host as t
+        L, n = moe.lib(), lambda **kw: moe.lib().moe_block_norm_workspace_size(t.norm(T=%d, H=%d, **kw))
+        none = {k: 0 for k, kind in t.fields("moe_norm_args") if kind == "Q"}
+        full = n()
+        assert full %% 256 == 0  # (0 where there is no device)
+        for kw in (none, dict(none, w_pre=t.PTR), dict(none, y=t.PTR), dict(y=0, w_post=0), dict(w_pre=0), dict(dr_out=0),
+                   dict(y=t.PTR + 2), dict(gate_kind=3), dict(none, gate_kind=1), dict(dtype=0, rdtype=0, wdtype=0)):
+            assert n(**kw) == full, kw
+        assert n(ld_dh=%d) >= full
+        assert L.moe_block_norm_workspace_size(t.norm(T=0)) == 0 and n(eps=-1.0) == 0
+    """ % (ROOT, os.path.dirname(os.path.abspath(__file__)), T, H, H + 1)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
 
 
 def test_missing_arguments(L):

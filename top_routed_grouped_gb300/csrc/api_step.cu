@@ -30,7 +30,8 @@ static int workspace_status(const void *ws, size_t have, size_t need) {
 }
 
 // ---------------------------------------------------------------- block_norm
-static int norm_dims(const moe_norm_args_t *a) {
+// What can be told without the buffers.
+static int norm_sizes(const moe_norm_args_t *a) {
   if (!a || a->T < 0 || a->H <= 0 || !type_ok(a->dtype) || !type_ok(a->wdtype) || !type_ok(a->rdtype) || a->reserved)
     return MOE_ERR_INVALID_ARG;
   if (a->rdtype != a->dtype && a->rdtype != MOE_F32) return MOE_ERR_INVALID_ARG;
@@ -39,8 +40,14 @@ static int norm_dims(const moe_norm_args_t *a) {
   if (!isfinite(a->scale) || !isfinite(a->weight_offset) || !(a->eps >= 0.f) || !isfinite(a->eps)) return MOE_ERR_INVALID_ARG;
   for (int64_t ld : {a->ld_r, a->ld_y, a->ld_gate, a->ld_r_out, a->ld_h, a->ld_dr_out, a->ld_dh, a->ld_dr, a->ld_dy, a->ld_dgate})
     if (!stride_ok(ld, a->H)) return MOE_ERR_INVALID_ARG;
-  if (a->T > 0 && !a->y && (a->w_post || a->gate_kind != MOE_GATE_NONE || !a->w_pre)) return MOE_ERR_INVALID_ARG;
   return a->H > NORM_MAX_H ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+static int norm_dims(const moe_norm_args_t *a) {
+  const int rc = norm_sizes(a);
+  if (rc == MOE_ERR_INVALID_ARG) return rc;
+  if (a->T > 0 && !a->y && (a->w_post || a->gate_kind != MOE_GATE_NONE || !a->w_pre)) return MOE_ERR_INVALID_ARG;
+  return rc;
 }
 
 static int norm_inputs(const moe_norm_args_t *a) {
@@ -113,8 +120,8 @@ MOE_API int moe_block_norm(const moe_norm_args_t *a, void *stream) {
 }
 
 MOE_API size_t moe_block_norm_workspace_size(const moe_norm_args_t *a) {
-  if (norm_dims(a) != MOE_OK) return 0;
-  return (size_t)round_up((int64_t)block_norm_scratch_bytes(norm_bwd_args(a)), 256);
+  if (norm_sizes(a) != MOE_OK) return 0;
+  return (size_t)round_up((int64_t)block_norm_scratch_bytes(norm_args(a)), 256);
 }
 
 MOE_API int moe_block_norm_backward(const moe_norm_args_t *a, void *ws, size_t ws_bytes, void *stream) {

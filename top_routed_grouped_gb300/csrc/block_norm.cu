@@ -38,14 +38,11 @@ static cudaError_t bn_any(const BnLaunch &l) {
 
 cudaError_t launch_block_norm(const NormArgs &a, int *status, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  return bn_any({a, false, nullptr, status, stream, nullptr, false});
+  return bn_any({a, false, nullptr, status, stream, nullptr});
 }
 
 size_t block_norm_scratch_bytes(const NormArgs &a) {
-  if (a.T == 0) return 0;
-  int groups = 0;
-  bn_any({a, true, nullptr, nullptr, nullptr, &groups, true});
-  return (size_t)3 * groups * a.H * sizeof(float);
+  return a.T == 0 ? 0 : (size_t)3 * bn_most_ctas(a) * a.H * sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(const NormArgs &a, void *scratch, int *status, cudaStream_t stream) {
@@ -57,7 +54,7 @@ cudaError_t launch_block_norm_bwd(const NormArgs &a, void *scratch, int *status,
     return e;
   }
   int groups = 0;
-  cudaError_t e = bn_any({a, true, (float *)scratch, status, stream, &groups, false});
+  cudaError_t e = bn_any({a, true, (float *)scratch, status, stream, &groups});
   if (e != cudaSuccess || (!a.dw_pre && !a.dw_post && !dg)) return e;
   return launch_pdl(block_norm_join_kernel, dim3((unsigned)ceil_div(a.H, 32), 3), dim3(32, 32), 0, stream,
                     (const float *)scratch, (int64_t)groups, a.H, a.dw_pre, a.dw_post, dg);

@@ -658,14 +658,13 @@ inline bool bn_wide(const NormArgs &a, int vec) {
   return ok;
 }
 
-// dense: the rows of every input stand behind one another.
-inline BnShape bn_shape(const NormArgs &a, bool dense) {
+// All but the load width.  dense: the rows of every input stand behind one another.
+inline BnShape bn_threads(int H, bool dense) {
   BnShape s;
-  s.vec = a.f32 ? 4 : 8;
-  if (!bn_wide(a, s.vec)) s.vec = 1;
+  s.vec = 0;
   s.pairs = 4;
-  while (s.pairs < 16 && ceil_div(a.H, 2 * s.pairs) > BN_MAX_THREADS) s.pairs *= 2;
-  const int need = (int)ceil_div(a.H, 2 * s.pairs);
+  while (s.pairs < 16 && ceil_div(H, 2 * s.pairs) > BN_MAX_THREADS) s.pairs *= 2;
+  const int need = (int)ceil_div(H, 2 * s.pairs);
   if (need <= 32) {
     s.group = 4;
     while (s.group < need) s.group *= 2;
@@ -676,6 +675,27 @@ inline BnShape bn_shape(const NormArgs &a, bool dense) {
     s.threads = s.group;
   }
   return s;
+}
+inline BnShape bn_shape(const NormArgs &a, bool dense) {
+  BnShape s = bn_threads(a.H, dense);
+  s.vec = a.f32 ? 4 : 8;
+  if (!bn_wide(a, s.vec)) s.vec = 1;
+  return s;
+}
+// CTAs of an SM, where a group takes r rows at a time.
+inline int bn_ctas(bool backward, const BnShape &s, int r) { return std::max(1, bn_resident(backward, s.pairs, r) / s.threads); }
+
+// The most CTAs that a gradient's launch has, whichever of its inputs are
+// there: their strides alone tell (where all are dense, those given are).
+inline int64_t bn_most_ctas(const NormArgs &a) {
+  bool dense = true;
+  for (int64_t ld : {a.ld_dr_out, a.ld_r_out, a.ld_dh, a.ld_y, a.ld_gate}) dense = dense && ld == a.H;
+  int64_t most = 0;
+  for (bool d : {true, dense}) {
+    const BnShape s = bn_threads(a.H, d);
+    most = std::max(most, std::min(ceil_div(a.T, s.threads / s.group), (int64_t)device_sms() * bn_ctas(true, s, 1)));
+  }
+  return most;
 }
 
 // The inputs that rows come from, in the order in which the kernels name them.
@@ -735,7 +755,6 @@ struct BnLaunch {
   int *status;
   cudaStream_t stream;
   int *groups;  // out: CTAs, each of which leaves partial sums
-  bool dry;     // only `groups` is wanted
 };
 
 template <typename TE, typename TR, int VEC, int CH, int R, bool BULK, bool FULL = false>
@@ -744,7 +763,6 @@ static cudaError_t bn_go(const BnLaunch &l, const BnShape &s, int ctas, const Bn
   const int per_cta = s.threads / s.group;
   const int grid = (int)std::min<int64_t>(ceil_div(a.T, per_cta * R), (int64_t)device_sms() * ctas);
   if (l.groups) *l.groups = grid;
-  if (l.dry) return cudaSuccess;
   const int smem = BULK ? st.bytes * st.stages : 0;
   auto go = [&](auto kernel, auto... args) {
     cudaError_t e = smem > 40 * 1024 ? ensure_smem((const void *)kernel, BN_SMEM) : cudaSuccess;
@@ -758,7 +776,7 @@ template <typename TE, typename TR, int VEC, int NP>
 static cudaError_t bn_launch(const BnLaunch &l, const BnShape &s) {
   constexpr int CH = 2 * NP / VEC;
   BnStages st = bn_inputs(l.a, l.backward);
-  int ctas = std::max(1, bn_resident(l.backward, NP, 2) / s.threads);
+  int ctas = bn_ctas(l.backward, s, 2);
   if constexpr (NP <= 4) {
     const bool full = VEC > 1 && l.a.H == s.group * VEC * CH;
     // Two rows a group where shared memory holds them and all CTAs still get two blocks.
@@ -767,7 +785,7 @@ static cudaError_t bn_launch(const BnLaunch &l, const BnShape &s) {
         if (full) return bn_go<TE, TR, VEC, CH, 2, true, true>(l, s, ctas, st);
       return bn_go<TE, TR, VEC, CH, 2, true>(l, s, ctas, st);
     }
-    ctas = std::max(1, bn_resident(l.backward, NP, 1) / s.threads);
+    ctas = bn_ctas(l.backward, s, 1);
     if (!bn_stages(l.a, s, ctas, 1, st)) return cudaErrorInvalidConfiguration;  // (at most 4096 elements: they fit)
     if constexpr (VEC > 1)
       if (full) return bn_go<TE, TR, VEC, CH, 1, true, true>(l, s, ctas, st);
