@@ -86,6 +86,26 @@ def test_outputs_without_gradient():
     assert torch.equal(gr, torch.ones_like(r)) and torch.equal(gy, torch.full_like(y, 0.5))
 
 
+def test_values_that_autograd_saved_are_not_overwritten_unseen():
+    """A product saves its factors; a call then writes over one of them."""
+    r, y, w = (torch.randn(s, device="cuda") for s in ((6, 16), (6, 16), (16,)))
+    z, t_ids, t = torch.randn(6, 16, device="cuda"), torch.zeros(6, 1, dtype=torch.int32, device="cuda"), torch.ones(6, 1, device="cuda")
+    one, lse = torch.ones(6, device="cuda"), torch.logsumexp(z, 1)
+    for x, write in ((r, lambda x: moe.block_norm(x, y, None, w, inplace=True)),
+                     (torch.zeros(9, 16, device="cuda"), lambda x: moe.embed_backward(t_ids[:, 0], y, 9, dtable=x)),
+                     (z, lambda x: moe.distill_step(x, t_ids, t, one, out=x)),
+                     (z, lambda x: moe.distill_backward(one, lse, x, t_ids, t, out=x)),
+                     (z[:, :9], lambda x: moe.distill_step(x, t_ids, t, one, out=x))):
+        k = torch.ones_like(x).requires_grad_()
+        out = k * x
+        write(x)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.sum().backward()
+    with torch.inference_mode():
+        x = torch.randn(6, 16, device="cuda")
+        assert moe.block_norm(x, y, None, w, inplace=True)[0] is x
+
+
 def test_modules():
     emb = moe.TokenEmbedding(50, 64, scale=8.0, padding_id=3, dtype=torch.bfloat16, out_dtype=torch.float32)
     ids = torch.tensor([3, 7, 7, 49], device="cuda")

@@ -168,3 +168,31 @@ def test_a_workspace_has_the_bytes_it_names():
     for ws in (one.expand(1 << 20), torch.empty(64, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError):
             step._ws(0, ws, cpu)
+
+
+def test_autograd_learns_of_writes_into_the_callers_tensors(monkeypatch):
+    """(the calls themselves are left out: only the bookkeeping runs here)"""
+    for n in ("moe_block_norm", "moe_embed_backward", "moe_distill_backward", "moe_distill_step"):
+        monkeypatch.setattr(step, n, lambda *a: None)
+    monkeypatch.setattr(step, "moe_embed_workspace_size", lambda a: 256)
+    monkeypatch.setattr(step, "_ws", lambda n, ws, dev: (torch.empty(n, dtype=torch.uint8), n))
+    r, y, w = torch.ones(4, 8), torch.ones(4, 8), torch.ones(8)
+    norm = lambda inplace, y: step._block_norm(None, r, y, None, w, None, 1.0, 1e-6, 0.0, None, inplace)  # noqa: E731
+    norm(False, y), norm(True, None)
+    assert r._version == 0 and y._version == 0
+    assert norm(True, y)[0] is r and r._version == 1 and y._version == 0 and w._version == 0
+    table = torch.zeros(5, 8)
+    back = lambda t: step._embed_backward(None, torch.zeros(4, dtype=torch.int64), y, 5, 1.0, None, t, None)  # noqa: E731
+    assert back(None)._version == 0 and back(table) is table and table._version == 1 and y._version == 0
+    z, ids, t, ones = torch.ones(4, 9), torch.zeros(4, 2, dtype=torch.int32), torch.ones(4, 2), torch.ones(4)
+    for n, mode in ((0, 2), (2, 3)):
+        call = lambda out: step._distill(None, z, ids, t, 1.0, 1.0, None, ones, ones, out, mode)  # noqa: E731
+        call(None)
+        assert z._version == n
+        other = torch.empty(4, 9)
+        call(other)
+        assert other._version == 1 and z._version == n
+        call(z)
+        assert z._version == n + 1
+        z.add_(0)
+    assert ids._version == t._version == ones._version == 0

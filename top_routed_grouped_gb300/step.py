@@ -124,6 +124,11 @@ def _ws(n: int, ws, dev):
     return ws, ws.numel() * ws.element_size()
 
 
+# A tensor of the caller's was written: autograd learns of it as of any write in
+# place, and refuses to use the old values where it has saved them.
+_written = torch.autograd.graph.increment_version
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -190,6 +195,8 @@ def _block_norm(stream, r, y, w_post, w_pre, gate, scale, eps, offset, dtype, in
     moe_block_norm(_NORM.pack(T, H, code, rcode, wcode, kind, scale, eps, offset, 0, ld_r, ld_y, ld_gate, ld_out, 0, 0, 0,
                               0, 0, 0, r.data_ptr(), _ptr(y), _ptr(w_post), _ptr(w_pre), _ptr(gate), _ptr(r_out),
                               _ptr(h), 0, 0, 0, 0, 0, 0, 0), stream)
+    if inplace and y is not None:
+        _written(given)
     return r_out, h
 
 
@@ -307,7 +314,7 @@ def _embed_backward(stream, ids, dout, V, scale, padding_id, dtable, ws):
     dev = dout.get_device()
     ids = _ids(ids, dev)
     dout, ld = _rows(dout, ids.shape[0], H, dout.dtype, dev, "dout")
-    accumulate = dtable is not None
+    accumulate = dtable is not None  # (into the caller's)
     if accumulate:
         if dtable.dtype is not torch.float32 or dtable.shape != (V, H) or not dtable.is_contiguous() or \
                 dtable.get_device() != dev:
@@ -319,6 +326,8 @@ def _embed_backward(stream, ids, dout, V, scale, padding_id, dtable, ws):
                        dtable.data_ptr())
     ws, n = _ws(moe_embed_workspace_size(args) if ws is None else 0, ws, dout.device)
     moe_embed_backward(args, ws.data_ptr(), n, stream)
+    if accumulate:
+        _written(dtable)
     return dtable
 
 
@@ -351,7 +360,7 @@ def _distill(stream, logits, t_ids, t_logits, temperature, scale, t_lse, weight,
     K, t_ids, t_logits, t_lse = _teacher(logits, t_ids, t_logits, t_lse)
     given = logits
     logits, ld = _rows(logits, T, V, logits.dtype, dev, "logits")
-    loss, ld_out = None, 0
+    loss, ld_out, theirs = None, 0, out is not None
     if mode & 1:
         loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     if mode == 1:
@@ -371,11 +380,10 @@ def _distill(stream, logits, t_ids, t_logits, temperature, scale, t_lse, weight,
     if mode == 1:
         moe_distill(args, stream)
         return loss, lse
-    if mode == 2:
-        moe_distill_backward(args, stream)
-        return out
-    moe_distill_step(args, stream)
-    return loss, out
+    (moe_distill_backward if mode == 2 else moe_distill_step)(args, stream)
+    if theirs:
+        _written(out)
+    return out if mode == 2 else (loss, out)
 
 
 def distill(logits, t_ids, t_logits, temperature: float = 1.0, scale: float = 1.0, t_lse=None, stream=None):
