@@ -196,3 +196,25 @@ def test_autograd_learns_of_writes_into_the_callers_tensors(monkeypatch):
         assert z._version == n + 1
         z.add_(0)
     assert ids._version == t._version == ones._version == 0
+
+
+def test_second_derivatives_raise(monkeypatch):
+    """Where another path keeps the graph alive, too: the gradient of a square
+    of a gradient would otherwise lack the operator's part without a word."""
+    from top_routed_grouped_gb300 import step_layer as m
+    monkeypatch.setattr(m, "embed", lambda table, ids, scale, out_dtype: table[ids] * scale)
+    monkeypatch.setattr(m, "embed_backward", lambda ids, dout, V, scale, padding_id: torch.zeros(V, dout.shape[1]).index_add_(0, ids, dout * scale))
+    monkeypatch.setattr(m, "block_norm", lambda r, y, *a, **k: (r + y, r * y))
+    monkeypatch.setattr(m, "block_norm_backward", lambda d, dh, r, y, *a, **k: dict(dr=d + dh, dy=d - dh, dw_post=None, dw_pre=y[0] + 0, dgate=None))
+    monkeypatch.setattr(m, "distill", lambda z, *a: (z.sum(1), z.sum(1)))
+    monkeypatch.setattr(m, "distill_backward", lambda w, lse, z, *a: w[:, None] * z)
+    ids, w = torch.tensor([0, 2]), torch.ones(3)
+    for f, shape in ((lambda x: m.EmbedFunction.apply(x, ids, 2.0, None, None), (4, 3)),
+                     (lambda x: sum(m.BlockNormFunction.apply(x, 2 * x, None, w, None, 1.0, 1e-6, 0.0, None)), (2, 3)),
+                     (lambda x: m.distillation_loss(x, ids[:, None], x.detach()), (2, 3))):
+        x = torch.randn(shape, requires_grad=True)
+        out = f(x)
+        (g,) = torch.autograd.grad(out.square().sum() + x.square().sum(), x, create_graph=True)
+        assert g.requires_grad
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.square().sum().backward()

@@ -4,11 +4,13 @@
 Like ``MoEFunction`` these only marshal: each ``torch.autograd.Function``
 calls the library's forward and backward on the current stream and hands
 their outputs to autograd.  Gradients of weights come out of the library in
-FP32; autograd casts one to its parameter's dtype.
+FP32; autograd casts one to its parameter's dtype.  There is no second
+derivative: asking for one raises.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .step import block_norm, block_norm_backward, distill, distill_backward, embed, embed_backward
 
@@ -23,6 +25,7 @@ class EmbedFunction(torch.autograd.Function):
         return embed(table, ids, scale=scale, out_dtype=out_dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         return embed_backward(ctx.saved_tensors[0], dout, ctx.shape, scale=ctx.scale,
                               padding_id=ctx.padding_id), None, None, None, None
@@ -43,6 +46,7 @@ class BlockNormFunction(torch.autograd.Function):
         return r_out if h is None else (r_out, h)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         r_out, y, w_post, w_pre, gate = ctx.saved_tensors
         dr_out = grads[0] if y is not None else None
@@ -66,6 +70,7 @@ class DistillFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         logits, t_ids, t_logits, t_lse, lse = ctx.saved_tensors
         return distill_backward(dloss, lse, logits, t_ids, t_logits, *ctx.args, t_lse), None, None, None, None, None
