@@ -218,3 +218,17 @@ def test_second_derivatives_raise(monkeypatch):
         assert g.requires_grad
         with pytest.raises(RuntimeError, match="once_differentiable"):
             g.square().sum().backward()
+
+
+def test_second_derivatives_of_the_layer_raise(monkeypatch):
+    from top_routed_grouped_gb300 import layer as m
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    saved = {n: torch.zeros(1) for n in m._ROUTING}
+    monkeypatch.setattr(m, "forward", lambda x, *a, **k: dict(saved, y=x * 2, saved={n: torch.zeros(1) for n in m._SAVED}))
+    names = ("dw_router", "dw_shared_gate", "dw_gate_up", "dw_down", "dws_gate_up", "dws_down")
+    monkeypatch.setattr(m, "backward", lambda f, dy, x, *w, **k: dict({n: v + 0 for n, v in zip(names, w)}, dx=dy * 2))
+    x = torch.randn(3, 4, requires_grad=True)
+    y = m.MoEFunction.apply(x, *[torch.zeros(2) for _ in names], 1)[0]
+    (g,) = torch.autograd.grad(y.square().sum() + x.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.square().sum().backward()

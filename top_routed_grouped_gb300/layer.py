@@ -13,7 +13,8 @@ overwritten, not accumulated).  Autograd casts a gradient to its
 parameter's dtype, so a bf16 parameter receives the FP32 gradient rounded
 once to bf16 (the FP32 router weight receives it unrounded); dx is the
 library's bf16 dx bit for bit.  The routes are held fixed in the backward
-(the top-k selection is piecewise constant), as in ``moe_backward``.
+(the top-k selection is piecewise constant), as in ``moe_backward``.  There is
+no second derivative: asking for one raises.
 
 Workspaces are caller-visible: pass ``ws_forward`` / ``ws_backward`` (uint8
 device tensors of at least ``moe_workspace_size`` bytes) to ``forward``, or
@@ -26,6 +27,7 @@ order.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (backward, dims_of, forward, moe_workspace_size)
 
@@ -57,6 +59,7 @@ class MoEFunction(torch.autograd.Function):
         return f["y"], f["topk_ids"], f["topk_w"], f["shared_sig"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, _d_ids=None, _d_w=None, _d_sig=None):
         t = ctx.saved_tensors
         x, weights = t[0], t[1:7]
