@@ -120,6 +120,12 @@ def test_modules():
     assert r_out.dtype == torch.float32 and h.dtype == torch.bfloat16
 
 
+def test_the_last_token_as_padding():
+    emb = moe.TokenEmbedding(50, 8, padding_id=-1, dtype=torch.float32)
+    emb(torch.tensor([49, 7, 49], device="cuda")).sum().backward()
+    assert not emb.weight.grad[49].any() and (emb.weight.grad[7] == 1).all()
+
+
 def test_example_learns():
     spec = importlib.util.spec_from_file_location("distill_training", os.path.join(ROOT, "examples", "distill_training.py"))
     m = importlib.util.module_from_spec(spec)

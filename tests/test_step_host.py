@@ -232,3 +232,14 @@ def test_second_derivatives_of_the_layer_raise(monkeypatch):
     (g,) = torch.autograd.grad(y.square().sum() + x.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.square().sum().backward()
+
+
+def test_padding_tokens():
+    """The module's -1 is the last token, as in torch, not none; one past the
+    table is an error."""
+    make = lambda p: moe.TokenEmbedding(10, 4, padding_id=p, device="cpu")  # noqa: E731
+    assert make(None).padding_id is None and make(3).padding_id == 3 and make(0).padding_id == 0
+    assert make(-1).padding_id == 9 and make(-10).padding_id == 0
+    for bad in (10, -11):
+        with pytest.raises(ValueError):
+            make(bad)

@@ -336,7 +336,8 @@ def embed_backward(ids, dout, num_embeddings: int, scale: float = 1.0, padding_i
     """The table's gradient, float32 [num_embeddings, H]: row v sums
     scale * dout[t] over the t with ids[t] = v, in ascending t.  ``dtable``:
     add to this tensor (only its rows that are hit are touched) instead of
-    returning a new one; ``padding_id``: a token without gradient."""
+    returning a new one; ``padding_id``: a token without gradient (one that is
+    not in the table, -1 say: none)."""
     return _on(dout, stream, _embed_backward, ids, dout, num_embeddings, scale, padding_id, dtable, ws)
 
 

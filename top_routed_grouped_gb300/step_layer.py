@@ -83,12 +83,18 @@ def distillation_loss(logits, t_ids, t_logits, temperature: float = 1.0, scale: 
 
 
 class TokenEmbedding(torch.nn.Module):
-    """A table [V, H] whose rows leave scaled: ``forward(ids [T])`` is [T, H]."""
+    """A table [V, H] whose rows leave scaled: ``forward(ids [T])`` is [T, H].
+    ``padding_id``: a token without gradient, counted from the end where it is
+    negative."""
 
     def __init__(self, num_embeddings: int, hidden: int, scale: float = 1.0, padding_id: int | None = None,
                  dtype: torch.dtype = torch.bfloat16, out_dtype: torch.dtype | None = None, device=None,
                  init_std: float = 0.02):
         super().__init__()
+        if padding_id is not None:
+            if not -num_embeddings <= padding_id < num_embeddings:
+                raise ValueError(f"padding_id {padding_id}: not one of {num_embeddings} tokens")
+            padding_id %= num_embeddings
         dev = torch.device("cuda") if device is None else torch.device(device)
         self.weight = torch.nn.Parameter(torch.empty(num_embeddings, hidden, dtype=dtype, device=dev).normal_(0.0, init_std))
         self.scale, self.padding_id, self.out_dtype = float(scale), padding_id, out_dtype
