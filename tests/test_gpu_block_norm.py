@@ -81,6 +81,14 @@ def test_forms(gate, post, pre, block, T, H, types):
         backward_ok(c, r_out, -1.5, 1.0)
 
 
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(str(x).split(".")[1] for x in t))
+def test_token_gate_of_one_channel(types):
+    """A float gate [T, 1] is a token's where rows have one channel, too."""
+    c = make(70, 1, *types, gate="token")
+    r_out, _ = forward_ok(c, types[0], 0.5, 0.0)
+    backward_ok(c, r_out, 0.5, 0.0)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_no_upstream_for_the_residual(dtype):
     c = make(19, 320, dtype, F32, F32, gate="element")

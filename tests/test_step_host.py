@@ -243,3 +243,14 @@ def test_padding_tokens():
     for bad in (10, -11):
         with pytest.raises(ValueError):
             make(bad)
+
+
+def test_kinds_of_gates():
+    """A float [T, 1] beside bfloat16 rows of one channel is a token's gate."""
+    kind = lambda gate, H, dtype: step._norm_weights(dtype, H, -1, None, None, gate, 5)[0]  # noqa: E731
+    ones, b16 = torch.ones(5, 1), torch.bfloat16
+    assert kind(ones, 1, b16) == kind(ones, 8, b16) == kind(ones, 8, torch.float32) == 1
+    assert kind(ones.to(b16), 1, b16) == kind(ones, 1, torch.float32) == 3
+    assert kind(torch.ones(8), 8, torch.float32) == 2 and kind(torch.ones(5, 8), 8, torch.float32) == 3
+    with pytest.raises(ValueError):
+        kind(ones.to(b16), 8, b16)

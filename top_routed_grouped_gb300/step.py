@@ -141,7 +141,7 @@ def _norm_weights(dtype, H, dev, w_post, w_pre, gate, T):
         if gate.dim() == 1:
             kind, wtype = 2, gate.dtype
             gate = _vec(gate, H, (dtype, torch.float32), dev, "gate")
-        elif gate.dim() == 2 and gate.shape[1] == 1 and H != 1:
+        elif gate.dim() == 2 and gate.shape[1] == 1 and (H != 1 or gate.dtype is not dtype):
             kind = 1
             gate, ld = _rows(gate, T, 1, torch.float32, dev, "gate of a token")
             if ld:
