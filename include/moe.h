@@ -574,8 +574,9 @@ typedef struct moe_norm_args {
  *
  * y = NULL: h = n(r; w_pre) and r_out is not written (no gate, no w_post).
  * Everything is FP32 inside, each output rounded once; h is computed from the
- * unrounded sum.  Every sum runs in an order that depends on H only, so a
- * row's outputs do not depend on T or on the other rows.
+ * unrounded sum.  Every sum runs in an order set by H, the types, whether all
+ * rows start on 16-byte boundaries and, for H <= 256, whether all inputs are
+ * dense; so a row's outputs do not depend on T or on the other rows.
  */
 int moe_block_norm(const moe_norm_args_t *a, void *stream);
 

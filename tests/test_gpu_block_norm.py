@@ -209,6 +209,22 @@ def test_rows_do_not_depend_on_the_batch(types, H):
     assert all(torch.equal(again[n], g[n]) for n in g)
 
 
+@pytest.mark.parametrize("types,H,ld", [(TYPES[0], 77, 80), (TYPES[1], 77, 78), (TYPES[2], 100, 101), (TYPES[1], 264, 267),
+                                        (TYPES[1], 2048, 2051), (TYPES[0], 2048, 2056)])
+def test_strided_rows_do_not_depend_on_the_batch(types, H, ld):
+    """One row of a strided batch, too, which torch takes for a contiguous one."""
+    w, window = windows(make(300, H, *types, gate="element"), ld, 0)
+    full = moe.block_norm(w["r"], w["y"], w["w_post"], w["w_pre"], w["gate"])
+    r_out = window(full[0])
+    g = moe.block_norm_backward(w["dr_out"], w["dh"], r_out, w["y"], w["w_post"], w["w_pre"], w["gate"])
+    for rows in (slice(0, 1), slice(5, 6), slice(8, 9), slice(100, 133), slice(299, 300)):
+        part = moe.block_norm(w["r"][rows], w["y"][rows], w["w_post"], w["w_pre"], w["gate"][rows])
+        assert torch.equal(part[0], full[0][rows]) and torch.equal(part[1], full[1][rows])
+        p = moe.block_norm_backward(w["dr_out"][rows], w["dh"][rows], r_out[rows], w["y"][rows], w["w_post"], w["w_pre"],
+                                    w["gate"][rows])
+        assert all(torch.equal(p[n], g[n][rows]) for n in ("dr", "dy", "dgate"))
+
+
 @pytest.mark.parametrize("types,H", [(TYPES[1], 2048), (TYPES[2], 256), (TYPES[0], 333)])
 def test_rows_of_a_large_batch_are_those_of_a_small_one(types, H):
     """Large batches take several rows at a time: the same bits all the same."""

@@ -180,6 +180,25 @@ def test_rows_do_not_depend_on_the_batch(dtype, V):
     ref.check(few[1], *want["dlogits"], ops=ref.ROW + V // 128, what="dlogits")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,ld", [(900, 901), (5003, 5003), (16384, 16385), (32000, 32003), (32000, 32008), (131072, 131073)])
+def test_rows_are_the_same_bits_in_any_batch(dtype, V, ld):
+    """The shape goes by the vocabulary and the rows' alignment alone: any rows
+    of a batch, one of them too, have the bits that they have in the whole."""
+    z, ids, t, w = make(150, V, 8, dtype)
+    rows = torch.zeros(149 * ld + V, device="cuda", dtype=dtype).as_strided((150, V), (ld, 1))
+    rows.copy_(z)
+    loss, lse = moe.distill(rows, ids, t)
+    step = moe.distill_step(rows, ids, t, w)
+    d = moe.distill_backward(w, lse, rows, ids, t)
+    for i in (slice(0, 1), slice(3, 5), slice(8, 9), slice(149, 150), slice(20, 111)):
+        p = moe.distill(rows[i], ids[i], t[i])
+        assert torch.equal(p[0], loss[i]) and torch.equal(p[1], lse[i])
+        p = moe.distill_step(rows[i], ids[i], t[i], w[i])
+        assert torch.equal(p[0], step[0][i]) and torch.equal(p[1], step[1][i])
+        assert torch.equal(moe.distill_backward(w[i], lse[i], rows[i], ids[i], t[i]), d[i])
+
+
 def test_rows_past_32_bit_offsets():
     T, V = 20000, 131072  # 2.6e9 elements
     z = torch.zeros(T, V, dtype=BF16, device="cuda")

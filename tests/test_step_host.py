@@ -254,3 +254,12 @@ def test_kinds_of_gates():
     assert kind(torch.ones(8), 8, torch.float32) == 2 and kind(torch.ones(5, 8), 8, torch.float32) == 3
     with pytest.raises(ValueError):
         kind(ones.to(b16), 8, b16)
+
+
+def test_a_row_keeps_the_stride_of_its_matrix():
+    wide = torch.zeros(6, 12)
+    rows = lambda t: step._rows(t, t.shape[0], t.shape[1], torch.float32, -1, "r")  # noqa: E731
+    assert rows(wide) == (wide, 0) and rows(wide[2:3])[1] == 0
+    assert rows(wide[:, :8])[1] == 12 and rows(wide[2:3, :8])[1] == 12 and rows(wide[2:3, 3:4])[1] == 12
+    assert rows(torch.zeros(1, 8))[1] == 0 and rows(torch.zeros(8, 1).t())[1] == 0
+    assert rows(torch.zeros(1, 8).expand(1, 8))[1] == 0 and rows(torch.zeros(1, 1).expand(1, 8))[1] == 0

@@ -83,12 +83,14 @@ def _on(t: torch.Tensor, stream, call, *args):
 
 def _rows(t, T: int, N: int, dtype, dev, name: str):
     """``t`` as [T, N] rows of ``dtype`` with neighbouring channels, and its
-    row stride (0 where the rows are dense).  An ``empty_like`` of it is dense."""
+    row stride (0 where the rows are dense).  An ``empty_like`` of it is dense.
+    One row of a wider matrix keeps that stride, so that it runs as among its
+    neighbours and gets the same bits."""
     if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != T or t.shape[1] != N:
         raise ValueError(f"{name}: {dtype} [{T}, {N}] on device {dev} expected, got {t.dtype} {list(t.shape)} "
                          f"on device {t.get_device()}")
     if t.is_contiguous():
-        return t, 0
+        return t, t.stride(0) if T == 1 and t.stride(0) > N else 0
     if (N > 1 and t.stride(1) != 1) or t.stride(0) < N:
         return t.contiguous(), 0
     return t, t.stride(0)
