@@ -8,6 +8,7 @@ import top_routed_grouped_gb300 as moe
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 EPS = 1e-6
+INF = float("inf")
 
 
 def make(T, H, dtype, rdtype, wdtype, post=True, pre=True, block=True, gate="none", offset=0.0, seed=0):
@@ -191,6 +192,26 @@ def test_zero_and_odd_rows():
     c["r"][5, 7] = float("inf")
     r_out, h = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"])
     assert torch.isnan(h[4]).all() and torch.isfinite(h[:4]).all() and torch.isnan(h[5, 7])
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 64), (33, 40), (5, 7), (10001, 256), (10001, 77), (4865, 2048)])
+@pytest.mark.parametrize("gate", ["none", "channel"])
+def test_infinite_gradients_are_not_lost(T, H, gate):
+    """An infinite gradient of one channel makes that channel's weight gradient
+    infinite, whatever the number of rows (blocks that rows do not fill have
+    others in their places, which add nothing)."""
+    c = make(T, H, F32, F32, F32, gate=gate, seed=5)
+    r_out, _ = moe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], c["gate"])
+    for t in {0, T // 2, T - 1}:
+        dh, dr = c["dh"].clone(), c["dr_out"].clone()
+        dh[t, 5] = INF
+        g = moe.block_norm_backward(dr, dh, r_out, c["y"], c["w_post"], c["w_pre"], c["gate"])
+        want = INF if r_out[t, 5] > 0 else -INF
+        assert g["dw_pre"][5] == want and torch.isfinite(torch.cat([g["dw_pre"][:5], g["dw_pre"][6:]])).all()
+        dr[t, 3] = INF
+        g = moe.block_norm_backward(dr, c["dh"], r_out, c["y"], c["w_post"], c["w_pre"], c["gate"])
+        assert torch.isinf(g["dw_post"][3]) and torch.isfinite(g["dw_post"][4:]).all()
+        assert gate == "none" or (torch.isinf(g["dgate"][3]) and torch.isfinite(g["dgate"][4:]).all())
 
 
 @pytest.mark.parametrize("types,H", [(TYPES[0], 1001), (TYPES[1], 2048), (TYPES[2], 64), (TYPES[1], 77)])

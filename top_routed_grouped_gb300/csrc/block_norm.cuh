@@ -102,7 +102,9 @@ __device__ inline void bn_start(const BnStages &st, uint8_t *stage, uint64_t *ba
 }
 // What the copies of a block may have missed (the whole CTA; the caller's
 // barrier follows): bytes of the pieces that an input starts or ends in, in
-// which only the first and the last `near` rows lie.
+// which only the first and the last `near` rows lie.  ZERO: rows of the last
+// block that the inputs lack are zeros.
+template <bool ZERO>
 __device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, int T, int H) {
   if (t0 >= st.near && t0 + st.rows + st.near <= T) return false;
   bool missed = false;
@@ -115,6 +117,16 @@ __device__ inline bool bn_mend(const BnStages &st, uint8_t *stage, int64_t t0, i
       for (uintptr_t b = p.lo + threadIdx.x; b < p.hi; b += blockDim.x)
         if (b < p.from || b >= p.to) dst[b] = *(const uint8_t *)b;
     }
+  if (ZERO && t0 + st.rows > T) {
+    const int rows = (int)(T - t0);
+    for (int k = 0; k < st.n; ++k) {
+      if (!st.base[k]) continue;
+      uint8_t *row = stage + st.off[k] + rows * st.row[k];
+      if (st.runs == 1) row += ((uintptr_t)st.base[k] + t0 * st.ld[k] * st.es[k]) & 15;
+      for (uint32_t b = 2 * threadIdx.x; b < (st.rows - rows) * st.row[k]; b += 2 * blockDim.x) *(uint16_t *)(row + b) = 0;
+    }
+    missed = true;
+  }
   // The stage is copied to again later; without this a copy may pass these writes.
   if (missed) umma::fence_proxy_async_smem();
   return missed;
@@ -269,7 +281,7 @@ static __device__ __noinline__ void bn_drain(BnBars &bars, int stages, int slot,
 }
 
 // A CTA's walk over its blocks of rows, with stages (BULK) or without.
-template <bool BULK, int R>
+template <bool BULK, int R, bool ZERO>
 struct BnWalk {
   const BnStages &st;
   const int T, H, per_cta;
@@ -306,7 +318,7 @@ struct BnWalk {
       bn_drain(bars, st.stages, slot, phase);
       return false;
     }
-    if (bn_mend(st, stage, t0, T, H)) __syncthreads();
+    if (bn_mend<ZERO>(st, stage, t0, T, H)) __syncthreads();
     return true;
   }
   // Row `at` of the block (row t in memory, of `p`) of input K.
@@ -349,8 +361,9 @@ struct BnOut {
 };
 
 // The rows of a block that a group takes: number, place in the block, whether
-// there is such a row (a row of the block stands in where there is none).
-template <int R>
+// there is such a row.  Where there is none, the block's first row stands in
+// or, with ZERO, a row of zeros.
+template <int R, bool ZERO>
 struct BnRows {
   int64_t t[R];
   int at[R];
@@ -359,8 +372,8 @@ struct BnRows {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       there[j] = t0 + j * per_cta + sub < T;
-      at[j] = there[j] ? j * per_cta + sub : 0;
-      t[j] = t0 + at[j];
+      at[j] = ZERO || there[j] ? j * per_cta + sub : 0;
+      t[j] = there[j] ? t0 + at[j] : t0;
     }
   }
 };
@@ -378,7 +391,7 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
   const BnRow<VEC, CH, FULL> io = {lane, group, a.H};
   if (threadIdx.x < 2 * R * 16) buf[0][0][threadIdx.x] = 0.f;
   if (!BULK) __syncthreads();
-  BnWalk<BULK, R> walk(st, a.T, a.H, per_cta, bn_smem, bars);
+  BnWalk<BULK, R, false> walk(st, a.T, a.H, per_cta, bn_smem, bars);
   BnOut<TR> r_out(a.r_out, a.ld_r_out, walk.t0 + sub, per_cta, walk.step);
   BnOut<TE> h_out(a.h, a.ld_h, walk.t0 + sub, per_cta, walk.step);
   F2 w_post[NP], w_pre[NP];
@@ -387,7 +400,7 @@ block_norm_kernel(const NormArgs a, int group, const BnStages st, int *status) {
   int round = 0;
   for (; walk.t0 < a.T; walk.next()) {
     if (!walk.arrive(status)) return;
-    const BnRows<R> rows(walk.t0, per_cta, sub, a.T);
+    const BnRows<R, false> rows(walk.t0, per_cta, sub, a.T);
     float s[R], rstd[R];
     F2 v[R][NP], y[NP];
 #pragma unroll
@@ -469,7 +482,7 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
   const BnRow<VEC, CH, FULL> io = {lane, group, a.H};
   for (int i = threadIdx.x; i < 2 * 3 * R * 16; i += blockDim.x) buf[0][0][i] = 0.f;
   if (!BULK) __syncthreads();
-  BnWalk<BULK, R> walk(st, a.T, a.H, per_cta, bn_smem, bars);
+  BnWalk<BULK, R, true> walk(st, a.T, a.H, per_cta, bn_smem, bars);
   BnOut<TR> dr_out(a.dr, a.ld_dr, walk.t0 + sub, per_cta, walk.step);
   BnOut<TE> dy_out(a.dy, a.ld_dy, walk.t0 + sub, per_cta, walk.step), dg_out(a.dgate, a.ld_dgate, walk.t0 + sub, per_cta, walk.step);
   F2 w_post[NP], w_pre[NP], dw_post[NP], dw_pre[NP], dgate[NP];
@@ -480,7 +493,7 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
   int round = 0;
   for (; walk.t0 < a.T; walk.next()) {
     if (!walk.arrive(status)) return;
-    const BnRows<R> rows(walk.t0, per_cta, sub, a.T);
+    const BnRows<R, true> rows(walk.t0, per_cta, sub, a.T);
     float s[3 * R];  // v^2, dh w v, y^2 of each row
     if (!HELD && a.w_pre) io.template weights<TE>(a.w_pre, a.wf32, a.offset, w_pre);
 #pragma unroll
@@ -513,9 +526,11 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int64_t t = rows.t[j];
-      const float one = rows.there[j] ? 1.f : 0.f;  // a row that stands in adds nothing
-      const float rv = rsqrtf(fmaf(s[3 * j], inv_h, a.eps));
-      ry[j] = a.w_post ? rsqrtf(fmaf(s[3 * j + 2], inv_h, a.eps)) : 1.f;
+      // A row of zeros in the place of one that is not there adds nothing to
+      // the sums over rows: with factors of zero not even where eps is 0.
+      const bool in = rows.there[j];
+      const float rv = in ? rsqrtf(fmaf(s[3 * j], inv_h, a.eps)) : 0.f;
+      ry[j] = !in ? 0.f : a.w_post ? rsqrtf(fmaf(s[3 * j + 2], inv_h, a.eps)) : 1.f;
       if (a.dr_out) {
         io.load(walk.template row<0, WIDE, TR>(a.dr_out, a.ld_dr_out, t, rows.at[j]), e[j]);
       } else {
@@ -526,10 +541,10 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
         F2 x[NP], d[NP];
         io.load(walk.template row<1, WIDE, TR>( a.r_out, a.ld_r_out, t, rows.at[j]), x);
         io.load(walk.template row<2, WIDE, TE>( a.dh, a.ld_dh, t, rows.at[j]), d);
-        const F2 rr(rv), r1(rv * one), cr(-(s[3 * j + 1] * inv_h * rv * rv * rv));
+        const F2 rr(rv), cr(-(s[3 * j + 1] * inv_h * rv * rv * rv));
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          dw_pre[p] = fma2(d[p], mul2(x[p], r1), dw_pre[p]);
+          dw_pre[p] = fma2(d[p], mul2(x[p], rr), dw_pre[p]);
           e[j][p] = add2(e[j][p], fma2(mul2(d[p], w_pre[p]), rr, mul2(x[p], cr)));
         }
         if (rows.there[j]) io.store(dr_out.row(j), e[j]);
@@ -538,14 +553,14 @@ block_norm_bwd_kernel(const NormArgs a, int group, const BnStages st, float *par
       if (a.y) {
         F2 y[NP], g[NP], q0(0.f), q1(0.f);
         io.load(walk.template row<3, WIDE, TE>( a.y, a.ld_y, t, rows.at[j]), y);
-        const F2 sc(a.scale * one), rr(ry[j]);
+        const F2 sc(a.scale), rr(ry[j]);
 #pragma unroll
         for (int p = 0; p < NP; ++p) e[j][p] = mul2(e[j][p], sc);
         if (a.gate_kind != MOE_GATE_NONE) {
           if (a.gate_kind == MOE_GATE_ELEMENT) io.load(walk.template row<4, WIDE, TE>( a.gate, a.ld_gate, t, rows.at[j]), g);
           else if (a.gate_kind == MOE_GATE_CHANNEL) io.template weights<TE>(a.gate, a.wf32, 0.f, g);
           else {
-            const F2 gt(((const float *)a.gate)[t]);
+            const F2 gt(in ? ((const float *)a.gate)[t] : 0.f);
 #pragma unroll
             for (int p = 0; p < NP; ++p) g[p] = gt;
           }
