@@ -65,6 +65,36 @@ def test_gradient_of_many_tokens(T, V, H):
     assert torch.equal(got, moe.embed_backward(ids, dout, V))
 
 
+@pytest.mark.parametrize("kind", ["same", "ends", "ranks", "any"])
+@pytest.mark.parametrize("T,V,H,pad", [(1, 3, 8, 0), (4095, 50, 16, 0), (16385, 1000, 24, 8), (65537, 400, 8, 0), (131072, 900, 8, 0), (131073, 900, 8, 0),
+                                       (131073, 70000, 12, 5), (200000, 33, 16, 16), (262145, 1025, 9, 0), (300000, 1 << 19, 8, 3),
+                                       ((1 << 20) - 1, 5000, 8, 0), ((1 << 20) + 77, 2100, 7, 1)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_whole_numbers_are_summed_exactly(kind, T, V, H, pad, dtype):
+    """Gradients of small whole numbers: every sum in FP32 is exact (below 2^24)
+    in any order, so a row that is lost, counted twice or given to another
+    token shows as a difference.  On both sides of the token counts at which the
+    sort and the tiles change; some tokens padding, some outside the table."""
+    g = gen(T + V)
+    ids = tokens(kind, T, V, seed=V, dtype=torch.int32 if T % 2 else torch.int64)
+    ids[::97] = -1
+    ids[::89] = V
+    dout = torch.randint(-8, 9, (T, H + pad), generator=g, device="cuda").to(dtype)[:, :H]
+    first = torch.randint(-8, 9, (V, H), generator=g, device="cuda").float()
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda")
+    ok = (ids >= 0) & (ids < V)
+    want.index_add_(0, ids[ok].long(), 2.0 * dout[ok].double())
+    assert float(want.abs().max()) < 2 ** 24
+    moe.moe_device_status(reset=True)
+    got = moe.embed_backward(ids, dout, V, scale=2.0)
+    assert moe.moe_device_status(reset=True) == 5
+    assert torch.equal(got.double(), want)
+    token, sums = int(ids[T // 2].clamp(0, V - 1)), first.clone()
+    moe.embed_backward(ids, dout, V, scale=2.0, padding_id=token, dtable=sums)
+    want[token] = 0
+    assert torch.equal(sums.double(), first.double() + want)
+
+
 @pytest.mark.parametrize("dtype,H", [(F32, 96), (BF16, 72), (BF16, 13)])
 def test_padding_bad_ids_and_accumulation(dtype, H):
     T, V = 900, 60
