@@ -244,6 +244,15 @@ def test_strided_rows_do_not_depend_on_the_batch(types, H, ld):
         p = moe.block_norm_backward(w["dr_out"][rows], w["dh"][rows], r_out[rows], w["y"][rows], w["w_post"], w["w_pre"],
                                     w["gate"][rows])
         assert all(torch.equal(p[n], g[n][rows]) for n in ("dr", "dy", "dgate"))
+    d = dict(w, y=w["y"].contiguous(), gate=w["gate"].contiguous())  # strided residual rows alone: what comes out is dense
+    full = moe.block_norm(d["r"], d["y"], d["w_post"], d["w_pre"], d["gate"])
+    args = (d["w_post"], d["w_pre"])
+    g = moe.block_norm_backward(full[0], full[1], full[0], d["y"], *args, d["gate"])
+    for rows in (slice(5, 6), slice(8, 10)):
+        part = moe.block_norm(d["r"][rows], d["y"][rows], *args, d["gate"][rows])
+        assert all(torch.equal(a, b[rows]) and a.stride() == (H, 1) for a, b in zip(part, full))
+        p = moe.block_norm_backward(part[0], part[1], part[0], d["y"][rows], *args, d["gate"][rows])
+        assert all(torch.equal(p[n], g[n][rows]) and p[n].stride() == (H, 1) for n in ("dr", "dy", "dgate"))
 
 
 @pytest.mark.parametrize("types,H", [(TYPES[1], 2048), (TYPES[2], 256), (TYPES[0], 333)])

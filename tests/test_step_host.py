@@ -263,3 +263,8 @@ def test_a_row_keeps_the_stride_of_its_matrix():
     assert rows(wide[:, :8])[1] == 12 and rows(wide[2:3, :8])[1] == 12 and rows(wide[2:3, 3:4])[1] == 12
     assert rows(torch.zeros(1, 8))[1] == 0 and rows(torch.zeros(8, 1).t())[1] == 0
     assert rows(torch.zeros(1, 8).expand(1, 8))[1] == 0 and rows(torch.zeros(1, 1).expand(1, 8))[1] == 0
+    for t in (wide[2:3, :8], wide[:, :8], wide, torch.zeros(8, 1).t(), wide[:, 5:6]):
+        ld = rows(t)[1]
+        like = step._like(t, ld, torch.bfloat16)
+        assert like.shape == t.shape and rows(like.float())[1] == 0 and like.dtype is torch.bfloat16
+        assert step._like(t, ld).dtype is torch.float32

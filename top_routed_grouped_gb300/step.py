@@ -81,11 +81,17 @@ def _on(t: torch.Tensor, stream, call, *args):
             return call(stream.cuda_stream, *args)
 
 
+def _like(t, ld, dtype=None):
+    """Dense rows of the shape of ``t``, whose row stride is ``ld``."""
+    if ld:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return torch.empty_like(t, dtype=dtype)
+
+
 def _rows(t, T: int, N: int, dtype, dev, name: str):
     """``t`` as [T, N] rows of ``dtype`` with neighbouring channels, and its
-    row stride (0 where the rows are dense).  An ``empty_like`` of it is dense.
-    One row of a wider matrix keeps that stride, so that it runs as among its
-    neighbours and gets the same bits."""
+    row stride (0 where the rows are dense).  One row of a wider matrix keeps
+    that stride, so that it runs as among its neighbours and gets the same bits."""
     if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != T or t.shape[1] != N:
         raise ValueError(f"{name}: {dtype} [{T}, {N}] on device {dev} expected, got {t.dtype} {list(t.shape)} "
                          f"on device {t.get_device()}")
@@ -191,9 +197,9 @@ def _block_norm(stream, r, y, w_post, w_pre, gate, scale, eps, offset, dtype, in
                 raise ValueError("r: rows that cannot be written in place")
             ld_out = ld_r
         else:
-            r_out = torch.empty_like(r)
+            r_out = _like(r, ld_r)
     if w_pre is not None:
-        h = torch.empty_like(r if dtype is r.dtype else y) if y is not None else torch.empty_like(r, dtype=dtype)
+        h = _like(r, ld_r) if dtype is r.dtype else _like(r, ld_r, dtype) if y is None else _like(y, ld_y)
     moe_block_norm(_NORM.pack(T, H, code, rcode, wcode, kind, scale, eps, offset, 0, ld_r, ld_y, ld_gate, ld_out, 0, 0, 0,
                               0, 0, 0, r.data_ptr(), _ptr(y), _ptr(w_post), _ptr(w_pre), _ptr(gate), _ptr(r_out),
                               _ptr(h), 0, 0, 0, 0, 0, 0, 0), stream)
@@ -245,17 +251,17 @@ def _block_norm_backward(stream, dr_out, dh, r_out, y, w_post, w_pre, gate, scal
     if w_pre is not None:
         r_out, ld_r = _rows(r_out, T, H, like.dtype, dev, "r_out")
         dh, ld_dh = _rows(dh, T, H, dtype, dev, "dh")
-        dr = torch.empty_like(r_out)
+        dr = _like(r_out, ld_r)
         dw_pre = torch.empty(H, dtype=torch.float32, device=device)
     else:
         r_out = None
     if y is not None:
         y, ld_y = _rows(y, T, H, dtype, dev, "y")
-        dy = torch.empty_like(y)
+        dy = _like(y, ld_y)
         if w_post is not None:
             dw_post = torch.empty(H, dtype=torch.float32, device=device)
         if kind == 3:
-            dgate = torch.empty_like(y)
+            dgate = _like(y, ld_y)
         elif kind:
             dgate = torch.empty((T, 1) if kind == 1 else (H,), dtype=torch.float32, device=device)
     args = _NORM.pack(T, H, code, rcode, wcode, kind, scale, eps, offset, 0, 0, ld_y, ld_gate, ld_r, 0, ld_dr, ld_dh,
@@ -373,7 +379,7 @@ def _distill(stream, logits, t_ids, t_logits, temperature, scale, t_lse, weight,
     if mode & 2:
         weight = _vec(weight, T, (torch.float32,), dev, "weight")
         if out is None:
-            out = torch.empty_like(logits)
+            out = _like(logits, ld)
         else:
             o, ld_out = _rows(out, T, V, logits.dtype, dev, "out")
             if o is not out or (out is given and logits is not given):
