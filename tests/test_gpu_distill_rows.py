@@ -152,3 +152,24 @@ def test_no_place_of_a_row_is_lost(dtype, V, ld, at, ld_out, at_out):
     moe.distill_step(inplace, ids, t, w, out=inplace)
     hold(z, ids, t, w, 1.0, grads=[(inplace, False)])
     assert torch.isnan(beside(buf, T, V, ld, at)).all()
+
+
+@pytest.mark.parametrize("V", [1000, 16001, 32000, 50257, 300001])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step_that_leaves_lse(dtype, V):
+    """The C entry point writes lse where it is asked to: of rows without a
+    teacher or of weight 0, too, which the step need not read otherwise; loss
+    and gradient are the same bits."""
+    from top_routed_grouped_gb300 import step
+    z, ids, t, w = make(300, V, 4, dtype)
+    ids[::3], w[::5] = -1, 0
+    loss, d = moe.distill_step(z, ids, t, w)
+    loss2, lse, d2 = torch.empty_like(loss), torch.empty_like(loss), torch.empty_like(d)
+    step.moe_distill_step(step._DISTILL.pack(300, V, 4, step._DTYPE[dtype], 1.0, 1.0, 0, 0, z.data_ptr(), ids.data_ptr(), t.data_ptr(), 0,
+                                             w.data_ptr(), loss2.data_ptr(), lse.data_ptr(), d2.data_ptr()),
+                          torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(loss2, loss) and torch.equal(d2, d)
+    assert not loss[::3].any() and not d[::3].any() and not d[::5].any()
+    y = z.double()
+    off_by(lse, torch.logsumexp(y, 1), U * (256 + 8 * (y.abs().amax(1) + torch.logsumexp(y, 1).abs())), "lse")
+    assert torch.equal(lse, moe.distill(z, ids, t)[1])
