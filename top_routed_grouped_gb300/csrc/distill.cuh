@@ -759,10 +759,10 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ready[r]);
       gather(j + DS_RING);
-      if (!wait(&sh.go[r], round)) break;
+      if (!wait(&sh.go[r], round)) return;
       if (LOSS && rank == 0) ds_loss(a, t, sl, DsStat{sl.m, sl.s}, k);
       if (GRAD) {
-        if (!wait(&sh.empty[r][1], round)) break;
+        if (!wait(&sh.empty[r][1], round)) return;
         if (sl.mul != 0.f)
           ds_places<T, LOSS>(a, sl, dz, lo, hi, sl.w,
                              DsGrad<LOSS>(sl.m, k, a.inv_tau, sl.mul), lane, 32);
@@ -771,38 +771,34 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
     }
   } else if (warp == W + 1) {
     // ------------------------------------------------------------ joiner
-    // (its lanes agree on whether a wait ran out)
-    auto came = [&](bool ok) { return __all_sync(FULL_MASK, ok) != 0; };
-    bool on = true;
-    for (int j = 0; j < rows; ++j) {
+    // One lane: what it does for a row is a chain, and it alone decides whether
+    // a wait ran out.
+    bool on = lane == 0;
+    for (int j = 0; on && j < rows; ++j) {
       const int r = j % DS_RING, q = j % DS_STATS;
       DsSlots &sl = sh.slots[r];
-      on = came((!LOSS || wait(&sh.taken[r], j / DS_RING)) && wait(&sh.ready[r], j / DS_RING));
+      on = (!LOSS || wait(&sh.taken[r], j / DS_RING)) && wait(&sh.ready[r], j / DS_RING);
       if (!on) break;
       DsStat st = {sl.lse, 1.f};
       if (LOSS) {
         st = ds_join<W>(sh.warp[r], k);
         if (ctas > 1) {
-          if (lane == 0) mbar_arrive_expect_tx(&sh.stats[q], ctas * (uint32_t)sizeof(DsStat));
-          if (lane < ctas) ds_st_async(mapa_shared(&sh.cta[q][rank], lane), st, mapa_shared(&sh.stats[q], lane));
-          __syncwarp();
-          on = came(mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status));
+          mbar_arrive_expect_tx(&sh.stats[q], ctas * (uint32_t)sizeof(DsStat));
+          for (int c = 0; c < ctas; ++c) ds_st_async(mapa_shared(&sh.cta[q][rank], c), st, mapa_shared(&sh.stats[q], c));
+          on = mbar_wait_cluster(&sh.stats[q], (j / DS_STATS) & 1, &sh.abort_flag, status);
           if (!on) break;
           st = ds_join<DS_MAX_CTAS>(sh.cta[q], k);
         }
       }
-      if (lane == 0) {
-        const bool none = LOSS ? ds_none(st) : st.m == ds_neg_inf();
-        sl.m = st.m;
-        sl.s = st.s;
-        sl.mul = !sl.any || sl.w == 0.f || none ? 0.f : sl.w * sl.total / st.s;
-        mbar_arrive(&sh.go[r]);
-      }
-      __syncwarp();
+      const bool none = LOSS ? ds_none(st) : st.m == ds_neg_inf();
+      sl.m = st.m;
+      sl.s = st.s;
+      sl.mul = !sl.any || sl.w == 0.f || none ? 0.f : sl.w * sl.total / st.s;
+      mbar_arrive(&sh.go[r]);
     }
     // Where a wait ran out the CTA stays until all of its cluster have ended or
     // given up too: until then they may write to it.
-    if (LOSS && ctas > 1 && !on) cluster_sync();
+    if (LOSS && ctas > 1 && lane == 0 && !on) cluster_sync();
   } else {
     // ------------------------------------------------------------ consumers
     constexpr int STEP = W * 32;
@@ -889,10 +885,10 @@ distill_kernel(const DistillArgs a, int shift, int span, int *status) {
       if (lane == 0) mbar_arrive(&sh.empty[r][1]);
       return true;
     };
-    bool on = !LOSS || rows == 0 || statistics(0);
-    for (int j = 0; on && j < rows; ++j) {
-      if (LOSS && j + 1 < rows) on = statistics(j + 1);
-      if (GRAD && on) on = gradient(j);
+    if (LOSS && rows > 0 && !statistics(0)) return;
+    for (int j = 0; j < rows; ++j) {
+      if (LOSS && j + 1 < rows && !statistics(j + 1)) return;
+      if (GRAD && !gradient(j)) return;
     }
   }
 }
