@@ -673,8 +673,12 @@ int moe_distill(const moe_distill_args_t *a, void *stream);
 
 /*
  * moe_distill_backward -- dlogits_t = weight_t * scale / tau * (P q - p at
- * its ids), P = sum p, from the forward's lse; one rounding.  Rows of weight
- * 0 or without slots are zeros whatever their logits hold.
+ * its ids), P = sum p, q = exp(logits / tau - lse) from the forward's lse; one
+ * rounding.  Rows of weight 0 or without slots are zeros whatever their logits
+ * hold.  lse has 24 bits, so q is known to about 2^-24 |lse| of itself: in rows
+ * of nothing but the type's lowest value lse is that value, log V is lost in
+ * it and q comes out as 1.  moe_distill_step takes q from the logits
+ * themselves and has it right there, too.
  */
 int moe_distill_backward(const moe_distill_args_t *a, void *stream);
 

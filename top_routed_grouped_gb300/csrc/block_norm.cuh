@@ -11,17 +11,21 @@
 // A group takes two rows at a time where there are enough of them, so that the
 // rounds of a sum over a row, which are latency, are shared.  Rows too long
 // for two stages are loaded straight from memory.  A row's statistics are
-// summed in an order set by H and the load width alone, so its outputs do not
-// depend on the other rows.
+// summed in an order set by H, the load width and, for up to 256 channels,
+// whether the inputs are dense, so its outputs do not depend on the other rows.
 //
 // What it moves is the floor: 29.6 us for the join of 8192 rows of 2048
 // (bfloat16 beside a float residual) at the measured copy rate, 158 us for the
 // gradient of 32768 rows with an element gate.  Measured: 38.5 us (77 %) and
-// 247 us (64 %).  The join loses its start and its last wave; the gradient is
-// bound by its instructions, some 70 for an element (unpacking, arithmetic in
-// pairs, sums over the row), not by waiting: a block of two rows takes 8600
-// cycles, of which 300 pass at its stage's barrier.  Measured on the way for
-// that gradient: row loads without stages 435 us, stages with one row a group
+// 245 us (64 %).  The join loses its start and its last wave.  The gradient
+// waits on its two rounds of sums over a row (shuffles, shared memory and, where
+// a CTA shares the row, a barrier each), with 16 warps an SM to fill them: its
+// issue slots are busy 48 % of the time and memory 43 %, while its stages are
+// there in time (300 of a block's 8600 cycles pass at their barrier).  Above
+// 4096 channels (8 or 16 pairs a thread) weights do not stay in registers, a
+// group takes one row at a time and one CTA fills the SM's registers: at 4096 x
+// 5120 ten warps an SM wait for weights and spilled registers, issue slots busy
+// 29 %.  Measured on the way for the gradient at 32768 x 2048: row loads without stages 435 us, stages with one row a group
 // 367, two 308, weights held and pairs 274, no test a load 244; one row a group
 // and five stages 289, three CTAs an SM with fewer registers 307.
 //

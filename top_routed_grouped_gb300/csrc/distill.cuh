@@ -24,8 +24,9 @@
 // only where that turns out too small (a sum above 2^40) or is -inf.  The
 // (reference, sum) pairs of threads, warps and CTAs are joined in a fixed
 // order.
-// The shape goes by the vocabulary alone, so a row's results do not depend on
-// the batch, and a thread's units do not depend on where the row starts.
+// The shape goes by the vocabulary and by whether all rows start on 16-byte
+// boundaries, so a row's results do not depend on the batch, and a thread's
+// units do not depend on where the row starts.
 // Short rows, where those hand-overs cost more than they hide, and rows too
 // long for the shared memory of a cluster take a plainer kernel: a cluster
 // (one CTA, for the short ones) for every row, many at once on an SM.

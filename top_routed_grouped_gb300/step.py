@@ -411,7 +411,9 @@ def distill(logits, t_ids, t_logits, temperature: float = 1.0, scale: float = 1.
 def distill_backward(weight, lse, logits, t_ids, t_logits, temperature: float = 1.0, scale: float = 1.0, t_lse=None,
                      out=None, stream=None):
     """dlogits of ``distill`` for upstream gradients ``weight`` [T] float32 and
-    the forward's lse.  ``out``: written there (it may be ``logits`` itself)."""
+    the forward's lse, whose 24 bits bound what is known of the softmax (not
+    for rows of nothing but the type's lowest value; ``distill_step`` takes
+    them).  ``out``: written there (it may be ``logits`` itself)."""
     return _on(logits, stream, _distill, logits, t_ids, t_logits, temperature, scale, t_lse, weight, lse, out, 2)
 
 

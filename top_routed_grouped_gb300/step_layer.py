@@ -78,7 +78,8 @@ class DistillFunction(torch.autograd.Function):
 
 def distillation_loss(logits, t_ids, t_logits, temperature: float = 1.0, scale: float = 1.0, t_lse=None):
     """Loss [T] float32 of the student's ``logits`` [T, V] against the
-    teacher's top logits (see ``distill``), differentiable in ``logits``."""
+    teacher's top logits (see ``distill``), differentiable in ``logits`` (by
+    ``distill_backward``, with its limit)."""
     return DistillFunction.apply(logits, t_ids, t_logits, temperature, scale, t_lse)
 
 
