@@ -36,6 +36,10 @@
  *                    residual sum and norm before the next block in one pass
  *   moe_distill, moe_distill_backward, moe_distill_step  distillation from a
  *                    teacher's top logits
+ *   moe_linear_ce, moe_linear_ce_backward, moe_linear_ce_step  cross entropy of
+ *                    the next token from hidden rows, without keeping logits
+ *   moe_grad_norm, moe_grad_clip, moe_grad_scale  the gradients' global norm,
+ *                    clipping
  *
  * Conventions that hold for every entry point:
  *  - Pointers named as device buffers are CUDA device (or managed) memory of
@@ -686,6 +690,110 @@ int moe_distill_backward(const moe_distill_args_t *a, void *stream);
  * once and stay on chip between the two (where they fit there). */
 int moe_distill_step(const moe_distill_args_t *a, void *stream);
 
+typedef struct moe_linear_ce_args {
+  int32_t T, D, V;      /* rows, T <= 2^24; hidden units, 1 <= D <= 16384; vocabulary, 1 <= V <= 2^20 */
+  int32_t dtype;        /* hidden, weight, dhidden */
+  int32_t dweight_dtype; /* dweight: dtype or MOE_F32 */
+  int32_t accumulate;   /* gradients: 1 adds to dweight (MOE_F32 only), 0 overwrites it */
+  int32_t targets64;    /* 1: targets are int64, 0: int32 */
+  float scale;          /* logits are scale * hidden . weight */
+  float z_loss;         /* factor of lse^2 in the loss; >= 0 */
+  int32_t reserved;     /* 0 */
+  int64_t ignore_index; /* rows with this target are left out */
+  int64_t ld_hidden, ld_weight, ld_dhidden; /* row strides, elements; 0 means D */
+  const void *hidden;   /* [T, D] dtype */
+  const void *weight;   /* [V, D] dtype: the output embedding */
+  const void *targets;  /* [T] */
+  const float *dloss;   /* [T]: d(total)/d(loss_t) (backward, step) */
+  float *loss;          /* [T] out (forward, step) */
+  float *lse;           /* [T] out of the forward, in for the backward; the step may leave it NULL */
+  void *dhidden;        /* [T, D] dtype out (backward, step) */
+  void *dweight;        /* [V, D] dense, dweight_dtype, out (backward, step) */
+} moe_linear_ce_args_t;
+
+/* The calls a workspace is asked for. */
+enum moe_linear_ce_call { MOE_CE_LOSS = 1, MOE_CE_GRAD = 2, MOE_CE_STEP = 3 };
+
+/*
+ * moe_linear_ce -- softmax cross entropy of the next token from the last
+ * block's rows.  With x_tv = scale * hidden_t . weight_v:
+ *
+ *   lse_t  = log sum_v exp(x_tv)
+ *   loss_t = lse_t - x_t[target_t] + z_loss * lse_t^2
+ *
+ * The logits live in tensor memory (MOE_BF16) or registers only: a tile of
+ * them leaves a maximum and a sum of exponentials for each row and 128 of its columns.
+ * Rows whose target is ignore_index (prompts, padding) are left out: they are
+ * not read, their loss and lse are 0.  A target outside [0, V) that is not
+ * ignore_index is left out the same way and recorded (code 7).  Logits that
+ * are not finite give a loss that is not.  Products are exact, sums FP32, in
+ * an order set by D, V and the type alone; a row's loss and lse do not depend
+ * on T, on the other rows or on how many of them are left out.
+ */
+int moe_linear_ce(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_linear_ce_backward -- gradients from the forward's lse:
+ *
+ *   g_tv    = scale * dloss_t * ((1 + 2 z_loss lse_t) exp(x_tv - lse_t) - [v = target_t])
+ *   dhidden = g weight        dweight (+)= g^T hidden
+ *
+ * The logits are recomputed a piece of the vocabulary at a time; g of one
+ * piece is in the workspace, in `dtype` (MOE_BF16: one rounding, as large
+ * as that of its two products' other operand), and both products take it from there.
+ * dhidden of rows that are left out is zero (whatever they hold), as is
+ * everything that such a row would add to dweight.  Sums are FP32; dhidden's run over chunks of the vocabulary
+ * whose bounds the type alone sets, in order, so that its rows do not depend
+ * on the batch; dweight's over the rows in order.  One rounding of each
+ * output.  T = 0 (or no row left) zeroes dweight unless `accumulate`.
+ * Workspace: moe_linear_ce_workspace_size(a, call) bytes, 256-byte aligned; it goes by
+ * T, D, V, the types, ld_weight and weight's alignment to 16 bytes (NULL:
+ * aligned; the other buffers need not be set).
+ */
+size_t moe_linear_ce_workspace_size(const moe_linear_ce_args_t *a, int32_t call);
+int moe_linear_ce_backward(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_linear_ce_step -- loss and gradients in one call, for a dloss that is
+ * known beforehand: the values of moe_linear_ce and moe_linear_ce_backward. */
+int moe_linear_ce_step(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+typedef struct moe_grads_args {
+  int32_t n;             /* tensors, 0 <= n <= 2^20 */
+  int32_t reserved;      /* 0 */
+  const void *const *in; /* host array of n device pointers */
+  void *const *out;      /* host array of n device pointers (clip, scale); out[i] may be in[i] */
+  const int64_t *numel;  /* host array: elements of each, >= 0, dense */
+  const int32_t *dtype;  /* host array: types of in */
+  const int32_t *odtype; /* host array: types of out */
+  float max_norm, eps;   /* max_norm >= 0, eps >= 0 */
+  float *norm;           /* device: out of the norm and the clip, in for the scale */
+} moe_grads_args_t;
+
+/*
+ * moe_grad_norm -- norm = sqrt(sum over all tensors and elements of g^2).
+ * Squares and short sums in FP32, longer ones in FP64; squares that FP32 cannot hold (|g|
+ * above about 1e18 or all below about 1e-15) are taken in FP64, so the norm is right wherever
+ * it fits a float.  An infinite or NaN element makes it infinite or NaN.  Fixed order of sums (set by
+ * the sizes, the order of the tensors and the device's number of SMs).  The host
+ * arrays are read before the call returns.  Workspace:
+ * moe_grad_workspace_size(a) bytes.
+ */
+size_t moe_grad_workspace_size(const moe_grads_args_t *a);
+int moe_grad_norm(const moe_grads_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_grad_clip -- the norm, then out_i = in_i * c, c = min(1, max_norm / (norm + eps)),
+ * one rounding.  Tensors that are their own output are not touched where c
+ * is 1.  A norm that is not finite goes the way of the arithmetic: infinite gives c = 0
+ * (and NaN where the element is infinite), NaN gives NaN.  Outputs may not overlap one
+ * another, nor inputs other than their own: MOE_ERR_INVALID_ARG where ranges do.
+ */
+int moe_grad_clip(const moe_grads_args_t *a, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_grad_scale -- the second half alone, for a norm on the device that was
+ * put together from several parts (ranks of an expert partition, say). */
+int moe_grad_scale(const moe_grads_args_t *a, void *stream);
+
 /*
  * moe_device_status -- read (and, if `reset`, clear) the device status word
  * of the current device.  Synchronises the device.  Returns MOE_OK when no
@@ -695,7 +803,8 @@ int moe_distill_step(const moe_distill_args_t *a, void *stream);
  * moe_route_replay, 4 = expert id repeated within a token in moe_route_replay,
  * 2 = a pipeline wait in a tensor-core kernel timed out,
  * 3 = tensor-memory allocation failed, 5 = token id out of range in moe_embed
- * or moe_embed_backward, 6 = teacher id out of range in moe_distill*.
+ * or moe_embed_backward, 6 = teacher id out of range in moe_distill*,
+ * 7 = target out of range in moe_linear_ce*.
  */
 int moe_device_status(int reset, int32_t *detail);
 

@@ -13,6 +13,9 @@ with ``python -m top_routed_grouped_gb300.build`` (or ``__graft_entry__.build()`
 The operators around the layer (``step.py``) are reached the same way:
 ``embed``, ``block_norm``, ``distill`` and their gradients, and under autograd
 (``step_layer.py``) ``TokenEmbedding``, ``BlockNorm``, ``distillation_loss``.
+So is the end of a training step (``train.py``): ``linear_cross_entropy`` with
+its gradient and step, ``grad_norm``, ``clip_grads``, ``scale_grads``, and
+(``train_layer.py``) ``cross_entropy_loss``, ``LMHead``, ``clip_grad_norm_``.
 
 ``MoELayer`` / ``MoEFunction`` (``layer.py``): the layer as a torch module
 whose autograd Function calls ``moe_forward`` and ``moe_backward``.
@@ -36,7 +39,8 @@ EXPORTED = ("moe_workspace_size", "moe_status_string", "moe_route", "moe_permute
             "moe_backward_ep", "moe_grouped_ffn_etp", "moe_etp_reduce", "moe_grouped_ffn_etp_fused",
             "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward", "moe_embed",
             "moe_embed_workspace_size", "moe_embed_backward", "moe_distill", "moe_distill_backward",
-            "moe_distill_step")
+            "moe_distill_step", "moe_linear_ce", "moe_linear_ce_workspace_size", "moe_linear_ce_backward",
+            "moe_linear_ce_step", "moe_grad_norm", "moe_grad_workspace_size", "moe_grad_clip", "moe_grad_scale")
 
 _vp = ctypes.c_void_p
 
@@ -120,6 +124,15 @@ def lib() -> ctypes.CDLL:
                 "moe_distill": ([ctypes.c_char_p, _vp], ctypes.c_int),
                 "moe_distill_backward": ([ctypes.c_char_p, _vp], ctypes.c_int),
                 "moe_distill_step": ([ctypes.c_char_p, _vp], ctypes.c_int),
+                # The end of a training step, the same way (see train.py).
+                "moe_linear_ce": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_linear_ce_workspace_size": ([ctypes.c_char_p, ctypes.c_int32], ctypes.c_size_t),
+                "moe_linear_ce_backward": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_linear_ce_step": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_grad_norm": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_grad_workspace_size": ([ctypes.c_char_p], ctypes.c_size_t),
+                "moe_grad_clip": ([ctypes.c_char_p, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+                "moe_grad_scale": ([ctypes.c_char_p, _vp], ctypes.c_int),
             }
             for name, (args, res) in sigs.items():
                 fn = getattr(L, name)
@@ -440,6 +453,9 @@ def backward(fwd: dict, dy, x, w_router, w_shared_gate, w_gate_up, w_down, ws_ga
 _STEP = ("block_norm", "block_norm_backward", "embed", "embed_backward", "distill", "distill_backward", "distill_step",
          "moe_block_norm", "moe_block_norm_workspace_size", "moe_block_norm_backward", "moe_embed",
          "moe_embed_workspace_size", "moe_embed_backward", "moe_distill", "moe_distill_backward", "moe_distill_step")
+_TRAIN = ("linear_cross_entropy", "linear_cross_entropy_backward", "linear_cross_entropy_step", "grad_norm",
+          "clip_grads", "scale_grads", "moe_linear_ce", "moe_linear_ce_workspace_size", "moe_linear_ce_backward",
+          "moe_linear_ce_step", "moe_grad_norm", "moe_grad_workspace_size", "moe_grad_clip", "moe_grad_scale")
 
 
 def __getattr__(name):
@@ -452,6 +468,13 @@ def __getattr__(name):
     if name in ("TokenEmbedding", "BlockNorm", "distillation_loss"):
         from . import step_layer
         return getattr(step_layer, name)
+    if name in ("cross_entropy_loss", "LMHead", "clip_grad_norm_"):
+        from . import train_layer
+        return getattr(train_layer, name)
+    if name in _TRAIN:
+        from . import train
+        globals().update({n: getattr(train, n) for n in _TRAIN})
+        return globals()[name]
     if name in _STEP:
         from . import step
         globals().update({n: getattr(step, n) for n in _STEP})

@@ -14,7 +14,7 @@ constexpr unsigned FULL_MASK = 0xffffffffu;
 
 // Device status codes (documented with moe_device_status in moe.h).
 enum : int { STATUS_BAD_EXPERT_ID = 1, STATUS_WAIT_TIMEOUT = 2, STATUS_TMEM_ALLOC = 3, STATUS_REPEATED_EXPERT_ID = 4,
-             STATUS_BAD_TOKEN_ID = 5, STATUS_BAD_TEACHER_ID = 6 };
+             STATUS_BAD_TOKEN_ID = 5, STATUS_BAD_TEACHER_ID = 6, STATUS_BAD_TARGET = 7 };
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }

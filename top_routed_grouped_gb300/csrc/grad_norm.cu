@@ -1,0 +1,312 @@
+// The global 2-norm of many tensors, and their scaling to a norm.
+//
+//   norm = sqrt(sum g^2)       out = in * min(1, max_norm / (norm + eps))
+//
+// Bound by memory: each gradient is read once for the norm and once more for
+// the scaling, which starts at the end where the norm has stopped, so that
+// what L2 still holds is read from there.  All tensors go in one launch: the
+// table of them is a kernel argument (nothing to copy to the device, and a
+// captured graph has it inside), chunks of a few thousand elements are dealt
+// out to the CTAs in turn, and a chunk finds its tensor by bisection.
+//
+// Squares are summed in FP32 over at most 128 elements of a thread, then in
+// FP64.  Where such a sum is out of the range in which FP32 squares keep their
+// bits (some |g| above 1e15, or all of them below 1e-12) the chunk's elements
+// are read again and summed in FP64.  No atomics: each CTA leaves one partial
+// sum, and all of them are added in one order.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_host.h"
+
+namespace moe {
+
+constexpr int GN_THREADS = 256;
+constexpr int GN_CTAS = 8;             // CTAs a SM
+constexpr int GN_MAX_CHUNK = 128 * GN_THREADS, GN_MIN_CHUNK = 8 * GN_THREADS;
+
+// CAP tensors: 28 bytes each, of the 32 KB that a kernel's arguments may take.
+template <int CAP>
+struct GradTable {
+  const void *in[CAP];
+  void *out[CAP];
+  int64_t size[CAP];    // elements
+  int first[CAP + 1];   // chunks before this tensor's
+  uint32_t f32[CAP / 32], of32[CAP / 32];
+  int n, chunk;         // tensors; elements a chunk
+};
+constexpr int GN_SMALL = 64, GN_LARGE = 1024;
+static_assert(sizeof(GradTable<GN_LARGE>) <= 32000, "a kernel's arguments");
+
+// The tensor of a chunk: the last one whose first chunk is not behind it.
+template <int CAP>
+__device__ inline int tensor_of(const GradTable<CAP> &t, int chunk) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Elements before the first 16-byte boundary.
+template <typename E>
+__device__ inline int head_of(const E *p, int64_t n) {
+  const int h = (int)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(E));
+  return n < h ? (int)n : h;
+}
+
+__device__ inline double warp_sum(double v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+  return v;
+}
+
+// The sum over the CTA, in every thread.
+__device__ inline double cta_sum(double v) {
+  __shared__ double sh[GN_THREADS / 32];
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int i = 0; i < GN_THREADS / 32; ++i) s += sh[i];
+  __syncthreads();
+  return s;
+}
+
+// Squares of this thread's elements of chunk c of a tensor: the head (chunk
+// 0), units of 16 bytes, the tail (the last chunk).
+template <typename E>
+__device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks, int chunk) {
+  constexpr int N = Vec16<E>::N;
+  const int head = head_of(p, n);
+  const int64_t units = (n - head) / N, per = chunk / N;
+  const int64_t u0 = c * per, u1 = c + 1 == nchunks ? units : min(units, u0 + per);
+  const uint4 *v = (const uint4 *)(p + head);
+  const int tail = (int)(n - head - units * N);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t any = 0;  // a bit that is not a sign
+  auto unit = [&](const uint4 &w, float &a, float &b) {
+    float x[N];
+    Vec16<E>::unpack(w, x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      a = fmaf(x[i], x[i], a);
+      b = fmaf(x[i + 1], x[i + 1], b);
+    }
+    any |= w.x | w.y | w.z | w.w;
+  };
+  int64_t u = u0 + threadIdx.x;
+  for (; u + 3 * GN_THREADS < u1; u += 4 * GN_THREADS) {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(v + u + i * GN_THREADS);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unit(w[i], s[i & 2], s[(i & 2) + 1]);
+  }
+  for (; u < u1; u += GN_THREADS) unit(__ldg(v + u), s[0], s[1]);
+  // At most one element of the head and one of the tail a thread.
+  float edge[2] = {0.f, 0.f};
+  if (c == 0 && (int)threadIdx.x < head) edge[0] = Elem<E>::load(p + threadIdx.x);
+  if (c + 1 == nchunks && (int)threadIdx.x < tail) edge[1] = Elem<E>::load(p + head + units * N + threadIdx.x);
+  s[2] = fmaf(edge[0], edge[0], s[2]);
+  s[3] = fmaf(edge[1], edge[1], s[3]);
+  any |= __float_as_uint(edge[0]) | __float_as_uint(edge[1]);
+  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+  const uint32_t signs = sizeof(E) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+  if (sum < 1e30f && (sum > 1e-24f || !(any & signs))) return sum;
+  double d = (double)edge[0] * edge[0] + (double)edge[1] * edge[1];
+  for (u = u0 + threadIdx.x; u < u1; u += GN_THREADS) {
+    float x[N];
+    Vec16<E>::unpack(__ldg(v + u), x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) d += (double)x[i] * x[i];
+  }
+  return d;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(GN_THREADS)
+grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, double *part) {
+  griddep_launch();
+  griddep_wait();
+  const int total = t.first[t.n];
+  double sum = 0;
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
+    const int i = tensor_of(t, c), first = t.first[i], k = t.first[i + 1] - first;
+    if (t.f32[i >> 5] >> (i & 31) & 1) sum += chunk_squares((const float *)t.in[i], t.size[i], c - first, k, t.chunk);
+    else sum += chunk_squares((const __nv_bfloat16 *)t.in[i], t.size[i], c - first, k, t.chunk);
+  }
+  sum = cta_sum(sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+// All partial sums, in one order, by a CTA.
+__device__ inline float norm_of(const double *part, int n) {
+  double s = 0;
+  for (int i = threadIdx.x; i < n; i += GN_THREADS) s += part[i];
+  return (float)sqrt(cta_sum(s));
+}
+
+__global__ void __launch_bounds__(GN_THREADS) grad_norm_finish_kernel(const double *part, int n, float *norm) {
+  griddep_launch();
+  griddep_wait();
+  const float r = norm_of(part, n);
+  if (threadIdx.x == 0) *norm = r;
+}
+
+template <typename I, typename O>
+__device__ inline void chunk_scale(const I *in, O *out, int64_t n, int c, int nchunks, int chunk, float f) {
+  // Groups of eight elements that start on a 16-byte boundary of the output.
+  const int head = head_of(out, n);
+  const int64_t groups = (n - head) / 8, per = chunk / 8;
+  const int64_t g0 = c * per, g1 = c + 1 == nchunks ? groups : min(groups, g0 + per);
+  const int tail = (int)(n - head - groups * 8);
+  const I *pi = in + head;
+  O *po = out + head;
+  constexpr int NI = Vec16<I>::N, NO = Vec16<O>::N;
+  const bool wide = ((uintptr_t)pi & 15) == 0;
+  for (int64_t g = g0 + threadIdx.x; g < g1; g += 2 * GN_THREADS) {
+    float x[2][8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t q = g + j * GN_THREADS;
+      if (q >= g1) break;
+      if (wide) {
+#pragma unroll
+        for (int i = 0; i < 8 / NI; ++i) Vec16<I>::load(pi + q * 8 + i * NI, *(float(*)[NI])&x[j][i * NI]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] = Elem<I>::load(pi + q * 8 + i);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t q = g + j * GN_THREADS;
+      if (q >= g1) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] *= f;
+#pragma unroll
+      for (int i = 0; i < 8 / NO; ++i) Vec16<O>::store(po + q * 8 + i * NO, *(float(*)[NO])&x[j][i * NO]);
+    }
+  }
+  if (c == 0 && (int)threadIdx.x < head)
+    out[threadIdx.x] = Elem<O>::from_f32(Elem<I>::load(in + threadIdx.x) * f);
+  if (c + 1 == nchunks && (int)threadIdx.x < tail) {
+    const int64_t at = groups * 8 + threadIdx.x;
+    po[at] = Elem<O>::from_f32(Elem<I>::load(pi + at) * f);
+  }
+}
+
+// part: the partial sums (the clip; CTA 0 writes the norm), or NULL: the norm is given.
+template <int CAP>
+__global__ void __launch_bounds__(GN_THREADS)
+grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const double *part, int nparts, float max_norm, float eps,
+                  float *norm) {
+  griddep_launch();
+  griddep_wait();
+  float r;
+  if (part) {
+    r = norm_of(part, nparts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = r;
+  } else {
+    r = *norm;
+  }
+  float f = max_norm / (r + eps);
+  if (f > 1.f) f = 1.f;  // (NaN stays)
+  const int total = t.first[t.n];
+  for (int c = total - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+    const int i = tensor_of(t, c), first = t.first[i], k = t.first[i + 1] - first;
+    if (f == 1.f && t.in[i] == t.out[i]) continue;
+    const int64_t n = t.size[i];
+    const bool a = t.f32[i >> 5] >> (i & 31) & 1, b = t.of32[i >> 5] >> (i & 31) & 1;
+    if (a && b) chunk_scale((const float *)t.in[i], (float *)t.out[i], n, c - first, k, t.chunk, f);
+    else if (a) chunk_scale((const float *)t.in[i], (__nv_bfloat16 *)t.out[i], n, c - first, k, t.chunk, f);
+    else if (b) chunk_scale((const __nv_bfloat16 *)t.in[i], (float *)t.out[i], n, c - first, k, t.chunk, f);
+    else chunk_scale((const __nv_bfloat16 *)t.in[i], (__nv_bfloat16 *)t.out[i], n, c - first, k, t.chunk, f);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+static int launches(const GradList &a) { return std::max(1, (int)ceil_div(a.n, GN_LARGE)); }
+
+// CTAs of a launch at most.
+static int most_ctas() { return std::max(1, device_sms()) * GN_CTAS; }
+
+size_t grad_scratch_bytes(const GradList &a) { return (size_t)launches(a) * most_ctas() * sizeof(double); }
+
+// Elements a chunk: enough chunks for every CTA to have some, up to 128 elements a thread.
+static int chunk_of(const GradList &a) {
+  int64_t total = 0;
+  for (int i = 0; i < a.n; ++i) total += a.numel[i];
+  const int64_t want = total / most_ctas();
+  return (int)std::min<int64_t>(GN_MAX_CHUNK, std::max<int64_t>(GN_MIN_CHUNK, round_up(want, GN_MIN_CHUNK)));
+}
+
+// Tensors [i0, i1) of the list; the number of chunks.
+template <int CAP>
+static int fill(GradTable<CAP> &t, const GradList &a, int i0, int i1, int chunk, bool out) {
+  t.n = 0;
+  t.chunk = chunk;
+  int chunks = 0;
+  for (int i = 0; i < CAP / 32; ++i) t.f32[i] = t.of32[i] = 0;
+  for (int i = i0; i < i1; ++i) {
+    if (a.numel[i] == 0) continue;
+    const int k = t.n++;
+    t.in[k] = a.in[i];
+    t.out[k] = out ? a.out[i] : nullptr;
+    t.size[k] = a.numel[i];
+    t.first[k] = chunks;
+    chunks += (int)ceil_div(a.numel[i], chunk);
+    if (a.dtype[i] == 0) t.f32[k >> 5] |= 1u << (k & 31);
+    if (out && a.odtype[i] == 0) t.of32[k >> 5] |= 1u << (k & 31);
+  }
+  t.first[t.n] = chunks;
+  return chunks;
+}
+
+template <int CAP>
+static cudaError_t run(const GradList &a, int mode, double *part, cudaStream_t stream) {
+  const int chunk = chunk_of(a), most = most_ctas();
+  const int nl = (int)ceil_div(a.n, CAP);
+  GradTable<CAP> t;
+  cudaError_t e;
+  int parts = 0;
+  if (mode & GRAD_NORM) {
+    for (int l = 0; l < nl; ++l) {
+      const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), chunk, false);
+      if (!chunks) continue;
+      const int grid = std::min(chunks, most);
+      if ((e = launch_pdl(grad_norm_kernel<CAP>, dim3(grid), dim3(GN_THREADS), 0, stream, t, part + parts)) != cudaSuccess)
+        return e;
+      parts += grid;
+    }
+  }
+  if (mode == GRAD_NORM)
+    return launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(GN_THREADS), 0, stream, (const double *)part, parts, a.norm);
+  const double *p = mode & GRAD_NORM ? part : nullptr;
+  bool any = false;
+  for (int l = nl - 1; l >= 0; --l) {
+    const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), chunk, true);
+    if (!chunks && (l || any)) continue;  // (of an empty list the norm is still written)
+    any = true;
+    e = launch_pdl(grad_scale_kernel<CAP>, dim3(std::max(1, std::min(chunks, most))), dim3(GN_THREADS), 0, stream, t, p,
+                   parts, a.max_norm, a.eps, a.norm);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_grads(const GradList &a, int mode, void *scratch, cudaStream_t stream) {
+  if (a.n == 0 && mode != GRAD_SCALE)
+    return launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(GN_THREADS), 0, stream, (const double *)scratch, 0, a.norm);
+  return a.n <= GN_SMALL ? run<GN_SMALL>(a, mode, (double *)scratch, stream)
+                         : run<GN_LARGE>(a, mode, (double *)scratch, stream);
+}
+
+}  // namespace moe

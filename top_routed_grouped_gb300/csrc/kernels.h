@@ -240,4 +240,35 @@ enum { DISTILL_LOSS = 1, DISTILL_GRAD = 2 };
 // mode: DISTILL_LOSS (loss, lse), DISTILL_GRAD (dlogits from lse) or both.
 cudaError_t launch_distill(const DistillArgs &a, int mode, int *status, cudaStream_t stream);
 
+// ---- linear_ce.cu, linear_ce_tc.cu, linear_ce_simt.cu ----
+struct CeArgs {
+  int T, D, V;
+  bool f32, gf32;  // hidden, weight, dhidden; dweight: float (else bf16)
+  bool accumulate, targets64;
+  float scale, z_loss;
+  int64_t ignore_index, ld_h, ld_w, ld_dh;
+  const void *hidden, *weight, *targets;
+  const float *dloss;
+  float *loss, *lse;
+  void *dh, *dw;
+};
+enum { CE_LOSS = 1, CE_GRAD = 2 };  // what a call computes: either or both
+constexpr int CE_MAX_T = 1 << 24, CE_MAX_D = 16384, CE_MAX_V = 1 << 20;
+size_t ce_scratch_bytes(const CeArgs &a, int mode);
+cudaError_t launch_linear_ce(const CeArgs &a, int mode, void *scratch, int *status, cudaStream_t stream);
+
+// ---- grad_norm.cu ----
+struct GradList {
+  int n;
+  const void *const *in;
+  void *const *out;
+  const int64_t *numel;
+  const int32_t *dtype, *odtype;
+  float max_norm, eps;
+  float *norm;
+};
+enum { GRAD_NORM = 1, GRAD_SCALE = 2 };
+size_t grad_scratch_bytes(const GradList &a);
+cudaError_t launch_grads(const GradList &a, int mode, void *scratch, cudaStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,300 @@
+// Cross entropy of the next token from hidden rows: the rows that count, the
+// join of the tiles' statistics, and the order of the launches.
+//
+//   x = scale h W^T    lse = log sum exp x    loss = lse - x[target] + z lse^2
+//   g = scale dloss ((1 + 2 z lse) exp(x - lse) - onehot)    dh = g W    dW = g^T h
+//
+// Rows that count are copied together first, in order: rows that are left out
+// cost nothing afterwards, what they hold reaches no product, and the copies
+// have the alignment that the tensor maps want whatever the caller's have.
+// Then one product leaves a maximum and a sum of exponentials for each row and
+// 128 columns (8 bytes for 256 of logits), which are joined per row; the
+// gradient recomputes the logits a piece of the vocabulary at a time (2 TDV of
+// the 8 TDV operations, where keeping them would take 4 TV bytes) and takes
+// both products of the piece while it is near L2's size.
+#include <math.h>
+
+#include "linear_ce.h"
+
+namespace moe {
+
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
+
+// ------------------------------------------------------------- which rows count
+// One CTA: place[t] is row t's place among those that count (-1: left out),
+// row_of the reverse; the order is kept.  T reads of 4 or 8 bytes: latency.
+template <typename Id>
+__global__ void __launch_bounds__(1024)
+ce_places_kernel(int T, int V, int64_t ignore, const Id *targets, int *count, int *row_of, int *place, CeRow *rows,
+                 float *loss, float *lse, int *status) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ int sums[33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int base = 0;
+  for (int t0 = 0; t0 < T; t0 += 1024) {
+    const int t = t0 + threadIdx.x;
+    const int64_t id = t < T ? (int64_t)targets[t] : ignore;
+    const bool in = id >= 0 && id < V;
+    const bool keep = t < T && id != ignore && in;
+    if (t < T && id != ignore && !in) record_status(status, STATUS_BAD_TARGET);
+    const unsigned vote = __ballot_sync(FULL_MASK, keep);
+    if (lane == 0) sums[warp] = __popc(vote);
+    __syncthreads();
+    if (warp == 0) {
+      const int own = sums[lane];
+      int s = own;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(FULL_MASK, s, d);
+        if (lane >= d) s += o;
+      }
+      sums[lane] = s - own;
+      if (lane == 31) sums[32] = s;
+    }
+    __syncthreads();
+    if (t < T) {
+      const int at = base + sums[warp] + __popc(vote & lanemask_lt());
+      place[t] = keep ? at : -1;
+      if (keep) {
+        row_of[at] = t;
+        rows[at].target = (int)id;
+      } else {
+        if (loss) loss[t] = 0.f;
+        if (lse) lse[t] = 0.f;
+      }
+    }
+    base += sums[32];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *count = base;
+  // The padding of the last row tile.
+  const int end = (int)round_up(base, CE_ROWS);
+  for (int i = base + threadIdx.x; i < end; i += 1024) rows[i] = CeRow{0.f, 0.f, 0.f, -1};
+}
+
+// A warp a row: the rows that count to their places, zeros behind them (in
+// the columns up to dp and the rows up to the tile's end), zeros into dhidden
+// where a row is left out, and, with the forward's lse, what the gradient
+// needs of a row.
+template <typename E>
+__global__ void __launch_bounds__(256)
+ce_rows_kernel(int T, int D, int64_t ld_h, int64_t dp, int64_t ld_dh, const E *h, E *hc, E *dh, const int *count,
+               const int *place, CeRow *rows, const float *lse, const float *dloss, float scale, float z, bool wide) {
+  constexpr int N = Vec16<E>::N;
+  griddep_launch();
+  griddep_wait();
+  const int t = (int)(((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  int at;
+  const E *src = nullptr;
+  if (t < T) {
+    at = place[t];
+    if (at < 0) {
+      if (dh)
+        for (int c = lane; c < D; c += 32) dh[t * ld_dh + c] = Elem<E>::from_f32(0.f);
+      return;
+    }
+    src = h + t * ld_h;
+    if (dloss && lse && lane == 0) {
+      const float l = lse[t], d = scale * dloss[t];
+      rows[at].lse2 = l * LOG2E;
+      rows[at].c = d * fmaf(2.f * z, l, 1.f);
+      rows[at].c1 = d;
+    }
+  } else {
+    at = *count + (t - T);
+    if (at >= (int)round_up(*count, CE_ROWS)) return;
+  }
+  E *dst = hc + at * dp;
+  if (src && wide) {  // every row starts on a 16-byte boundary and D is whole units
+    const int nu = D / N;
+    for (int u = lane; u < (int)(dp / N); u += 32)
+      ((uint4 *)dst)[u] = u < nu ? ((const uint4 *)src)[u] : make_uint4(0, 0, 0, 0);
+  } else {
+    for (int c = lane; c < (int)dp; c += 32) dst[c] = src && c < D ? src[c] : Elem<E>::from_f32(0.f);
+  }
+}
+
+// Weights whose rows do not start on 16-byte boundaries, copied to where they do.
+__global__ void __launch_bounds__(256)
+ce_weight_copy_kernel(int64_t V, int D, int64_t ld, int64_t ldw, const __nv_bfloat16 *w, __nv_bfloat16 *wc) {
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  for (int64_t v = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; v < V; v += (int64_t)gridDim.x * 8)
+    for (int c = lane; c < (int)ldw; c += 32)
+      wc[v * ldw + c] = c < D ? w[v * ld + c] : __float2bfloat16_rn(0.f);
+}
+
+// ------------------------------------------------------------- the rows' statistics
+// A CTA joins 32 rows: 32 warps take every 32nd part each (a row a lane: 256
+// bytes a load), then the warps' results are joined in order.
+__global__ void __launch_bounds__(1024)
+ce_join_kernel(const int *count, int nparts, int tpad, const float2 *part, const float *xt, const int *row_of,
+               CeRow *rows, float *loss, float *lse, const float *dloss, float scale, float z) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float2 sh[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = *count, r = blockIdx.x * 32 + lane;
+  if ((int)blockIdx.x * 32 >= n) return;
+  float m = -INFINITY, s = 0.f;
+  auto add = [](float &m, float &s, float2 p) {
+    const float big = fmaxf(m, p.x);
+    if (big == -INFINITY) return;
+    s = s * exp2f(m - big) + p.y * exp2f(p.x - big);
+    m = big;
+  };
+  for (int i = warp; i < nparts; i += 32) add(m, s, part[(int64_t)i * tpad + r]);
+  sh[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp != 0 || r >= n) return;
+  m = -INFINITY;
+  s = 0.f;
+  for (int w = 0; w < 32; ++w) add(m, s, sh[w][lane]);
+  // m and the target's logit are in units of log 2: their difference is exact
+  // where it is small, and 0 where the target has the largest logit.
+  const float ln = logf(s), l = fmaf(m, LN2, ln);
+  const int t = row_of[r];
+  loss[t] = fmaf(m - xt[r], LN2, ln) + z * l * l;
+  if (lse) lse[t] = l;
+  if (dloss) {
+    const float d = scale * dloss[t];
+    rows[r].lse2 = l * LOG2E;
+    rows[r].c = d * fmaf(2.f * z, l, 1.f);
+    rows[r].c1 = d;
+  }
+}
+
+// dhidden's sums of the chunks of one piece, in order, onto those of the pieces before.
+template <typename E>
+__global__ void __launch_bounds__(256)
+ce_planes_kernel(const int *count, const int *row_of, int D, int64_t dp, int tpad, int nplanes, const float *planes,
+                 float *acc, E *dh, int64_t ld_dh, bool first, bool last) {
+  griddep_launch();
+  griddep_wait();
+  const int n = *count;
+  const int64_t plane = (int64_t)tpad * dp;
+  for (int64_t r = blockIdx.y; r < n; r += gridDim.y) {
+    const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (c >= D) continue;
+    const int64_t at = r * dp + c;
+    float4 s = first ? *(const float4 *)(planes + at) : *(const float4 *)(acc + at);
+#pragma unroll 4
+    for (int i = first ? 1 : 0; i < nplanes; ++i) {
+      const float4 p = *(const float4 *)(planes + i * plane + at);
+      s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+    }
+    if (!last) {
+      *(float4 *)(acc + at) = s;
+      continue;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    E *out = dh + row_of[r] * ld_dh + c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < D) out[j] = Elem<E>::from_f32(v[j]);
+  }
+}
+
+// ------------------------------------------------------------- the call
+size_t ce_scratch_bytes(const CeArgs &a, int mode) { return ce_layout(a, mode).bytes; }
+
+template <typename E>
+static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaStream_t stream) {
+  const CeLayout l = ce_layout(a, mode);
+  const bool grad = mode & CE_GRAD, loss = mode & CE_LOSS;
+  int *count = (int *)(w + l.count), *row_of = (int *)(w + l.row_of), *place = (int *)(w + l.place);
+  CeRow *rows = (CeRow *)(w + l.rows);
+  E *hc = (E *)(w + l.hc);
+  cudaError_t e;
+  float *lo = loss ? a.loss : nullptr, *ls = loss ? a.lse : nullptr;
+  if (a.targets64)
+    e = launch_pdl(ce_places_kernel<int64_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
+                   (const int64_t *)a.targets, count, row_of, place, rows, lo, ls, status);
+  else
+    e = launch_pdl(ce_places_kernel<int32_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
+                   (const int32_t *)a.targets, count, row_of, place, rows, lo, ls, status);
+  if (e != cudaSuccess) return e;
+  const bool wide = a.D % Vec16<E>::N == 0 && a.ld_h % Vec16<E>::N == 0 && ((uintptr_t)a.hidden & 15) == 0;
+  e = launch_pdl(ce_rows_kernel<E>, dim3((unsigned)ceil_div((int64_t)a.T + CE_ROWS, 8)), dim3(256), 0, stream, a.T, a.D,
+                 a.ld_h, l.dp, a.ld_dh, (const E *)a.hidden, hc, grad ? (E *)a.dh : (E *)nullptr, (const int *)count,
+                 (const int *)place, rows, (const float *)(grad && !loss ? a.lse : nullptr), a.dloss, a.scale, a.z_loss,
+                 wide);
+  if (e != cudaSuccess) return e;
+  if (l.ldw) {
+    e = launch_pdl(ce_weight_copy_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(a.V, 8), 8 * 152)), dim3(256), 0,
+                   stream, (int64_t)a.V, a.D, a.ld_w, l.ldw, (const __nv_bfloat16 *)a.weight, (__nv_bfloat16 *)(w + l.wc));
+    if (e != cudaSuccess) return e;
+  }
+  CeMats m = {};
+  m.V = a.V;
+  m.D = a.D;
+  m.tpad = l.tpad;
+  m.ldh = l.dp;
+  m.ldw = l.ldw ? l.ldw : a.ld_w;
+  m.ldg = l.ldg;
+  m.count = count;
+  m.row_of = row_of;
+  m.rows = rows;
+  m.h = hc;
+  m.w = l.ldw ? w + l.wc : a.weight;
+  m.g = w + l.g;
+  m.scale = a.scale;
+  m.part = (float2 *)(w + l.part);
+  m.xt = (float *)(w + l.xt);
+  m.gf32 = a.gf32;
+  m.accumulate = a.accumulate;
+  m.dh = a.dh;
+  m.dw = a.dw;
+  m.ld_dh = a.ld_dh;
+  m.planes = (float *)(w + l.acc);
+  m.acc = m.planes + (l.per_piece > 1 ? (int64_t)l.per_piece * l.tpad * l.dp : 0);
+  m.status = status;
+  if (loss) {
+    if ((e = a.f32 ? ce_simt_stats(m, stream) : ce_tc_stats(m, stream)) != cudaSuccess) return e;
+    e = launch_pdl(ce_join_kernel, dim3(l.tpad / 32), dim3(1024), 0, stream, (const int *)count, l.nparts, l.tpad,
+                   (const float2 *)m.part, (const float *)m.xt, (const int *)row_of, rows, a.loss, a.lse,
+                   (const float *)(grad ? a.dloss : nullptr), a.scale, a.z_loss);
+    if (e != cudaSuccess) return e;
+  }
+  if (!grad) return cudaSuccess;
+  for (int i = 0; i < l.npieces; ++i) {
+    CePiece p = {};
+    p.chunk = l.chunk;
+    p.v0 = i * l.per_piece * l.chunk;
+    p.n = std::min(l.per_piece * l.chunk, a.V - p.v0);
+    p.nchunks = (int)ceil_div(p.n, l.chunk);
+    p.first = i == 0;
+    p.last = i + 1 == l.npieces;
+    CeMats mp = m;
+    if (l.per_piece == 1) mp.planes = nullptr;
+    if ((e = a.f32 ? ce_simt_logits_grad(mp, p, stream) : ce_tc_logits_grad(mp, p, stream)) != cudaSuccess) return e;
+    if ((e = a.f32 ? ce_simt_grads(mp, p, stream) : ce_tc_grads(mp, p, stream)) != cudaSuccess) return e;
+    if (l.per_piece > 1) {
+      e = launch_pdl(ce_planes_kernel<E>, dim3((unsigned)ceil_div(a.D, 1024), (unsigned)std::min(l.tpad, 16384)), dim3(256),
+                     0, stream, (const int *)count, (const int *)row_of, a.D, l.dp, l.tpad, p.nchunks,
+                     (const float *)mp.planes, mp.acc, (E *)a.dh, a.ld_dh, p.first, p.last);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+// dweight where there are no rows at all.
+__global__ void __launch_bounds__(256) ce_zero_kernel(int64_t bytes2, uint16_t *p) {
+  griddep_launch();
+  griddep_wait();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < bytes2; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+cudaError_t launch_linear_ce(const CeArgs &a, int mode, void *scratch, int *status, cudaStream_t stream) {
+  if (a.T == 0) {
+    if (!(mode & CE_GRAD) || a.accumulate) return cudaSuccess;
+    return launch_pdl(ce_zero_kernel, dim3(1216), dim3(256), 0, stream, (int64_t)a.V * a.D * (a.gf32 ? 2 : 1),
+                      (uint16_t *)a.dw);
+  }
+  return a.f32 ? run<float>(a, mode, (uint8_t *)scratch, status, stream)
+               : run<__nv_bfloat16>(a, mode, (uint8_t *)scratch, status, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,228 @@
+// The linear cross entropy's matrix products in float, on CUDA cores.
+//
+// Products of floats need 24 bits, which the tensor cores' formats do not
+// hold, so float models (small ones, and checks) take FFMA: tiles of 128 x
+// 128 outputs, 256 threads with 8 x 8 outputs each, K steps of 16 through
+// shared memory, one step ahead in registers.  The epilogues are those of the
+// tensor-core kernels: the same statistics per 128 columns, the same pieces.
+// Each output is summed over K in order.
+#include "linear_ce.h"
+
+namespace moe {
+
+constexpr int SM_STATS = 0, SM_LOGITS = 1, SM_DH = 2, SM_DW = 3;
+constexpr int ST = 128, SK = 16;
+
+struct SimtParams {
+  CeMats m;
+  CePiece p;
+  int nparts;
+};
+
+// Four consecutive floats of a matrix, those past `n` as zeros.
+__device__ inline float4 four(const float *p, int n, bool wide) {
+  if (n >= 4 && wide) return *(const float4 *)p;
+  return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+}
+
+// An operand of one tile: 128 rows (of the output's rows or columns) x 16 K,
+// two units of four floats a thread.  KMAJOR: K runs along the row.
+template <bool KMAJOR>
+struct Operand {
+  const float *p;
+  int64_t ld;
+  int rows, k;  // valid extents from the tile's origin
+  bool wide;    // units are on 16-byte boundaries
+  float4 r[2];
+  __device__ void load(int k0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int u = threadIdx.x + 256 * i;
+      if (KMAJOR) {
+        const int row = u >> 2, kk = k0 + (u & 3) * 4;
+        r[i] = row < rows ? four(p + row * ld + kk, k - kk, wide) : make_float4(0, 0, 0, 0);
+      } else {
+        const int kk = k0 + (u >> 5), row = (u & 31) * 4;
+        r[i] = kk < k ? four(p + kk * ld + row, rows - row, wide) : make_float4(0, 0, 0, 0);
+      }
+    }
+  }
+  __device__ void store(float (*s)[ST + 4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int u = threadIdx.x + 256 * i;
+      if (KMAJOR) {
+        const int row = u >> 2, kk = (u & 3) * 4;
+        s[kk][row] = r[i].x;
+        s[kk + 1][row] = r[i].y;
+        s[kk + 2][row] = r[i].z;
+        s[kk + 3][row] = r[i].w;
+      } else {
+        *(float4 *)&s[u >> 5][(u & 31) * 4] = r[i];
+      }
+    }
+  }
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(256, 2)
+ce_simt_kernel(const SimtParams a) {
+  griddep_launch();
+  griddep_wait();
+  const CeMats &m = a.m;
+  const CePiece &pc = a.p;
+  __shared__ float sA[2][SK][ST + 4], sB[2][SK][ST + 4];
+  const int count = *m.count;
+  const int r0 = blockIdx.x * ST, c0 = blockIdx.y * ST;  // the tile's rows and columns
+  if (KIND != SM_DW && r0 >= (KIND == SM_LOGITS ? (int)round_up(count, CE_ROWS) : count)) return;
+  const float *h = (const float *)m.h, *w = (const float *)m.w, *g = (const float *)m.g;
+  const bool ww = m.ldw % 4 == 0 && ((uintptr_t)m.w & 15) == 0;
+  constexpr bool AK = KIND != SM_DW, BK = KIND == SM_STATS || KIND == SM_LOGITS;
+  Operand<AK> A;
+  Operand<BK> B;
+  A.wide = true;
+  const int v0 = pc.v0;
+  int k;
+  if (KIND == SM_STATS || KIND == SM_LOGITS) {
+    k = m.D;
+    A.p = h + r0 * m.ldh; A.ld = m.ldh; A.rows = m.tpad - r0;
+    B.p = w + (v0 + c0) * m.ldw; B.ld = m.ldw; B.rows = m.V - v0 - c0; B.wide = ww;
+  } else if (KIND == SM_DH) {
+    const int ch = blockIdx.z * pc.chunk;
+    k = min(pc.chunk, pc.n - ch);
+    A.p = g + r0 * m.ldg + ch; A.ld = m.ldg; A.rows = m.tpad - r0;
+    B.p = w + (v0 + ch) * m.ldw + c0; B.ld = m.ldw; B.rows = m.D - c0; B.wide = ww;
+  } else {
+    k = count;
+    A.p = g + r0; A.ld = m.ldg; A.rows = pc.n - r0;
+    B.p = h + c0; B.ld = m.ldh; B.rows = m.D - c0; B.wide = true;
+  }
+  A.k = B.k = k;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  // A thread's rows are r0 + 4 ty + {0..3} and + 64, its columns alike.
+  float acc[8][8] = {};
+  A.load(0);
+  B.load(0);
+  int buf = 0;
+  for (int k0 = 0; k0 < k; k0 += SK) {
+    A.store(sA[buf]);
+    B.store(sB[buf]);
+    __syncthreads();
+    if (k0 + SK < k) {
+      A.load(k0 + SK);
+      B.load(k0 + SK);
+    }
+#pragma unroll
+    for (int kk = 0; kk < SK; ++kk) {
+      float x[8], y[8];
+      *(float4 *)&x[0] = *(const float4 *)&sA[buf][kk][ty * 4];
+      *(float4 *)&x[4] = *(const float4 *)&sA[buf][kk][64 + ty * 4];
+      *(float4 *)&y[0] = *(const float4 *)&sB[buf][kk][tx * 4];
+      *(float4 *)&y[4] = *(const float4 *)&sB[buf][kk][64 + tx * 4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    }
+    buf ^= 1;  // the other buffer was last read before the barrier of this step
+  }
+  auto rowof = [&](int i) { return (i & 3) + (i >> 2) * 64 + ty * 4; };
+  auto colof = [&](int j) { return (j & 3) + (j >> 2) * 64 + tx * 4; };
+  constexpr float L2E = 1.44269504088896340736f;
+  if (KIND == SM_STATS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + rowof(i);
+      const int target = m.rows[row].target - c0;
+      float big = -INFINITY, s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = colof(j);
+        const float x = acc[i][j] * (m.scale * L2E);
+        if (c == target) m.xt[row] = x;
+        acc[i][j] = c0 + c < m.V ? x : -INFINITY;
+        big = fmaxf(big, acc[i][j]);
+      }
+      for (int d = 8; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, d));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += big == -INFINITY ? (acc[i][j] == -INFINITY ? 0.f : acc[i][j]) : exp2f(acc[i][j] - big);
+      for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(FULL_MASK, s, d);
+      if (tx == 0) m.part[(int64_t)blockIdx.y * m.tpad + row] = make_float2(big, s);
+    }
+  } else if (KIND == SM_LOGITS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + rowof(i);
+      const CeRow R = m.rows[row];
+      const int target = R.target - v0 - c0;
+      const bool zero = R.c == 0.f && R.c1 == 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = colof(j);
+        float x = R.c * exp2f(fmaf(acc[i][j], m.scale * L2E, -R.lse2));
+        if (c == target) x -= R.c1;
+        acc[i][j] = zero || v0 + c0 + c >= m.V ? 0.f : x;
+      }
+      float *out = (float *)m.g + row * m.ldg + c0 + tx * 4;
+      *(float4 *)out = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *(float4 *)(out + 64) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  } else if (KIND == SM_DH) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + rowof(i);
+      if (row >= count) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = c0 + colof(j);
+        if (c >= m.D) continue;
+        const int64_t at = row * m.ldh + c;
+        if (m.planes) {
+          m.planes[(int64_t)blockIdx.z * m.tpad * m.ldh + at] = acc[i][j];
+          continue;
+        }
+        const float x = pc.first ? acc[i][j] : m.acc[at] + acc[i][j];
+        if (pc.last) ((float *)m.dh)[m.row_of[row] * m.ld_dh + c] = x;
+        else m.acc[at] = x;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + rowof(i);
+      if (row >= pc.n) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = c0 + colof(j);
+        if (c >= m.D) continue;
+        float *o = (float *)m.dw + (int64_t)(v0 + row) * m.D + c;
+        *o = m.accumulate ? *o + acc[i][j] : acc[i][j];
+      }
+    }
+  }
+}
+
+template <int KIND>
+static cudaError_t launch(const CeMats &m, const CePiece &p, dim3 grid, cudaStream_t stream) {
+  SimtParams a = {m, p, (int)ceil_div(m.V, CE_PART)};
+  return launch_pdl(ce_simt_kernel<KIND>, grid, dim3(256), 0, stream, a);
+}
+
+cudaError_t ce_simt_stats(const CeMats &m, cudaStream_t stream) {
+  CePiece p = {};
+  p.n = m.V;
+  return launch<SM_STATS>(m, p, dim3(m.tpad / ST, (unsigned)ceil_div(m.V, ST)), stream);
+}
+
+cudaError_t ce_simt_logits_grad(const CeMats &m, const CePiece &p, cudaStream_t stream) {
+  return launch<SM_LOGITS>(m, p, dim3(m.tpad / ST, (unsigned)ceil_div(p.n, ST)), stream);
+}
+
+cudaError_t ce_simt_grads(const CeMats &m, const CePiece &p, cudaStream_t stream) {
+  const unsigned nt = (unsigned)ceil_div(m.D, ST);
+  cudaError_t e = launch<SM_DH>(m, p, dim3(m.tpad / ST, nt, p.nchunks), stream);
+  if (e != cudaSuccess) return e;
+  return launch<SM_DW>(m, p, dim3((unsigned)ceil_div(p.n, ST), nt), stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,612 @@
+// Matrix products of the linear cross entropy on CTA pairs (tcgen05, bf16).
+//
+// Three persistent kernels on one skeleton; an item is a tile of 256 x 256
+// outputs of one product, run by a cluster of two CTAs as M = 256 MMAs
+// (cta_group::2): each CTA holds 128 rows of A and half of B's columns, and
+// its tensor memory receives 128 rows of the tile.
+//
+//   STATS   x[t, v] = sum_d h[t, d] w[v, d]     epilogue: for each row and 128 columns the
+//           maximum and the sum of exponentials, and the target's logit
+//   LOGITS  the same product for the columns of a piece; epilogue: g, one
+//           rounding to bf16, by TMA stores
+//   GRADS   dh[t, d] = sum_v g[t, v] w[v, d]    (A K-major, B MN-major)
+//           dw[v, d] = sum_t g[t, v] h[t, d]    (both MN-major)
+//           in one launch: the two have the same tiles and, at 8192 rows,
+//           the same K, so that together they fill the last wave better
+//
+// Rows of the accumulator are tokens in the first two, so a thread of the
+// epilogue has a row's columns in its own lane and takes maximum and sum
+// without a shuffle.  Two accumulators of 256 columns alternate: an item's
+// epilogue runs under the next item's MMAs.  A stage is one K block of 64: 16
+// KB of A and 16 KB of B a CTA, six stages deep.  Every output is summed in K
+// blocks of 64 in order, in one accumulator; the tile it falls in does not
+// change that.
+#include <cuda.h>
+
+#include "linear_ce.h"
+#include "tc_host.h"
+#include "umma.cuh"
+
+namespace moe {
+
+using namespace umma;
+
+constexpr int CE_STATS = 0, CE_LOGITS = 1, CE_GRADS = 2;
+constexpr int CT_STAGES = 6, CT_A_BYTES = 16384, CT_STAGE_BYTES = 2 * CT_A_BYTES;
+constexpr int CT_EPI_FIRST = 2, CT_EPI_WARPS = 8, CT_EPI_BYTES = 4096;
+constexpr int CT_THREADS = 32 * (CT_EPI_FIRST + CT_EPI_WARPS);
+constexpr int CT_SMEM = 1024 + CT_STAGES * CT_STAGE_BYTES + CT_EPI_WARPS * CT_EPI_BYTES + 512;
+static_assert(CT_SMEM <= 232448, "shared memory of a CTA");
+constexpr uint32_t CT_TMEM_COLS = 512;
+constexpr float CE_LOG2E = 1.44269504088896340736f;
+
+struct CtMaps {
+  CUtensorMap h, w, g;     // K-major tiles: boxes of 128 rows x 64
+  CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64
+  CUtensorMap gout;        // 32 rows x 64: g's stores
+  CUtensorMap dw;          // dweight: 32 rows x 128 bytes
+};
+
+struct CtParams {
+  int V, D, tpad;
+  const int *count;
+  const int *row_of;
+  const CeRow *rows;
+  float s2;  // scale * log2(e)
+  float2 *part;
+  float *xt;
+  int nparts;
+  int v0, n, chunk, nchunks;  // the piece
+  bool first, last;
+  bool dw_tma, accumulate, gf32, dh_wide;
+  __nv_bfloat16 *dh;
+  int64_t ld_dh, ldh;
+  void *dw;
+  float *acc, *planes;
+  int *status;
+};
+
+struct CtItem {
+  int kind;   // 0: logits, 1: dhidden, 2: dweight
+  int m, n, chunk, nk;
+  int cols;   // columns of the tile: 256 or 128
+};
+
+template <int KIND>
+struct CtWork {
+  int mt, nt, ndh, ndw, total, kd, kr;
+  bool dw_first;
+  __device__ CtWork(const CtParams &p) {
+    const int count = __ldg(p.count);
+    mt = (count + CE_ROWS - 1) / CE_ROWS;
+    kd = (p.D + 63) / 64;
+    kr = (count + 63) / 64;
+    const int vt = (p.n + 255) / 256;
+    if (KIND == CE_GRADS) {
+      nt = (p.D + 255) / 256;
+      ndh = p.nchunks * mt * nt;
+      ndw = vt * nt;
+      total = ndh + ndw;
+      dw_first = kr > 128;  // the longer items first: they do not form the tail
+    } else {
+      nt = vt;
+      total = mt * nt;
+    }
+  }
+  __device__ CtItem item(int it, const CtParams &p) const {
+    CtItem r;
+    r.chunk = 0;
+    r.cols = 256;
+    if (KIND != CE_GRADS) {  // row tiles fastest: a tile of the weights is read by all of them at about the same time
+      r.kind = 0;
+      r.m = it % mt;
+      r.n = it / mt;
+      r.nk = kd;
+      return r;
+    }
+    const bool dw = dw_first ? it < ndw : it >= ndh;
+    const int i = dw ? (dw_first ? it : it - ndh) : (dw_first ? it - ndw : it);
+    r.n = i % nt;
+    const int rest = i / nt;
+    if (p.D - r.n * 256 <= 128) r.cols = 128;
+    if (dw) {
+      r.kind = 2;
+      r.m = rest;
+      r.nk = kr;
+    } else {
+      r.kind = 1;
+      r.m = rest % mt;
+      r.chunk = rest / mt;
+      r.nk = (min(p.chunk, p.n - r.chunk * p.chunk) + 63) / 64;
+    }
+    return r;
+  }
+};
+
+__device__ inline float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A tile of 32 rows x 128 bytes from shared memory, added to what is there.
+__device__ inline void tma_reduce_add_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m),
+               "r"(c0), "r"(c1), "r"(smem_u32(src))
+               : "memory");
+}
+
+// ---- epilogues: a warp's 32 rows (lane = row) x cols / 2 columns from c0 of the tile ----
+__device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, uint32_t taddr, int row, int half) {
+  const int col0 = im.n * 256 + half * 128;
+  if (col0 >= p.V) return;
+  const int target = p.rows[row].target - col0;
+  float m = -INFINITY, s = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    tmem_ld32(taddr + c * 32, v);
+    const unsigned at = (unsigned)(target - c * 32);
+    if (at < 32u) {
+      float x = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x = at == (unsigned)j ? v[j] : x;
+      p.xt[row] = x * p.s2;
+    }
+    const int left = p.V - col0 - c * 32;
+    if (left < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = j < left ? v[j] * p.s2 : -INFINITY;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= p.s2;
+    }
+    float big = m;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) big = fmaxf(big, v[j]);
+    if (big == -INFINITY) {  // nothing yet (NaN does not get past fmaxf, but does get into the sum)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s += v[j] == -INFINITY ? 0.f : v[j];
+      continue;
+    }
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      s0 += ex2(v[j] - big);
+      s1 += ex2(v[j + 1] - big);
+    }
+    s = s * ex2(m - big) + (s0 + s1);
+    m = big;
+  }
+  p.part[(int64_t)(im.n * 2 + half) * p.tpad + row] = make_float2(m, s);
+}
+
+__device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row,
+                                       int half, uint8_t *stg, int lane) {
+  const int pc0 = im.n * 256 + half * 128;  // column in the piece
+  const CeRow R = p.rows[row];
+  const int target = R.target - p.v0 - pc0;
+  const bool zero = R.c == 0.f && R.c1 == 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float v[2][32];
+    tmem_ld32x2(taddr + c * 64, taddr + c * 64 + 32, v[0], v[1]);
+    const int left = p.V - p.v0 - pc0 - c * 64;
+    uint32_t w[32];
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[hh][j] = R.c * ex2(fmaf(v[hh][j], p.s2, -R.lse2));
+      const unsigned at = (unsigned)(target - c * 64 - hh * 32);
+      if (at < 32u) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[hh][j] -= at == (unsigned)j ? R.c1 : 0.f;
+      }
+      if (zero || left < 64) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (zero || hh * 32 + j >= left) v[hh][j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[hh][2 * j], v[hh][2 * j + 1]);
+        w[hh * 16 + j] = *(const uint32_t *)&b;
+      }
+    }
+    if (lane == 0) bulk_wait_read<0>();  // the last store has read the buffer
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *(uint4 *)(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&maps.gout, stg, pc0 + c * 64, row);
+      bulk_commit();
+    }
+  }
+}
+
+// 32 rows x 32 float columns of a warp through its buffer: f(row of the 32,
+// column of the 32, four values) with eight lanes a row.
+template <typename F>
+__device__ inline void by_rows(uint8_t *stg, const float (&v)[32], int lane, F &&f) {
+  if (lane == 0) bulk_wait_read<0>();  // a store of the item before has read the buffer
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *(float4 *)(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (lane >> 3) + 4 * i, ch = lane & 7;
+    f(r, ch * 4, *(const float4 *)(stg + r * 128 + ((ch ^ (r & 7)) << 4)));
+  }
+  __syncwarp();
+}
+
+__device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uint32_t taddr, int row0, int count, int half,
+                                        uint8_t *stg, int lane) {
+  const int wcols = im.cols / 2, col0 = im.n * 256 + half * wcols;
+  float *plane = p.planes ? p.planes + (int64_t)im.chunk * p.tpad * p.ldh : nullptr;
+  for (int c = 0; c < wcols && col0 + c < p.D; c += 32) {
+    float v[32];
+    tmem_ld32(taddr + c, v);
+    by_rows(stg, v, lane, [&](int r, int cc, float4 x) {
+      const int row = row0 + r, col = col0 + c + cc;
+      if (row >= count || col >= p.D) return;
+      const int64_t at = row * p.ldh + col;
+      if (plane) {
+        *(float4 *)(plane + at) = x;
+        return;
+      }
+      if (!p.first) {
+        const float4 y = *(const float4 *)(p.acc + at);
+        x.x = y.x + x.x; x.y = y.y + x.y; x.z = y.z + x.z; x.w = y.w + x.w;
+      }
+      if (!p.last) {
+        *(float4 *)(p.acc + at) = x;
+        return;
+      }
+      __nv_bfloat16 *out = p.dh + p.row_of[row] * p.ld_dh + col;
+      const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+      if (p.dh_wide) {
+        *(uint2 *)out = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+      } else {
+        const __nv_bfloat16 e[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < p.D) out[j] = e[j];
+      }
+    });
+  }
+}
+
+// v: the tile's values (zero where no row counts: then there is no accumulator).
+__device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row0,
+                                        int half, uint8_t *stg, int lane) {
+  const int wcols = im.cols / 2, col0 = im.n * 256 + half * wcols;  // row0: row of dweight
+  if (row0 >= p.V) return;
+  for (int c = 0; c < wcols && col0 + c < p.D; c += p.gf32 || !p.dw_tma ? 32 : 64) {
+    float v[2][32];
+    if (im.nk == 0) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0.f;
+    } else if (p.gf32 || !p.dw_tma) {
+      tmem_ld32(taddr + c, v[0]);
+    } else {
+      tmem_ld32x2(taddr + c, taddr + c + 32, v[0], v[1]);
+    }
+    if (p.dw_tma) {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint4 u;
+        if (p.gf32) {
+          u = make_uint4(__float_as_uint(v[0][4 * j]), __float_as_uint(v[0][4 * j + 1]), __float_as_uint(v[0][4 * j + 2]),
+                         __float_as_uint(v[0][4 * j + 3]));
+        } else {
+          const float *s = &v[j >> 2][(j & 3) * 8];
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
+            w[i] = *(const uint32_t *)&b;
+          }
+          u = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *(uint4 *)(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (p.accumulate) tma_reduce_add_2d(&maps.dw, stg, col0 + c, row0);
+        else tma_store_2d(&maps.dw, stg, col0 + c, row0);
+        bulk_commit();
+      }
+    } else {
+      by_rows(stg, v[0], lane, [&](int r, int cc, float4 x) {
+        const int row = row0 + r, col = col0 + c + cc;
+        if (row >= p.V) return;
+        const float e[4] = {x.x, x.y, x.z, x.w};
+        const int64_t at = (int64_t)row * p.D + col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (col + j >= p.D) break;
+          if (p.gf32) {
+            float *o = (float *)p.dw + at + j;
+            *o = p.accumulate ? *o + e[j] : e[j];
+          } else {
+            ((__nv_bfloat16 *)p.dw)[at + j] = __float2bfloat16_rn(e[j]);
+          }
+        }
+      });
+    }
+  }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(CT_THREADS, 1)
+ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  auto sa = [&](int s) { return base + s * CT_STAGE_BYTES; };
+  auto sb = [&](int s) { return base + s * CT_STAGE_BYTES + CT_A_BYTES; };
+  uint8_t *epi = base + CT_STAGES * CT_STAGE_BYTES;
+  uint64_t *bars = (uint64_t *)(epi + CT_EPI_WARPS * CT_EPI_BYTES);
+  uint64_t *full = bars, *empty = full + CT_STAGES;
+  uint64_t *tfull = empty + CT_STAGES, *tempty = tfull + 2, *mma_done = tempty + 2;
+  uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
+  volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < CT_STAGES; ++s) {
+      mbar_init(&full[s], 1);  // used in the even CTA
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * CT_EPI_WARPS);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  cluster_sync();  // both CTAs' barriers exist before either touches the other's
+  if (warp == 1) tmem_alloc_pair(tmem_slot, CT_TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch();
+  griddep_wait();
+  const CtWork<KIND> work(p);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
+      const uint32_t full0 = mapa_shared(&full[0], 0);
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_phase = 0;
+      bool ok = true;
+      for (int it = cid; it < work.total && ok; it += ncl) {
+        const CtItem im = work.item(it, p);
+        const int mrow = im.m * 256 + (int)rank * 128;
+        const int half = im.cols / 2, ncol = im.n * 256 + (int)rank * half;
+        const uint32_t bytes = 2 * (CT_A_BYTES + (uint32_t)half * 128);
+        for (int kb = 0; kb < im.nk; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
+          // Both CTAs' tiles complete on the even CTA's barrier.
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
+          const int k = kb * 64;
+          if (KIND != CE_GRADS) {
+            tma_load_2d_pair(sa(stage), &maps.h, bar, k, mrow, keep);
+            tma_load_2d_pair(sb(stage), &maps.w, bar, k, p.v0 + ncol, pass);
+          } else if (im.kind == 1) {
+            const int v = im.chunk * p.chunk + k;
+            tma_load_2d_pair(sa(stage), &maps.g, bar, v, mrow, pass);
+            for (int j = 0; j < half; j += 64)
+              tma_load_2d_pair(sb(stage) + j * 128, &maps.wt, bar, ncol + j, p.v0 + v, keep);
+          } else {
+            for (int j = 0; j < 128; j += 64) tma_load_2d_pair(sa(stage) + j * 128, &maps.gt, bar, mrow + j, k, pass);
+            for (int j = 0; j < half; j += 64) tma_load_2d_pair(sb(stage) + j * 128, &maps.ht, bar, ncol + j, k, keep);
+          }
+          issued |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == CT_STAGES) stage = 0, phase ^= 1;
+        }
+      }
+      if (!ok && leader) {
+        // The stages in flight (both CTAs' copies complete here) land before the pair exits.
+        volatile int never = 0;
+        for (int s = 0; s < CT_STAGES; ++s)
+          if (issued & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1, &never, nullptr, 100000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      if (leader) {
+        // -------------------------------------------------------- MMA issuer (both CTAs' tensor memory)
+        int stage = 0;
+        uint32_t phase = 0, cnt = 0;
+        bool ok = true;
+        for (int it = cid; it < work.total && ok; it += ncl) {
+          const CtItem im = work.item(it, p);
+          if (im.nk == 0) continue;
+          const int b = cnt & 1;
+          if (!mbar_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+          tc_fence_after();
+          const bool a_mn = KIND == CE_GRADS && im.kind == 2, b_mn = KIND == CE_GRADS;
+          const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
+          const uint32_t astep = a_mn ? 128 : 2, bstep = b_mn ? 128 : 2;  // K = 16: 2048 or 32 bytes
+          for (int kb = 0; kb < im.nk; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(sa(stage)), b0 = smem_u32(sb(stage));
+            const uint64_t ad = a_mn ? smem_desc_mn_sw128(a0, 8192) : smem_desc_sw128(a0);
+            const uint64_t bd = b_mn ? smem_desc_mn_sw128(b0, 8192) : smem_desc_sw128(b0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kb | kk) != 0);
+            mma_commit_pair(&empty[stage]);
+            if (++stage == CT_STAGES) stage = 0, phase ^= 1;
+          }
+          if (!ok) break;
+          mma_commit_pair(&tfull[b]);
+          ++cnt;
+        }
+        mma_commit_pair(mma_done);
+      }
+      // Every pair MMA has finished (it wrote both CTAs' tensor memory) before TMEM is released.
+      volatile int never = 0;
+      mbar_wait(mma_done, 0, &never, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;
+    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * CT_EPI_BYTES;
+    const uint32_t tempty_leader0 = mapa_shared(&tempty[0], 0);
+    const int count = __ldg(p.count);
+    uint32_t cnt = 0;
+    for (int it = cid; it < work.total; it += ncl) {
+      const CtItem im = work.item(it, p);
+      const int b = cnt & 1;
+      if (im.nk != 0) {
+        int ok = 0;
+        if (lane == 0) ok = mbar_wait(&tfull[b], (cnt >> 1) & 1, abort_flag, p.status) ? 1 : 0;
+        if (!__shfl_sync(FULL_MASK, ok, 0)) break;
+        tc_fence_after();
+      }
+      const int row0 = im.m * 256 + (int)rank * 128 + q * 32;
+      const uint32_t taddr = tmem + b * 256 + ((uint32_t)(q * 32) << 16) + half * (im.cols / 2);
+      if (KIND == CE_STATS) stats_epilogue(p, im, taddr, row0 + lane, half);
+      else if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
+      else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, count, half, stg, lane);
+      else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane);
+      if (im.nk == 0) continue;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(&tempty[b]);
+        else mbar_arrive_remote(tempty_leader0 + (uint32_t)(b * sizeof(uint64_t)));
+      }
+      ++cnt;
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no remote arrival, copy or commit targets this CTA any more
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, CT_TMEM_COLS);
+}
+
+// ------------------------------------------------------------------ host side
+// Row-major [rows, cols] of bf16 (or float) with a row stride of ld elements.
+static bool map_ld(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows,
+                   bool f32 = false) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)ld * (f32 ? 4 : 2)};
+  const uint32_t box[2] = {f32 ? 32u : 64u, box_rows};
+  return encode_map(m, ptr, 2, dims, strides, box, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
+template <int KIND>
+static cudaError_t launch(const CtMaps &maps, const CtParams &p, int64_t items, cudaStream_t stream) {
+  cudaError_t e = ensure_smem((const void *)ce_pair_kernel<KIND>, CT_SMEM);
+  if (e != cudaSuccess) return e;
+  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(items, device_sms() / 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(CT_THREADS);
+  cfg.dynamicSmemBytes = CT_SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, ce_pair_kernel<KIND>, maps, p);
+}
+
+static CtParams params(const CeMats &m) {
+  CtParams p = {};
+  p.V = m.V;
+  p.D = m.D;
+  p.tpad = m.tpad;
+  p.count = m.count;
+  p.row_of = m.row_of;
+  p.rows = m.rows;
+  p.s2 = m.scale * CE_LOG2E;
+  p.part = m.part;
+  p.xt = m.xt;
+  p.nparts = (int)ceil_div(m.V, CE_PART);
+  p.n = m.V;
+  p.ldh = m.ldh;
+  p.status = m.status;
+  return p;
+}
+
+static void piece(CtParams &p, const CePiece &c) {
+  p.v0 = c.v0;
+  p.n = c.n;
+  p.chunk = c.chunk;
+  p.nchunks = c.nchunks;
+  p.first = c.first;
+  p.last = c.last;
+}
+
+cudaError_t ce_tc_stats(const CeMats &m, cudaStream_t stream) {
+  CtMaps maps = {};
+  if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128))
+    return cudaErrorInvalidValue;
+  return launch<CE_STATS>(maps, params(m), (int64_t)(m.tpad / 256) * ceil_div(m.V, 256), stream);
+}
+
+cudaError_t ce_tc_logits_grad(const CeMats &m, const CePiece &c, cudaStream_t stream) {
+  CtMaps maps = {};
+  CtParams p = params(m);
+  piece(p, c);
+  if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128) ||
+      !map_ld(&maps.gout, m.g, m.tpad, m.ldg, m.ldg, 32))
+    return cudaErrorInvalidValue;
+  return launch<CE_LOGITS>(maps, p, (int64_t)(m.tpad / 256) * ceil_div(c.n, 256), stream);
+}
+
+cudaError_t ce_tc_grads(const CeMats &m, const CePiece &c, cudaStream_t stream) {
+  CtMaps maps = {};
+  CtParams p = params(m);
+  piece(p, c);
+  p.accumulate = m.accumulate;
+  p.gf32 = m.gf32;
+  p.dw = m.dw;
+  p.dh = (__nv_bfloat16 *)m.dh;
+  p.ld_dh = m.ld_dh;
+  p.dh_wide = m.D % 4 == 0 && m.ld_dh % 4 == 0 && ((uintptr_t)m.dh & 7) == 0;
+  p.acc = m.acc;
+  p.planes = m.planes;
+  // Tensor maps of dweight want its dense rows on 16-byte boundaries.
+  p.dw_tma = ((uintptr_t)m.dw & 15) == 0 && m.D % (m.gf32 ? 4 : 8) == 0;
+  if (!map_ld(&maps.g, m.g, m.tpad, m.ldg, m.ldg, 128) || !map_ld(&maps.gt, m.g, m.tpad, m.ldg, m.ldg, 64) ||
+      !map_ld(&maps.wt, m.w, m.V, m.D, m.ldw, 64) || !map_ld(&maps.ht, m.h, m.tpad, m.ldh, m.ldh, 64) ||
+      (p.dw_tma && !map_ld(&maps.dw, m.dw, m.V, m.D, m.D, 32, m.gf32)))
+    return cudaErrorInvalidValue;
+  const int64_t nt = ceil_div(m.D, 256);
+  return launch<CE_GRADS>(maps, p, nt * ((int64_t)c.nchunks * (m.tpad / 256) + ceil_div(c.n, 256)), stream);
+}
+
+}  // namespace moe
