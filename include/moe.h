@@ -722,7 +722,7 @@ enum moe_linear_ce_call { MOE_CE_LOSS = 1, MOE_CE_GRAD = 2, MOE_CE_STEP = 3 };
  *   loss_t = lse_t - x_t[target_t] + z_loss * lse_t^2
  *
  * The logits live in tensor memory (MOE_BF16) or registers only: a tile of
- * them leaves a maximum and a sum of exponentials for each row and 128 of its columns.
+ * them leaves a maximum and a sum of exponentials for each row and 64 of its columns.
  * Rows whose target is ignore_index (prompts, padding) are left out: they are
  * not read, their loss and lse are 0.  A target outside [0, V) that is not
  * ignore_index is left out the same way and recorded (code 7).  Logits that

@@ -8,7 +8,7 @@
 // cost nothing afterwards, what they hold reaches no product, and the copies
 // have the alignment that the tensor maps want whatever the caller's have.
 // Then one product leaves a maximum and a sum of exponentials for each row and
-// 128 columns (8 bytes for 256 of logits), which are joined per row; the
+// 64 columns (8 bytes for 128 of logits), which are joined per row; the
 // gradient recomputes the logits a piece of the vocabulary at a time (2 TDV of
 // the 8 TDV operations, where keeping them would take 4 TV bytes) and takes
 // both products of the piece while it is near L2's size.
@@ -72,46 +72,109 @@ ce_places_kernel(int T, int V, int64_t ignore, const Id *targets, int *count, in
   for (int i = base + threadIdx.x; i < end; i += 1024) rows[i] = CeRow{0.f, 0.f, 0.f, -1};
 }
 
+// What the gradient needs of a row: d = scale * dloss, l its lse, nll = l -
+// x[target].  The target's entry is d (p - 1 + 2 z l p); p - 1 by expm1, exact
+// where the model is nearly sure.  Returns 1 / the row's factor.
+template <typename E>
+__device__ inline float grad_row(CeRow &r, float d, float l, float nll, float z) {
+  const float zl = 2.f * z * l, p = expf(-nll);
+  const float g = d * fmaf(zl, p, expm1f(-nll));
+  float c = d * (1.f + zl), b = g, inv = 1.f;
+  if (sizeof(E) == 2) {
+    b = Elem<E>::to_f32(Elem<E>::from_f32(g));
+    if (fabsf(g) > 1e-30f && fabsf(b) < 1e38f) {
+      inv = g / b;
+      c *= b / g;
+    }
+  }
+  r.lse2 = l * LOG2E;
+  r.c = c;
+  r.b = b;
+  return inv;
+}
+
+// One row to its place: D elements times f, zeros up to dp.  wide: units of 16 bytes.
+template <typename E, bool SCALED>
+__device__ inline void put_row(E *dst, const E *src, int D, int64_t dp, float f, bool wide, int lane) {
+  constexpr int N = Vec16<E>::N;
+  if (wide) {
+    const int nu = src ? D / N : 0;
+    for (int u = lane; u < (int)(dp / N); u += 32) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (u < nu) {
+        w = ((const uint4 *)src)[u];
+        if (SCALED) {
+          float x[N];
+          Vec16<E>::unpack(w, x);
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] *= f;
+          Vec16<E>::store(dst + u * N, x);
+          continue;
+        }
+      }
+      ((uint4 *)dst)[u] = w;
+    }
+  } else {
+    for (int c = lane; c < (int)dp; c += 32) {
+      E x = src && c < D ? src[c] : Elem<E>::from_f32(0.f);
+      if (SCALED) x = Elem<E>::from_f32(Elem<E>::to_f32(x) * f);
+      dst[c] = x;
+    }
+  }
+}
+
 // A warp a row: the rows that count to their places, zeros behind them (in
 // the columns up to dp and the rows up to the tile's end), zeros into dhidden
-// where a row is left out, and, with the forward's lse, what the gradient
-// needs of a row.
+// where a row is left out.  For the gradient alone also what it needs of a
+// row: the target's logit is a dot product of the row with one of the weights.
 template <typename E>
 __global__ void __launch_bounds__(256)
-ce_rows_kernel(int T, int D, int64_t ld_h, int64_t dp, int64_t ld_dh, const E *h, E *hc, E *dh, const int *count,
-               const int *place, CeRow *rows, const float *lse, const float *dloss, float scale, float z, bool wide) {
+ce_rows_kernel(CeArgs a, int64_t dp, E *hc, E *hc2, const int *count, const int *place, CeRow *rows, float *inv,
+               bool zero_dh, bool grad_only, bool wide, bool wide_w) {
   constexpr int N = Vec16<E>::N;
   griddep_launch();
   griddep_wait();
   const int t = (int)(((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   int at;
   const E *src = nullptr;
-  if (t < T) {
+  float f = 1.f;
+  if (t < a.T) {
     at = place[t];
     if (at < 0) {
-      if (dh)
-        for (int c = lane; c < D; c += 32) dh[t * ld_dh + c] = Elem<E>::from_f32(0.f);
+      if (zero_dh)
+        for (int c = lane; c < a.D; c += 32) ((E *)a.dh)[t * a.ld_dh + c] = Elem<E>::from_f32(0.f);
       return;
     }
-    src = h + t * ld_h;
-    if (dloss && lse && lane == 0) {
-      const float l = lse[t], d = scale * dloss[t];
-      rows[at].lse2 = l * LOG2E;
-      rows[at].c = d * fmaf(2.f * z, l, 1.f);
-      rows[at].c1 = d;
+    src = (const E *)a.hidden + t * a.ld_h;
+    if (grad_only) {
+      const E *w = (const E *)a.weight + rows[at].target * a.ld_w;
+      float x = 0.f;
+      if (wide && wide_w) {
+        for (int u = lane; u < a.D / N; u += 32) {
+          float p[N], q[N];
+          Vec16<E>::load(src + u * N, p);
+          Vec16<E>::load(w + u * N, q);
+#pragma unroll
+          for (int i = 0; i < N; ++i) x = fmaf(p[i], q[i], x);
+        }
+      } else {
+        for (int c = lane; c < a.D; c += 32) x = fmaf(Elem<E>::load(src + c), Elem<E>::load(w + c), x);
+      }
+      for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(FULL_MASK, x, d);
+      const float l = a.lse[t];
+      CeRow r = rows[at];
+      f = grad_row<E>(r, a.scale * a.dloss[t], l, fmaf(-x, a.scale, l), a.z_loss);
+      if (lane == 0) {
+        rows[at] = r;
+        inv[at] = f;
+      }
     }
   } else {
-    at = *count + (t - T);
+    at = *count + (t - a.T);
     if (at >= (int)round_up(*count, CE_ROWS)) return;
   }
-  E *dst = hc + at * dp;
-  if (src && wide) {  // every row starts on a 16-byte boundary and D is whole units
-    const int nu = D / N;
-    for (int u = lane; u < (int)(dp / N); u += 32)
-      ((uint4 *)dst)[u] = u < nu ? ((const uint4 *)src)[u] : make_uint4(0, 0, 0, 0);
-  } else {
-    for (int c = lane; c < (int)dp; c += 32) dst[c] = src && c < D ? src[c] : Elem<E>::from_f32(0.f);
-  }
+  put_row<E, false>(hc + at * dp, src, a.D, dp, 1.f, wide, lane);
+  if (grad_only && sizeof(E) == 2) put_row<E, true>(hc2 + at * dp, src, a.D, dp, f, wide, lane);
 }
 
 // Weights whose rows do not start on 16-byte boundaries, copied to where they do.
@@ -127,16 +190,20 @@ ce_weight_copy_kernel(int64_t V, int D, int64_t ld, int64_t ldw, const __nv_bflo
 
 // ------------------------------------------------------------- the rows' statistics
 // A CTA joins 32 rows: 32 warps take every 32nd part each (a row a lane: 256
-// bytes a load), then the warps' results are joined in order.
+// bytes a load), then the warps' results are joined in order.  In a step what
+// the gradient needs of the rows, too, and the rows over their factors.
+template <typename E>
 __global__ void __launch_bounds__(1024)
 ce_join_kernel(const int *count, int nparts, int tpad, const float2 *part, const float *xt, const int *row_of,
-               CeRow *rows, float *loss, float *lse, const float *dloss, float scale, float z) {
+               CeRow *rows, float *inv, float *loss, float *lse, const float *dloss, float scale, float z, const E *hc,
+               E *hc2, int64_t dp) {
   griddep_launch();
   griddep_wait();
   __shared__ float2 sh[32][33];
+  __shared__ float factor[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = *count, r = blockIdx.x * 32 + lane;
-  if ((int)blockIdx.x * 32 >= n) return;
+  const int n = *count, r0 = blockIdx.x * 32, r = r0 + lane;
+  if (r0 >= (dloss ? (int)round_up(n, CE_ROWS) : n)) return;
   float m = -INFINITY, s = 0.f;
   auto add = [](float &m, float &s, float2 p) {
     const float big = fmaxf(m, p.x);
@@ -144,31 +211,41 @@ ce_join_kernel(const int *count, int nparts, int tpad, const float2 *part, const
     s = s * exp2f(m - big) + p.y * exp2f(p.x - big);
     m = big;
   };
-  for (int i = warp; i < nparts; i += 32) add(m, s, part[(int64_t)i * tpad + r]);
+  if (r0 < n)
+    for (int i = warp; i < nparts; i += 32) add(m, s, part[(int64_t)i * tpad + r]);
   sh[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if (warp != 0 || r >= n) return;
-  m = -INFINITY;
-  s = 0.f;
-  for (int w = 0; w < 32; ++w) add(m, s, sh[w][lane]);
-  // m and the target's logit are in units of log 2: their difference is exact
-  // where it is small, and 0 where the target has the largest logit.
-  const float ln = logf(s), l = fmaf(m, LN2, ln);
-  const int t = row_of[r];
-  loss[t] = fmaf(m - xt[r], LN2, ln) + z * l * l;
-  if (lse) lse[t] = l;
-  if (dloss) {
-    const float d = scale * dloss[t];
-    rows[r].lse2 = l * LOG2E;
-    rows[r].c = d * fmaf(2.f * z, l, 1.f);
-    rows[r].c1 = d;
+  if (warp == 0) {
+    float f = 1.f;
+    if (r < n) {
+      m = -INFINITY;
+      s = 0.f;
+      for (int w = 0; w < 32; ++w) add(m, s, sh[w][lane]);
+      // m and the target's logit are in units of log 2: their difference is exact
+      // where it is small, and 0 where the target has the largest logit.
+      const float ln = logf(s), l = fmaf(m, LN2, ln), nll = fmaf(m - xt[r], LN2, ln);
+      const int t = row_of[r];
+      loss[t] = fmaf(z * l, l, nll);
+      if (lse) lse[t] = l;
+      if (dloss) {
+        CeRow row = rows[r];
+        f = grad_row<E>(row, scale * dloss[t], l, nll, z);
+        rows[r] = row;
+        inv[r] = f;
+      }
+    }
+    factor[lane] = f;
   }
+  if (!dloss || sizeof(E) != 2) return;
+  __syncthreads();
+  const int64_t at = (r0 + warp) * dp;
+  put_row<E, true>(hc2 + at, hc + at, (int)dp, dp, factor[warp], true, lane);
 }
 
 // dhidden's sums of the chunks of one piece, in order, onto those of the pieces before.
 template <typename E>
 __global__ void __launch_bounds__(256)
-ce_planes_kernel(const int *count, const int *row_of, int D, int64_t dp, int tpad, int nplanes, const float *planes,
+ce_planes_kernel(const int *count, const int *row_of, const float *inv, int D, int64_t dp, int tpad, int nplanes, const float *planes,
                  float *acc, E *dh, int64_t ld_dh, bool first, bool last) {
   griddep_launch();
   griddep_wait();
@@ -188,7 +265,8 @@ ce_planes_kernel(const int *count, const int *row_of, int D, int64_t dp, int tpa
       *(float4 *)(acc + at) = s;
       continue;
     }
-    const float v[4] = {s.x, s.y, s.z, s.w};
+    const float f = sizeof(E) == 2 ? inv[r] : 1.f;
+    const float v[4] = {s.x * f, s.y * f, s.z * f, s.w * f};
     E *out = dh + row_of[r] * ld_dh + c;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -205,7 +283,8 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
   const bool grad = mode & CE_GRAD, loss = mode & CE_LOSS;
   int *count = (int *)(w + l.count), *row_of = (int *)(w + l.row_of), *place = (int *)(w + l.place);
   CeRow *rows = (CeRow *)(w + l.rows);
-  E *hc = (E *)(w + l.hc);
+  E *hc = (E *)(w + l.hc), *hc2 = (E *)(w + l.hc2);
+  float *inv = (float *)(w + l.inv);
   cudaError_t e;
   float *lo = loss ? a.loss : nullptr, *ls = loss ? a.lse : nullptr;
   if (a.targets64)
@@ -215,11 +294,11 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
     e = launch_pdl(ce_places_kernel<int32_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
                    (const int32_t *)a.targets, count, row_of, place, rows, lo, ls, status);
   if (e != cudaSuccess) return e;
-  const bool wide = a.D % Vec16<E>::N == 0 && a.ld_h % Vec16<E>::N == 0 && ((uintptr_t)a.hidden & 15) == 0;
-  e = launch_pdl(ce_rows_kernel<E>, dim3((unsigned)ceil_div((int64_t)a.T + CE_ROWS, 8)), dim3(256), 0, stream, a.T, a.D,
-                 a.ld_h, l.dp, a.ld_dh, (const E *)a.hidden, hc, grad ? (E *)a.dh : (E *)nullptr, (const int *)count,
-                 (const int *)place, rows, (const float *)(grad && !loss ? a.lse : nullptr), a.dloss, a.scale, a.z_loss,
-                 wide);
+  constexpr int N = Vec16<E>::N;
+  const bool wide = a.D % N == 0 && a.ld_h % N == 0 && ((uintptr_t)a.hidden & 15) == 0;
+  const bool wide_w = a.ld_w % N == 0 && ((uintptr_t)a.weight & 15) == 0;
+  e = launch_pdl(ce_rows_kernel<E>, dim3((unsigned)ceil_div((int64_t)a.T + CE_ROWS, 8)), dim3(256), 0, stream, a, l.dp, hc,
+                 hc2, (const int *)count, (const int *)place, rows, inv, grad, grad && !loss, wide, wide_w);
   if (e != cudaSuccess) return e;
   if (l.ldw) {
     e = launch_pdl(ce_weight_copy_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(a.V, 8), 8 * 152)), dim3(256), 0,
@@ -236,7 +315,9 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
   m.count = count;
   m.row_of = row_of;
   m.rows = rows;
+  m.inv = inv;
   m.h = hc;
+  m.h2 = hc2;
   m.w = l.ldw ? w + l.wc : a.weight;
   m.g = w + l.g;
   m.scale = a.scale;
@@ -252,9 +333,9 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
   m.status = status;
   if (loss) {
     if ((e = a.f32 ? ce_simt_stats(m, stream) : ce_tc_stats(m, stream)) != cudaSuccess) return e;
-    e = launch_pdl(ce_join_kernel, dim3(l.tpad / 32), dim3(1024), 0, stream, (const int *)count, l.nparts, l.tpad,
-                   (const float2 *)m.part, (const float *)m.xt, (const int *)row_of, rows, a.loss, a.lse,
-                   (const float *)(grad ? a.dloss : nullptr), a.scale, a.z_loss);
+    e = launch_pdl(ce_join_kernel<E>, dim3(l.tpad / 32), dim3(1024), 0, stream, (const int *)count, l.nparts, l.tpad,
+                   (const float2 *)m.part, (const float *)m.xt, (const int *)row_of, rows, inv, a.loss, a.lse,
+                   (const float *)(grad ? a.dloss : nullptr), a.scale, a.z_loss, (const E *)hc, hc2, l.dp);
     if (e != cudaSuccess) return e;
   }
   if (!grad) return cudaSuccess;
@@ -272,7 +353,7 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
     if ((e = a.f32 ? ce_simt_grads(mp, p, stream) : ce_tc_grads(mp, p, stream)) != cudaSuccess) return e;
     if (l.per_piece > 1) {
       e = launch_pdl(ce_planes_kernel<E>, dim3((unsigned)ceil_div(a.D, 1024), (unsigned)std::min(l.tpad, 16384)), dim3(256),
-                     0, stream, (const int *)count, (const int *)row_of, a.D, l.dp, l.tpad, p.nchunks,
+                     0, stream, (const int *)count, (const int *)row_of, (const float *)m.inv, a.D, l.dp, l.tpad, p.nchunks,
                      (const float *)mp.planes, mp.acc, (E *)a.dh, a.ld_dh, p.first, p.last);
       if (e != cudaSuccess) return e;
     }

@@ -10,7 +10,7 @@
 namespace moe {
 
 // Columns of the logits that leave one (maximum, sum) a row.
-constexpr int CE_PART = 128;
+constexpr int CE_PART = 64;
 // Row tiles are CE_ROWS high: the compacted rows are padded to that with zeros.
 constexpr int CE_ROWS = 256;
 // Chunks of the vocabulary over which dhidden is summed: a chunk's sum stays in
@@ -18,11 +18,17 @@ constexpr int CE_ROWS = 256;
 // alone, so that a row's sums do not depend on the batch.
 constexpr int CE_CHUNK_BF16 = 8192, CE_CHUNK_F32 = 512;
 
-// Of a row that counts, in compacted order.
+// Of a row that counts, in compacted order.  In bfloat16 a row of g is kept
+// times a factor within 2^-8 of 1, chosen so that the target's entry, the
+// largest by far in most rows, is a bfloat16 number: rounding it would put one
+// and the same relative error of up to 2^-8 on nearly all of the row's dhidden
+// and of its part of dweight.  The factor is taken back out in FP32 from dhidden, and
+// from the row of h that meets the row of g in dweight's product (rounded
+// element by element, errors that have nothing to do with one another).
 struct CeRow {
   float lse2;  // lse * log2(e)
-  float c;     // scale * dloss * (1 + 2 z lse)
-  float c1;    // scale * dloss
+  float c;     // scale * dloss * (1 + 2 z lse), times the factor
+  float b;     // the target's entry of g, times the factor
   int target;  // -1: a row of padding
 };
 
@@ -31,7 +37,7 @@ struct CeLayout {
   int64_t dp;       // row length of the compacted rows, elements
   int64_t ldw;      // row length of the weights' copy (0: the caller's weights are read)
   int64_t ldg;      // row length of a piece of g
-  size_t count, row_of, place, rows, hc, wc, part, xt, g, acc, bytes;
+  size_t count, row_of, place, rows, inv, hc, hc2, wc, part, xt, g, acc, bytes;
 };
 
 inline CeLayout ce_layout(const CeArgs &a, int mode) {
@@ -60,7 +66,9 @@ inline CeLayout ce_layout(const CeArgs &a, int mode) {
   l.row_of = take((int64_t)l.tpad * 4);
   l.place = take((int64_t)l.tpad * 4);
   l.rows = take((int64_t)l.tpad * sizeof(CeRow));
+  l.inv = take((int64_t)l.tpad * 4);
   l.hc = take(l.tpad * l.dp * e);
+  l.hc2 = take(!a.f32 && (mode & CE_GRAD) ? l.tpad * l.dp * e : 0);
   l.wc = take(l.ldw ? a.V * l.ldw * e : 0);
   l.part = take(mode & CE_LOSS ? (int64_t)l.nparts * l.tpad * 8 : 0);
   l.xt = take(mode & CE_LOSS ? (int64_t)l.tpad * 4 : 0);
@@ -80,7 +88,8 @@ struct CeMats {
   const int *count;     // rows that count
   const int *row_of;    // their places among the caller's rows
   const CeRow *rows;
-  const void *h, *w;    // compacted rows; weights
+  const float *inv;     // 1 / the rows' factors
+  const void *h, *h2, *w;  // compacted rows; over their factors; weights
   void *g;              // [tpad, ldg]
   float scale;
   float2 *part;         // [nparts, tpad]
@@ -99,7 +108,7 @@ struct CePiece {
   bool first, last;
 };
 
-// The logits' (maximum, sum) of every 128 columns, and the targets' logits.
+// The logits' (maximum, sum) of every 64 columns, and the targets' logits.
 cudaError_t ce_tc_stats(const CeMats &m, cudaStream_t stream);
 cudaError_t ce_simt_stats(const CeMats &m, cudaStream_t stream);
 // g of a piece.

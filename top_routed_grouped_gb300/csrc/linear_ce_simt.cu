@@ -4,7 +4,7 @@
 // hold, so float models (small ones, and checks) take FFMA: tiles of 128 x
 // 128 outputs, 256 threads with 8 x 8 outputs each, K steps of 16 through
 // shared memory, one step ahead in registers.  The epilogues are those of the
-// tensor-core kernels: the same statistics per 128 columns, the same pieces.
+// tensor-core kernels: the same statistics per 64 columns, the same pieces.
 // Each output is summed over K in order.
 #include "linear_ce.h"
 
@@ -134,20 +134,25 @@ ce_simt_kernel(const SimtParams a) {
     for (int i = 0; i < 8; ++i) {
       const int row = r0 + rowof(i);
       const int target = m.rows[row].target - c0;
-      float big = -INFINITY, s = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = colof(j);
-        const float x = acc[i][j] * (m.scale * L2E);
-        if (c == target) m.xt[row] = x;
-        acc[i][j] = c0 + c < m.V ? x : -INFINITY;
-        big = fmaxf(big, acc[i][j]);
+      for (int hf = 0; hf < 2; ++hf) {  // 64 columns each
+        float big = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int j = 4 * hf; j < 4 * hf + 4; ++j) {
+          const int c = colof(j);
+          const float x = acc[i][j] * (m.scale * L2E);
+          if (c == target) m.xt[row] = x;
+          acc[i][j] = c0 + c < m.V ? x : -INFINITY;
+          big = fmaxf(big, acc[i][j]);
+        }
+        for (int d = 8; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, d));
+        const float ref = big == -INFINITY ? 0.f : big;
+#pragma unroll
+        for (int j = 4 * hf; j < 4 * hf + 4; ++j) s += exp2f(acc[i][j] - ref);
+        for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(FULL_MASK, s, d);
+        const int part = blockIdx.y * 2 + hf;
+        if (tx == 0 && part < a.nparts) m.part[(int64_t)part * m.tpad + row] = make_float2(big, s);
       }
-      for (int d = 8; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, d));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += big == -INFINITY ? (acc[i][j] == -INFINITY ? 0.f : acc[i][j]) : exp2f(acc[i][j] - big);
-      for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(FULL_MASK, s, d);
-      if (tx == 0) m.part[(int64_t)blockIdx.y * m.tpad + row] = make_float2(big, s);
     }
   } else if (KIND == SM_LOGITS) {
 #pragma unroll
@@ -155,12 +160,12 @@ ce_simt_kernel(const SimtParams a) {
       const int row = r0 + rowof(i);
       const CeRow R = m.rows[row];
       const int target = R.target - v0 - c0;
-      const bool zero = R.c == 0.f && R.c1 == 0.f;
+      const bool zero = R.c == 0.f && R.b == 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = colof(j);
         float x = R.c * exp2f(fmaf(acc[i][j], m.scale * L2E, -R.lse2));
-        if (c == target) x -= R.c1;
+        if (c == target) x = R.b;
         acc[i][j] = zero || v0 + c0 + c >= m.V ? 0.f : x;
       }
       float *out = (float *)m.g + row * m.ldg + c0 + tx * 4;

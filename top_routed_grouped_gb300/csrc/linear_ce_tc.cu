@@ -5,12 +5,12 @@
 // (cta_group::2): each CTA holds 128 rows of A and half of B's columns, and
 // its tensor memory receives 128 rows of the tile.
 //
-//   STATS   x[t, v] = sum_d h[t, d] w[v, d]     epilogue: for each row and 128 columns the
+//   STATS   x[t, v] = sum_d h[t, d] w[v, d]     epilogue: for each row and 64 columns the
 //           maximum and the sum of exponentials, and the target's logit
 //   LOGITS  the same product for the columns of a piece; epilogue: g, one
 //           rounding to bf16, by TMA stores
 //   GRADS   dh[t, d] = sum_v g[t, v] w[v, d]    (A K-major, B MN-major)
-//           dw[v, d] = sum_t g[t, v] h[t, d]    (both MN-major)
+//           dw[v, d] = sum_t g[t, v] h2[t, d]   (both MN-major; h2: h over the row's factor)
 //           in one launch: the two have the same tiles and, at 8192 rows,
 //           the same K, so that together they fill the last wave better
 //
@@ -33,15 +33,27 @@ using namespace umma;
 
 constexpr int CE_STATS = 0, CE_LOGITS = 1, CE_GRADS = 2;
 constexpr int CT_STAGES = 6, CT_A_BYTES = 16384, CT_STAGE_BYTES = 2 * CT_A_BYTES;
-constexpr int CT_EPI_FIRST = 2, CT_EPI_WARPS = 8, CT_EPI_BYTES = 4096;
-constexpr int CT_THREADS = 32 * (CT_EPI_FIRST + CT_EPI_WARPS);
-constexpr int CT_SMEM = 1024 + CT_STAGES * CT_STAGE_BYTES + CT_EPI_WARPS * CT_EPI_BYTES + 512;
+// Epilogue warps: eight, half of the columns each, with 4 KB of staging; for
+// the statistics sixteen with a quarter each, so that a thread's sums over the
+// K chunks (64) stay in registers.
+constexpr int CT_EPI_FIRST = 2, CT_EPI_BYTES = 8 * 4096;
+template <int KIND>
+constexpr int ct_epi_warps() { return KIND == CE_STATS ? 16 : 8; }
+template <int KIND>
+constexpr int ct_threads() { return 32 * (CT_EPI_FIRST + ct_epi_warps<KIND>()); }
+constexpr int CT_SMEM = 1024 + CT_STAGES * CT_STAGE_BYTES + CT_EPI_BYTES + 512;
 static_assert(CT_SMEM <= 232448, "shared memory of a CTA");
 constexpr uint32_t CT_TMEM_COLS = 512;
+// The statistics' products are summed in chunks of 512 of K, each in an
+// accumulator of its own, and the chunks in FP32 registers: the tensor cores
+// cut each of their sums off instead of rounding it, which shows in a float
+// loss as 1.2e-6 of it at K = 2048 in one chain and 3e-7 in chunks.
+constexpr int CT_KCHUNK = 8;
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
   CUtensorMap h, w, g;     // K-major tiles: boxes of 128 rows x 64
+  CUtensorMap h32;         // the same rows, 32 at a time
   CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64
   CUtensorMap gout;        // 32 rows x 64: g's stores
   CUtensorMap dw;          // dweight: 32 rows x 128 bytes
@@ -52,6 +64,7 @@ struct CtParams {
   const int *count;
   const int *row_of;
   const CeRow *rows;
+  const float *inv;
   float s2;  // scale * log2(e)
   float2 *part;
   float *xt;
@@ -74,10 +87,10 @@ struct CtItem {
 
 template <int KIND>
 struct CtWork {
-  int mt, nt, ndh, ndw, total, kd, kr;
+  int count, mt, nt, ndh, ndw, total, kd, kr;
   bool dw_first;
   __device__ CtWork(const CtParams &p) {
-    const int count = __ldg(p.count);
+    count = __ldg(p.count);
     mt = (count + CE_ROWS - 1) / CE_ROWS;
     kd = (p.D + 63) / 64;
     kr = (count + 63) / 64;
@@ -136,49 +149,35 @@ __device__ inline void tma_reduce_add_2d(const CUtensorMap *m, const void *src, 
                : "memory");
 }
 
-// ---- epilogues: a warp's 32 rows (lane = row) x cols / 2 columns from c0 of the tile ----
-__device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, uint32_t taddr, int row, int half) {
-  const int col0 = im.n * 256 + half * 128;
-  if (col0 >= p.V) return;
-  const int target = p.rows[row].target - col0;
-  float m = -INFINITY, s = 0.f;
+// ---- epilogues: a warp's 32 rows (lane = row) x half of the tile's columns ----
+// v: the thread's 64 logits (columns from 64 cq of the tile), summed over the
+// K chunks.
+__device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, float (&v)[64], int row, int cq) {
+  const int col0 = im.n * 256 + cq * 64;
+  const int target = p.rows[row].target - col0, left = p.V - col0;
+  if (left <= 0) return;
+  if ((unsigned)target < 64u) {
+    float x = 0.f;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float v[32];
-    tmem_ld32(taddr + c * 32, v);
-    const unsigned at = (unsigned)(target - c * 32);
-    if (at < 32u) {
-      float x = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x = at == (unsigned)j ? v[j] : x;
-      p.xt[row] = x * p.s2;
-    }
-    const int left = p.V - col0 - c * 32;
-    if (left < 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = j < left ? v[j] * p.s2 : -INFINITY;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= p.s2;
-    }
-    float big = m;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) big = fmaxf(big, v[j]);
-    if (big == -INFINITY) {  // nothing yet (NaN does not get past fmaxf, but does get into the sum)
-#pragma unroll
-      for (int j = 0; j < 32; ++j) s += v[j] == -INFINITY ? 0.f : v[j];
-      continue;
-    }
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      s0 += ex2(v[j] - big);
-      s1 += ex2(v[j + 1] - big);
-    }
-    s = s * ex2(m - big) + (s0 + s1);
-    m = big;
+    for (int j = 0; j < 64; ++j) x = target == j ? v[j] : x;
+    p.xt[row] = x * p.s2;
   }
-  p.part[(int64_t)(im.n * 2 + half) * p.tpad + row] = make_float2(m, s);
+#pragma unroll
+  for (int j = 0; j < 64; ++j) v[j] *= p.s2;
+  if (left < 64) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      if (j >= left) v[j] = -INFINITY;
+  }
+  float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int j = 4; j < 64; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+  float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  const float ref = m == -INFINITY ? 0.f : m;  // (NaN does not get past fmaxf, but does get into the sum)
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 64; ++j) s[j & 3] += ex2(v[j] - ref);
+  p.part[(int64_t)(im.n * 4 + cq) * p.tpad + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
 __device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row,
@@ -186,7 +185,7 @@ __device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, co
   const int pc0 = im.n * 256 + half * 128;  // column in the piece
   const CeRow R = p.rows[row];
   const int target = R.target - p.v0 - pc0;
-  const bool zero = R.c == 0.f && R.c1 == 0.f;
+  const bool zero = R.c == 0.f && R.b == 0.f;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     float v[2][32];
@@ -200,7 +199,7 @@ __device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, co
       const unsigned at = (unsigned)(target - c * 64 - hh * 32);
       if (at < 32u) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[hh][j] -= at == (unsigned)j ? R.c1 : 0.f;
+        for (int j = 0; j < 32; ++j) v[hh][j] = at == (unsigned)j ? R.b : v[hh][j];
       }
       if (zero || left < 64) {
 #pragma unroll
@@ -269,6 +268,8 @@ __device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uin
         return;
       }
       __nv_bfloat16 *out = p.dh + p.row_of[row] * p.ld_dh + col;
+      const float f = p.inv[row];
+      x.x *= f; x.y *= f; x.z *= f; x.w *= f;
       const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
       if (p.dh_wide) {
         *(uint2 *)out = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
@@ -347,14 +348,15 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(CT_THREADS, 1)
+__global__ void __launch_bounds__(ct_threads<KIND>(), 1)
 ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
+  constexpr int EPI_WARPS = ct_epi_warps<KIND>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   auto sa = [&](int s) { return base + s * CT_STAGE_BYTES; };
   auto sb = [&](int s) { return base + s * CT_STAGE_BYTES + CT_A_BYTES; };
   uint8_t *epi = base + CT_STAGES * CT_STAGE_BYTES;
-  uint64_t *bars = (uint64_t *)(epi + CT_EPI_WARPS * CT_EPI_BYTES);
+  uint64_t *bars = (uint64_t *)(epi + CT_EPI_BYTES);
   uint64_t *full = bars, *empty = full + CT_STAGES;
   uint64_t *tfull = empty + CT_STAGES, *tempty = tfull + 2, *mma_done = tempty + 2;
   uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
@@ -371,7 +373,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * CT_EPI_WARPS);
+      mbar_init(&tempty[b], 2 * EPI_WARPS);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -399,7 +401,11 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         const CtItem im = work.item(it, p);
         const int mrow = im.m * 256 + (int)rank * 128;
         const int half = im.cols / 2, ncol = im.n * 256 + (int)rank * half;
-        const uint32_t bytes = 2 * (CT_A_BYTES + (uint32_t)half * 128);
+        // Of the last rows only those that are there are read, 32 at a time: the
+        // lines behind them reach nothing but accumulator rows that nobody reads.
+        const int arows = KIND == CE_GRADS ? 128 : min(128, max(0, (work.count - mrow + 31) & ~31));
+        const int arows2 = KIND == CE_GRADS ? 256 : min(256, max(0, (work.count - im.m * 256 + 31) & ~31));
+        const uint32_t bytes = 128 * (arows2 + 2 * (uint32_t)half);
         for (int kb = 0; kb < im.nk; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
           // Both CTAs' tiles complete on the even CTA's barrier.
@@ -407,7 +413,9 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
           const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
           const int k = kb * 64;
           if (KIND != CE_GRADS) {
-            tma_load_2d_pair(sa(stage), &maps.h, bar, k, mrow, keep);
+            if (arows == 128) tma_load_2d_pair(sa(stage), &maps.h, bar, k, mrow, keep);
+            else
+              for (int j = 0; j < arows; j += 32) tma_load_2d_pair(sa(stage) + j * 128, &maps.h32, bar, k, mrow + j, keep);
             tma_load_2d_pair(sb(stage), &maps.w, bar, k, p.v0 + ncol, pass);
           } else if (im.kind == 1) {
             const int v = im.chunk * p.chunk + k;
@@ -441,13 +449,16 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         for (int it = cid; it < work.total && ok; it += ncl) {
           const CtItem im = work.item(it, p);
           if (im.nk == 0) continue;
-          const int b = cnt & 1;
-          if (!mbar_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) break;
-          tc_fence_after();
           const bool a_mn = KIND == CE_GRADS && im.kind == 2, b_mn = KIND == CE_GRADS;
           const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
           const uint32_t astep = a_mn ? 128 : 2, bstep = b_mn ? 128 : 2;  // K = 16: 2048 or 32 bytes
           for (int kb = 0; kb < im.nk; ++kb) {
+            const int kc = KIND == CE_STATS ? kb % CT_KCHUNK : kb;  // in this accumulator
+            const int b = cnt & 1;
+            if (kc == 0) {
+              if (!mbar_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
+              tc_fence_after();
+            }
             if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a0 = smem_u32(sa(stage)), b0 = smem_u32(sb(stage));
@@ -455,13 +466,14 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
             const uint64_t bd = b_mn ? smem_desc_mn_sw128(b0, 8192) : smem_desc_sw128(b0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kb | kk) != 0);
+              mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kc | kk) != 0);
             mma_commit_pair(&empty[stage]);
             if (++stage == CT_STAGES) stage = 0, phase ^= 1;
+            if (kb + 1 == im.nk || (KIND == CE_STATS && kc + 1 == CT_KCHUNK)) {
+              mma_commit_pair(&tfull[b]);
+              ++cnt;
+            }
           }
-          if (!ok) break;
-          mma_commit_pair(&tfull[b]);
-          ++cnt;
         }
         mma_commit_pair(mma_done);
       }
@@ -472,34 +484,56 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;
-    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * CT_EPI_BYTES;
+    const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;  // TMEM lane quarter; which of the columns
+    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * 4096;
     const uint32_t tempty_leader0 = mapa_shared(&tempty[0], 0);
-    const int count = __ldg(p.count);
     uint32_t cnt = 0;
-    for (int it = cid; it < work.total; it += ncl) {
-      const CtItem im = work.item(it, p);
-      const int b = cnt & 1;
-      if (im.nk != 0) {
-        int ok = 0;
-        if (lane == 0) ok = mbar_wait(&tfull[b], (cnt >> 1) & 1, abort_flag, p.status) ? 1 : 0;
-        if (!__shfl_sync(FULL_MASK, ok, 0)) break;
-        tc_fence_after();
-      }
-      const int row0 = im.m * 256 + (int)rank * 128 + q * 32;
-      const uint32_t taddr = tmem + b * 256 + ((uint32_t)(q * 32) << 16) + half * (im.cols / 2);
-      if (KIND == CE_STATS) stats_epilogue(p, im, taddr, row0 + lane, half);
-      else if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
-      else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, count, half, stg, lane);
-      else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane);
-      if (im.nk == 0) continue;
+    auto wait = [&] {
+      int ok = 0;
+      if (lane == 0) ok = mbar_wait(&tfull[cnt & 1], (cnt >> 1) & 1, abort_flag, p.status) ? 1 : 0;
+      if (!__shfl_sync(FULL_MASK, ok, 0)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto release = [&] {  // the accumulator, to the MMA thread
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (leader) mbar_arrive(&tempty[b]);
-        else mbar_arrive_remote(tempty_leader0 + (uint32_t)(b * sizeof(uint64_t)));
+        if (leader) mbar_arrive(&tempty[cnt & 1]);
+        else mbar_arrive_remote(tempty_leader0 + (uint32_t)((cnt & 1) * sizeof(uint64_t)));
       }
       ++cnt;
+    };
+    for (int it = cid; it < work.total; it += ncl) {
+      const CtItem im = work.item(it, p);
+      const int row0 = im.m * 256 + (int)rank * 128 + q * 32;
+      const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
+      if (KIND == CE_STATS) {
+        float v[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] = 0.f;
+        bool ok = true;
+        for (int kb = 0; kb < im.nk; kb += CT_KCHUNK) {
+          if (!(ok = wait())) break;
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            float x[16];
+            tmem_ld16(tq + (cnt & 1) * 256 + half * 64 + c, x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[c + j] += x[j];
+          }
+          release();
+        }
+        if (!ok) break;
+        stats_epilogue(p, im, v, row0 + lane, half);
+        continue;
+      }
+      if (im.nk != 0 && !wait()) break;
+      const uint32_t taddr = tq + (cnt & 1) * 256 + half * (im.cols / 2);
+      if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
+      else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, work.count, half, stg, lane);
+      else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane);
+      if (im.nk != 0) release();
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
@@ -528,7 +562,7 @@ static cudaError_t launch(const CtMaps &maps, const CtParams &p, int64_t items, 
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(items, device_sms() / 2));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(CT_THREADS);
+  cfg.blockDim = dim3(ct_threads<KIND>());
   cfg.dynamicSmemBytes = CT_SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
@@ -551,6 +585,7 @@ static CtParams params(const CeMats &m) {
   p.count = m.count;
   p.row_of = m.row_of;
   p.rows = m.rows;
+  p.inv = m.inv;
   p.s2 = m.scale * CE_LOG2E;
   p.part = m.part;
   p.xt = m.xt;
@@ -572,7 +607,8 @@ static void piece(CtParams &p, const CePiece &c) {
 
 cudaError_t ce_tc_stats(const CeMats &m, cudaStream_t stream) {
   CtMaps maps = {};
-  if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128))
+  if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.h32, m.h, m.tpad, m.ldh, m.ldh, 32) ||
+      !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128))
     return cudaErrorInvalidValue;
   return launch<CE_STATS>(maps, params(m), (int64_t)(m.tpad / 256) * ceil_div(m.V, 256), stream);
 }
@@ -581,7 +617,8 @@ cudaError_t ce_tc_logits_grad(const CeMats &m, const CePiece &c, cudaStream_t st
   CtMaps maps = {};
   CtParams p = params(m);
   piece(p, c);
-  if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128) ||
+  if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.h32, m.h, m.tpad, m.ldh, m.ldh, 32) ||
+      !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128) ||
       !map_ld(&maps.gout, m.g, m.tpad, m.ldg, m.ldg, 32))
     return cudaErrorInvalidValue;
   return launch<CE_LOGITS>(maps, p, (int64_t)(m.tpad / 256) * ceil_div(c.n, 256), stream);
@@ -602,7 +639,7 @@ cudaError_t ce_tc_grads(const CeMats &m, const CePiece &c, cudaStream_t stream) 
   // Tensor maps of dweight want its dense rows on 16-byte boundaries.
   p.dw_tma = ((uintptr_t)m.dw & 15) == 0 && m.D % (m.gf32 ? 4 : 8) == 0;
   if (!map_ld(&maps.g, m.g, m.tpad, m.ldg, m.ldg, 128) || !map_ld(&maps.gt, m.g, m.tpad, m.ldg, m.ldg, 64) ||
-      !map_ld(&maps.wt, m.w, m.V, m.D, m.ldw, 64) || !map_ld(&maps.ht, m.h, m.tpad, m.ldh, m.ldh, 64) ||
+      !map_ld(&maps.wt, m.w, m.V, m.D, m.ldw, 64) || !map_ld(&maps.ht, m.h2, m.tpad, m.ldh, m.ldh, 64) ||
       (p.dw_tma && !map_ld(&maps.dw, m.dw, m.V, m.D, m.D, 32, m.gf32)))
     return cudaErrorInvalidValue;
   const int64_t nt = ceil_div(m.D, 256);

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import struct
 from array import array
+from operator import attrgetter
 
 import torch
 
@@ -146,50 +147,57 @@ def _gapless(t) -> bool:
     return True
 
 
+_dtype_of = attrgetter("dtype")
+
+
 def _tensors(ts, dev, name: str):
-    """Addresses, sizes and type codes, as the library's host arrays."""
-    codes = [_DTYPE.get(t.dtype, -1) for t in ts]
-    if -1 in codes:
-        raise ValueError(f"{name}: float32 or bfloat16 expected, got {ts[codes.index(-1)].dtype}")
-    for t in ts:
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: tensors on device {dev} expected, got one on {t.device}")
-        if not t.is_contiguous() and not _gapless(t) and t.numel():
-            raise ValueError(f"{name}: tensors without gaps expected, got strides {t.stride()} of {list(t.shape)}")
-    return array("Q", [t.data_ptr() for t in ts]), array("q", [t.numel() for t in ts]), array("i", codes)
-
-
-def _at(a) -> int:
-    return a.buffer_info()[0] if len(a) else 0
+    """Addresses, sizes and type codes, as the library's host arrays.  Lists
+    are long (a thousand tensors and more), so each property is asked of all of
+    them in one ``map``."""
+    T = torch.Tensor
+    codes = list(map(_DTYPE.get, map(_dtype_of, ts)))
+    if None in codes:
+        raise ValueError(f"{name}: float32 or bfloat16 expected, got {ts[codes.index(None)].dtype}")
+    devices = set(map(T.get_device, ts))
+    if devices != {dev}:
+        raise ValueError(f"{name}: tensors on device {dev} expected, got some on {sorted(devices - {dev})}")
+    dense = all(map(T.is_contiguous, ts))
+    if not dense:
+        for t in ts:
+            if not t.is_contiguous() and t.numel() and not _gapless(t):
+                raise ValueError(f"{name}: tensors without gaps expected, got strides {t.stride()} of {list(t.shape)}")
+    return array("Q", list(map(T.data_ptr, ts))), array("q", list(map(T.numel, ts))), array("i", codes), dense
 
 
 def _grads(stream, grads, out, norm, max_norm, eps, ws, mode):
     dev, device = grads[0].get_device(), grads[0].device
-    src, numel, code = _tensors(grads, dev, "grads")
+    src, numel, code, dense = _tensors(grads, dev, "grads")
     dst, ocode, written = src, code, grads
     if out is not None:
         if len(out) != len(grads):
             raise ValueError(f"out: {len(grads)} tensors expected, got {len(out)}")
-        for g, o in zip(grads, out):
-            if g.shape != o.shape or (not (g.is_contiguous() and o.is_contiguous()) and g.stride() != o.stride()):
-                raise ValueError(f"out: {list(g.shape)} with strides {g.stride()} expected, got {list(o.shape)} with "
-                                 f"{o.stride()}")
-        dst, _, ocode = _tensors(out, dev, "out")
+        dst, onumel, ocode, odense = _tensors(out, dev, "out")
+        if numel != onumel:
+            raise ValueError("out: tensors of the sizes of grads expected")
+        if not (dense and odense):
+            for g, o in zip(grads, out):
+                if not (g.is_contiguous() and o.is_contiguous()) and (g.shape != o.shape or g.stride() != o.stride()):
+                    raise ValueError(f"out: {list(g.shape)} with strides {g.stride()} expected, got {list(o.shape)} with "
+                                     f"{o.stride()}")
         written = out
     if mode & 1:
         norm = torch.empty((), dtype=torch.float32, device=device)
     elif norm.dtype is not torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
         raise ValueError(f"norm: one float32 on device {dev} expected")
-    args = _GRADS.pack(len(grads), 0, _at(src), _at(dst), _at(numel), _at(code), _at(ocode), max_norm, eps,
-                       norm.data_ptr())
+    args = _GRADS.pack(len(grads), 0, src.buffer_info()[0], dst.buffer_info()[0], numel.buffer_info()[0],
+                       code.buffer_info()[0], ocode.buffer_info()[0], max_norm, eps, norm.data_ptr())
     if mode & 1:
         ws, n = _ws(moe_grad_workspace_size(args) if ws is None else 0, ws, device)
         (moe_grad_norm if mode == 1 else moe_grad_clip)(args, ws.data_ptr(), n, stream)
     else:
         moe_grad_scale(args, stream)
     if mode & 2:
-        for t in written:
-            _written(t)
+        _written(written)
     return norm
 
 
@@ -205,7 +213,7 @@ def grad_norm(grads, ws=None, stream=None):
 def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, ws=None, stream=None):
     """Scale ``grads`` by min(1, max_norm / (norm + eps)) and return the norm
     that they had.  In place, or into ``out``: as many tensors of the same
-    shapes, of float32 or bfloat16 (accumulated float32 gradients become their
+    sizes, of float32 or bfloat16 (accumulated float32 gradients become their
     parameters' type this way)."""
     grads, out = list(grads), None if out is None else list(out)
     if not grads:
