@@ -6,10 +6,11 @@
 // the scaling, which starts at the end where the norm has stopped, so that
 // what L2 still holds is read from there.  All tensors go in one launch: the
 // table of them is a kernel argument (nothing to copy to the device, and a
-// captured graph has it inside), chunks of a few thousand elements are dealt
-// out to the CTAs in turn, and a chunk finds its tensor by bisection.
+// captured graph has it inside).  Tensors are cut into chunks of 8192
+// elements; a CTA has a run of neighbouring chunks, finds the tensor of the first by
+// bisection and goes on from there, forwards for the norm, backwards for the scaling.
 //
-// Squares are summed in FP32 over at most 128 elements of a thread, then in
+// Squares are summed in FP32 over at most 32 elements of a thread, then in
 // FP64.  Where such a sum is out of the range in which FP32 squares keep their
 // bits (some |g| above 1e15, or all of them below 1e-12) the chunk's elements
 // are read again and summed in FP64.  No atomics: each CTA leaves one partial
@@ -25,8 +26,8 @@
 namespace moe {
 
 constexpr int GN_THREADS = 256;
-constexpr int GN_CTAS = 8;             // CTAs a SM
-constexpr int GN_MAX_CHUNK = 128 * GN_THREADS, GN_MIN_CHUNK = 8 * GN_THREADS;
+constexpr int GN_CTAS = 8;                   // CTAs a SM
+constexpr int GN_CHUNK = 32 * GN_THREADS;    // elements
 
 // CAP tensors: 28 bytes each, of the 32 KB that a kernel's arguments may take.
 template <int CAP>
@@ -36,7 +37,7 @@ struct GradTable {
   int64_t size[CAP];    // elements
   int first[CAP + 1];   // chunks before this tensor's
   uint32_t f32[CAP / 32], of32[CAP / 32];
-  int n, chunk;         // tensors; elements a chunk
+  int n;
 };
 constexpr int GN_SMALL = 64, GN_LARGE = 1024;
 static_assert(sizeof(GradTable<GN_LARGE>) <= 32000, "a kernel's arguments");
@@ -82,10 +83,10 @@ __device__ inline double cta_sum(double v) {
 // Squares of this thread's elements of chunk c of a tensor: the head (chunk
 // 0), units of 16 bytes, the tail (the last chunk).
 template <typename E>
-__device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks, int chunk) {
+__device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks) {
   constexpr int N = Vec16<E>::N;
   const int head = head_of(p, n);
-  const int64_t units = (n - head) / N, per = chunk / N;
+  const int64_t units = (n - head) / N, per = GN_CHUNK / N;
   const int64_t u0 = c * per, u1 = c + 1 == nchunks ? units : min(units, u0 + per);
   const uint4 *v = (const uint4 *)(p + head);
   const int tail = (int)(n - head - units * N);
@@ -102,14 +103,16 @@ __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks
     any |= w.x | w.y | w.z | w.w;
   };
   int64_t u = u0 + threadIdx.x;
-  for (; u + 3 * GN_THREADS < u1; u += 4 * GN_THREADS) {
-    uint4 w[4];
+  constexpr int B = 32 / N;  // units of a thread: all of them in flight
+  if (u0 + per <= u1) {
+    uint4 w[B];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __ldg(v + u + i * GN_THREADS);
+    for (int i = 0; i < B; ++i) w[i] = __ldg(v + u + i * GN_THREADS);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unit(w[i], s[i & 2], s[(i & 2) + 1]);
+    for (int i = 0; i < B; ++i) unit(w[i], s[2 * i & 2], s[(2 * i & 2) + 1]);
+  } else {
+    for (; u < u1; u += GN_THREADS) unit(__ldg(v + u), s[0], s[1]);
   }
-  for (; u < u1; u += GN_THREADS) unit(__ldg(v + u), s[0], s[1]);
   // At most one element of the head and one of the tail a thread.
   float edge[2] = {0.f, 0.f};
   if (c == 0 && (int)threadIdx.x < head) edge[0] = Elem<E>::load(p + threadIdx.x);
@@ -130,17 +133,26 @@ __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks
   return d;
 }
 
+// The run of chunks of this CTA.
+__device__ inline void run_of(int total, int &c0, int &c1) {
+  c0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
+  c1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(GN_THREADS)
 grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, double *part) {
   griddep_launch();
+  int c0, c1;
+  run_of(t.first[t.n], c0, c1);
+  int i = tensor_of(t, c0);
   griddep_wait();
-  const int total = t.first[t.n];
   double sum = 0;
-  for (int c = blockIdx.x; c < total; c += gridDim.x) {
-    const int i = tensor_of(t, c), first = t.first[i], k = t.first[i + 1] - first;
-    if (t.f32[i >> 5] >> (i & 31) & 1) sum += chunk_squares((const float *)t.in[i], t.size[i], c - first, k, t.chunk);
-    else sum += chunk_squares((const __nv_bfloat16 *)t.in[i], t.size[i], c - first, k, t.chunk);
+  for (int c = c0; c < c1; ++c) {
+    if (c == t.first[i + 1]) ++i;  // (no tensor of the table is empty)
+    const int first = t.first[i], k = t.first[i + 1] - first;
+    if (t.f32[i >> 5] >> (i & 31) & 1) sum += chunk_squares((const float *)t.in[i], t.size[i], c - first, k);
+    else sum += chunk_squares((const __nv_bfloat16 *)t.in[i], t.size[i], c - first, k);
   }
   sum = cta_sum(sum);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
@@ -161,38 +173,40 @@ __global__ void __launch_bounds__(GN_THREADS) grad_norm_finish_kernel(const doub
 }
 
 template <typename I, typename O>
-__device__ inline void chunk_scale(const I *in, O *out, int64_t n, int c, int nchunks, int chunk, float f) {
+__device__ inline void chunk_scale(const I *in, O *out, int64_t n, int c, int nchunks, float f) {
   // Groups of eight elements that start on a 16-byte boundary of the output.
   const int head = head_of(out, n);
-  const int64_t groups = (n - head) / 8, per = chunk / 8;
+  const int64_t groups = (n - head) / 8, per = GN_CHUNK / 8;
   const int64_t g0 = c * per, g1 = c + 1 == nchunks ? groups : min(groups, g0 + per);
   const int tail = (int)(n - head - groups * 8);
   const I *pi = in + head;
   O *po = out + head;
   constexpr int NI = Vec16<I>::N, NO = Vec16<O>::N;
   const bool wide = ((uintptr_t)pi & 15) == 0;
-  for (int64_t g = g0 + threadIdx.x; g < g1; g += 2 * GN_THREADS) {
-    float x[2][8];
+  if (wide && g0 + per <= g1) {  // a whole chunk: all of a thread's groups in flight
+    const int64_t g = g0 + threadIdx.x;
+    uint4 w[4][8 / NI];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t q = g + j * GN_THREADS;
-      if (q >= g1) break;
-      if (wide) {
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 8 / NI; ++i) Vec16<I>::load(pi + q * 8 + i * NI, *(float(*)[NI])&x[j][i * NI]);
-      } else {
+      for (int i = 0; i < 8 / NI; ++i) w[j][i] = *((const uint4 *)(pi + (g + j * GN_THREADS) * 8) + i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[j][i] = Elem<I>::load(pi + q * 8 + i);
-      }
+    for (int j = 0; j < 4; ++j) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8 / NI; ++i) Vec16<I>::unpack(w[j][i], *(float(*)[NI])&x[i * NI]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= f;
+#pragma unroll
+      for (int i = 0; i < 8 / NO; ++i) Vec16<O>::store(po + (g + j * GN_THREADS) * 8 + i * NO, *(float(*)[NO])&x[i * NO]);
     }
+  } else {
+    for (int64_t g = g0 + threadIdx.x; g < g1; g += GN_THREADS) {
+      float x[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t q = g + j * GN_THREADS;
-      if (q >= g1) break;
+      for (int i = 0; i < 8; ++i) x[i] = Elem<I>::load(pi + g * 8 + i) * f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] *= f;
-#pragma unroll
-      for (int i = 0; i < 8 / NO; ++i) Vec16<O>::store(po + q * 8 + i * NO, *(float(*)[NO])&x[j][i * NO]);
+      for (int i = 0; i < 8 / NO; ++i) Vec16<O>::store(po + g * 8 + i * NO, *(float(*)[NO])&x[i * NO]);
     }
   }
   if (c == 0 && (int)threadIdx.x < head)
@@ -209,6 +223,9 @@ __global__ void __launch_bounds__(GN_THREADS)
 grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const double *part, int nparts, float max_norm, float eps,
                   float *norm) {
   griddep_launch();
+  int c0, c1;
+  run_of(t.first[t.n], c0, c1);
+  int i = c1 > c0 ? tensor_of(t, c1 - 1) : 0;
   griddep_wait();
   float r;
   if (part) {
@@ -219,16 +236,16 @@ grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const double *part, 
   }
   float f = max_norm / (r + eps);
   if (f > 1.f) f = 1.f;  // (NaN stays)
-  const int total = t.first[t.n];
-  for (int c = total - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-    const int i = tensor_of(t, c), first = t.first[i], k = t.first[i + 1] - first;
+  for (int c = c1 - 1; c >= c0; --c) {
+    if (c < t.first[i]) --i;
     if (f == 1.f && t.in[i] == t.out[i]) continue;
+    const int first = t.first[i], k = t.first[i + 1] - first;
     const int64_t n = t.size[i];
     const bool a = t.f32[i >> 5] >> (i & 31) & 1, b = t.of32[i >> 5] >> (i & 31) & 1;
-    if (a && b) chunk_scale((const float *)t.in[i], (float *)t.out[i], n, c - first, k, t.chunk, f);
-    else if (a) chunk_scale((const float *)t.in[i], (__nv_bfloat16 *)t.out[i], n, c - first, k, t.chunk, f);
-    else if (b) chunk_scale((const __nv_bfloat16 *)t.in[i], (float *)t.out[i], n, c - first, k, t.chunk, f);
-    else chunk_scale((const __nv_bfloat16 *)t.in[i], (__nv_bfloat16 *)t.out[i], n, c - first, k, t.chunk, f);
+    if (a && b) chunk_scale((const float *)t.in[i], (float *)t.out[i], n, c - first, k, f);
+    else if (a) chunk_scale((const float *)t.in[i], (__nv_bfloat16 *)t.out[i], n, c - first, k, f);
+    else if (b) chunk_scale((const __nv_bfloat16 *)t.in[i], (float *)t.out[i], n, c - first, k, f);
+    else chunk_scale((const __nv_bfloat16 *)t.in[i], (__nv_bfloat16 *)t.out[i], n, c - first, k, f);
   }
 }
 
@@ -240,19 +257,10 @@ static int most_ctas() { return std::max(1, device_sms()) * GN_CTAS; }
 
 size_t grad_scratch_bytes(const GradList &a) { return (size_t)launches(a) * most_ctas() * sizeof(double); }
 
-// Elements a chunk: enough chunks for every CTA to have some, up to 128 elements a thread.
-static int chunk_of(const GradList &a) {
-  int64_t total = 0;
-  for (int i = 0; i < a.n; ++i) total += a.numel[i];
-  const int64_t want = total / most_ctas();
-  return (int)std::min<int64_t>(GN_MAX_CHUNK, std::max<int64_t>(GN_MIN_CHUNK, round_up(want, GN_MIN_CHUNK)));
-}
-
 // Tensors [i0, i1) of the list; the number of chunks.
 template <int CAP>
-static int fill(GradTable<CAP> &t, const GradList &a, int i0, int i1, int chunk, bool out) {
+static int fill(GradTable<CAP> &t, const GradList &a, int i0, int i1, bool out) {
   t.n = 0;
-  t.chunk = chunk;
   int chunks = 0;
   for (int i = 0; i < CAP / 32; ++i) t.f32[i] = t.of32[i] = 0;
   for (int i = i0; i < i1; ++i) {
@@ -262,7 +270,7 @@ static int fill(GradTable<CAP> &t, const GradList &a, int i0, int i1, int chunk,
     t.out[k] = out ? a.out[i] : nullptr;
     t.size[k] = a.numel[i];
     t.first[k] = chunks;
-    chunks += (int)ceil_div(a.numel[i], chunk);
+    chunks += (int)ceil_div(a.numel[i], GN_CHUNK);
     if (a.dtype[i] == 0) t.f32[k >> 5] |= 1u << (k & 31);
     if (out && a.odtype[i] == 0) t.of32[k >> 5] |= 1u << (k & 31);
   }
@@ -272,14 +280,14 @@ static int fill(GradTable<CAP> &t, const GradList &a, int i0, int i1, int chunk,
 
 template <int CAP>
 static cudaError_t run(const GradList &a, int mode, double *part, cudaStream_t stream) {
-  const int chunk = chunk_of(a), most = most_ctas();
+  const int most = most_ctas();
   const int nl = (int)ceil_div(a.n, CAP);
   GradTable<CAP> t;
   cudaError_t e;
   int parts = 0;
   if (mode & GRAD_NORM) {
     for (int l = 0; l < nl; ++l) {
-      const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), chunk, false);
+      const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), false);
       if (!chunks) continue;
       const int grid = std::min(chunks, most);
       if ((e = launch_pdl(grad_norm_kernel<CAP>, dim3(grid), dim3(GN_THREADS), 0, stream, t, part + parts)) != cudaSuccess)
@@ -292,7 +300,7 @@ static cudaError_t run(const GradList &a, int mode, double *part, cudaStream_t s
   const double *p = mode & GRAD_NORM ? part : nullptr;
   bool any = false;
   for (int l = nl - 1; l >= 0; --l) {
-    const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), chunk, true);
+    const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), true);
     if (!chunks && (l || any)) continue;  // (of an empty list the norm is still written)
     any = true;
     e = launch_pdl(grad_scale_kernel<CAP>, dim3(std::max(1, std::min(chunks, most))), dim3(GN_THREADS), 0, stream, t, p,

@@ -189,57 +189,94 @@ ce_weight_copy_kernel(int64_t V, int D, int64_t ld, int64_t ldw, const __nv_bflo
 }
 
 // ------------------------------------------------------------- the rows' statistics
-// A CTA joins 32 rows: 32 warps take every 32nd part each (a row a lane: 256
-// bytes a load), then the warps' results are joined in order.  In a step what
-// the gradient needs of the rows, too, and the rows over their factors.
+// A CTA joins 8 rows (64 bytes of each part): a row has 64 threads, which take
+// every 64th part each, first the maximum of eight parts at a time, then
+// their sums; the 64 results are joined in order of the threads.  In a step
+// also what the gradient needs of the rows, and the rows over their factors.
+constexpr int JOIN_ROWS = 8, JOIN_THREADS = 512;
 template <typename E>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(JOIN_THREADS)
 ce_join_kernel(const int *count, int nparts, int tpad, const float2 *part, const float *xt, const int *row_of,
                CeRow *rows, float *inv, float *loss, float *lse, const float *dloss, float scale, float z, const E *hc,
                E *hc2, int64_t dp) {
   griddep_launch();
   griddep_wait();
-  __shared__ float2 sh[32][33];
-  __shared__ float factor[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = *count, r0 = blockIdx.x * 32, r = r0 + lane;
+  constexpr int SL = JOIN_THREADS / JOIN_ROWS;
+  __shared__ float2 sh[SL][JOIN_ROWS];
+  __shared__ float factor[JOIN_ROWS];
+  const int n = *count, r0 = blockIdx.x * JOIN_ROWS;
   if (r0 >= (dloss ? (int)round_up(n, CE_ROWS) : n)) return;
+  const int sl = threadIdx.x / JOIN_ROWS, q = threadIdx.x % JOIN_ROWS;
+  const float2 *p = part + r0 + q;
   float m = -INFINITY, s = 0.f;
-  auto add = [](float &m, float &s, float2 p) {
-    const float big = fmaxf(m, p.x);
-    if (big == -INFINITY) return;
-    s = s * exp2f(m - big) + p.y * exp2f(p.x - big);
-    m = big;
-  };
-  if (r0 < n)
-    for (int i = warp; i < nparts; i += 32) add(m, s, part[(int64_t)i * tpad + r]);
-  sh[warp][lane] = make_float2(m, s);
-  __syncthreads();
-  if (warp == 0) {
-    float f = 1.f;
-    if (r < n) {
-      m = -INFINITY;
-      s = 0.f;
-      for (int w = 0; w < 32; ++w) add(m, s, sh[w][lane]);
-      // m and the target's logit are in units of log 2: their difference is exact
-      // where it is small, and 0 where the target has the largest logit.
-      const float ln = logf(s), l = fmaf(m, LN2, ln), nll = fmaf(m - xt[r], LN2, ln);
-      const int t = row_of[r];
-      loss[t] = fmaf(z * l, l, nll);
-      if (lse) lse[t] = l;
-      if (dloss) {
-        CeRow row = rows[r];
-        f = grad_row<E>(row, scale * dloss[t], l, nll, z);
-        rows[r] = row;
-        inv[r] = f;
+  if (r0 < n) {
+    for (int i = sl; i < nparts; i += 8 * SL) {
+      float2 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = i + j * SL;
+        v[j] = k < nparts ? p[(int64_t)k * tpad] : make_float2(-INFINITY, 0.f);
       }
+      float big = m;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) big = fmaxf(big, v[j].x);
+      const float ref = big == -INFINITY ? 0.f : big;
+      s *= exp2f(m - ref);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j].y * exp2f(v[j].x - ref);
+      m = big;
     }
-    factor[lane] = f;
+  }
+  sh[sl][q] = make_float2(m, s);
+  __syncthreads();
+  // A warp's quarter of the 64 (rows across the lanes), then the four of a row.
+  if (threadIdx.x < 32) {
+    const int row = threadIdx.x & 7, part4 = threadIdx.x >> 3;
+    m = -INFINITY;
+    s = 0.f;
+    auto add = [&](float2 o) {
+      const float big = fmaxf(m, o.x), ref = big == -INFINITY ? 0.f : big;
+      s = s * exp2f(m - ref) + o.y * exp2f(o.x - ref);
+      m = big;
+    };
+#pragma unroll
+    for (int i = 0; i < SL / 4; ++i) add(sh[part4 * (SL / 4) + i][row]);
+    float2 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i].x = __shfl_sync(FULL_MASK, m, row + 8 * i);
+      o[i].y = __shfl_sync(FULL_MASK, s, row + 8 * i);
+    }
+    m = -INFINITY;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add(o[i]);
+    const int r = r0 + row;
+    if (part4 == 0) {
+      float f = 1.f;
+      if (r < n) {
+        // m and the target's logit are in units of log 2: their difference is exact
+        // where it is small, and 0 where the target has the largest logit.
+        const float ln = logf(s), l = fmaf(m, LN2, ln), nll = fmaf(m - xt[r], LN2, ln);
+        const int t = row_of[r];
+        loss[t] = fmaf(z * l, l, nll);
+        if (lse) lse[t] = l;
+        if (dloss) {
+          CeRow info = rows[r];
+          f = grad_row<E>(info, scale * dloss[t], l, nll, z);
+          rows[r] = info;
+          inv[r] = f;
+        }
+      }
+      factor[row] = f;
+    }
   }
   if (!dloss || sizeof(E) != 2) return;
   __syncthreads();
+  const int warp = threadIdx.x >> 5;
+  if (warp >= JOIN_ROWS) return;
   const int64_t at = (r0 + warp) * dp;
-  put_row<E, true>(hc2 + at, hc + at, (int)dp, dp, factor[warp], true, lane);
+  put_row<E, true>(hc2 + at, hc + at, (int)dp, dp, factor[warp], true, threadIdx.x & 31);
 }
 
 // dhidden's sums of the chunks of one piece, in order, onto those of the pieces before.
@@ -333,7 +370,7 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
   m.status = status;
   if (loss) {
     if ((e = a.f32 ? ce_simt_stats(m, stream) : ce_tc_stats(m, stream)) != cudaSuccess) return e;
-    e = launch_pdl(ce_join_kernel<E>, dim3(l.tpad / 32), dim3(1024), 0, stream, (const int *)count, l.nparts, l.tpad,
+    e = launch_pdl(ce_join_kernel<E>, dim3(l.tpad / JOIN_ROWS), dim3(JOIN_THREADS), 0, stream, (const int *)count, l.nparts, l.tpad,
                    (const float2 *)m.part, (const float *)m.xt, (const int *)row_of, rows, inv, a.loss, a.lse,
                    (const float *)(grad ? a.dloss : nullptr), a.scale, a.z_loss, (const E *)hc, hc2, l.dp);
     if (e != cudaSuccess) return e;

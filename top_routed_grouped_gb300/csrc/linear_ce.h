@@ -50,10 +50,15 @@ inline CeLayout ce_layout(const CeArgs &a, int mode) {
   l.dp = round_up(a.D, 64);
   // Tensor maps want rows on 16-byte boundaries; other weights are copied first.
   l.ldw = !a.f32 && (a.ld_w % 8 || ((uintptr_t)a.weight & 15)) ? round_up(a.D, 8) : 0;
-  // A piece: as many chunks as keep g and dhidden's sums at about the size of L2, one at least.
-  const int64_t budget = (int64_t)128 << 20;
+  // A piece: as many chunks as keep g and dhidden's sums within twice the size
+  // of L2, one at least; all pieces about equally long.  With only a few chunks a
+  // piece its sums would be written and read once more for little, so
+  // then it is one chunk, added to the sums before it in the product's epilogue.
+  const int64_t budget = (int64_t)256 << 20;
   int64_t per = std::min(budget / (l.tpad * (int64_t)l.chunk * e), budget / (l.tpad * l.dp * 4));
+  if (per < 3 && per < l.nchunks) per = 1;
   l.per_piece = (int)std::min<int64_t>(std::max<int64_t>(per, 1), l.nchunks);
+  l.per_piece = (int)ceil_div(l.nchunks, ceil_div(l.nchunks, l.per_piece));
   l.npieces = (int)ceil_div(l.nchunks, l.per_piece);
   l.ldg = std::min((int64_t)l.per_piece * l.chunk, round_up(a.V, CE_ROWS));
   size_t at = 0;

@@ -2,16 +2,17 @@
 //
 // Products of floats need 24 bits, which the tensor cores' formats do not
 // hold, so float models (small ones, and checks) take FFMA: tiles of 128 x
-// 128 outputs, 256 threads with 8 x 8 outputs each, K steps of 16 through
+// 128 outputs (64 x 64 where those would leave SMs without one), 256 threads with 8 x 8 (4 x 4) outputs each, K steps of 16 through
 // shared memory, one step ahead in registers.  The epilogues are those of the
 // tensor-core kernels: the same statistics per 64 columns, the same pieces.
 // Each output is summed over K in order.
 #include "linear_ce.h"
+#include "tc_host.h"
 
 namespace moe {
 
 constexpr int SM_STATS = 0, SM_LOGITS = 1, SM_DH = 2, SM_DW = 3;
-constexpr int ST = 128, SK = 16;
+constexpr int SK = 16;
 
 struct SimtParams {
   CeMats m;
@@ -25,31 +26,31 @@ __device__ inline float4 four(const float *p, int n, bool wide) {
   return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
 }
 
-// An operand of one tile: 128 rows (of the output's rows or columns) x 16 K,
-// two units of four floats a thread.  KMAJOR: K runs along the row.
-template <bool KMAJOR>
+// An operand of one tile: 64 S rows (of the output's rows or columns) x 16 K,
+// S units of four floats a thread.  KMAJOR: K runs along the row.
+template <bool KMAJOR, int S>
 struct Operand {
   const float *p;
   int64_t ld;
   int rows, k;  // valid extents from the tile's origin
   bool wide;    // units are on 16-byte boundaries
-  float4 r[2];
+  float4 r[S];
   __device__ void load(int k0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S; ++i) {
       const int u = threadIdx.x + 256 * i;
       if (KMAJOR) {
         const int row = u >> 2, kk = k0 + (u & 3) * 4;
         r[i] = row < rows ? four(p + row * ld + kk, k - kk, wide) : make_float4(0, 0, 0, 0);
       } else {
-        const int kk = k0 + (u >> 5), row = (u & 31) * 4;
+        const int kk = k0 + u / (16 * S), row = u % (16 * S) * 4;
         r[i] = kk < k ? four(p + kk * ld + row, rows - row, wide) : make_float4(0, 0, 0, 0);
       }
     }
   }
-  __device__ void store(float (*s)[ST + 4]) const {
+  __device__ void store(float (*s)[64 * S + 4]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S; ++i) {
       const int u = threadIdx.x + 256 * i;
       if (KMAJOR) {
         const int row = u >> 2, kk = (u & 3) * 4;
@@ -58,19 +59,20 @@ struct Operand {
         s[kk + 2][row] = r[i].z;
         s[kk + 3][row] = r[i].w;
       } else {
-        *(float4 *)&s[u >> 5][(u & 31) * 4] = r[i];
+        *(float4 *)&s[u / (16 * S)][u % (16 * S) * 4] = r[i];
       }
     }
   }
 };
 
-template <int KIND>
-__global__ void __launch_bounds__(256, 2)
+template <int KIND, int S>
+__global__ void __launch_bounds__(256, S == 2 ? 2 : 4)
 ce_simt_kernel(const SimtParams a) {
   griddep_launch();
   griddep_wait();
   const CeMats &m = a.m;
   const CePiece &pc = a.p;
+  constexpr int ST = 64 * S, RT = 4 * S;
   __shared__ float sA[2][SK][ST + 4], sB[2][SK][ST + 4];
   const int count = *m.count;
   const int r0 = blockIdx.x * ST, c0 = blockIdx.y * ST;  // the tile's rows and columns
@@ -78,8 +80,8 @@ ce_simt_kernel(const SimtParams a) {
   const float *h = (const float *)m.h, *w = (const float *)m.w, *g = (const float *)m.g;
   const bool ww = m.ldw % 4 == 0 && ((uintptr_t)m.w & 15) == 0;
   constexpr bool AK = KIND != SM_DW, BK = KIND == SM_STATS || KIND == SM_LOGITS;
-  Operand<AK> A;
-  Operand<BK> B;
+  Operand<AK, S> A;
+  Operand<BK, S> B;
   A.wide = true;
   const int v0 = pc.v0;
   int k;
@@ -100,7 +102,7 @@ ce_simt_kernel(const SimtParams a) {
   A.k = B.k = k;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   // A thread's rows are r0 + 4 ty + {0..3} and + 64, its columns alike.
-  float acc[8][8] = {};
+  float acc[RT][RT] = {};
   A.load(0);
   B.load(0);
   int buf = 0;
@@ -114,15 +116,16 @@ ce_simt_kernel(const SimtParams a) {
     }
 #pragma unroll
     for (int kk = 0; kk < SK; ++kk) {
-      float x[8], y[8];
-      *(float4 *)&x[0] = *(const float4 *)&sA[buf][kk][ty * 4];
-      *(float4 *)&x[4] = *(const float4 *)&sA[buf][kk][64 + ty * 4];
-      *(float4 *)&y[0] = *(const float4 *)&sB[buf][kk][tx * 4];
-      *(float4 *)&y[4] = *(const float4 *)&sB[buf][kk][64 + tx * 4];
+      float x[RT], y[RT];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int h = 0; h < S; ++h) {
+        *(float4 *)&x[4 * h] = *(const float4 *)&sA[buf][kk][64 * h + ty * 4];
+        *(float4 *)&y[4 * h] = *(const float4 *)&sB[buf][kk][64 * h + tx * 4];
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
     }
     buf ^= 1;  // the other buffer was last read before the barrier of this step
   }
@@ -131,11 +134,11 @@ ce_simt_kernel(const SimtParams a) {
   constexpr float L2E = 1.44269504088896340736f;
   if (KIND == SM_STATS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
       const int row = r0 + rowof(i);
       const int target = m.rows[row].target - c0;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {  // 64 columns each
+      for (int hf = 0; hf < S; ++hf) {  // 64 columns each
         float big = -INFINITY, s = 0.f;
 #pragma unroll
         for (int j = 4 * hf; j < 4 * hf + 4; ++j) {
@@ -150,35 +153,36 @@ ce_simt_kernel(const SimtParams a) {
 #pragma unroll
         for (int j = 4 * hf; j < 4 * hf + 4; ++j) s += exp2f(acc[i][j] - ref);
         for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(FULL_MASK, s, d);
-        const int part = blockIdx.y * 2 + hf;
+        const int part = blockIdx.y * S + hf;
         if (tx == 0 && part < a.nparts) m.part[(int64_t)part * m.tpad + row] = make_float2(big, s);
       }
     }
   } else if (KIND == SM_LOGITS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
       const int row = r0 + rowof(i);
       const CeRow R = m.rows[row];
       const int target = R.target - v0 - c0;
       const bool zero = R.c == 0.f && R.b == 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < RT; ++j) {
         const int c = colof(j);
         float x = R.c * exp2f(fmaf(acc[i][j], m.scale * L2E, -R.lse2));
         if (c == target) x = R.b;
         acc[i][j] = zero || v0 + c0 + c >= m.V ? 0.f : x;
       }
       float *out = (float *)m.g + row * m.ldg + c0 + tx * 4;
-      *(float4 *)out = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      *(float4 *)(out + 64) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+#pragma unroll
+      for (int h = 0; h < S; ++h)
+        *(float4 *)(out + 64 * h) = make_float4(acc[i][4 * h], acc[i][4 * h + 1], acc[i][4 * h + 2], acc[i][4 * h + 3]);
     }
   } else if (KIND == SM_DH) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
       const int row = r0 + rowof(i);
       if (row >= count) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < RT; ++j) {
         const int c = c0 + colof(j);
         if (c >= m.D) continue;
         const int64_t at = row * m.ldh + c;
@@ -193,11 +197,11 @@ ce_simt_kernel(const SimtParams a) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
       const int row = r0 + rowof(i);
       if (row >= pc.n) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < RT; ++j) {
         const int c = c0 + colof(j);
         if (c >= m.D) continue;
         float *o = (float *)m.dw + (int64_t)(v0 + row) * m.D + c;
@@ -207,27 +211,30 @@ ce_simt_kernel(const SimtParams a) {
   }
 }
 
+// rows x cols outputs (z of them); the larger tiles where they fill the SMs twice.
 template <int KIND>
-static cudaError_t launch(const CeMats &m, const CePiece &p, dim3 grid, cudaStream_t stream) {
+static cudaError_t launch(const CeMats &m, const CePiece &p, int64_t rows, int64_t cols, int z, cudaStream_t stream) {
   SimtParams a = {m, p, (int)ceil_div(m.V, CE_PART)};
-  return launch_pdl(ce_simt_kernel<KIND>, grid, dim3(256), 0, stream, a);
+  auto grid = [&](int t) { return dim3((unsigned)ceil_div(rows, t), (unsigned)ceil_div(cols, t), z); };
+  if (ceil_div(rows, 128) * ceil_div(cols, 128) * z >= 2 * device_sms())
+    return launch_pdl(ce_simt_kernel<KIND, 2>, grid(128), dim3(256), 0, stream, a);
+  return launch_pdl(ce_simt_kernel<KIND, 1>, grid(64), dim3(256), 0, stream, a);
 }
 
 cudaError_t ce_simt_stats(const CeMats &m, cudaStream_t stream) {
   CePiece p = {};
   p.n = m.V;
-  return launch<SM_STATS>(m, p, dim3(m.tpad / ST, (unsigned)ceil_div(m.V, ST)), stream);
+  return launch<SM_STATS>(m, p, m.tpad, m.V, 1, stream);
 }
 
 cudaError_t ce_simt_logits_grad(const CeMats &m, const CePiece &p, cudaStream_t stream) {
-  return launch<SM_LOGITS>(m, p, dim3(m.tpad / ST, (unsigned)ceil_div(p.n, ST)), stream);
+  return launch<SM_LOGITS>(m, p, m.tpad, p.n, 1, stream);
 }
 
 cudaError_t ce_simt_grads(const CeMats &m, const CePiece &p, cudaStream_t stream) {
-  const unsigned nt = (unsigned)ceil_div(m.D, ST);
-  cudaError_t e = launch<SM_DH>(m, p, dim3(m.tpad / ST, nt, p.nchunks), stream);
+  cudaError_t e = launch<SM_DH>(m, p, m.tpad, m.D, p.nchunks, stream);
   if (e != cudaSuccess) return e;
-  return launch<SM_DW>(m, p, dim3((unsigned)ceil_div(p.n, ST), nt), stream);
+  return launch<SM_DW>(m, p, p.n, m.D, 1, stream);
 }
 
 }  // namespace moe

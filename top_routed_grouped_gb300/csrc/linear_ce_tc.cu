@@ -32,17 +32,22 @@ namespace moe {
 using namespace umma;
 
 constexpr int CE_STATS = 0, CE_LOGITS = 1, CE_GRADS = 2;
-constexpr int CT_STAGES = 6, CT_A_BYTES = 16384, CT_STAGE_BYTES = 2 * CT_A_BYTES;
-// Epilogue warps: eight, half of the columns each, with 4 KB of staging; for
-// the statistics sixteen with a quarter each, so that a thread's sums over the
-// K chunks (64) stay in registers.
-constexpr int CT_EPI_FIRST = 2, CT_EPI_BYTES = 8 * 4096;
+constexpr int CT_A_BYTES = 16384, CT_STAGE_BYTES = 2 * CT_A_BYTES;
+// Epilogue warps: eight, half of the columns each, with one (LOGITS) or two
+// staging tiles of 4 KB; for the statistics sixteen with a quarter each, so
+// that a thread's sums over the K chunks (64) stay in registers.  With two
+// tiles and a stage less GRADS at few rows, where the stores of dweight are what it
+// does, does not wait for one store to read its tile before it fills the next.
+constexpr int CT_EPI_FIRST = 2;
 template <int KIND>
-constexpr int ct_epi_warps() { return KIND == CE_STATS ? 16 : 8; }
-template <int KIND>
-constexpr int ct_threads() { return 32 * (CT_EPI_FIRST + ct_epi_warps<KIND>()); }
-constexpr int CT_SMEM = 1024 + CT_STAGES * CT_STAGE_BYTES + CT_EPI_BYTES + 512;
-static_assert(CT_SMEM <= 232448, "shared memory of a CTA");
+struct CtCfg {
+  static constexpr int EPI_WARPS = KIND == CE_STATS ? 16 : 8;
+  static constexpr int THREADS = 32 * (CT_EPI_FIRST + EPI_WARPS);
+  static constexpr int STAGES = KIND == CE_GRADS ? 5 : 6;
+  static constexpr int NSTG = KIND == CE_STATS ? 0 : KIND == CE_GRADS ? 2 : 1;
+  static constexpr int SMEM = 1024 + STAGES * CT_STAGE_BYTES + EPI_WARPS * NSTG * 4096 + 512;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
 constexpr uint32_t CT_TMEM_COLS = 512;
 // The statistics' products are summed in chunks of 512 of K, each in an
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
@@ -53,7 +58,7 @@ constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
   CUtensorMap h, w, g;     // K-major tiles: boxes of 128 rows x 64
-  CUtensorMap h32;         // the same rows, 32 at a time
+  CUtensorMap h32, w32;    // the same rows, 32 at a time
   CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64
   CUtensorMap gout;        // 32 rows x 64: g's stores
   CUtensorMap dw;          // dweight: 32 rows x 128 bytes
@@ -81,58 +86,122 @@ struct CtParams {
 
 struct CtItem {
   int kind;   // 0: logits, 1: dhidden, 2: dweight
-  int m, n, chunk, nk;
-  int cols;   // columns of the tile: 256 or 128
+  int m, chunk, nk;
+  int n0;     // first column of the tile: of the piece's vocabulary (logits), of D (gradients)
+  int cols;   // columns of the tile: a multiple of 64 up to 256 (gradients: 128 or 256)
 };
 
+// The items of a pair, in order.
+//
+// Logits, one row tile (few rows, bound by reading the weights): the
+// vocabulary in units of 64 columns, a contiguous run of them to each pair, so
+// that no pair has more than one unit above the mean (32000 x 2048: 7 units
+// instead of two whole tiles of 4).  More row tiles: tiles of 256 columns, row
+// tiles fastest, so that a tile of the weights is read by all of them at about
+// the same time; narrower ones where a wave of whole tiles would be empty for the most part.
+//
+// Gradients: the items of the product with the longer sums (dhidden's up to
+// 8192 rows, dweight's above) are dealt out in turn; the pairs that have one
+// less of them get as many more of the other's as make up for it, the rest goes round.
 template <int KIND>
 struct CtWork {
-  int count, mt, nt, ndh, ndw, total, kd, kr;
-  bool dw_first;
-  __device__ CtWork(const CtParams &p) {
+  int count, mt, kd, kr;
+  int it, end;                   // logits: the pair's next unit or tile, and the last one's end
+  int step, nt, cols;
+  int nl, ns, heavy, extra, delta, pair, pairs;  // gradients: longer items, shorter ones
+  bool long_dw;
+  bool run;
+  __device__ CtWork(const CtParams &p, int pair_, int pairs_) {
+    pair = pair_;
+    pairs = pairs_;
     count = __ldg(p.count);
     mt = (count + CE_ROWS - 1) / CE_ROWS;
     kd = (p.D + 63) / 64;
     kr = (count + 63) / 64;
-    const int vt = (p.n + 255) / 256;
     if (KIND == CE_GRADS) {
       nt = (p.D + 255) / 256;
-      ndh = p.nchunks * mt * nt;
-      ndw = vt * nt;
-      total = ndh + ndw;
-      dw_first = kr > 128;  // the longer items first: they do not form the tail
-    } else {
-      nt = vt;
-      total = mt * nt;
+      const int ndh = p.nchunks * mt * nt, ndw = (p.n + 255) / 256 * nt;
+      // K blocks of an item; one of dweight takes the time of its stores (about eight blocks) at least.
+      const int kh = (min(p.chunk, p.n) + 63) / 64, kw = max(kr, 8);
+      long_dw = kw > kh;
+      nl = long_dw ? ndw : ndh;
+      ns = long_dw ? ndh : ndw;
+      heavy = nl % pairs;  // pairs with one more of the longer items
+      const int kl = long_dw ? kw : kh, ks = long_dw ? kh : kw;
+      delta = heavy ? (kl + ks / 2) / ks : 0;
+      extra = min(ns, (pairs - heavy) * delta);
+      it = 0;
+      return;
     }
+    run = mt == 1;
+    if (run) {
+      const int units = (p.n + 63) / 64;
+      it = (int)((int64_t)units * pair / pairs);
+      end = (int)((int64_t)units * (pair + 1) / pairs);
+      return;
+    }
+    cols = 256;
+    int best = 0x7fffffff;
+    for (int c = 256; c >= 64; c -= 64) {  // waves x (columns + the cost of a tile by itself)
+      const int waves = (mt * ((p.n + c - 1) / c) + pairs - 1) / pairs;
+      if (waves * (c + 64) < best) {
+        best = waves * (c + 64);
+        cols = c;
+      }
+      if (waves > 8) break;  // (then the last wave does not matter)
+    }
+    nt = (p.n + cols - 1) / cols;
+    it = pair;
+    end = mt * nt;
   }
-  __device__ CtItem item(int it, const CtParams &p) const {
-    CtItem r;
+  __device__ bool next(const CtParams &p, CtItem &r) {
     r.chunk = 0;
-    r.cols = 256;
-    if (KIND != CE_GRADS) {  // row tiles fastest: a tile of the weights is read by all of them at about the same time
-      r.kind = 0;
-      r.m = it % mt;
-      r.n = it / mt;
+    r.kind = 0;
+    if (KIND != CE_GRADS) {
+      if (it >= end) return false;
       r.nk = kd;
-      return r;
+      if (run) {
+        const int u = min(4, end - it);
+        r.m = 0;
+        r.n0 = it * 64;
+        r.cols = u * 64;
+        it += u;
+      } else {
+        r.m = it % mt;
+        r.n0 = it / mt * cols;
+        r.cols = cols;
+        it += pairs;
+      }
+      return true;
     }
-    const bool dw = dw_first ? it < ndw : it >= ndh;
-    const int i = dw ? (dw_first ? it : it - ndh) : (dw_first ? it - ndw : it);
-    r.n = i % nt;
+    const int own = nl / pairs + (pair < heavy ? 1 : 0);
+    int i = it++;
+    bool longer = i < own;
+    if (longer) {
+      i = pair + i * pairs;
+    } else {
+      i -= own;
+      if (pair >= heavy && i < delta) {
+        i = pair - heavy + i * (pairs - heavy);
+        if (i >= extra) return false;  // (then there are no others)
+      } else {
+        i = extra + pair + (i - (pair >= heavy ? delta : 0)) * pairs;
+        if (i >= ns) return false;
+      }
+    }
+    r.kind = longer == long_dw ? 2 : 1;
+    r.n0 = i % nt * 256;
     const int rest = i / nt;
-    if (p.D - r.n * 256 <= 128) r.cols = 128;
-    if (dw) {
-      r.kind = 2;
+    r.cols = p.D - r.n0 <= 128 ? 128 : 256;
+    if (r.kind == 2) {
       r.m = rest;
       r.nk = kr;
     } else {
-      r.kind = 1;
       r.m = rest % mt;
       r.chunk = rest / mt;
       r.nk = (min(p.chunk, p.n - r.chunk * p.chunk) + 63) / 64;
     }
-    return r;
+    return true;
   }
 };
 
@@ -153,9 +222,9 @@ __device__ inline void tma_reduce_add_2d(const CUtensorMap *m, const void *src, 
 // v: the thread's 64 logits (columns from 64 cq of the tile), summed over the
 // K chunks.
 __device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, float (&v)[64], int row, int cq) {
-  const int col0 = im.n * 256 + cq * 64;
+  const int col0 = im.n0 + cq * 64;
   const int target = p.rows[row].target - col0, left = p.V - col0;
-  if (left <= 0) return;
+  if (cq * 64 >= im.cols || left <= 0) return;
   if ((unsigned)target < 64u) {
     float x = 0.f;
 #pragma unroll
@@ -177,26 +246,27 @@ __device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, float
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < 64; ++j) s[j & 3] += ex2(v[j] - ref);
-  p.part[(int64_t)(im.n * 4 + cq) * p.tpad + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+  p.part[(int64_t)(col0 / 64) * p.tpad + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
 __device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row,
                                        int half, uint8_t *stg, int lane) {
-  const int pc0 = im.n * 256 + half * 128;  // column in the piece
   const CeRow R = p.rows[row];
-  const int target = R.target - p.v0 - pc0;
   const bool zero = R.c == 0.f && R.b == 0.f;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
+#pragma unroll 1
+  for (int c = half * 64; c < im.cols; c += 128) {
+    const int pc = im.n0 + c;  // column in the piece
+    if (pc >= p.n) break;
+    const int target = R.target - p.v0 - pc;
     float v[2][32];
-    tmem_ld32x2(taddr + c * 64, taddr + c * 64 + 32, v[0], v[1]);
-    const int left = p.V - p.v0 - pc0 - c * 64;
+    tmem_ld32x2(taddr + c, taddr + c + 32, v[0], v[1]);
+    const int left = p.V - p.v0 - pc;
     uint32_t w[32];
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[hh][j] = R.c * ex2(fmaf(v[hh][j], p.s2, -R.lse2));
-      const unsigned at = (unsigned)(target - c * 64 - hh * 32);
+      const unsigned at = (unsigned)(target - hh * 32);
       if (at < 32u) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[hh][j] = at == (unsigned)j ? R.b : v[hh][j];
@@ -220,7 +290,7 @@ __device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, co
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(&maps.gout, stg, pc0 + c * 64, row);
+      tma_store_2d(&maps.gout, stg, pc, row);
       bulk_commit();
     }
   }
@@ -246,7 +316,7 @@ __device__ inline void by_rows(uint8_t *stg, const float (&v)[32], int lane, F &
 
 __device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uint32_t taddr, int row0, int count, int half,
                                         uint8_t *stg, int lane) {
-  const int wcols = im.cols / 2, col0 = im.n * 256 + half * wcols;
+  const int wcols = im.cols / 2, col0 = im.n0 + half * wcols;
   float *plane = p.planes ? p.planes + (int64_t)im.chunk * p.tpad * p.ldh : nullptr;
   for (int c = 0; c < wcols && col0 + c < p.D; c += 32) {
     float v[32];
@@ -285,8 +355,8 @@ __device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uin
 
 // v: the tile's values (zero where no row counts: then there is no accumulator).
 __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row0,
-                                        int half, uint8_t *stg, int lane) {
-  const int wcols = im.cols / 2, col0 = im.n * 256 + half * wcols;  // row0: row of dweight
+                                        int half, uint8_t *stg2, int lane) {
+  const int wcols = im.cols / 2, col0 = im.n0 + half * wcols;  // row0: row of dweight
   if (row0 >= p.V) return;
   for (int c = 0; c < wcols && col0 + c < p.D; c += p.gf32 || !p.dw_tma ? 32 : 64) {
     float v[2][32];
@@ -299,7 +369,8 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
       tmem_ld32x2(taddr + c, taddr + c + 32, v[0], v[1]);
     }
     if (p.dw_tma) {
-      if (lane == 0) bulk_wait_read<0>();
+      uint8_t *stg = stg2 + (c / 32 & (p.gf32 ? 1 : 2) ? 4096 : 0);  // the two tiles in turn
+      if (lane == 0) bulk_wait_read<1>();  // the store before the last has read its tile
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -327,7 +398,7 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
         bulk_commit();
       }
     } else {
-      by_rows(stg, v[0], lane, [&](int r, int cc, float4 x) {
+      by_rows(stg2, v[0], lane, [&](int r, int cc, float4 x) {
         const int row = row0 + r, col = col0 + c + cc;
         if (row >= p.V) return;
         const float e[4] = {x.x, x.y, x.z, x.w};
@@ -348,15 +419,15 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(ct_threads<KIND>(), 1)
+__global__ void __launch_bounds__(CtCfg<KIND>::THREADS, 1)
 ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
-  constexpr int EPI_WARPS = ct_epi_warps<KIND>();
+  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, CT_STAGES = CtCfg<KIND>::STAGES, NSTG = CtCfg<KIND>::NSTG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   auto sa = [&](int s) { return base + s * CT_STAGE_BYTES; };
   auto sb = [&](int s) { return base + s * CT_STAGE_BYTES + CT_A_BYTES; };
   uint8_t *epi = base + CT_STAGES * CT_STAGE_BYTES;
-  uint64_t *bars = (uint64_t *)(epi + CT_EPI_BYTES);
+  uint64_t *bars = (uint64_t *)(epi + EPI_WARPS * NSTG * 4096);
   uint64_t *full = bars, *empty = full + CT_STAGES;
   uint64_t *tfull = empty + CT_STAGES, *tempty = tfull + 2, *mma_done = tempty + 2;
   uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
@@ -387,7 +458,8 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
   griddep_wait();
-  const CtWork<KIND> work(p);
+  CtWork<KIND> work(p, cid, ncl);
+  CtItem im;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -397,10 +469,9 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int it = cid; it < work.total && ok; it += ncl) {
-        const CtItem im = work.item(it, p);
+      while (ok && work.next(p, im)) {
         const int mrow = im.m * 256 + (int)rank * 128;
-        const int half = im.cols / 2, ncol = im.n * 256 + (int)rank * half;
+        const int half = im.cols / 2, ncol = im.n0 + (int)rank * half;
         // Of the last rows only those that are there are read, 32 at a time: the
         // lines behind them reach nothing but accumulator rows that nobody reads.
         const int arows = KIND == CE_GRADS ? 128 : min(128, max(0, (work.count - mrow + 31) & ~31));
@@ -416,7 +487,9 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
             if (arows == 128) tma_load_2d_pair(sa(stage), &maps.h, bar, k, mrow, keep);
             else
               for (int j = 0; j < arows; j += 32) tma_load_2d_pair(sa(stage) + j * 128, &maps.h32, bar, k, mrow + j, keep);
-            tma_load_2d_pair(sb(stage), &maps.w, bar, k, p.v0 + ncol, pass);
+            if (half == 128) tma_load_2d_pair(sb(stage), &maps.w, bar, k, p.v0 + ncol, pass);
+            else
+              for (int j = 0; j < half; j += 32) tma_load_2d_pair(sb(stage) + j * 128, &maps.w32, bar, k, p.v0 + ncol + j, pass);
           } else if (im.kind == 1) {
             const int v = im.chunk * p.chunk + k;
             tma_load_2d_pair(sa(stage), &maps.g, bar, v, mrow, pass);
@@ -446,8 +519,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         int stage = 0;
         uint32_t phase = 0, cnt = 0;
         bool ok = true;
-        for (int it = cid; it < work.total && ok; it += ncl) {
-          const CtItem im = work.item(it, p);
+        while (ok && work.next(p, im)) {
           if (im.nk == 0) continue;
           const bool a_mn = KIND == CE_GRADS && im.kind == 2, b_mn = KIND == CE_GRADS;
           const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
@@ -485,7 +557,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;  // TMEM lane quarter; which of the columns
-    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * 4096;
+    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * NSTG * 4096;
     const uint32_t tempty_leader0 = mapa_shared(&tempty[0], 0);
     uint32_t cnt = 0;
     auto wait = [&] {
@@ -504,8 +576,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
       }
       ++cnt;
     };
-    for (int it = cid; it < work.total; it += ncl) {
-      const CtItem im = work.item(it, p);
+    while (work.next(p, im)) {
       const int row0 = im.m * 256 + (int)rank * 128 + q * 32;
       const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
       if (KIND == CE_STATS) {
@@ -517,6 +588,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
           if (!(ok = wait())) break;
 #pragma unroll
           for (int c = 0; c < 64; c += 16) {
+            if (half * 64 >= im.cols) break;
             float x[16];
             tmem_ld16(tq + (cnt & 1) * 256 + half * 64 + c, x);
 #pragma unroll
@@ -529,7 +601,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         continue;
       }
       if (im.nk != 0 && !wait()) break;
-      const uint32_t taddr = tq + (cnt & 1) * 256 + half * (im.cols / 2);
+      const uint32_t taddr = tq + (cnt & 1) * 256 + (KIND == CE_LOGITS ? 0 : half * (im.cols / 2));
       if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
       else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, work.count, half, stg, lane);
       else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane);
@@ -557,13 +629,13 @@ static bool map_ld(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, 
 
 template <int KIND>
 static cudaError_t launch(const CtMaps &maps, const CtParams &p, int64_t items, cudaStream_t stream) {
-  cudaError_t e = ensure_smem((const void *)ce_pair_kernel<KIND>, CT_SMEM);
+  cudaError_t e = ensure_smem((const void *)ce_pair_kernel<KIND>, CtCfg<KIND>::SMEM);
   if (e != cudaSuccess) return e;
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(items, device_sms() / 2));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(ct_threads<KIND>());
-  cfg.dynamicSmemBytes = CT_SMEM;
+  cfg.blockDim = dim3(CtCfg<KIND>::THREADS);
+  cfg.dynamicSmemBytes = CtCfg<KIND>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -608,9 +680,10 @@ static void piece(CtParams &p, const CePiece &c) {
 cudaError_t ce_tc_stats(const CeMats &m, cudaStream_t stream) {
   CtMaps maps = {};
   if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.h32, m.h, m.tpad, m.ldh, m.ldh, 32) ||
-      !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128))
+      !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128) ||
+      !map_ld(&maps.w32, m.w, m.V, m.D, m.ldw, 32))
     return cudaErrorInvalidValue;
-  return launch<CE_STATS>(maps, params(m), (int64_t)(m.tpad / 256) * ceil_div(m.V, 256), stream);
+  return launch<CE_STATS>(maps, params(m), (int64_t)(m.tpad / 256) * ceil_div(m.V, 64), stream);
 }
 
 cudaError_t ce_tc_logits_grad(const CeMats &m, const CePiece &c, cudaStream_t stream) {
@@ -619,9 +692,10 @@ cudaError_t ce_tc_logits_grad(const CeMats &m, const CePiece &c, cudaStream_t st
   piece(p, c);
   if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.h32, m.h, m.tpad, m.ldh, m.ldh, 32) ||
       !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128) ||
+      !map_ld(&maps.w32, m.w, m.V, m.D, m.ldw, 32) ||
       !map_ld(&maps.gout, m.g, m.tpad, m.ldg, m.ldg, 32))
     return cudaErrorInvalidValue;
-  return launch<CE_LOGITS>(maps, p, (int64_t)(m.tpad / 256) * ceil_div(c.n, 256), stream);
+  return launch<CE_LOGITS>(maps, p, (int64_t)(m.tpad / 256) * ceil_div(c.n, 64), stream);
 }
 
 cudaError_t ce_tc_grads(const CeMats &m, const CePiece &c, cudaStream_t stream) {
