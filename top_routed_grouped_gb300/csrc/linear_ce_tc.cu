@@ -18,7 +18,11 @@
 // epilogue has a row's columns in its own lane and takes maximum and sum
 // without a shuffle.  Two accumulators of 256 columns alternate: an item's
 // epilogue runs under the next item's MMAs.  A stage is one K block of 64: 16
-// KB of A and 16 KB of B a CTA, six stages deep.  Every output is summed in K
+// KB of A and 16 KB of B a CTA, five to seven stages deep; where a few rows
+// are all there is, a stage has room for those alone (the MMAs read on into
+// B's bytes for rows that nobody looks at) and the ring is up to eleven deep: the bytes in
+// flight are what bounds the reading of the weights then (5 rows x 2048 x
+// 32000: NN us with six stages).  Every output is summed in K
 // blocks of 64 in order, in one accumulator; the tile it falls in does not
 // change that.
 #include <cuda.h>
@@ -32,7 +36,7 @@ namespace moe {
 using namespace umma;
 
 constexpr int CE_STATS = 0, CE_LOGITS = 1, CE_GRADS = 2;
-constexpr int CT_A_BYTES = 16384, CT_STAGE_BYTES = 2 * CT_A_BYTES;
+constexpr int CT_TILE = 16384;  // a K block of 64: 128 rows of A, or half of B's columns, of a CTA
 // Epilogue warps: eight, half of the columns each, with one (LOGITS) or two
 // staging tiles of 4 KB; for the statistics sixteen with a quarter each, so
 // that a thread's sums over the K chunks (64) stay in registers.  With two
@@ -43,17 +47,19 @@ template <int KIND>
 struct CtCfg {
   static constexpr int EPI_WARPS = KIND == CE_STATS ? 16 : 8;
   static constexpr int THREADS = 32 * (CT_EPI_FIRST + EPI_WARPS);
-  static constexpr int STAGES = KIND == CE_GRADS ? 5 : 6;
   static constexpr int NSTG = KIND == CE_STATS ? 0 : KIND == CE_GRADS ? 2 : 1;
-  static constexpr int SMEM = 1024 + STAGES * CT_STAGE_BYTES + EPI_WARPS * NSTG * 4096 + 512;
-  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static constexpr int RING = (7 - NSTG) * 2 * CT_TILE;  // bytes of the stages
+  static constexpr int SMEM = 1024 + RING + EPI_WARPS * NSTG * 4096 + 512;
+  static_assert(SMEM <= 232448 && NSTG * EPI_WARPS * 4096 <= NSTG * 2 * CT_TILE, "shared memory of a CTA");
 };
+constexpr int CT_MAX_STAGES = 11;
+constexpr uint32_t CT_HINT = 100000;
 constexpr uint32_t CT_TMEM_COLS = 512;
-// The statistics' products are summed in chunks of 512 of K, each in an
+// The statistics' products are summed in chunks of 1024 of K, each in an
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
 // cut each of their sums off instead of rounding it, which shows in a float
 // loss as 1.2e-6 of it at K = 2048 in one chain and 3e-7 in chunks.
-constexpr int CT_KCHUNK = 8;
+constexpr int CT_KCHUNK = 16;
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
@@ -205,12 +211,45 @@ struct CtWork {
   }
 };
 
+// mbar_wait of these kernels: the thread is suspended for up to `hint` ns at a
+// time instead of asking again and again.
+__device__ inline bool ct_try_wait(uint64_t *bar, uint32_t parity, uint32_t hint) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
+      : "memory");
+  return ok != 0;
+}
+__device__ inline bool ct_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status) {
+  if (ct_try_wait(bar, parity, CT_HINT)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!ct_try_wait(bar, parity, CT_HINT)) {
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > WAIT_TIMEOUT_NS) {
+      *abort_flag = 1;
+      record_status(status, STATUS_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ inline float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
+// A tile store with an L2 policy.
+__device__ inline void tma_store_2d_hint(const CUtensorMap *m, const void *src, int c0, int c1, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;" ::"l"(m),
+               "r"(c0), "r"(c1), "r"(smem_u32(src)), "l"(policy)
+               : "memory");
+}
 // A tile of 32 rows x 128 bytes from shared memory, added to what is there.
 __device__ inline void tma_reduce_add_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m),
@@ -355,7 +394,7 @@ __device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uin
 
 // v: the tile's values (zero where no row counts: then there is no accumulator).
 __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row0,
-                                        int half, uint8_t *stg2, int lane) {
+                                        int half, uint8_t *stg2, int lane, uint64_t out_policy) {
   const int wcols = im.cols / 2, col0 = im.n0 + half * wcols;  // row0: row of dweight
   if (row0 >= p.V) return;
   for (int c = 0; c < wcols && col0 + c < p.D; c += p.gf32 || !p.dw_tma ? 32 : 64) {
@@ -394,7 +433,7 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
       __syncwarp();
       if (lane == 0) {
         if (p.accumulate) tma_reduce_add_2d(&maps.dw, stg, col0 + c, row0);
-        else tma_store_2d(&maps.dw, stg, col0 + c, row0);
+        else tma_store_2d_hint(&maps.dw, stg, col0 + c, row0, out_policy);
         bulk_commit();
       }
     } else {
@@ -421,15 +460,13 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
 template <int KIND>
 __global__ void __launch_bounds__(CtCfg<KIND>::THREADS, 1)
 ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
-  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, CT_STAGES = CtCfg<KIND>::STAGES, NSTG = CtCfg<KIND>::NSTG;
+  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, NSTG = CtCfg<KIND>::NSTG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  auto sa = [&](int s) { return base + s * CT_STAGE_BYTES; };
-  auto sb = [&](int s) { return base + s * CT_STAGE_BYTES + CT_A_BYTES; };
-  uint8_t *epi = base + CT_STAGES * CT_STAGE_BYTES;
+  uint8_t *epi = base + CtCfg<KIND>::RING;
   uint64_t *bars = (uint64_t *)(epi + EPI_WARPS * NSTG * 4096);
-  uint64_t *full = bars, *empty = full + CT_STAGES;
-  uint64_t *tfull = empty + CT_STAGES, *tempty = tfull + 2, *mma_done = tempty + 2;
+  uint64_t *full = bars, *empty = full + CT_MAX_STAGES;
+  uint64_t *tfull = empty + CT_MAX_STAGES, *tempty = tfull + 2, *mma_done = tempty + 2;
   uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
   volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
 
@@ -438,7 +475,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < CT_STAGES; ++s) {
+    for (int s = 0; s < CT_MAX_STAGES; ++s) {
       mbar_init(&full[s], 1);  // used in the even CTA
       mbar_init(&empty[s], 1);
     }
@@ -450,6 +487,21 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == 0 && lane == 0) {
+    if (KIND == CE_GRADS) {
+      prefetch_tmap(&maps.g);
+      prefetch_tmap(&maps.wt);
+      prefetch_tmap(&maps.gt);
+      prefetch_tmap(&maps.ht);
+      prefetch_tmap(&maps.dw);
+    } else {
+      prefetch_tmap(&maps.h);
+      prefetch_tmap(&maps.w);
+      prefetch_tmap(&maps.h32);
+      prefetch_tmap(&maps.w32);
+      if (KIND == CE_LOGITS) prefetch_tmap(&maps.gout);
+    }
+  }
   cluster_sync();  // both CTAs' barriers exist before either touches the other's
   if (warp == 1) tmem_alloc_pair(tmem_slot, CT_TMEM_COLS);
   tc_fence_before();
@@ -460,11 +512,17 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   griddep_wait();
   CtWork<KIND> work(p, cid, ncl);
   CtItem im;
+  const int a_bytes = KIND != CE_GRADS && work.count <= 64 ? (work.count <= 32 ? 4096 : 8192) : CT_TILE;
+  const int stages = min(CT_MAX_STAGES, CtCfg<KIND>::RING / (a_bytes + CT_TILE));
+  auto sa = [&](int s) { return base + s * (a_bytes + CT_TILE); };
+  auto sb = [&](int s) { return base + s * (a_bytes + CT_TILE) + a_bytes; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
+      // The weights' rows of a chunk are read by every row tile, those of one row tile once.
+      const uint64_t wpol = work.mt > 1 ? keep : pass;
       const uint32_t full0 = mapa_shared(&full[0], 0);
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
@@ -478,7 +536,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         const int arows2 = KIND == CE_GRADS ? 256 : min(256, max(0, (work.count - im.m * 256 + 31) & ~31));
         const uint32_t bytes = 128 * (arows2 + 2 * (uint32_t)half);
         for (int kb = 0; kb < im.nk; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
+          if (!ct_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
           // Both CTAs' tiles complete on the even CTA's barrier.
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
@@ -492,22 +550,22 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
               for (int j = 0; j < half; j += 32) tma_load_2d_pair(sb(stage) + j * 128, &maps.w32, bar, k, p.v0 + ncol + j, pass);
           } else if (im.kind == 1) {
             const int v = im.chunk * p.chunk + k;
-            tma_load_2d_pair(sa(stage), &maps.g, bar, v, mrow, pass);
+            tma_load_2d_pair(sa(stage), &maps.g, bar, v, mrow, keep);
             for (int j = 0; j < half; j += 64)
-              tma_load_2d_pair(sb(stage) + j * 128, &maps.wt, bar, ncol + j, p.v0 + v, keep);
+              tma_load_2d_pair(sb(stage) + j * 128, &maps.wt, bar, ncol + j, p.v0 + v, wpol);
           } else {
-            for (int j = 0; j < 128; j += 64) tma_load_2d_pair(sa(stage) + j * 128, &maps.gt, bar, mrow + j, k, pass);
+            for (int j = 0; j < 128; j += 64) tma_load_2d_pair(sa(stage) + j * 128, &maps.gt, bar, mrow + j, k, keep);
             for (int j = 0; j < half; j += 64) tma_load_2d_pair(sb(stage) + j * 128, &maps.ht, bar, ncol + j, k, keep);
           }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == CT_STAGES) stage = 0, phase ^= 1;
+          if (++stage == stages) stage = 0, phase ^= 1;
         }
       }
       if (!ok && leader) {
         // The stages in flight (both CTAs' copies complete here) land before the pair exits.
         volatile int never = 0;
-        for (int s = 0; s < CT_STAGES; ++s)
+        for (int s = 0; s < stages; ++s)
           if (issued & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1, &never, nullptr, 100000000ull);
       }
     }
@@ -528,10 +586,10 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
             const int kc = KIND == CE_STATS ? kb % CT_KCHUNK : kb;  // in this accumulator
             const int b = cnt & 1;
             if (kc == 0) {
-              if (!mbar_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
+              if (!ct_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
               tc_fence_after();
             }
-            if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+            if (!ct_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a0 = smem_u32(sa(stage)), b0 = smem_u32(sb(stage));
             const uint64_t ad = a_mn ? smem_desc_mn_sw128(a0, 8192) : smem_desc_sw128(a0);
@@ -540,7 +598,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
             for (int kk = 0; kk < 4; ++kk)
               mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kc | kk) != 0);
             mma_commit_pair(&empty[stage]);
-            if (++stage == CT_STAGES) stage = 0, phase ^= 1;
+            if (++stage == stages) stage = 0, phase ^= 1;
             if (kb + 1 == im.nk || (KIND == CE_STATS && kc + 1 == CT_KCHUNK)) {
               mma_commit_pair(&tfull[b]);
               ++cnt;
@@ -551,7 +609,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
       }
       // Every pair MMA has finished (it wrote both CTAs' tensor memory) before TMEM is released.
       volatile int never = 0;
-      mbar_wait(mma_done, 0, &never, p.status);
+      ct_wait(mma_done, 0, &never, p.status);
     }
     __syncwarp();
   } else {
@@ -559,10 +617,11 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;  // TMEM lane quarter; which of the columns
     uint8_t *stg = epi + (warp - CT_EPI_FIRST) * NSTG * 4096;
     const uint32_t tempty_leader0 = mapa_shared(&tempty[0], 0);
+    const uint64_t out_policy = policy_evict_first();  // dweight is written once and not read again
     uint32_t cnt = 0;
     auto wait = [&] {
       int ok = 0;
-      if (lane == 0) ok = mbar_wait(&tfull[cnt & 1], (cnt >> 1) & 1, abort_flag, p.status) ? 1 : 0;
+      if (lane == 0) ok = ct_wait(&tfull[cnt & 1], (cnt >> 1) & 1, abort_flag, p.status) ? 1 : 0;
       if (!__shfl_sync(FULL_MASK, ok, 0)) return false;
       tc_fence_after();
       return true;
@@ -604,7 +663,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
       const uint32_t taddr = tq + (cnt & 1) * 256 + (KIND == CE_LOGITS ? 0 : half * (im.cols / 2));
       if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
       else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, work.count, half, stg, lane);
-      else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane);
+      else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane, out_policy);
       if (im.nk != 0) release();
     }
     if (lane == 0) bulk_wait<0>();
