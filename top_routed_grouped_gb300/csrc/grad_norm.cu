@@ -107,11 +107,11 @@ __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks
   if (u0 + per <= u1) {
     uint4 w[B];
 #pragma unroll
-    for (int i = 0; i < B; ++i) w[i] = __ldg(v + u + i * GN_THREADS);
+    for (int i = 0; i < B; ++i) w[i] = v[u + i * GN_THREADS];
 #pragma unroll
     for (int i = 0; i < B; ++i) unit(w[i], s[2 * i & 2], s[(2 * i & 2) + 1]);
   } else {
-    for (; u < u1; u += GN_THREADS) unit(__ldg(v + u), s[0], s[1]);
+    for (; u < u1; u += GN_THREADS) unit(v[u], s[0], s[1]);
   }
   // At most one element of the head and one of the tail a thread.
   float edge[2] = {0.f, 0.f};
@@ -126,7 +126,7 @@ __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks
   double d = (double)edge[0] * edge[0] + (double)edge[1] * edge[1];
   for (u = u0 + threadIdx.x; u < u1; u += GN_THREADS) {
     float x[N];
-    Vec16<E>::unpack(__ldg(v + u), x);
+    Vec16<E>::unpack(v[u], x);
 #pragma unroll
     for (int i = 0; i < N; ++i) d += (double)x[i] * x[i];
   }

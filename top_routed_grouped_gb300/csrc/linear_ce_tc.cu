@@ -120,7 +120,9 @@ struct CtWork {
   __device__ CtWork(const CtParams &p, int pair_, int pairs_) {
     pair = pair_;
     pairs = pairs_;
-    count = __ldg(p.count);
+    // Not through the read-only path, whose loads may be moved above the wait
+    // for the kernel that writes it.
+    count = *(const volatile int *)p.count;
     mt = (count + CE_ROWS - 1) / CE_ROWS;
     kd = (p.D + 63) / 64;
     kr = (count + 63) / 64;
