@@ -43,11 +43,14 @@ constexpr int CT_TILE = 16384;  // a K block of 64: 128 rows of A, or half of B'
 // tiles and a stage less GRADS at few rows, where the stores of dweight are what it
 // does, does not wait for one store to read its tile before it fills the next.
 constexpr int CT_EPI_FIRST = 2;
+constexpr int GNSTG = 1;
+constexpr int GSUB = 2;
 template <int KIND>
 struct CtCfg {
   static constexpr int EPI_WARPS = KIND == CE_STATS ? 16 : 8;
   static constexpr int THREADS = 32 * (CT_EPI_FIRST + EPI_WARPS);
-  static constexpr int NSTG = KIND == CE_STATS ? 0 : KIND == CE_GRADS ? 2 : 1;
+  static constexpr int NSTG = KIND == CE_STATS ? 0 : KIND == CE_GRADS ? GNSTG : 1;
+  static constexpr int SUB = KIND == CE_GRADS ? GSUB : 2;  // K blocks a stage
   static constexpr int RING = (7 - NSTG) * 2 * CT_TILE;  // bytes of the stages
   static constexpr int SMEM = 1024 + RING + EPI_WARPS * NSTG * 4096 + 512;
   static_assert(SMEM <= 232448 && NSTG * EPI_WARPS * 4096 <= NSTG * 2 * CT_TILE, "shared memory of a CTA");
@@ -59,13 +62,14 @@ constexpr uint32_t CT_TMEM_COLS = 512;
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
 // cut each of their sums off instead of rounding it, which shows in a float
 // loss as 1.2e-6 of it at K = 2048 in one chain and 3e-7 in chunks.
-constexpr int CT_KCHUNK = 16;
+constexpr int CT_KCHUNK = 16;  // a multiple of CT_SUB
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
   CUtensorMap h, w, g;     // K-major tiles: boxes of 128 rows x 64
   CUtensorMap h32, w32;    // the same rows, 32 at a time
-  CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64
+  CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64, two blocks of columns at once (wt: one where D is no multiple of 64)
+  CUtensorMap ht1, wt1;    // one block of columns
   CUtensorMap gout;        // 32 rows x 64: g's stores
   CUtensorMap dw;          // dweight: 32 rows x 128 bytes
 };
@@ -82,7 +86,7 @@ struct CtParams {
   int nparts;
   int v0, n, chunk, nchunks;  // the piece
   bool first, last;
-  bool dw_tma, accumulate, gf32, dh_wide;
+  bool w_blocks, dw_tma, accumulate, gf32, dh_wide;
   __nv_bfloat16 *dh;
   int64_t ld_dh, ldh;
   void *dw;
@@ -246,6 +250,15 @@ __device__ inline float ex2(float x) {
   return r;
 }
 
+// Boxes of several blocks of 64 columns, for the pair's barrier.
+__device__ inline void tma_load_3d_pair(void *dst, const CUtensorMap *m, uint32_t bar_cluster, int c0, int c1, int c2,
+                                        uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster), "l"(policy)
+      : "memory");
+}
 // A tile store with an L2 policy.
 __device__ inline void tma_store_2d_hint(const CUtensorMap *m, const void *src, int c0, int c1, uint64_t policy) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;" ::"l"(m),
@@ -410,8 +423,8 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
       tmem_ld32x2(taddr + c, taddr + c + 32, v[0], v[1]);
     }
     if (p.dw_tma) {
-      uint8_t *stg = stg2 + (c / 32 & (p.gf32 ? 1 : 2) ? 4096 : 0);  // the two tiles in turn
-      if (lane == 0) bulk_wait_read<1>();  // the store before the last has read its tile
+      uint8_t *stg = stg2 + (GNSTG == 2 && (c / 32 & (p.gf32 ? 1 : 2)) ? 4096 : 0);  // the two tiles in turn
+      if (lane == 0) bulk_wait_read<GNSTG - 1>();  // the store before the last has read its tile
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -462,7 +475,7 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
 template <int KIND>
 __global__ void __launch_bounds__(CtCfg<KIND>::THREADS, 1)
 ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
-  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, NSTG = CtCfg<KIND>::NSTG;
+  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, NSTG = CtCfg<KIND>::NSTG, CT_SUB = CtCfg<KIND>::SUB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *epi = base + CtCfg<KIND>::RING;
@@ -492,7 +505,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   if (warp == 0 && lane == 0) {
     if (KIND == CE_GRADS) {
       prefetch_tmap(&maps.g);
-      prefetch_tmap(&maps.wt);
+      prefetch_tmap(p.w_blocks ? &maps.wt : &maps.wt1);
       prefetch_tmap(&maps.gt);
       prefetch_tmap(&maps.ht);
       prefetch_tmap(&maps.dw);
@@ -515,9 +528,9 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   CtWork<KIND> work(p, cid, ncl);
   CtItem im;
   const int a_bytes = KIND != CE_GRADS && work.count <= 64 ? (work.count <= 32 ? 4096 : 8192) : CT_TILE;
-  const int stages = min(CT_MAX_STAGES, CtCfg<KIND>::RING / (a_bytes + CT_TILE));
-  auto sa = [&](int s) { return base + s * (a_bytes + CT_TILE); };
-  auto sb = [&](int s) { return base + s * (a_bytes + CT_TILE) + a_bytes; };
+  const int stages = min(CT_MAX_STAGES, CtCfg<KIND>::RING / (CT_SUB * (a_bytes + CT_TILE)));
+  auto sa = [&](int s, int j) { return base + (s * CT_SUB + j) * (a_bytes + CT_TILE); };
+  auto sb = [&](int s, int j) { return base + (s * CT_SUB + j) * (a_bytes + CT_TILE) + a_bytes; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -537,27 +550,33 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         const int arows = KIND == CE_GRADS ? 128 : min(128, max(0, (work.count - mrow + 31) & ~31));
         const int arows2 = KIND == CE_GRADS ? 256 : min(256, max(0, (work.count - im.m * 256 + 31) & ~31));
         const uint32_t bytes = 128 * (arows2 + 2 * (uint32_t)half);
-        for (int kb = 0; kb < im.nk; ++kb) {
+        for (int kb = 0; kb < im.nk; kb += CT_SUB) {
+          const int sub = min(CT_SUB, im.nk - kb);
           if (!ct_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
           // Both CTAs' tiles complete on the even CTA's barrier.
-          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          if (leader) mbar_arrive_expect_tx(&full[stage], sub * bytes);
           const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
-          const int k = kb * 64;
-          if (KIND != CE_GRADS) {
-            if (arows == 128) tma_load_2d_pair(sa(stage), &maps.h, bar, k, mrow, keep);
-            else
-              for (int j = 0; j < arows; j += 32) tma_load_2d_pair(sa(stage) + j * 128, &maps.h32, bar, k, mrow + j, keep);
-            if (half == 128) tma_load_2d_pair(sb(stage), &maps.w, bar, k, p.v0 + ncol, pass);
-            else
-              for (int j = 0; j < half; j += 32) tma_load_2d_pair(sb(stage) + j * 128, &maps.w32, bar, k, p.v0 + ncol + j, pass);
-          } else if (im.kind == 1) {
-            const int v = im.chunk * p.chunk + k;
-            tma_load_2d_pair(sa(stage), &maps.g, bar, v, mrow, keep);
-            for (int j = 0; j < half; j += 64)
-              tma_load_2d_pair(sb(stage) + j * 128, &maps.wt, bar, ncol + j, p.v0 + v, wpol);
-          } else {
-            for (int j = 0; j < 128; j += 64) tma_load_2d_pair(sa(stage) + j * 128, &maps.gt, bar, mrow + j, k, keep);
-            for (int j = 0; j < half; j += 64) tma_load_2d_pair(sb(stage) + j * 128, &maps.ht, bar, ncol + j, k, keep);
+          for (int s = 0; s < sub; ++s) {
+            const int k = (kb + s) * 64;
+            uint8_t *pa = sa(stage, s), *pb = sb(stage, s);
+            if (KIND != CE_GRADS) {
+              if (arows == 128) tma_load_2d_pair(pa, &maps.h, bar, k, mrow, keep);
+              else
+                for (int j = 0; j < arows; j += 32) tma_load_2d_pair(pa + j * 128, &maps.h32, bar, k, mrow + j, keep);
+              if (half == 128) tma_load_2d_pair(pb, &maps.w, bar, k, p.v0 + ncol, pass);
+              else
+                for (int j = 0; j < half; j += 32) tma_load_2d_pair(pb + j * 128, &maps.w32, bar, k, p.v0 + ncol + j, pass);
+            } else if (im.kind == 1) {
+              const int v = im.chunk * p.chunk + k;
+              tma_load_2d_pair(pa, &maps.g, bar, v, mrow, keep);
+              if (p.w_blocks && half == 128) tma_load_3d_pair(pb, &maps.wt, bar, 0, p.v0 + v, ncol / 64, wpol);
+              else
+                for (int j = 0; j < half; j += 64) tma_load_2d_pair(pb + j * 128, &maps.wt1, bar, ncol + j, p.v0 + v, wpol);
+            } else {
+              tma_load_3d_pair(pa, &maps.gt, bar, 0, k, mrow / 64, keep);
+              if (half == 128) tma_load_3d_pair(pb, &maps.ht, bar, 0, k, ncol / 64, keep);
+              else tma_load_2d_pair(pb, &maps.ht1, bar, ncol, k, keep);
+            }
           }
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -584,8 +603,9 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
           const bool a_mn = KIND == CE_GRADS && im.kind == 2, b_mn = KIND == CE_GRADS;
           const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
           const uint32_t astep = a_mn ? 128 : 2, bstep = b_mn ? 128 : 2;  // K = 16: 2048 or 32 bytes
-          for (int kb = 0; kb < im.nk; ++kb) {
+          for (int kb = 0; kb < im.nk; kb += CT_SUB) {
             const int kc = KIND == CE_STATS ? kb % CT_KCHUNK : kb;  // in this accumulator
+            const int sub = min(CT_SUB, im.nk - kb);
             const int b = cnt & 1;
             if (kc == 0) {
               if (!ct_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
@@ -593,15 +613,17 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
             }
             if (!ct_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t a0 = smem_u32(sa(stage)), b0 = smem_u32(sb(stage));
-            const uint64_t ad = a_mn ? smem_desc_mn_sw128(a0, 8192) : smem_desc_sw128(a0);
-            const uint64_t bd = b_mn ? smem_desc_mn_sw128(b0, 8192) : smem_desc_sw128(b0);
+            for (int s = 0; s < sub; ++s) {
+              const uint32_t a0 = smem_u32(sa(stage, s)), b0 = smem_u32(sb(stage, s));
+              const uint64_t ad = a_mn ? smem_desc_mn_sw128(a0, 8192) : smem_desc_sw128(a0);
+              const uint64_t bd = b_mn ? smem_desc_mn_sw128(b0, 8192) : smem_desc_sw128(b0);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kc | kk) != 0);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kc | s | kk) != 0);
+            }
             mma_commit_pair(&empty[stage]);
             if (++stage == stages) stage = 0, phase ^= 1;
-            if (kb + 1 == im.nk || (KIND == CE_STATS && kc + 1 == CT_KCHUNK)) {
+            if (kb + sub == im.nk || (KIND == CE_STATS && kc + sub == CT_KCHUNK)) {
               mma_commit_pair(&tfull[b]);
               ++cnt;
             }
@@ -688,6 +710,14 @@ static bool map_ld(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, 
   return encode_map(m, ptr, 2, dims, strides, box, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
+// The same (cols % 64 == 0) in blocks of 64 columns: boxes of 64 rows x 64 x 2.
+static bool map_blocks(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld) {
+  const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)cols / 64};
+  const uint64_t strides[2] = {(uint64_t)ld * 2, 128};
+  const uint32_t box[3] = {64, 64, 2};
+  return encode_map(m, ptr, 3, dims, strides, box);
+}
+
 template <int KIND>
 static cudaError_t launch(const CtMaps &maps, const CtParams &p, int64_t items, cudaStream_t stream) {
   cudaError_t e = ensure_smem((const void *)ce_pair_kernel<KIND>, CtCfg<KIND>::SMEM);
@@ -771,10 +801,12 @@ cudaError_t ce_tc_grads(const CeMats &m, const CePiece &c, cudaStream_t stream) 
   p.dh_wide = m.D % 4 == 0 && m.ld_dh % 4 == 0 && ((uintptr_t)m.dh & 7) == 0;
   p.acc = m.acc;
   p.planes = m.planes;
+  p.w_blocks = m.D % 64 == 0;
   // Tensor maps of dweight want its dense rows on 16-byte boundaries.
   p.dw_tma = ((uintptr_t)m.dw & 15) == 0 && m.D % (m.gf32 ? 4 : 8) == 0;
-  if (!map_ld(&maps.g, m.g, m.tpad, m.ldg, m.ldg, 128) || !map_ld(&maps.gt, m.g, m.tpad, m.ldg, m.ldg, 64) ||
-      !map_ld(&maps.wt, m.w, m.V, m.D, m.ldw, 64) || !map_ld(&maps.ht, m.h2, m.tpad, m.ldh, m.ldh, 64) ||
+  if (!map_ld(&maps.g, m.g, m.tpad, m.ldg, m.ldg, 128) || !map_blocks(&maps.gt, m.g, m.tpad, m.ldg, m.ldg) ||
+      (p.w_blocks && !map_blocks(&maps.wt, m.w, m.V, m.D, m.ldw)) || !map_ld(&maps.wt1, m.w, m.V, m.D, m.ldw, 64) ||
+      !map_blocks(&maps.ht, m.h2, m.tpad, m.ldh, m.ldh) || !map_ld(&maps.ht1, m.h2, m.tpad, m.ldh, m.ldh, 64) ||
       (p.dw_tma && !map_ld(&maps.dw, m.dw, m.V, m.D, m.D, 32, m.gf32)))
     return cudaErrorInvalidValue;
   const int64_t nt = ceil_div(m.D, 256);
