@@ -42,7 +42,7 @@ constexpr int CT_TILE = 16384;  // a K block of 64: 128 rows of A, or half of B'
 // that a thread's sums over the K chunks (64) stay in registers.  With two
 // tiles and a stage less GRADS at few rows, where the stores of dweight are what it
 // does, does not wait for one store to read its tile before it fills the next.
-constexpr int CT_EPI_FIRST = 2;
+constexpr int CT_EPI_FIRST = 4;
 constexpr int GNSTG = 1;
 constexpr int GSUB = 2;
 template <int KIND>
@@ -62,7 +62,7 @@ constexpr uint32_t CT_TMEM_COLS = 512;
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
 // cut each of their sums off instead of rounding it, which shows in a float
 // loss as 1.2e-6 of it at K = 2048 in one chain and 3e-7 in chunks.
-constexpr int CT_KCHUNK = 16;  // a multiple of CT_SUB
+constexpr int CT_KCHUNK = 16;  // a multiple of SUB
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
@@ -126,7 +126,7 @@ struct CtWork {
     pairs = pairs_;
     // Not through the read-only path, whose loads may be moved above the wait
     // for the kernel that writes it.
-    count = *(const volatile int *)p.count;
+    count = __shfl_sync(FULL_MASK, *(const volatile int *)p.count, 0);
     mt = (count + CE_ROWS - 1) / CE_ROWS;
     kd = (p.D + 63) / 64;
     kr = (count + 63) / 64;
@@ -242,6 +242,21 @@ __device__ inline bool ct_wait(uint64_t *bar, uint32_t parity, volatile int *abo
     }
   }
   return true;
+}
+
+// The same by a whole warp, with one answer for all of it.
+__device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status) {
+  return __all_sync(FULL_MASK, ct_wait(bar, parity, abort_flag, status));
+}
+// One lane of a whole warp, the same each time.
+__device__ inline bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 __device__ inline float ex2(float x) {
@@ -475,7 +490,7 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
 template <int KIND>
 __global__ void __launch_bounds__(CtCfg<KIND>::THREADS, 1)
 ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
-  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, NSTG = CtCfg<KIND>::NSTG, CT_SUB = CtCfg<KIND>::SUB;
+  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, NSTG = CtCfg<KIND>::NSTG, SUB = CtCfg<KIND>::SUB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *epi = base + CtCfg<KIND>::RING;
@@ -485,7 +500,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
   volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(FULL_MASK, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
@@ -522,121 +537,137 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(FULL_MASK, *tmem_slot, 0);
   griddep_launch();
   griddep_wait();
   CtWork<KIND> work(p, cid, ncl);
   CtItem im;
   const int a_bytes = KIND != CE_GRADS && work.count <= 64 ? (work.count <= 32 ? 4096 : 8192) : CT_TILE;
-  const int stages = min(CT_MAX_STAGES, CtCfg<KIND>::RING / (CT_SUB * (a_bytes + CT_TILE)));
-  auto sa = [&](int s, int j) { return base + (s * CT_SUB + j) * (a_bytes + CT_TILE); };
-  auto sb = [&](int s, int j) { return base + (s * CT_SUB + j) * (a_bytes + CT_TILE) + a_bytes; };
+  const int stages = min(CT_MAX_STAGES, CtCfg<KIND>::RING / (SUB * (a_bytes + CT_TILE)));
+  auto sa = [&](int s, int j) { return base + (s * SUB + j) * (a_bytes + CT_TILE); };
+  auto sb = [&](int s, int j) { return base + (s * SUB + j) * (a_bytes + CT_TILE) + a_bytes; };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
-      // The weights' rows of a chunk are read by every row tile, those of one row tile once.
-      const uint64_t wpol = work.mt > 1 ? keep : pass;
-      const uint32_t full0 = mapa_shared(&full[0], 0);
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_phase = 0;
-      bool ok = true;
-      while (ok && work.next(p, im)) {
-        const int mrow = im.m * 256 + (int)rank * 128;
-        const int half = im.cols / 2, ncol = im.n0 + (int)rank * half;
-        // Of the last rows only those that are there are read, 32 at a time: the
-        // lines behind them reach nothing but accumulator rows that nobody reads.
-        const int arows = KIND == CE_GRADS ? 128 : min(128, max(0, (work.count - mrow + 31) & ~31));
-        const int arows2 = KIND == CE_GRADS ? 256 : min(256, max(0, (work.count - im.m * 256 + 31) & ~31));
-        const uint32_t bytes = 128 * (arows2 + 2 * (uint32_t)half);
-        for (int kb = 0; kb < im.nk; kb += CT_SUB) {
-          const int sub = min(CT_SUB, im.nk - kb);
-          if (!ct_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
-          // Both CTAs' tiles complete on the even CTA's barrier.
-          if (leader) mbar_arrive_expect_tx(&full[stage], sub * bytes);
-          const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
-          for (int s = 0; s < sub; ++s) {
-            const int k = (kb + s) * 64;
-            uint8_t *pa = sa(stage, s), *pb = sb(stage, s);
-            if (KIND != CE_GRADS) {
+  // The producers and the MMA issuer run their loops as whole warps, on values
+  // that are the same in all lanes, and one elected lane issues: operands of
+  // copies and MMAs then are in uniform registers from the start.  (Computed by a
+  // single lane inside its branch, each copy took 410 cycles and each MMA 90.)
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA producers: A (warp 0), B (warp 2)
+    const bool is_a = warp == 0, elected = elect_one();
+    const uint64_t keep = policy_evict_last(), pass = policy_evict_first();
+    // The weights' rows of a chunk are read by every row tile, those of one row tile once.
+    const uint64_t wpol = work.mt > 1 ? keep : pass;
+    const uint32_t full0 = mapa_shared(&full[0], 0);
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    bool ok = true;
+    while (ok && work.next(p, im)) {
+      const int mrow = im.m * 256 + (int)rank * 128;
+      const int half = im.cols / 2, ncol = im.n0 + (int)rank * half;
+      // Of the last rows only those that are there are read, 32 at a time: the
+      // lines behind them reach nothing but accumulator rows that nobody reads.
+      const int arows = KIND == CE_GRADS ? 128 : min(128, max(0, (work.count - mrow + 31) & ~31));
+      const int arows2 = KIND == CE_GRADS ? 256 : min(256, max(0, (work.count - im.m * 256 + 31) & ~31));
+      const uint32_t bytes = 128 * (arows2 + 2 * (uint32_t)half);
+      for (int kb = 0; kb < im.nk; kb += SUB) {
+        const int sub = min(SUB, im.nk - kb);
+        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) { ok = false; break; }
+        const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
+        // Both CTAs' tiles complete on the even CTA's barrier.
+        if (leader && is_a && elected) mbar_arrive_expect_tx(&full[stage], sub * bytes);
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          if (s >= sub) break;
+          const int k = (kb + s) * 64;
+          uint8_t *pa = sa(stage, s), *pb = sb(stage, s);
+          if (!elected) continue;
+          if (KIND != CE_GRADS) {
+            if (is_a) {
               if (arows == 128) tma_load_2d_pair(pa, &maps.h, bar, k, mrow, keep);
               else
                 for (int j = 0; j < arows; j += 32) tma_load_2d_pair(pa + j * 128, &maps.h32, bar, k, mrow + j, keep);
+            } else {
               if (half == 128) tma_load_2d_pair(pb, &maps.w, bar, k, p.v0 + ncol, pass);
               else
                 for (int j = 0; j < half; j += 32) tma_load_2d_pair(pb + j * 128, &maps.w32, bar, k, p.v0 + ncol + j, pass);
-            } else if (im.kind == 1) {
-              const int v = im.chunk * p.chunk + k;
-              tma_load_2d_pair(pa, &maps.g, bar, v, mrow, keep);
-              if (p.w_blocks && half == 128) tma_load_3d_pair(pb, &maps.wt, bar, 0, p.v0 + v, ncol / 64, wpol);
-              else
-                for (int j = 0; j < half; j += 64) tma_load_2d_pair(pb + j * 128, &maps.wt1, bar, ncol + j, p.v0 + v, wpol);
-            } else {
-              tma_load_3d_pair(pa, &maps.gt, bar, 0, k, mrow / 64, keep);
-              if (half == 128) tma_load_3d_pair(pb, &maps.ht, bar, 0, k, ncol / 64, keep);
-              else tma_load_2d_pair(pb, &maps.ht1, bar, ncol, k, keep);
             }
+          } else if (im.kind == 1) {
+            const int v = im.chunk * p.chunk + k;
+            if (is_a) tma_load_2d_pair(pa, &maps.g, bar, v, mrow, keep);
+            else if (p.w_blocks && half == 128) tma_load_3d_pair(pb, &maps.wt, bar, 0, p.v0 + v, ncol / 64, wpol);
+            else
+              for (int j = 0; j < half; j += 64) tma_load_2d_pair(pb + j * 128, &maps.wt1, bar, ncol + j, p.v0 + v, wpol);
+          } else {
+            if (is_a) tma_load_3d_pair(pa, &maps.gt, bar, 0, k, mrow / 64, keep);
+            else if (half == 128) tma_load_3d_pair(pb, &maps.ht, bar, 0, k, ncol / 64, keep);
+            else tma_load_2d_pair(pb, &maps.ht1, bar, ncol, k, keep);
           }
-          issued |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == stages) stage = 0, phase ^= 1;
         }
+        issued |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == stages) stage = 0, phase ^= 1;
       }
-      if (!ok && leader) {
-        // The stages in flight (both CTAs' copies complete here) land before the pair exits.
-        volatile int never = 0;
-        for (int s = 0; s < stages; ++s)
-          if (issued & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1, &never, nullptr, 100000000ull);
-      }
+    }
+    if (!ok) {
+      // The copies in flight land before the pair exits: those that complete a
+      // stage (both CTAs' do in the even CTA) are waited for, the others given the same time.
+      volatile int never = 0;
+      for (int s = 0; s < stages; ++s)
+        if (issued & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1, &never, nullptr, 100000000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      if (leader) {
-        // -------------------------------------------------------- MMA issuer (both CTAs' tensor memory)
-        int stage = 0;
-        uint32_t phase = 0, cnt = 0;
-        bool ok = true;
-        while (ok && work.next(p, im)) {
-          if (im.nk == 0) continue;
-          const bool a_mn = KIND == CE_GRADS && im.kind == 2, b_mn = KIND == CE_GRADS;
-          const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
-          const uint32_t astep = a_mn ? 128 : 2, bstep = b_mn ? 128 : 2;  // K = 16: 2048 or 32 bytes
-          for (int kb = 0; kb < im.nk; kb += CT_SUB) {
-            const int kc = KIND == CE_STATS ? kb % CT_KCHUNK : kb;  // in this accumulator
-            const int sub = min(CT_SUB, im.nk - kb);
-            const int b = cnt & 1;
-            if (kc == 0) {
-              if (!ct_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
-              tc_fence_after();
-            }
-            if (!ct_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+    if (leader) {
+      // ---------------------------------------------------------- MMA issuer (both CTAs' tensor memory)
+      const bool elected = elect_one();
+      int stage = 0;
+      uint32_t phase = 0, cnt = 0;
+      bool ok = true;
+      while (ok && work.next(p, im)) {
+        if (im.nk == 0) continue;
+        const bool a_mn = KIND == CE_GRADS && im.kind == 2, b_mn = KIND == CE_GRADS;
+        const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
+        const uint32_t astep = a_mn ? 128 : 2, bstep = b_mn ? 128 : 2;  // K = 16: 2048 or 32 bytes
+        for (int kb = 0; kb < im.nk; kb += SUB) {
+          const int kc = KIND == CE_STATS ? kb % CT_KCHUNK : kb;  // in this accumulator
+          const int sub = min(SUB, im.nk - kb);
+          const int b = cnt & 1;
+          if (kc == 0) {
+            if (!warp_wait(&tempty[b], ((cnt >> 1) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
             tc_fence_after();
-            for (int s = 0; s < sub; ++s) {
-              const uint32_t a0 = smem_u32(sa(stage, s)), b0 = smem_u32(sb(stage, s));
-              const uint64_t ad = a_mn ? smem_desc_mn_sw128(a0, 8192) : smem_desc_sw128(a0);
-              const uint64_t bd = b_mn ? smem_desc_mn_sw128(b0, 8192) : smem_desc_sw128(b0);
+          }
+          if (!warp_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < SUB; ++s) {
+            if (s >= sub) break;
+            const uint32_t a0 = smem_u32(sa(stage, s)), b0 = smem_u32(sb(stage, s));
+            const uint64_t ad = a_mn ? smem_desc_mn_sw128(a0, 8192) : smem_desc_sw128(a0);
+            const uint64_t bd = b_mn ? smem_desc_mn_sw128(b0, 8192) : smem_desc_sw128(b0);
+            if (elected) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kc | s | kk) != 0);
             }
-            mma_commit_pair(&empty[stage]);
-            if (++stage == stages) stage = 0, phase ^= 1;
-            if (kb + sub == im.nk || (KIND == CE_STATS && kc + sub == CT_KCHUNK)) {
-              mma_commit_pair(&tfull[b]);
-              ++cnt;
-            }
           }
+          const bool last = kb + sub == im.nk || (KIND == CE_STATS && kc + sub == CT_KCHUNK);
+          if (elected) {
+            mma_commit_pair(&empty[stage]);
+            if (last) mma_commit_pair(&tfull[b]);
+          }
+          __syncwarp();
+          if (last) ++cnt;
+          if (++stage == stages) stage = 0, phase ^= 1;
         }
-        mma_commit_pair(mma_done);
       }
-      // Every pair MMA has finished (it wrote both CTAs' tensor memory) before TMEM is released.
-      volatile int never = 0;
-      ct_wait(mma_done, 0, &never, p.status);
+      if (elected) mma_commit_pair(mma_done);
+      __syncwarp();
     }
+    // Every pair MMA has finished (it wrote both CTAs' tensor memory) before TMEM is released.
+    volatile int never = 0;
+    if (lane == 0) ct_wait(mma_done, 0, &never, p.status);
     __syncwarp();
-  } else {
+  } else if (warp >= CT_EPI_FIRST) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;  // TMEM lane quarter; which of the columns
     uint8_t *stg = epi + (warp - CT_EPI_FIRST) * NSTG * 4096;
@@ -644,9 +675,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     const uint64_t out_policy = policy_evict_first();  // dweight is written once and not read again
     uint32_t cnt = 0;
     auto wait = [&] {
-      int ok = 0;
-      if (lane == 0) ok = ct_wait(&tfull[cnt & 1], (cnt >> 1) & 1, abort_flag, p.status) ? 1 : 0;
-      if (!__shfl_sync(FULL_MASK, ok, 0)) return false;
+      if (!warp_wait(&tfull[cnt & 1], (cnt >> 1) & 1, abort_flag, p.status)) return false;
       tc_fence_after();
       return true;
     };
