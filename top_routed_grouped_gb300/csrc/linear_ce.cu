@@ -21,7 +21,7 @@ namespace moe {
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
 
 // ------------------------------------------------------------- which rows count
-// One CTA: place[t] is row t's place among those that count (-1: left out),
+// One CTA, for more than CE_FUSE rows: place[t] is row t's place among those that count (-1: left out),
 // row_of the reverse; the order is kept.  T reads of 4 or 8 bytes: latency.
 template <typename Id>
 __global__ void __launch_bounds__(1024)
@@ -123,23 +123,77 @@ __device__ inline void put_row(E *dst, const E *src, int D, int64_t dp, float f,
   }
 }
 
+// Up to this many rows each CTA of ce_rows_kernel counts the rows before its
+// own by itself: reading all targets again costs less than a launch.
+constexpr int CE_FUSE = 4096;
+
 // A warp a row: the rows that count to their places, zeros behind them (in
 // the columns up to dp and the rows up to the tile's end), zeros into dhidden
 // where a row is left out.  For the gradient alone also what it needs of a
 // row: the target's logit is a dot product of the row with one of the weights.
-template <typename E>
+// FUSED: the places, too.
+template <typename E, bool FUSED>
 __global__ void __launch_bounds__(256)
-ce_rows_kernel(CeArgs a, int64_t dp, E *hc, E *hc2, const int *count, const int *place, CeRow *rows, float *inv,
-               bool zero_dh, bool grad_only, bool wide, bool wide_w) {
+ce_rows_kernel(CeArgs a, int64_t dp, E *hc, E *hc2, int *count, int *row_of, const int *place, CeRow *rows, float *inv,
+               float *loss, float *lse, bool zero_dh, bool grad_only, bool wide, bool wide_w, int *status) {
   constexpr int N = Vec16<E>::N;
   griddep_launch();
   griddep_wait();
   const int t = (int)(((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  int at;
+  int at, n;
+  CeRow info = {0.f, 0.f, 0.f, -1};
+  if (FUSED) {
+    __shared__ uint32_t flags[CE_FUSE / 32];  // rows that count
+    auto target = [&](int i) {
+      return a.targets64 ? ((const int64_t *)a.targets)[i] : (int64_t)((const int32_t *)a.targets)[i];
+    };
+    for (int i0 = 0; i0 < CE_FUSE; i0 += 256) {
+      if (i0 >= a.T) {
+        if (lane == 0) flags[(i0 + threadIdx.x) / 32] = 0;
+        continue;
+      }
+      const int i = i0 + threadIdx.x;
+      const int64_t id = i < a.T ? target(i) : a.ignore_index;
+      const bool in = id >= 0 && id < a.V;
+      if (!in && id != a.ignore_index) record_status(status, STATUS_BAD_TARGET);
+      const unsigned vote = __ballot_sync(FULL_MASK, in && id != a.ignore_index && i < a.T);
+      if (lane == 0) flags[i / 32] = vote;
+    }
+    __syncthreads();
+    // Lane i has the four words of rows 128 i and on.
+    int before = 0, all = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int w = lane * 4 + j;
+      const uint32_t b = flags[w];
+      all += __popc(b);
+      if (w * 32 + 32 <= t) before += __popc(b);
+      else if (w * 32 < t) before += __popc(b & ((1u << (t - w * 32)) - 1));
+    }
+    for (int d = 16; d; d >>= 1) {
+      before += __shfl_xor_sync(FULL_MASK, before, d);
+      all += __shfl_xor_sync(FULL_MASK, all, d);
+    }
+    n = all;
+    at = -1;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *count = n;
+    if (t < a.T && (flags[t / 32] >> (t & 31) & 1)) {
+      at = before;
+      info.target = (int)target(t);
+      if (lane == 0) row_of[at] = t;
+    }
+    if (t < a.T && at < 0 && lane == 0) {
+      if (loss) loss[t] = 0.f;
+      if (lse) lse[t] = 0.f;
+    }
+  } else {
+    n = *count;
+    at = t < a.T ? place[t] : -1;
+    if (at >= 0) info = rows[at];
+  }
   const E *src = nullptr;
   float f = 1.f;
   if (t < a.T) {
-    at = place[t];
     if (at < 0) {
       if (zero_dh)
         for (int c = lane; c < a.D; c += 32) ((E *)a.dh)[t * a.ld_dh + c] = Elem<E>::from_f32(0.f);
@@ -147,7 +201,7 @@ ce_rows_kernel(CeArgs a, int64_t dp, E *hc, E *hc2, const int *count, const int 
     }
     src = (const E *)a.hidden + t * a.ld_h;
     if (grad_only) {
-      const E *w = (const E *)a.weight + rows[at].target * a.ld_w;
+      const E *w = (const E *)a.weight + info.target * a.ld_w;
       float x = 0.f;
       if (wide && wide_w) {
         for (int u = lane; u < a.D / N; u += 32) {
@@ -162,17 +216,14 @@ ce_rows_kernel(CeArgs a, int64_t dp, E *hc, E *hc2, const int *count, const int 
       }
       for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(FULL_MASK, x, d);
       const float l = a.lse[t];
-      CeRow r = rows[at];
-      f = grad_row<E>(r, a.scale * a.dloss[t], l, fmaf(-x, a.scale, l), a.z_loss);
-      if (lane == 0) {
-        rows[at] = r;
-        inv[at] = f;
-      }
+      f = grad_row<E>(info, a.scale * a.dloss[t], l, fmaf(-x, a.scale, l), a.z_loss);
+      if (lane == 0) inv[at] = f;
     }
   } else {
-    at = *count + (t - a.T);
-    if (at >= (int)round_up(*count, CE_ROWS)) return;
+    at = n + (t - a.T);
+    if (at >= (int)round_up(n, CE_ROWS)) return;
   }
+  if (lane == 0) rows[at] = info;
   put_row<E, false>(hc + at * dp, src, a.D, dp, 1.f, wide, lane);
   if (grad_only && sizeof(E) == 2) put_row<E, true>(hc2 + at * dp, src, a.D, dp, f, wide, lane);
 }
@@ -324,18 +375,22 @@ static cudaError_t run(const CeArgs &a, int mode, uint8_t *w, int *status, cudaS
   float *inv = (float *)(w + l.inv);
   cudaError_t e;
   float *lo = loss ? a.loss : nullptr, *ls = loss ? a.lse : nullptr;
-  if (a.targets64)
-    e = launch_pdl(ce_places_kernel<int64_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
-                   (const int64_t *)a.targets, count, row_of, place, rows, lo, ls, status);
-  else
-    e = launch_pdl(ce_places_kernel<int32_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
-                   (const int32_t *)a.targets, count, row_of, place, rows, lo, ls, status);
-  if (e != cudaSuccess) return e;
+  const bool fused = a.T <= CE_FUSE;
+  if (!fused) {
+    if (a.targets64)
+      e = launch_pdl(ce_places_kernel<int64_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
+                     (const int64_t *)a.targets, count, row_of, place, rows, lo, ls, status);
+    else
+      e = launch_pdl(ce_places_kernel<int32_t>, dim3(1), dim3(1024), 0, stream, a.T, a.V, a.ignore_index,
+                     (const int32_t *)a.targets, count, row_of, place, rows, lo, ls, status);
+    if (e != cudaSuccess) return e;
+  }
   constexpr int N = Vec16<E>::N;
   const bool wide = a.D % N == 0 && a.ld_h % N == 0 && ((uintptr_t)a.hidden & 15) == 0;
   const bool wide_w = a.ld_w % N == 0 && ((uintptr_t)a.weight & 15) == 0;
-  e = launch_pdl(ce_rows_kernel<E>, dim3((unsigned)ceil_div((int64_t)a.T + CE_ROWS, 8)), dim3(256), 0, stream, a, l.dp, hc,
-                 hc2, (const int *)count, (const int *)place, rows, inv, grad, grad && !loss, wide, wide_w);
+  e = launch_pdl(fused ? ce_rows_kernel<E, true> : ce_rows_kernel<E, false>,
+                 dim3((unsigned)ceil_div((int64_t)a.T + CE_ROWS, 8)), dim3(256), 0, stream, a, l.dp, hc, hc2, count, row_of,
+                 (const int *)place, rows, inv, lo, ls, grad, grad && !loss, wide, wide_w, status);
   if (e != cudaSuccess) return e;
   if (l.ldw) {
     e = launch_pdl(ce_weight_copy_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(a.V, 8), 8 * 152)), dim3(256), 0,
