@@ -1,4 +1,5 @@
-"""Build ``libmoe_gb300.so`` from ``csrc/*.cu`` for sm_103a with nvcc.
+"""Build ``libmoe_gb300.so`` from ``csrc/*.cu`` for sm_103a with nvcc, and the
+``_tensor_list`` module from ``csrc/bind/`` with the host compiler.
 
 Each translation unit compiles in parallel into ``_build/``; the objects are
 linked into the shared library next to this file (in-tree).  Rebuilds only
@@ -19,6 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
+BIND_SRC = os.path.join(CSRC, "bind", "tensor_list.cpp")
+BIND = os.path.join(HERE, "_tensor_list.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -46,8 +49,29 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_bind(force: bool = False) -> str:
+    """The Python module that packs lists of tensors (against the torch that is installed)."""
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND_SRC) <= os.path.getmtime(BIND):
+        return BIND
+    import sysconfig
+
+    import torch
+    tmp = BIND + f".tmp{os.getpid()}"
+    home = os.path.dirname(torch.__file__)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-I{home}/include", f"-I{home}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
+           BIND_SRC, f"-L{home}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and not ptxas_info and up_to_date():
+        build_bind()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -63,8 +87,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(9, os.cpu_count() or 1))) as ex:
+        bind = ex.submit(build_bind, force)
         objs = list(ex.map(compile_one, sources()))
+        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -102,7 +102,11 @@ ce_simt_kernel(const SimtParams a) {
   A.k = B.k = k;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   // A thread's rows are r0 + 4 ty + {0..3} and + 64, its columns alike.
-  float acc[RT][RT] = {};
+  F2 sum[RT][RT / 2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < RT / 2; ++j) sum[i][j] = F2(0.f);
   A.load(0);
   B.load(0);
   int buf = 0;
@@ -116,19 +120,34 @@ ce_simt_kernel(const SimtParams a) {
     }
 #pragma unroll
     for (int kk = 0; kk < SK; ++kk) {
-      float x[RT], y[RT];
+      float4 x[S], y[S];
 #pragma unroll
       for (int h = 0; h < S; ++h) {
-        *(float4 *)&x[4 * h] = *(const float4 *)&sA[buf][kk][64 * h + ty * 4];
-        *(float4 *)&y[4 * h] = *(const float4 *)&sB[buf][kk][64 * h + tx * 4];
+        x[h] = *(const float4 *)&sA[buf][kk][64 * h + ty * 4];
+        y[h] = *(const float4 *)&sB[buf][kk][64 * h + tx * 4];
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int h = 0; h < S; ++h) {
+        const F2 y0(y[h].x, y[h].y), y1(y[h].z, y[h].w);
 #pragma unroll
-        for (int j = 0; j < RT; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+        for (int g = 0; g < S; ++g) {
+          const float v[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const F2 d(v[i]);
+            sum[4 * g + i][2 * h] = fma2(d, y0, sum[4 * g + i][2 * h]);
+            sum[4 * g + i][2 * h + 1] = fma2(d, y1, sum[4 * g + i][2 * h + 1]);
+          }
+        }
+      }
     }
     buf ^= 1;  // the other buffer was last read before the barrier of this step
   }
+  float acc[RT][RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < RT / 2; ++j) sum[i][j].get(acc[i][2 * j], acc[i][2 * j + 1]);
   auto rowof = [&](int i) { return (i & 3) + (i >> 2) * 64 + ty * 4; };
   auto colof = [&](int j) { return (j & 3) + (j >> 2) * 64 + tx * 4; };
   constexpr float L2E = 1.44269504088896340736f;

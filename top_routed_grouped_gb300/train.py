@@ -11,13 +11,11 @@ outputs and call.
 from __future__ import annotations
 
 import struct
-from array import array
-from operator import attrgetter
 
 import torch
 
 from . import _check, lib
-from .step import _DTYPE, _ids, _like, _on, _ptr, _row_type, _rows, _same_or_f32, _vec, _written, _ws
+from .step import _ids, _like, _on, _ptr, _row_type, _rows, _same_or_f32, _vec, _written, _ws
 
 _CE = struct.Struct("7i2fi4q8Q")     # moe_linear_ce_args_t
 _GRADS = struct.Struct("2i5Q2fQ")    # moe_grads_args_t
@@ -137,67 +135,32 @@ def linear_cross_entropy_step(hidden, weight, targets, dloss, scale: float = 1.0
 
 
 # ---------------------------------------------------------------- gradients
-def _gapless(t) -> bool:
-    """Whether the elements of ``t`` are neighbours in memory, in whatever order."""
-    n = 1
-    for stride, size in sorted((s, z) for s, z in zip(t.stride(), t.shape) if z != 1):
-        if stride != n:
-            return False
-        n *= size
-    return True
-
-
-_dtype_of = attrgetter("dtype")
-
-
-def _tensors(ts, dev, name: str):
-    """Addresses, sizes and type codes, as the library's host arrays.  Lists
-    are long (a thousand tensors and more), so each property is asked of all of
-    them in one ``map``."""
-    T = torch.Tensor
-    codes = list(map(_DTYPE.get, map(_dtype_of, ts)))
-    if None in codes:
-        raise ValueError(f"{name}: float32 or bfloat16 expected, got {ts[codes.index(None)].dtype}")
-    devices = set(map(T.get_device, ts))
-    if devices != {dev}:
-        raise ValueError(f"{name}: tensors on device {dev} expected, got some on {sorted(devices - {dev})}")
-    dense = all(map(T.is_contiguous, ts))
-    if not dense:
-        for t in ts:
-            if not t.is_contiguous() and t.numel() and not _gapless(t):
-                raise ValueError(f"{name}: tensors without gaps expected, got strides {t.stride()} of {list(t.shape)}")
-    return array("Q", list(map(T.data_ptr, ts))), array("q", list(map(T.numel, ts))), array("i", codes), dense
+def _pack(grads, out, dev):
+    global _pack
+    try:
+        from ._tensor_list import pack as _pack
+    except ImportError as e:
+        raise RuntimeError("_tensor_list.so is missing or of another torch: build it with "
+                           "`python -m top_routed_grouped_gb300.build`") from e
+    return _pack(grads, out, dev)
 
 
 def _grads(stream, grads, out, norm, max_norm, eps, ws, mode):
     dev, device = grads[0].get_device(), grads[0].device
-    src, numel, code, dense = _tensors(grads, dev, "grads")
-    dst, ocode, written = src, code, grads
-    if out is not None:
-        if len(out) != len(grads):
-            raise ValueError(f"out: {len(grads)} tensors expected, got {len(out)}")
-        dst, onumel, ocode, odense = _tensors(out, dev, "out")
-        if numel != onumel:
-            raise ValueError("out: tensors of the sizes of grads expected")
-        if not (dense and odense):
-            for g, o in zip(grads, out):
-                if not (g.is_contiguous() and o.is_contiguous()) and (g.shape != o.shape or g.stride() != o.stride()):
-                    raise ValueError(f"out: {list(g.shape)} with strides {g.stride()} expected, got {list(o.shape)} with "
-                                     f"{o.stride()}")
-        written = out
+    held, src, dst, numel, code, ocode = _pack(grads, out, dev)
     if mode & 1:
         norm = torch.empty((), dtype=torch.float32, device=device)
     elif norm.dtype is not torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
         raise ValueError(f"norm: one float32 on device {dev} expected")
-    args = _GRADS.pack(len(grads), 0, src.buffer_info()[0], dst.buffer_info()[0], numel.buffer_info()[0],
-                       code.buffer_info()[0], ocode.buffer_info()[0], max_norm, eps, norm.data_ptr())
+    args = _GRADS.pack(len(grads), 0, src, dst, numel, code, ocode, max_norm, eps, norm.data_ptr())
     if mode & 1:
         ws, n = _ws(moe_grad_workspace_size(args) if ws is None else 0, ws, device)
         (moe_grad_norm if mode == 1 else moe_grad_clip)(args, ws.data_ptr(), n, stream)
     else:
         moe_grad_scale(args, stream)
+    del held
     if mode & 2:
-        _written(written)
+        _written(grads if out is None else out)
     return norm
 
 
