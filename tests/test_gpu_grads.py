@@ -1,8 +1,8 @@
 """grad_norm, clip_grads and scale_grads against 64 bits.
 
-The norm: squares in FP32 (2^-24 each), at most 40 of them a thread in sums of
-FP32 (4 chains: 12 roundings), the rest in FP64, the root halves it, one
-rounding to float: 16 * 2^-24 relative.  A scaled element: the factor's own
+The norm: squares in FP32 (2^-24 each), at most 34 of them a thread in sums of
+FP32 (4 chains and their joining: 12 roundings, then 5 of a warp's tree), the
+rest in FP64, the root halves it, one rounding to float: below 16 * 2^-24 relative.  A scaled element: the factor's own
 few roundings (the norm's, the sum with eps, the quotient: 20 * 2^-24), the
 product, and half an ulp of the output's type (2^-8, 2^-24)."""
 import pytest

@@ -10,10 +10,12 @@
 // elements; a CTA has a run of neighbouring chunks, finds the tensor of the first by
 // bisection and goes on from there, forwards for the norm, backwards for the scaling.
 //
-// Squares are summed in FP32 over at most 32 elements of a thread, then in
-// FP64.  Where such a sum is out of the range in which FP32 squares keep their
-// bits (some |g| above 1e15, or all of them below 1e-12) the chunk's elements
-// are read again and summed in FP64.  No atomics: each CTA leaves one partial
+// Squares are summed in FP32 over a chunk's 1024 elements of a warp (32 of a
+// thread in four chains, then a tree), and only those sums in FP64: an SM adds
+// two doubles a clock, and joining 256 threads' by a tree of them took as long
+// as reading 40 MB.  Where a warp's sum is out of the range in which FP32 squares keep
+// their bits (some |g| above 1e13, or all of them below 1e-12) its elements
+// are read again and summed in FP64.  No atomics: each cluster leaves one partial
 // sum, and all of them are added in one order.
 #include <math.h>
 
@@ -22,12 +24,16 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_host.h"
+#include "umma.cuh"
 
 namespace moe {
 
 constexpr int GN_THREADS = 256;
 constexpr int GN_CTAS = 8;                   // CTAs a SM
 constexpr int GN_CHUNK = 32 * GN_THREADS;    // elements
+// CTAs of a cluster put their sums together on chip: every CTA of the scaling
+// adds all partial sums up.
+constexpr int GN_CLUSTER = 8;
 
 // CAP tensors: 28 bytes each, of the 32 KB that a kernel's arguments may take.
 template <int CAP>
@@ -61,27 +67,15 @@ __device__ inline int head_of(const E *p, int64_t n) {
   return n < h ? (int)n : h;
 }
 
-__device__ inline double warp_sum(double v) {
+template <typename T>
+__device__ inline T warp_sum(T v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
   return v;
 }
 
-// The sum over the CTA, in every thread.
-__device__ inline double cta_sum(double v) {
-  __shared__ double sh[GN_THREADS / 32];
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0;
-#pragma unroll
-  for (int i = 0; i < GN_THREADS / 32; ++i) s += sh[i];
-  __syncthreads();
-  return s;
-}
-
-// Squares of this thread's elements of chunk c of a tensor: the head (chunk
-// 0), units of 16 bytes, the tail (the last chunk).
+// The sum of the squares of this warp's elements of chunk c of a tensor: the
+// head (chunk 0), units of 16 bytes, the tail (the last chunk).
 template <typename E>
 __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks) {
   constexpr int N = Vec16<E>::N;
@@ -120,9 +114,9 @@ __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks
   s[2] = fmaf(edge[0], edge[0], s[2]);
   s[3] = fmaf(edge[1], edge[1], s[3]);
   any |= __float_as_uint(edge[0]) | __float_as_uint(edge[1]);
-  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+  const float sum = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
   const uint32_t signs = sizeof(E) == 2 ? 0x7fff7fffu : 0x7fffffffu;
-  if (sum < 1e30f && (sum > 1e-24f || !(any & signs))) return sum;
+  if (sum < 1e30f && (sum > 1e-24f || !__any_sync(FULL_MASK, (any & signs) != 0))) return sum;
   double d = (double)edge[0] * edge[0] + (double)edge[1] * edge[1];
   for (u = u0 + threadIdx.x; u < u1; u += GN_THREADS) {
     float x[N];
@@ -130,7 +124,7 @@ __device__ inline double chunk_squares(const E *p, int64_t n, int c, int nchunks
 #pragma unroll
     for (int i = 0; i < N; ++i) d += (double)x[i] * x[i];
   }
-  return d;
+  return warp_sum(d);
 }
 
 // The run of chunks of this CTA.
@@ -145,7 +139,7 @@ grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, double *part) {
   griddep_launch();
   int c0, c1;
   run_of(t.first[t.n], c0, c1);
-  int i = tensor_of(t, c0);
+  int i = c1 > c0 ? tensor_of(t, c0) : 0;
   griddep_wait();
   double sum = 0;
   for (int c = c0; c < c1; ++c) {
@@ -154,18 +148,39 @@ grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, double *part) {
     if (t.f32[i >> 5] >> (i & 31) & 1) sum += chunk_squares((const float *)t.in[i], t.size[i], c - first, k);
     else sum += chunk_squares((const __nv_bfloat16 *)t.in[i], t.size[i], c - first, k);
   }
-  sum = cta_sum(sum);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  // All warps of the cluster to its first CTA, where one thread adds them in order.
+  constexpr int WARPS = GN_THREADS / 32;
+  __shared__ double of_cluster[GN_CLUSTER * WARPS];
+  const uint32_t rank = umma::cluster_ctarank();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
+                     umma::mapa_shared(&of_cluster[rank * WARPS + (threadIdx.x >> 5)], 0)),
+                 "d"(sum)
+                 : "memory");
+  umma::cluster_sync();
+  if (rank == 0 && threadIdx.x < 32) {
+    double s = 0;
+#pragma unroll
+    for (int i = 0; i < GN_CLUSTER * WARPS / 32; ++i) s += of_cluster[i * 32 + threadIdx.x];
+    s = warp_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x / GN_CLUSTER] = s;
+  }
 }
 
-// All partial sums, in one order, by a CTA.
+// All partial sums, in one order, by the CTA's first warp.
 __device__ inline float norm_of(const double *part, int n) {
-  double s = 0;
-  for (int i = threadIdx.x; i < n; i += GN_THREADS) s += part[i];
-  return (float)sqrt(cta_sum(s));
+  __shared__ float norm;
+  if (threadIdx.x < 32) {
+    double s = 0;
+    for (int i = threadIdx.x; i < n; i += 32) s += part[i];
+    s = warp_sum(s);
+    if (threadIdx.x == 0) norm = (float)sqrt(s);
+  }
+  __syncthreads();
+  return norm;
 }
 
-__global__ void __launch_bounds__(GN_THREADS) grad_norm_finish_kernel(const double *part, int n, float *norm) {
+__global__ void __launch_bounds__(32) grad_norm_finish_kernel(const double *part, int n, float *norm) {
   griddep_launch();
   griddep_wait();
   const float r = norm_of(part, n);
@@ -255,7 +270,7 @@ static int launches(const GradList &a) { return std::max(1, (int)ceil_div(a.n, G
 // CTAs of a launch at most.
 static int most_ctas() { return std::max(1, device_sms()) * GN_CTAS; }
 
-size_t grad_scratch_bytes(const GradList &a) { return (size_t)launches(a) * most_ctas() * sizeof(double); }
+size_t grad_scratch_bytes(const GradList &a) { return (size_t)launches(a) * (most_ctas() / GN_CLUSTER) * sizeof(double); }
 
 // Tensors [i0, i1) of the list; the number of chunks.
 template <int CAP>
@@ -289,14 +304,25 @@ static cudaError_t run(const GradList &a, int mode, double *part, cudaStream_t s
     for (int l = 0; l < nl; ++l) {
       const int chunks = fill(t, a, l * CAP, std::min(a.n, (l + 1) * CAP), false);
       if (!chunks) continue;
-      const int grid = std::min(chunks, most);
-      if ((e = launch_pdl(grad_norm_kernel<CAP>, dim3(grid), dim3(GN_THREADS), 0, stream, t, part + parts)) != cudaSuccess)
-        return e;
-      parts += grid;
+      const int grid = (int)round_up(std::min(chunks, most), GN_CLUSTER);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(grid);
+      cfg.blockDim = dim3(GN_THREADS);
+      cfg.stream = stream;
+      cudaLaunchAttribute at[2];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = GN_CLUSTER;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[1].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 2;
+      if ((e = cudaLaunchKernelEx(&cfg, grad_norm_kernel<CAP>, t, part + parts)) != cudaSuccess) return e;
+      parts += grid / GN_CLUSTER;
     }
   }
   if (mode == GRAD_NORM)
-    return launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(GN_THREADS), 0, stream, (const double *)part, parts, a.norm);
+    return launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(32), 0, stream, (const double *)part, parts, a.norm);
   const double *p = mode & GRAD_NORM ? part : nullptr;
   bool any = false;
   for (int l = nl - 1; l >= 0; --l) {
@@ -312,7 +338,7 @@ static cudaError_t run(const GradList &a, int mode, double *part, cudaStream_t s
 
 cudaError_t launch_grads(const GradList &a, int mode, void *scratch, cudaStream_t stream) {
   if (a.n == 0 && mode != GRAD_SCALE)
-    return launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(GN_THREADS), 0, stream, (const double *)scratch, 0, a.norm);
+    return launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(32), 0, stream, (const double *)scratch, 0, a.norm);
   return a.n <= GN_SMALL ? run<GN_SMALL>(a, mode, (double *)scratch, stream)
                          : run<GN_LARGE>(a, mode, (double *)scratch, stream);
 }
