@@ -29,41 +29,61 @@ ce_places_kernel(int T, int V, int64_t ignore, const Id *targets, int *count, in
                  float *loss, float *lse, int *status) {
   griddep_launch();
   griddep_wait();
-  __shared__ int sums[33];
+  constexpr int M = 8;  // rows of a thread at a time, 1024 apart: their loads are in flight together
+  __shared__ int sums[M * 32 + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int base = 0;
-  for (int t0 = 0; t0 < T; t0 += 1024) {
-    const int t = t0 + threadIdx.x;
-    const int64_t id = t < T ? (int64_t)targets[t] : ignore;
-    const bool in = id >= 0 && id < V;
-    const bool keep = t < T && id != ignore && in;
-    if (t < T && id != ignore && !in) record_status(status, STATUS_BAD_TARGET);
-    const unsigned vote = __ballot_sync(FULL_MASK, keep);
-    if (lane == 0) sums[warp] = __popc(vote);
+  for (int t0 = 0; t0 < T; t0 += M * 1024) {
+    int64_t id[M];
+    unsigned vote[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int t = t0 + j * 1024 + threadIdx.x;
+      id[j] = t < T ? (int64_t)targets[t] : ignore;
+    }
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int t = t0 + j * 1024 + threadIdx.x;
+      const bool in = id[j] >= 0 && id[j] < V;
+      if (!in && id[j] != ignore) record_status(status, STATUS_BAD_TARGET);
+      vote[j] = __ballot_sync(FULL_MASK, t < T && in && id[j] != ignore);
+      if (lane == 0) sums[j * 32 + warp] = __popc(vote[j]);
+    }
     __syncthreads();
-    if (warp == 0) {
-      const int own = sums[lane];
-      int s = own;
+    if (warp == 0) {  // the sums before each warp's, in the order of the rows: eight of them a lane
+      int own[M], all = 0;
+#pragma unroll
+      for (int j = 0; j < M; ++j) {
+        own[j] = all;
+        all += sums[lane * M + j];
+      }
+      int s = all;
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(FULL_MASK, s, d);
         if (lane >= d) s += o;
       }
-      sums[lane] = s - own;
-      if (lane == 31) sums[32] = s;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < M; ++j) sums[lane * M + j] = s - all + own[j];
+      if (lane == 31) sums[M * 32] = s;
     }
     __syncthreads();
-    if (t < T) {
-      const int at = base + sums[warp] + __popc(vote & lanemask_lt());
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int t = t0 + j * 1024 + threadIdx.x;
+      if (t >= T) break;
+      const bool keep = vote[j] >> lane & 1;
+      const int at = base + sums[j * 32 + warp] + __popc(vote[j] & lanemask_lt());
       place[t] = keep ? at : -1;
       if (keep) {
         row_of[at] = t;
-        rows[at].target = (int)id;
+        rows[at].target = (int)id[j];
       } else {
         if (loss) loss[t] = 0.f;
         if (lse) lse[t] = 0.f;
       }
     }
-    base += sums[32];
+    base += sums[M * 32];
     __syncthreads();
   }
   if (threadIdx.x == 0) *count = base;
@@ -147,16 +167,19 @@ ce_rows_kernel(CeArgs a, int64_t dp, E *hc, E *hc2, int *count, int *row_of, con
     auto target = [&](int i) {
       return a.targets64 ? ((const int64_t *)a.targets)[i] : (int64_t)((const int32_t *)a.targets)[i];
     };
-    for (int i0 = 0; i0 < CE_FUSE; i0 += 256) {
-      if (i0 >= a.T) {
-        if (lane == 0) flags[(i0 + threadIdx.x) / 32] = 0;
-        continue;
-      }
-      const int i = i0 + threadIdx.x;
-      const int64_t id = i < a.T ? target(i) : a.ignore_index;
-      const bool in = id >= 0 && id < a.V;
-      if (!in && id != a.ignore_index) record_status(status, STATUS_BAD_TARGET);
-      const unsigned vote = __ballot_sync(FULL_MASK, in && id != a.ignore_index && i < a.T);
+    constexpr int M = CE_FUSE / 256;
+    int64_t id[M];  // all loads in flight
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int i = j * 256 + threadIdx.x;
+      id[j] = i < a.T ? target(i) : a.ignore_index;
+    }
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int i = j * 256 + threadIdx.x;
+      const bool in = id[j] >= 0 && id[j] < a.V;
+      if (!in && id[j] != a.ignore_index) record_status(status, STATUS_BAD_TARGET);
+      const unsigned vote = __ballot_sync(FULL_MASK, in && id[j] != a.ignore_index && i < a.T);
       if (lane == 0) flags[i / 32] = vote;
     }
     __syncthreads();
