@@ -722,13 +722,14 @@ enum moe_linear_ce_call { MOE_CE_LOSS = 1, MOE_CE_GRAD = 2, MOE_CE_STEP = 3 };
  *   loss_t = lse_t - x_t[target_t] + z_loss * lse_t^2
  *
  * The logits live in tensor memory (MOE_BF16) or registers only: a tile of
- * them leaves a maximum and a sum of exponentials for each row and 64 of its columns.
- * Rows whose target is ignore_index (prompts, padding) are left out: they are
- * not read, their loss and lse are 0.  A target outside [0, V) that is not
- * ignore_index is left out the same way and recorded (code 7).  Logits that
- * are not finite give a loss that is not.  Products are exact, sums FP32, in
- * an order set by D, V and the type alone; a row's loss and lse do not depend
- * on T, on the other rows or on how many of them are left out.
+ * them leaves a maximum and a sum of exponentials for each row and 64 of its
+ * columns.  Rows whose target is ignore_index (prompts, padding) are left out:
+ * they are not read, their loss and lse are 0.  A target outside [0, V) that
+ * is not ignore_index is left out the same way and recorded (code 7).  Logits
+ * that are not finite give a loss that is not.  Products are exact, sums FP32,
+ * in an order set by D, V and the type alone; a row's loss and lse do not
+ * depend on T, on the other rows or on how many of them are left out.
+ * Workspace: as for the gradient, below.
  */
 int moe_linear_ce(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
 
@@ -739,22 +740,27 @@ int moe_linear_ce(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void
  *   dhidden = g weight        dweight (+)= g^T hidden
  *
  * The logits are recomputed a piece of the vocabulary at a time; g of one
- * piece is in the workspace, in `dtype` (MOE_BF16: one rounding, as large
- * as that of its two products' other operand), and both products take it from there.
+ * piece is in the workspace, in `dtype`, and both products take it from there.
+ * MOE_BF16: each entry of g is rounded once but the target's, which a factor
+ * of the row makes exact, and that factor is taken out of dhidden in FP32 and
+ * put into the row of hidden that dweight's product reads (rounded once).
  * dhidden of rows that are left out is zero (whatever they hold), as is
- * everything that such a row would add to dweight.  Sums are FP32; dhidden's run over chunks of the vocabulary
- * whose bounds the type alone sets, in order, so that its rows do not depend
- * on the batch; dweight's over the rows in order.  One rounding of each
- * output.  T = 0 (or no row left) zeroes dweight unless `accumulate`.
- * Workspace: moe_linear_ce_workspace_size(a, call) bytes, 256-byte aligned; it goes by
- * T, D, V, the types, ld_weight and weight's alignment to 16 bytes (NULL:
- * aligned; the other buffers need not be set).
+ * everything that such a row would add to dweight.  Sums are FP32; dhidden's
+ * run over chunks of the vocabulary whose bounds the type alone sets, in
+ * order, so that its rows do not depend on the batch; dweight's over the rows
+ * in order.  One rounding of each output.  T = 0 (or no row left) zeroes
+ * dweight unless `accumulate`.  Workspace: moe_linear_ce_workspace_size(a,
+ * call) bytes, 256-byte aligned; it goes by T, D, V, the types, ld_weight and
+ * weight's alignment to 16 bytes (NULL: aligned; the other buffers need not be
+ * set).
  */
 size_t moe_linear_ce_workspace_size(const moe_linear_ce_args_t *a, int32_t call);
 int moe_linear_ce_backward(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
 
 /* moe_linear_ce_step -- loss and gradients in one call, for a dloss that is
- * known beforehand: the values of moe_linear_ce and moe_linear_ce_backward. */
+ * known beforehand: moe_linear_ce's loss and lse, and the gradients from the
+ * statistics themselves (moe_linear_ce_backward has the target's probability
+ * from lse and a dot product of its own; the two differ by that rounding). */
 int moe_linear_ce_step(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
 
 typedef struct moe_grads_args {
@@ -771,22 +777,24 @@ typedef struct moe_grads_args {
 
 /*
  * moe_grad_norm -- norm = sqrt(sum over all tensors and elements of g^2).
- * Squares and short sums in FP32, longer ones in FP64; squares that FP32 cannot hold (|g|
- * above about 1e18 or all below about 1e-15) are taken in FP64, so the norm is right wherever
- * it fits a float.  An infinite or NaN element makes it infinite or NaN.  Fixed order of sums (set by
- * the sizes, the order of the tensors and the device's number of SMs).  The host
- * arrays are read before the call returns.  Workspace:
- * moe_grad_workspace_size(a) bytes.
+ * Squares and sums of a thousand of them in FP32, longer sums in FP64; where
+ * FP32 squares would lose their bits (some |g| above about 1e13, or all of a
+ * warp's below 1e-12) in FP64 from the start, so the norm is right wherever it
+ * fits a float.  An infinite or NaN element makes it infinite or NaN.  The
+ * order of the sums is fixed (set by the sizes, their order and the device's
+ * number of SMs).  The host arrays are read before the call returns.
+ * Workspace: moe_grad_workspace_size(a) bytes, 256-byte aligned.
  */
 size_t moe_grad_workspace_size(const moe_grads_args_t *a);
 int moe_grad_norm(const moe_grads_args_t *a, void *ws, size_t ws_bytes, void *stream);
 
 /*
- * moe_grad_clip -- the norm, then out_i = in_i * c, c = min(1, max_norm / (norm + eps)),
- * one rounding.  Tensors that are their own output are not touched where c
- * is 1.  A norm that is not finite goes the way of the arithmetic: infinite gives c = 0
- * (and NaN where the element is infinite), NaN gives NaN.  Outputs may not overlap one
- * another, nor inputs other than their own: MOE_ERR_INVALID_ARG where ranges do.
+ * moe_grad_clip -- the norm, then out_i = in_i * c, c = min(1, max_norm /
+ * (norm + eps)), one rounding.  Tensors that are their own output are not
+ * touched where c is 1.  A norm that is not finite goes the way of the
+ * arithmetic: infinite gives c = 0 (and NaN where the element is infinite), NaN
+ * gives NaN.  Outputs may not overlap one another, nor inputs other than their
+ * own whole one: MOE_ERR_INVALID_ARG where ranges do.
  */
 int moe_grad_clip(const moe_grads_args_t *a, void *ws, size_t ws_bytes, void *stream);
 

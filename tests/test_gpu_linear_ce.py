@@ -213,6 +213,48 @@ def test_infinities_and_nan_stay_in_their_rows():
     assert not torch.isfinite(dh[~rest]).all(1).any()
 
 
+@pytest.mark.parametrize("dtype,D,pad,shift", [(B, 64, 16, 0), (B, 64, 8, 1), (B, 77, 3, 2), (F, 60, 4, 1)])
+def test_dhidden_between_others_bytes(dtype, D, pad, shift):
+    """Through the C entry points: rows with a stride, off any wide boundary; what lies between them stays."""
+    from top_routed_grouped_gb300 import train
+    T, V = 70, 300
+    h, w, t, d = make(T, D, V, dtype, left_out=9)
+    _, lse = moe.linear_cross_entropy(h, w, t)
+    want = moe.linear_cross_entropy_backward(d, lse, h, w, t)
+    rows = torch.full((T * (D + pad) + shift,), 5.0, device="cuda", dtype=dtype)
+    dw = torch.empty_like(w)
+    code = 0 if dtype is F else 1
+    args = train._CE.pack(T, D, V, code, code, 0, 1, 1.0, 0.0, 0, -100, 0, 0, D + pad, h.data_ptr(), w.data_ptr(),
+                          t.data_ptr(), d.data_ptr(), 0, lse.data_ptr(), rows.data_ptr() + shift * rows.element_size(),
+                          dw.data_ptr())
+    n = train.moe_linear_ce_workspace_size(args, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    train.moe_linear_ce_backward(args, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    view = rows[shift:].view(T, D + pad)
+    assert torch.equal(view[:, :D], want[0]) and torch.equal(dw, want[1])
+    assert bool((view[:, D:] == 5).all()) and bool((rows[:shift] == 5).all())
+
+
+@pytest.mark.parametrize("D", [64, 72, 77])
+def test_dweight_off_any_boundary(D):
+    """A gradient that starts between 16-byte boundaries takes another path to memory."""
+    from top_routed_grouped_gb300 import train
+    T, V = 70, 300
+    h, w, t, d = make(T, D, V, B)
+    for dtype, accumulate in ((B, 0), (F, 0), (F, 1)):
+        flat = torch.full((V * D + 6,), 5.0, device="cuda", dtype=dtype)
+        want = moe.linear_cross_entropy_step(h, w, t, d, dweight_dtype=dtype)[2]
+        dh, loss = torch.empty_like(h), torch.empty(T, device="cuda")
+        args = train._CE.pack(T, D, V, 1, 0 if dtype is F else 1, accumulate, 1, 1.0, 0.0, 0, -100, 0, 0, 0, h.data_ptr(),
+                              w.data_ptr(), t.data_ptr(), d.data_ptr(), loss.data_ptr(), 0, dh.data_ptr(),
+                              flat.data_ptr() + 3 * flat.element_size())
+        n = train.moe_linear_ce_workspace_size(args, 3)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        train.moe_linear_ce_step(args, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(flat[3:-3].view(V, D), want + 5 if accumulate else want)
+        assert bool((flat[:3] == 5).all()) and bool((flat[-3:] == 5).all())
+
+
 def test_dloss_of_zero():
     h, w, t, d = make(70, 64, 400, B)
     d[10:20] = 0
