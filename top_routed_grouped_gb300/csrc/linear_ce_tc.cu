@@ -17,14 +17,20 @@
 // Rows of the accumulator are tokens in the first two, so a thread of the
 // epilogue has a row's columns in its own lane and takes maximum and sum
 // without a shuffle.  Two accumulators of 256 columns alternate: an item's
-// epilogue runs under the next item's MMAs.  A stage is one K block of 64: 16
-// KB of A and 16 KB of B a CTA, five to seven stages deep; where a few rows
-// are all there is, a stage has room for those alone (the MMAs read on into
-// B's bytes for rows that nobody looks at) and the ring is up to eleven deep: the bytes in
-// flight are what bounds the reading of the weights then (5 rows x 2048 x
-// 32000: NN us with six stages).  Every output is summed in K
-// blocks of 64 in order, in one accumulator; the tile it falls in does not
-// change that.
+// epilogue runs under the next item's MMAs.  A stage is two K blocks of 64: 32
+// KB of A and 32 KB of B a CTA, three of them; where a few rows are all there
+// is, a stage has room for those alone (the MMAs read on into B's bytes for
+// rows that nobody looks at) and there are five: reading the weights is bound
+// by the bytes in flight then (5 rows x 2048 x 32000: 33.1 us with three, 31.3
+// with five).  Every output is summed in K blocks of 64 in order; the tile it
+// falls in does not change that.
+//
+// What bounds them: the tensor cores.  At 4096 x 2048 x 50257 STATS runs at 1.93
+// PFLOP/s, as cuBLAS does in a burst; a step of 8192 x 2048 x 131072 at 1.72
+// over its four products, as cuBLAS does under the power cap.  Counters at
+// 4096 x 2048 x 24576: the tensor pipe is busy 88 % of STATS, 79 % of LOGITS, 86 % of
+// GRADS.  At few columns of K (1000) the SMs' reads of L2 (64 KB a K block and
+// pair, 13 TB/s in all) share it with g's stores, and LOGITS takes a fifth longer than its MMAs.
 #include <cuda.h>
 
 #include "linear_ce.h"
@@ -37,32 +43,31 @@ using namespace umma;
 
 constexpr int CE_STATS = 0, CE_LOGITS = 1, CE_GRADS = 2;
 constexpr int CT_TILE = 16384;  // a K block of 64: 128 rows of A, or half of B's columns, of a CTA
-// Epilogue warps: eight, half of the columns each, with one (LOGITS) or two
-// staging tiles of 4 KB; for the statistics sixteen with a quarter each, so
-// that a thread's sums over the K chunks (64) stay in registers.  With two
-// tiles and a stage less GRADS at few rows, where the stores of dweight are what it
-// does, does not wait for one store to read its tile before it fills the next.
-constexpr int CT_EPI_FIRST = 4;
-constexpr int GNSTG = 1;
-constexpr int GSUB = 2;
+// Epilogue warps: eight, half of the columns each, with a staging tile of 4 KB;
+// for the statistics sixteen with a quarter each, so that a thread's sums over
+// the K chunks (64) stay in registers.  Stages of two K blocks: one handshake
+// and one commit for eight MMAs (forward 4096 x 2048 x 50257: 527 us with one block,
+// 459 with two; the gradients' products 1620 and 1569; three blocks leave too
+// few stages: 1720).
+constexpr int CT_EPI_FIRST = 4, SUB = 2;
 template <int KIND>
 struct CtCfg {
   static constexpr int EPI_WARPS = KIND == CE_STATS ? 16 : 8;
   static constexpr int THREADS = 32 * (CT_EPI_FIRST + EPI_WARPS);
-  static constexpr int NSTG = KIND == CE_STATS ? 0 : KIND == CE_GRADS ? GNSTG : 1;
-  static constexpr int SUB = KIND == CE_GRADS ? GSUB : 2;  // K blocks a stage
-  static constexpr int RING = (7 - NSTG) * 2 * CT_TILE;  // bytes of the stages
-  static constexpr int SMEM = 1024 + RING + EPI_WARPS * NSTG * 4096 + 512;
-  static_assert(SMEM <= 232448 && NSTG * EPI_WARPS * 4096 <= NSTG * 2 * CT_TILE, "shared memory of a CTA");
+  static constexpr int STG_BYTES = KIND == CE_STATS ? 0 : EPI_WARPS * 4096;
+  static constexpr int RING = 7 * 2 * CT_TILE - STG_BYTES;  // bytes of the stages
+  static constexpr int SMEM = 1024 + RING + STG_BYTES + 512;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 constexpr int CT_PREFETCH = 8;  // K blocks (none: 33.3 us at 5 rows x 2048 x 32000, 8 or 16: 31.3, 32: 35.5)
-constexpr int CT_MAX_STAGES = 11;
-constexpr uint32_t CT_HINT = 100000;
+constexpr int CT_MAX_STAGES = 5;
+constexpr uint32_t CT_HINT = 100000;  // ns
 constexpr uint32_t CT_TMEM_COLS = 512;
 // The statistics' products are summed in chunks of 1024 of K, each in an
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
-// cut each of their sums off instead of rounding it, which shows in a float
-// loss as 1.2e-6 of it at K = 2048 in one chain and 3e-7 in chunks.
+// cut each of their sums off instead of rounding it, which leaves a float
+// loss 1.0e-6 off at K = 2048 in one chain and 5e-7 in chunks of 1024 (2.4e-7
+// in chunks of 512, which cost 3 % more time).
 constexpr int CT_KCHUNK = 16;  // a multiple of SUB
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
@@ -429,7 +434,7 @@ __device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uin
 
 // v: the tile's values (zero where no row counts: then there is no accumulator).
 __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row0,
-                                        int half, uint8_t *stg2, int lane, uint64_t out_policy) {
+                                        int half, uint8_t *stg, int lane, uint64_t out_policy) {
   const int wcols = im.cols / 2, col0 = im.n0 + half * wcols;  // row0: row of dweight
   if (row0 >= p.V) return;
   for (int c = 0; c < wcols && col0 + c < p.D; c += p.gf32 || !p.dw_tma ? 32 : 64) {
@@ -443,8 +448,7 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
       tmem_ld32x2(taddr + c, taddr + c + 32, v[0], v[1]);
     }
     if (p.dw_tma) {
-      uint8_t *stg = stg2 + (GNSTG == 2 && (c / 32 & (p.gf32 ? 1 : 2)) ? 4096 : 0);  // the two tiles in turn
-      if (lane == 0) bulk_wait_read<GNSTG - 1>();  // the store before the last has read its tile
+      if (lane == 0) bulk_wait_read<0>();  // the last store has read the tile
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -472,7 +476,7 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
         bulk_commit();
       }
     } else {
-      by_rows(stg2, v[0], lane, [&](int r, int cc, float4 x) {
+      by_rows(stg, v[0], lane, [&](int r, int cc, float4 x) {
         const int row = row0 + r, col = col0 + c + cc;
         if (row >= p.V) return;
         const float e[4] = {x.x, x.y, x.z, x.w};
@@ -495,11 +499,11 @@ __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, c
 template <int KIND>
 __global__ void __launch_bounds__(CtCfg<KIND>::THREADS, 1)
 ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtParams p) {
-  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS, NSTG = CtCfg<KIND>::NSTG, SUB = CtCfg<KIND>::SUB;
+  constexpr int EPI_WARPS = CtCfg<KIND>::EPI_WARPS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *epi = base + CtCfg<KIND>::RING;
-  uint64_t *bars = (uint64_t *)(epi + EPI_WARPS * NSTG * 4096);
+  uint64_t *bars = (uint64_t *)(epi + CtCfg<KIND>::STG_BYTES);
   uint64_t *full = bars, *empty = full + CT_MAX_STAGES;
   uint64_t *tfull = empty + CT_MAX_STAGES, *tempty = tfull + 2, *mma_done = tempty + 2;
   uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
@@ -684,7 +688,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   } else if (warp >= CT_EPI_FIRST) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;  // TMEM lane quarter; which of the columns
-    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * NSTG * 4096;
+    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * 4096;
     const uint32_t tempty_leader0 = mapa_shared(&tempty[0], 0);
     const uint64_t out_policy = policy_evict_first();  // dweight is written once and not read again
     uint32_t cnt = 0;
