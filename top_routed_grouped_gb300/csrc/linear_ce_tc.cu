@@ -63,12 +63,13 @@ constexpr int CT_PREFETCH = 8;  // K blocks (none: 33.3 us at 5 rows x 2048 x 32
 constexpr int CT_MAX_STAGES = 5;
 constexpr uint32_t CT_HINT = 100000;  // ns
 constexpr uint32_t CT_TMEM_COLS = 512;
-// The statistics' products are summed in chunks of 1024 of K, each in an
+// The statistics' products are summed in chunks of 512 of K, each in an
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
-// cut each of their sums off instead of rounding it, which leaves a float
-// loss 1.0e-6 off at K = 2048 in one chain and 5e-7 in chunks of 1024 (2.4e-7
-// in chunks of 512, which cost 3 % more time).
-constexpr int CT_KCHUNK = 16;  // a multiple of SUB
+// cut each of their sums off instead of rounding it, which leaves a loss
+// 1.0e-6 off at K = 2048 in one chain, 5e-7 in chunks of 1024 and 2.4e-7 in
+// chunks of 512 (1.1e-7 in 256; a rounded FP32 product of the kind that keeps
+// its logits: 4.6e-7).  512 takes 2 to 3 % more time than 1024, 256 six more.
+constexpr int CT_KCHUNK = 8;   // a multiple of SUB
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
