@@ -729,7 +729,8 @@ enum moe_linear_ce_call { MOE_CE_LOSS = 1, MOE_CE_GRAD = 2, MOE_CE_STEP = 3 };
  * that are not finite give a loss that is not.  Products are exact, sums FP32,
  * in an order set by D, V and the type alone; a row's loss and lse do not
  * depend on T, on the other rows or on how many of them are left out.
- * Workspace: as for the gradient, below.
+ * MOE_BF16 weights whose rows do not all start on 16-byte boundaries are first
+ * copied to where they do.  Workspace: as for the gradient, below.
  */
 int moe_linear_ce(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
 

@@ -128,6 +128,7 @@ def test_clip_refusals(L, ranges, out, kw):  # noqa: F811
 def test_tensors_on_the_host_are_refused():
     t = torch.zeros(3, 4)
     for f in (lambda: moe.linear_cross_entropy(t, t, torch.zeros(3, dtype=torch.int64)), lambda: moe.grad_norm([t]),
-              lambda: moe.clip_grads([t], 1.0), lambda: moe.scale_grads([t], torch.ones(()), 1.0)):
+              lambda: moe.clip_grads([t], 1.0), lambda: moe.scale_grads([t], torch.ones(()), 1.0),
+              lambda: moe.grad_norm([None]), lambda: moe.clip_grads([1.0], 1.0)):
         with pytest.raises(ValueError):
             f()

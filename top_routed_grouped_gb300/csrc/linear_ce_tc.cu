@@ -75,7 +75,7 @@ constexpr float CE_LOG2E = 1.44269504088896340736f;
 struct CtMaps {
   CUtensorMap h, w, g;     // K-major tiles: boxes of 128 rows x 64
   CUtensorMap h32, w32;    // the same rows, 32 at a time
-  CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64, two blocks of columns at once (wt: one where D is no multiple of 64)
+  CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64, two blocks of columns at once
   CUtensorMap ht1, wt1;    // one block of columns
   CUtensorMap gout;        // 32 rows x 64: g's stores
   CUtensorMap dw;          // dweight: 32 rows x 128 bytes
@@ -90,7 +90,6 @@ struct CtParams {
   float s2;  // scale * log2(e)
   float2 *part;
   float *xt;
-  int nparts;
   int v0, n, chunk, nchunks;  // the piece
   bool first, last;
   bool w_blocks, dw_tma, accumulate, gf32, dh_wide;
@@ -124,7 +123,7 @@ template <int KIND>
 struct CtWork {
   int count, mt, kd, kr;
   int it, end;                   // logits: the pair's next unit or tile, and the last one's end
-  int step, nt, cols;
+  int nt, cols;
   int nl, ns, heavy, extra, delta, pair, pairs;  // gradients: longer items, shorter ones
   bool long_dw;
   bool run;
@@ -433,7 +432,7 @@ __device__ inline void dhidden_epilogue(const CtParams &p, const CtItem &im, uin
   }
 }
 
-// v: the tile's values (zero where no row counts: then there is no accumulator).
+// Where no row counts there is no accumulator, and the values are zero.
 __device__ inline void dweight_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row0,
                                         int half, uint8_t *stg, int lane, uint64_t out_policy) {
   const int wcols = im.cols / 2, col0 = im.n0 + half * wcols;  // row0: row of dweight
@@ -800,7 +799,6 @@ static CtParams params(const CeMats &m) {
   p.s2 = m.scale * CE_LOG2E;
   p.part = m.part;
   p.xt = m.xt;
-  p.nparts = (int)ceil_div(m.V, CE_PART);
   p.n = m.V;
   p.ldh = m.ldh;
   p.status = m.status;

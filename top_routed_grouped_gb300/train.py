@@ -164,10 +164,17 @@ def _grads(stream, grads, out, norm, max_norm, eps, ws, mode):
     return norm
 
 
+def _listed(ts, name: str) -> list:
+    ts = list(ts)
+    if ts and not isinstance(ts[0], torch.Tensor):
+        raise ValueError(f"{name}: tensors expected, got {type(ts[0]).__name__}")
+    return ts
+
+
 def grad_norm(grads, ws=None, stream=None):
     """The 2-norm over all elements of ``grads`` (tensors of float32 or
     bfloat16 on one device, in any gapless order), a float32 scalar there."""
-    grads = list(grads)
+    grads = _listed(grads, "grads")
     if not grads:
         return torch.zeros((), dtype=torch.float32, device="cuda")
     return _on(grads[0], stream, _grads, grads, None, None, 0.0, 0.0, ws, 1)
@@ -178,7 +185,7 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, ws=None, str
     that they had.  In place, or into ``out``: as many tensors of the same
     sizes, of float32 or bfloat16 (accumulated float32 gradients become their
     parameters' type this way)."""
-    grads, out = list(grads), None if out is None else list(out)
+    grads, out = _listed(grads, "grads"), None if out is None else _listed(out, "out")
     if not grads:
         return grad_norm(grads)
     return _on(grads[0], stream, _grads, grads, out, None, max_norm, eps, ws, 3)
@@ -187,6 +194,6 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, ws=None, str
 def scale_grads(grads, norm, max_norm: float, eps: float = 1e-6, out=None, stream=None) -> None:
     """``clip_grads`` for a norm [1] float32 that is on the device already: one
     put together from the norms of several ranks, say."""
-    grads, out = list(grads), None if out is None else list(out)
+    grads, out = _listed(grads, "grads"), None if out is None else _listed(out, "out")
     if grads:
         _on(grads[0], stream, _grads, grads, out, norm, max_norm, eps, None, 2)
