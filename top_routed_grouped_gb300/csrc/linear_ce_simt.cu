@@ -65,17 +65,15 @@ struct Operand {
   }
 };
 
+// Tile (bx, by) of a product, for dhidden of chunk bz.  sA, sB: two buffers each.
 template <int KIND, int S>
-__global__ void __launch_bounds__(256, S == 2 ? 2 : 4)
-ce_simt_kernel(const SimtParams a) {
-  griddep_launch();
-  griddep_wait();
+__device__ inline void simt_tile(const SimtParams &a, float (*sA)[SK][64 * S + 4], float (*sB)[SK][64 * S + 4], int bx,
+                                 int by, int bz) {
   const CeMats &m = a.m;
   const CePiece &pc = a.p;
   constexpr int ST = 64 * S, RT = 4 * S;
-  __shared__ float sA[2][SK][ST + 4], sB[2][SK][ST + 4];
   const int count = *m.count;
-  const int r0 = blockIdx.x * ST, c0 = blockIdx.y * ST;  // the tile's rows and columns
+  const int r0 = bx * ST, c0 = by * ST;  // the tile's rows and columns
   if (KIND != SM_DW && r0 >= (KIND == SM_LOGITS ? (int)round_up(count, CE_ROWS) : count)) return;
   const float *h = (const float *)m.h, *w = (const float *)m.w, *g = (const float *)m.g;
   const bool ww = m.ldw % 4 == 0 && ((uintptr_t)m.w & 15) == 0;
@@ -90,7 +88,7 @@ ce_simt_kernel(const SimtParams a) {
     A.p = h + r0 * m.ldh; A.ld = m.ldh; A.rows = m.tpad - r0;
     B.p = w + (v0 + c0) * m.ldw; B.ld = m.ldw; B.rows = m.V - v0 - c0; B.wide = ww;
   } else if (KIND == SM_DH) {
-    const int ch = blockIdx.z * pc.chunk;
+    const int ch = bz * pc.chunk;
     k = min(pc.chunk, pc.n - ch);
     A.p = g + r0 * m.ldg + ch; A.ld = m.ldg; A.rows = m.tpad - r0;
     B.p = w + (v0 + ch) * m.ldw + c0; B.ld = m.ldw; B.rows = m.D - c0; B.wide = ww;
@@ -172,7 +170,7 @@ ce_simt_kernel(const SimtParams a) {
 #pragma unroll
         for (int j = 4 * hf; j < 4 * hf + 4; ++j) s += exp2f(acc[i][j] - ref);
         for (int d = 8; d; d >>= 1) s += __shfl_xor_sync(FULL_MASK, s, d);
-        const int part = blockIdx.y * S + hf;
+        const int part = by * S + hf;
         if (tx == 0 && part < a.nparts) m.part[(int64_t)part * m.tpad + row] = make_float2(big, s);
       }
     }
@@ -206,7 +204,7 @@ ce_simt_kernel(const SimtParams a) {
         if (c >= m.D) continue;
         const int64_t at = row * m.ldh + c;
         if (m.planes) {
-          m.planes[(int64_t)blockIdx.z * m.tpad * m.ldh + at] = acc[i][j];
+          m.planes[(int64_t)bz * m.tpad * m.ldh + at] = acc[i][j];
           continue;
         }
         const float x = pc.first ? acc[i][j] : m.acc[at] + acc[i][j];
@@ -230,12 +228,36 @@ ce_simt_kernel(const SimtParams a) {
   }
 }
 
-// rows x cols outputs (z of them); the larger tiles where they fill the SMs twice.
+// The logits' products: a grid of tiles.
+template <int KIND, int S>
+__global__ void __launch_bounds__(256, S == 2 ? 2 : 4) ce_simt_kernel(const SimtParams a) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float sA[2][SK][64 * S + 4], sB[2][SK][64 * S + 4];
+  simt_tile<KIND, S>(a, sA, sB, blockIdx.x, blockIdx.y, 0);
+}
+
+// Both products of g, side by side in one launch (they have little more than a
+// wave of tiles each at the sizes that float models have): dhidden's tiles,
+// rows fastest, then dweight's.
+template <int S>
+__global__ void __launch_bounds__(256, S == 2 ? 2 : 4) ce_simt_grads_kernel(const SimtParams a, int mt, int nt, int ndh, int vt) {
+  griddep_launch();
+  griddep_wait();
+  __shared__ float sA[2][SK][64 * S + 4], sB[2][SK][64 * S + 4];
+  const int i = blockIdx.x;
+  if (i < ndh) simt_tile<SM_DH, S>(a, sA, sB, i % mt, i / mt % nt, i / mt / nt);
+  else simt_tile<SM_DW, S>(a, sA, sB, (i - ndh) % vt, (i - ndh) / vt, 0);
+}
+
+// Whether tiles of 128 x 128 fill the SMs twice.
+static bool large(int64_t tiles) { return tiles >= 2 * device_sms(); }
+
 template <int KIND>
-static cudaError_t launch(const CeMats &m, const CePiece &p, int64_t rows, int64_t cols, int z, cudaStream_t stream) {
+static cudaError_t launch(const CeMats &m, const CePiece &p, int64_t rows, int64_t cols, cudaStream_t stream) {
   SimtParams a = {m, p, (int)ceil_div(m.V, CE_PART)};
-  auto grid = [&](int t) { return dim3((unsigned)ceil_div(rows, t), (unsigned)ceil_div(cols, t), z); };
-  if (ceil_div(rows, 128) * ceil_div(cols, 128) * z >= 2 * device_sms())
+  auto grid = [&](int t) { return dim3((unsigned)ceil_div(rows, t), (unsigned)ceil_div(cols, t)); };
+  if (large(ceil_div(rows, 128) * ceil_div(cols, 128)))
     return launch_pdl(ce_simt_kernel<KIND, 2>, grid(128), dim3(256), 0, stream, a);
   return launch_pdl(ce_simt_kernel<KIND, 1>, grid(64), dim3(256), 0, stream, a);
 }
@@ -243,17 +265,27 @@ static cudaError_t launch(const CeMats &m, const CePiece &p, int64_t rows, int64
 cudaError_t ce_simt_stats(const CeMats &m, cudaStream_t stream) {
   CePiece p = {};
   p.n = m.V;
-  return launch<SM_STATS>(m, p, m.tpad, m.V, 1, stream);
+  return launch<SM_STATS>(m, p, m.tpad, m.V, stream);
 }
 
 cudaError_t ce_simt_logits_grad(const CeMats &m, const CePiece &p, cudaStream_t stream) {
-  return launch<SM_LOGITS>(m, p, m.tpad, p.n, 1, stream);
+  return launch<SM_LOGITS>(m, p, m.tpad, p.n, stream);
 }
 
 cudaError_t ce_simt_grads(const CeMats &m, const CePiece &p, cudaStream_t stream) {
-  cudaError_t e = launch<SM_DH>(m, p, m.tpad, m.D, p.nchunks, stream);
-  if (e != cudaSuccess) return e;
-  return launch<SM_DW>(m, p, p.n, m.D, 1, stream);
+  SimtParams a = {m, p, (int)ceil_div(m.V, CE_PART)};
+  auto tiles = [&](int t, int &mt, int &nt, int &ndh, int &vt) {
+    mt = (int)ceil_div(m.tpad, t);
+    nt = (int)ceil_div(m.D, t);
+    ndh = mt * nt * p.nchunks;
+    vt = (int)ceil_div(p.n, t);
+    return (unsigned)(ndh + vt * nt);
+  };
+  int mt, nt, ndh, vt;
+  unsigned n = tiles(128, mt, nt, ndh, vt);
+  if (large(n)) return launch_pdl(ce_simt_grads_kernel<2>, dim3(n), dim3(256), 0, stream, a, mt, nt, ndh, vt);
+  n = tiles(64, mt, nt, ndh, vt);
+  return launch_pdl(ce_simt_grads_kernel<1>, dim3(n), dim3(256), 0, stream, a, mt, nt, ndh, vt);
 }
 
 }  // namespace moe
