@@ -54,7 +54,8 @@ def test_sizes(T, D, V, dtype):
     all_ok(*make(T, D, V, dtype))
 
 
-@pytest.mark.parametrize("T,D,V", [(4097, 64, 20000), (5600, 136, 17000), (130, 1032, 40000), (2049, 1000, 9000)])
+@pytest.mark.parametrize("T,D,V", [(4097, 64, 20000), (5600, 136, 17000), (130, 1032, 40000), (2049, 1000, 9000),
+                                   (20011, 72, 8300)])
 def test_larger_sizes(T, D, V):
     all_ok(*make(T, D, V, B, left_out=T // 3))
 
@@ -340,6 +341,24 @@ def test_workspaces_and_streams():
         moe.linear_cross_entropy(h, w, t, ws=ws.cpu())
     with pytest.raises(ValueError):
         moe.linear_cross_entropy(h, w, t, ws=ws[::2])
+
+
+def test_calls_one_after_another_in_one_workspace():
+    """Kernels start while those before them finish: calls of different sizes, types and numbers of
+    rows, through one workspace and without a pause, see nothing of one another."""
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    cases = [make(T, D, V, dtype, seed=i, left_out=left) for i, (T, D, V, dtype, left) in enumerate(
+        [(300, 200, 9000, B, 20), (5, 64, 100, F, 0), (5000, 64, 3000, B, 4000), (1, 8, 20000, B, 0), (700, 72, 500, F, 100),
+         (64, 512, 17000, B, 63)])]
+    want = [moe.linear_cross_entropy_step(*c) for c in cases]
+    torch.cuda.synchronize()
+    got = [moe.linear_cross_entropy_step(*cases[i], ws=ws) for _ in range(6) for i in range(6)]
+    losses = [moe.linear_cross_entropy(*cases[i % 6][:3], ws=ws)[0] for i in range(30)]
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 6])), i
+    for i, loss in enumerate(losses):
+        assert torch.equal(loss, want[i % 6][0]), i
+    assert status() == 0
 
 
 @pytest.mark.parametrize("dtype", [F, B])
