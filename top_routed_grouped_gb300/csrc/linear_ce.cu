@@ -12,6 +12,11 @@
 // gradient recomputes the logits a piece of the vocabulary at a time (2 TDV of
 // the 8 TDV operations, where keeping them would take 4 TV bytes) and takes
 // both products of the piece while it is near L2's size.
+//
+// The kernels here move little and are bound by latency, at large sizes by
+// memory: 5 rows x 2048 x 32000 spend 9 of their 31 us in them and in starts; 4096 x 2048
+// rows are copied in 13 us, their statistics over 24576 columns joined in 21
+// and the planes of three chunks added in 26 (under ncu, from a cold L2).
 #include <math.h>
 
 #include "linear_ce.h"
@@ -21,8 +26,8 @@ namespace moe {
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
 
 // ------------------------------------------------------------- which rows count
-// One CTA, for more than CE_FUSE rows: place[t] is row t's place among those that count (-1: left out),
-// row_of the reverse; the order is kept.  T reads of 4 or 8 bytes: latency.
+// One CTA, for more than CE_FUSE rows: place[t] is row t's place among those
+// that count (-1: left out), row_of the reverse; the order is kept.
 template <typename Id>
 __global__ void __launch_bounds__(1024)
 ce_places_kernel(int T, int V, int64_t ignore, const Id *targets, int *count, int *row_of, int *place, CeRow *rows,
