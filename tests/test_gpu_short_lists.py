@@ -1,0 +1,21 @@
+"""Norms of lists so short that most CTAs of a cluster have nothing to read: they
+meet the one that adds up before they write to it."""
+import pytest
+import torch
+
+import top_routed_grouped_gb300 as moe
+from test_gpu_grads import NORM_TOL, make, near, norm64
+
+pytestmark = pytest.mark.gpu
+F, B = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("sizes", [[1], [3], [8192], [8193], [1, 1], [5000, 1, 7], [8192] * 9], ids=str)
+@pytest.mark.parametrize("dtype", [F, B])
+def test_many_short_lists_one_after_another(sizes, dtype):
+    ts = make(sizes, (dtype,))
+    want = norm64(ts)
+    norms = [moe.grad_norm(ts) for _ in range(300)]
+    clips = [moe.clip_grads(ts, 2 * want + 1) for _ in range(100)]
+    near(norms[0], want, NORM_TOL)
+    assert all(torch.equal(n, norms[0]) for n in norms + clips)

@@ -140,6 +140,7 @@ __device__ inline void run_of(int total, int &c0, int &c1) {
 template <int CAP>
 __global__ void __launch_bounds__(GN_THREADS)
 grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, double *part) {
+  umma::cluster_meet_arrive();
   griddep_launch();
   int c0, c1;
   run_of(t.first[t.n], c0, c1);
@@ -156,6 +157,7 @@ grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, double *part) {
   constexpr int WARPS = GN_THREADS / 32;
   __shared__ double of_cluster[GN_CLUSTER * WARPS];
   const uint32_t rank = umma::cluster_ctarank();
+  umma::cluster_meet_wait();  // the first CTA runs: its shared memory is there to be written (behind the reads at no cost)
   if ((threadIdx.x & 31) == 0)
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
                      umma::mapa_shared(&of_cluster[rank * WARPS + (threadIdx.x >> 5)], 0)),

@@ -320,6 +320,10 @@ __device__ inline uint32_t cluster_ctarank() {
 __device__ inline void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// The same in two halves, to meet without waiting: all CTAs of the cluster run
+// behind cluster_meet_wait.  Orders no memory.
+__device__ inline void cluster_meet_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ inline void cluster_meet_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 // Address of the same shared-memory location in CTA `rank` of the cluster.
 __device__ inline uint32_t mapa_shared(const void *p, uint32_t rank) {
   uint32_t r;
