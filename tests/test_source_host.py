@@ -41,3 +41,14 @@ def test_clusters_meet_before_remote_stores(path):
         if store >= 0:
             meet = [body.find(s) for s in ("cluster_sync()", "cluster_meet_wait()") if s in body[:store]]
             assert meet, f"{name}: a remote store before the cluster is known to run"
+
+
+@pytest.mark.parametrize("path", FILES, ids=os.path.basename)
+def test_no_load_may_pass_the_wait_for_the_kernel_before(path):
+    """Kernels start while the one before them runs.  A load through the read-only
+    path, or one that the compiler takes for a pure function of its address, may be
+    moved above the wait and read what is not written yet."""
+    found = re.findall(r"__ld(?:g|cs|cg|ca|lu|cv)\b|\bld\.global\.(?:\w+\.)*nc\b|__restrict__|\b__constant__", source(path))
+    assert not found, found
+    for m in re.finditer(r"asm\s+(volatile)?[^;]*?\bld\.global\b", source(path)):
+        assert m.group(1), "a load that is not volatile"

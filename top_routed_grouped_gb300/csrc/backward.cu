@@ -32,10 +32,10 @@ namespace moe {
 // ---------------------------------------------------------------- b1
 template <typename TE>
 __global__ void __launch_bounds__(256)
-combine_bwd_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE *__restrict__ yr,
-                   const TE *__restrict__ ys, const float *__restrict__ w, const float *__restrict__ sig,
-                   const int32_t *__restrict__ route_pos, TE *__restrict__ dyr_sorted, TE *__restrict__ dys,
-                   float *__restrict__ dlogit, float *__restrict__ dz, int yr_sorted) {
+combine_bwd_kernel(int T, int H, int k, const TE *dy, const TE *yr,
+                   const TE *ys, const float *w, const float *sig,
+                   const int32_t *route_pos, TE *dyr_sorted, TE *dys,
+                   float *dlogit, float *dz, int yr_sorted) {
   griddep_launch();
   griddep_wait();
   constexpr int VN = Vec16<TE>::N;
@@ -103,10 +103,10 @@ combine_bwd_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE *__r
 // and store is the one above in the same order: the results are identical.
 template <typename TE, int NCH, int KMAX>
 __global__ void __launch_bounds__(128)
-combine_bwd_rows_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE *__restrict__ yr,
-                        const TE *__restrict__ ys, const float *__restrict__ w, const float *__restrict__ sig,
-                        const int32_t *__restrict__ route_pos, TE *__restrict__ dyr_sorted, TE *__restrict__ dys,
-                        float *__restrict__ dlogit, float *__restrict__ dz, int yr_sorted) {
+combine_bwd_rows_kernel(int T, int H, int k, const TE *dy, const TE *yr,
+                        const TE *ys, const float *w, const float *sig,
+                        const int32_t *route_pos, TE *dyr_sorted, TE *dys,
+                        float *dlogit, float *dz, int yr_sorted) {
   griddep_launch();
   griddep_wait();
   constexpr int VN = Vec16<TE>::N;
@@ -116,16 +116,16 @@ combine_bwd_rows_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE
   const TE *dyr = dy + t * H + lane * VN;
   uint4 a[NCH];
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) a[i] = __ldg((const uint4 *)(dyr + i * 32 * VN));
+  for (int i = 0; i < NCH; ++i) a[i] = ld_plain((const uint4 *)(dyr + i * 32 * VN));
   float dws[KMAX];
 #pragma unroll
   for (int s = 0; s < KMAX; ++s) {
     dws[s] = 0.f;
     if (s < k) {
-      const TE *row = yr + (yr_sorted ? (int64_t)__ldg(route_pos + t * k + s) : t * k + s) * H + lane * VN;
+      const TE *row = yr + (yr_sorted ? (int64_t)ld_plain(route_pos + t * k + s) : t * k + s) * H + lane * VN;
       uint4 b[NCH];
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) b[i] = __ldg((const uint4 *)(row + i * 32 * VN));
+      for (int i = 0; i < NCH; ++i) b[i] = ld_plain((const uint4 *)(row + i * 32 * VN));
       float part = 0.f;
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
@@ -144,7 +144,7 @@ combine_bwd_rows_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE
   {
     uint4 b[NCH];
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) b[i] = __ldg((const uint4 *)(ys + t * H + lane * VN + i * 32 * VN));
+    for (int i = 0; i < NCH; ++i) b[i] = ld_plain((const uint4 *)(ys + t * H + lane * VN + i * 32 * VN));
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       float av[VN], bv[VN];
@@ -161,7 +161,7 @@ combine_bwd_rows_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE
   float wdw = 0.f;
 #pragma unroll
   for (int s = 0; s < KMAX; ++s) {
-    wv[s] = s < k ? __ldg(w + t * k + s) : 0.f;
+    wv[s] = s < k ? ld_plain(w + t * k + s) : 0.f;
     if (s < k) wdw = fmaf(wv[s], dws[s], wdw);
   }
   if (lane < k) {
@@ -171,12 +171,12 @@ combine_bwd_rows_kernel(int T, int H, int k, const TE *__restrict__ dy, const TE
       if (s == lane) dwl = dws[s], wl = wv[s];
     dlogit[t * k + lane] = wl * (dwl - wdw);
   }
-  const float g = __ldg(sig + t);
+  const float g = ld_plain(sig + t);
   if (lane == 0) dz[t] = ps * g * (1.f - g);
   // scaled rows
   int pos[KMAX];
 #pragma unroll
-  for (int s = 0; s < KMAX; ++s) pos[s] = s < k ? __ldg(route_pos + t * k + s) : 0;
+  for (int s = 0; s < KMAX; ++s) pos[s] = s < k ? ld_plain(route_pos + t * k + s) : 0;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int h = lane * VN + i * 32 * VN;
@@ -264,7 +264,7 @@ __device__ inline BwTile bw_decode(int ti, int E, int T, const int32_t *tile_sta
 // dGU[j] = [dh u silu'(g) | dh silu(g)] from the saved [g | u] of row j.
 template <typename TE>
 __global__ void __launch_bounds__(256)
-down_dgrad_swiglu_kernel(BwArgs a, const int32_t *__restrict__ tile_start) {
+down_dgrad_swiglu_kernel(BwArgs a, const int32_t *tile_start) {
   griddep_launch();
   griddep_wait();
   __shared__ float ds[32][BW_BM + 1];   // [h][row]
@@ -328,7 +328,7 @@ down_dgrad_swiglu_kernel(BwArgs a, const int32_t *__restrict__ tile_start) {
 // dXr[j, h] = sum_f dGU[j, f] Wgu[e][f, h] (f ascending), FP32 rows.
 template <typename TE>
 __global__ void __launch_bounds__(256)
-gate_up_dgrad_kernel(BwArgs a, const int32_t *__restrict__ tile_start) {
+gate_up_dgrad_kernel(BwArgs a, const int32_t *tile_start) {
   griddep_launch();
   griddep_wait();
   __shared__ float gs[32][BW_BM + 1];  // [f][row]
@@ -465,7 +465,7 @@ constexpr int RG_CHUNK = 64;
 
 template <typename TE>
 __global__ void __launch_bounds__(256)
-router_gate_partial_kernel(BwArgs a, const int32_t *__restrict__ chunk_start, float *__restrict__ partial) {
+router_gate_partial_kernel(BwArgs a, const int32_t *chunk_start, float *partial) {
   griddep_launch();
   griddep_wait();
   constexpr int VN = Vec16<TE>::N;  // columns per thread (16 bytes of x)
@@ -509,7 +509,7 @@ router_gate_partial_kernel(BwArgs a, const int32_t *__restrict__ chunk_start, fl
 }
 
 __global__ void __launch_bounds__(256)
-router_gate_reduce_kernel(BwArgs a, const int32_t *__restrict__ chunk_start, const float *__restrict__ partial) {
+router_gate_reduce_kernel(BwArgs a, const int32_t *chunk_start, const float *partial) {
   griddep_launch();
   griddep_wait();
   const int seg = blockIdx.y;

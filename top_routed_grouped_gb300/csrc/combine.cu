@@ -26,9 +26,9 @@ namespace moe {
 // same loads measured +4 µs and are not used).
 template <typename TE, bool SORTED, int KMAX>
 __global__ void __launch_bounds__(256)
-combine_kernel(int T, int H, int k, const TE *__restrict__ yr, const TE *__restrict__ ys,
-               const float *__restrict__ w, const float *__restrict__ sig, TE *__restrict__ y,
-               const int32_t *__restrict__ route_pos, int stream_rows) {
+combine_kernel(int T, int H, int k, const TE *yr, const TE *ys,
+               const float *w, const float *sig, TE *y,
+               const int32_t *route_pos, int stream_rows) {
   griddep_launch();
   griddep_wait();
   constexpr int VN = Vec16<TE>::N;
@@ -45,14 +45,14 @@ combine_kernel(int T, int H, int k, const TE *__restrict__ yr, const TE *__restr
 #pragma unroll
   for (int s = 0; s < KMAX; ++s) {
     if (s < k) {
-      const int64_t row = SORTED ? (int64_t)__ldg(route_pos + t * k + s) : t * k + s;
+      const int64_t row = SORTED ? (int64_t)ld_plain(route_pos + t * k + s) : t * k + s;
       const uint4 *src = (const uint4 *)(yr + row * H + h);
-      raw[s] = stream_rows ? __ldcs(src) : __ldg(src);
-      wv[s] = __ldg(w + t * k + s);
+      raw[s] = stream_rows ? ld_once(src) : ld_plain(src);
+      wv[s] = ld_plain(w + t * k + s);
     }
   }
-  const uint4 rs = __ldg((const uint4 *)(ys + t * H + h));
-  const float g = __ldg(sig + t);
+  const uint4 rs = ld_plain((const uint4 *)(ys + t * H + h));
+  const float g = ld_plain(sig + t);
   float acc[VN];
 #pragma unroll
   for (int j = 0; j < VN; ++j) acc[j] = 0.f;

@@ -114,6 +114,28 @@ __device__ inline F2 fma2(F2 a, F2 b, F2 c) {
 __device__ inline void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ inline void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Loads of what a kernel before may still be writing until griddep_wait()
+// returns: inputs and what the layer's own kernels leave, nearly everything.
+// A load through the read-only path (__ldg, or of a parameter that is const
+// and __restrict__) is one of memory that never changes, to the compiler, and
+// may be moved above the wait; one of a row count was, and what it read sent
+// the kernel out of its buffers.  So neither is used here.  ld_once is for
+// what is read once (evicted first), ld_l2 for what other SMs have written.
+template <typename T>
+__device__ inline T ld_plain(const T *p) {
+  return *p;
+}
+__device__ inline uint4 ld_once(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ inline int32_t ld_l2(const int32_t *p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // Launch `kernel` on `stream` with programmatic stream serialization.  The
 // kernel must call griddep_wait() before reading or writing global memory.
 template <typename... KArgs, typename... Args>

@@ -171,8 +171,8 @@ embed_sort_kernel(const EmbedArgs a, int bits, int32_t *mark, int32_t *key1, int
       const int j = begin + 32 * q + lane;
       keys[q] = tokens[q] = -1;
       if (j < end) {
-        keys[q] = pass ? __ldcg(key1 + j) : em_key(a, j, status);
-        tokens[q] = pass ? __ldcg(pos1 + j) : j;
+        keys[q] = pass ? ld_l2(key1 + j) : em_key(a, j, status);
+        tokens[q] = pass ? ld_l2(pos1 + j) : j;
       }
     }
     for (int d = threadIdx.x; d < ES_WARPS * D; d += ES_THREADS) hist[d] = 0;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(512) embed_zero_kernel(const EmbedArgs a, cons
   for (int64_t v0 = ((int64_t)blockIdx.x * 16 + (threadIdx.x >> 5)) * rows; v0 < a.V; v0 += step) {
     bool hit = lane >= rows || v0 + lane >= a.V;
     if (mark && !hit) {
-      const int32_t t = __ldcg(mark + v0 + lane);
+      const int32_t t = ld_l2(mark + v0 + lane);
       if (t >= 0 && t < a.T) {
         const int64_t id = em_id(a, t);
         hit = id == v0 + lane && id != a.padding_id;
@@ -378,7 +378,7 @@ embed_sum_kernel(const EmbedArgs a, int tile, int group, const int32_t *key, con
           const TO *row = (const TO *)a.dout + (int64_t)sorder[at + p + r] * a.ld_out;
           if constexpr (VEC != 0) {
             static_assert(VEC == Vec16<TO>::N, "one 16-byte load");
-            raw[r] = __ldcs((const uint4 *)(row + i));
+            raw[r] = ld_once((const uint4 *)(row + i));
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)

@@ -29,14 +29,14 @@ __device__ inline void store4(__nv_bfloat16 *p, const float (&o)[4]) {
 }
 
 template <typename TO>
-__global__ void __launch_bounds__(256) etp_reduce_kernel(const __grid_constant__ EtpParts parts, int n, int64_t count4, TO *__restrict__ out) {
+__global__ void __launch_bounds__(256) etp_reduce_kernel(const __grid_constant__ EtpParts parts, int n, int64_t count4, TO *out) {
   griddep_launch();
   griddep_wait();
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count4; i += stride) {
-    float4 acc = __ldg(reinterpret_cast<const float4 *>(parts.p[0]) + i);
+    float4 acc = ld_plain(reinterpret_cast<const float4 *>(parts.p[0]) + i);
     for (int q = 1; q < n; ++q) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(parts.p[q]) + i);
+      const float4 v = ld_plain(reinterpret_cast<const float4 *>(parts.p[q]) + i);
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;

@@ -105,9 +105,9 @@ struct EfItem {
 
 // Item `it` of this CTA's sequence: the shared segment's items first.
 __device__ inline EfItem ef_item(int it, const EfParams &p) {
-  const int routed = __ldg(p.item_start + p.E), total = __ldg(p.item_start + p.E + 1);
+  const int routed = ld_plain(p.item_start + p.E), total = ld_plain(p.item_start + p.E + 1);
   const int n_sh = total - routed;
-  const int4 d = __ldg(p.items + (it < n_sh ? routed + it : it - n_sh));
+  const int4 d = ld_plain(p.items + (it < n_sh ? routed + it : it - n_sh));
   EfItem r;
   r.seg = d.x;
   r.row0 = d.z;
@@ -187,7 +187,7 @@ etp_fused_kernel(const __grid_constant__ EfMaps maps, const EfParams p) {
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
   griddep_wait();
-  const int total = __ldg(p.item_start + p.E + 1);
+  const int total = ld_plain(p.item_start + p.E + 1);
   const int n_mine = total > (int)blockIdx.x ? (int)ceil_div(total - (int)blockIdx.x, gridDim.x) : 0;
   const int NT = p.H / 128;  // phase-2 output tiles per item = phase-1 K blocks / 2
   auto item_of = [&](int c) { return ef_item((int)blockIdx.x + c * (int)gridDim.x, p); };
@@ -320,9 +320,9 @@ etp_fused_kernel(const __grid_constant__ EfMaps maps, const EfParams p) {
             else
               tmem_ld32(tmem + 256 + b * 128 + lane_off + c0, v0);
             if (c0 + lane < im.rows)
-              d0 = sh ? (int)(im.row0 + c0 + lane) : __ldg(p.sorted_route + im.row0 + c0 + lane);
+              d0 = sh ? (int)(im.row0 + c0 + lane) : ld_plain(p.sorted_route + im.row0 + c0 + lane);
             if (EF_CPW == 64 && c0 + 32 + lane < im.rows)
-              d1 = sh ? (int)(im.row0 + c0 + 32 + lane) : __ldg(p.sorted_route + im.row0 + c0 + 32 + lane);
+              d1 = sh ? (int)(im.row0 + c0 + 32 + lane) : ld_plain(p.sorted_route + im.row0 + c0 + 32 + lane);
           }
           tc_fence_before();
           mbar_arrive(&t2empty[b]);
@@ -395,7 +395,7 @@ etp_fused_kernel(const __grid_constant__ EfMaps maps, const EfParams p) {
           const int r = 4 * lane + j;
           if (r < cur.rows) {
             const int64_t row = cur.row0 + r;
-            t4[j] = cur.seg == p.E ? (int)row : __ldg(p.sorted_route + row) / p.k;
+            t4[j] = cur.seg == p.E ? (int)row : ld_plain(p.sorted_route + row) / p.k;
           }
         }
       }

@@ -49,7 +49,7 @@ __device__ inline TileRows decode_tile(int ti, int E, int T, const int32_t *tile
 // gate_up + SwiGLU: tile of 32 rows x 32 features; thread (ty, tx) owns rows
 // 2ty, 2ty+1 and features 2tx, 2tx+1 (gate and up for each).
 template <typename TE>
-__global__ void __launch_bounds__(256) ffn_gate_up_simt_kernel(FfnArgs a, const int32_t *__restrict__ tile_start) {
+__global__ void __launch_bounds__(256) ffn_gate_up_simt_kernel(FfnArgs a, const int32_t *tile_start) {
   griddep_launch();
   griddep_wait();
   __shared__ float xs[SIMT_BK][SIMT_BM + 1];
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) ffn_gate_up_simt_kernel(FfnArgs a, const 
 // down: tile of 32 rows x 64 outputs; thread (ty, tx) owns rows 2ty, 2ty+1
 // and outputs 4tx..4tx+3.  Routed row j is written to y_routed[sorted_route[j]].
 template <typename TE>
-__global__ void __launch_bounds__(256) ffn_down_simt_kernel(FfnArgs a, const int32_t *__restrict__ tile_start) {
+__global__ void __launch_bounds__(256) ffn_down_simt_kernel(FfnArgs a, const int32_t *tile_start) {
   griddep_launch();
   griddep_wait();
   __shared__ float hs[SIMT_BK][SIMT_BM + 1];

@@ -146,7 +146,7 @@ struct Item {
 // ones of the table; its row tiles are the largest) are taken first, so the
 // heaviest items do not form the tail of the launch.
 __device__ inline int item_slot(int it, const int32_t *item_start, int E) {
-  const int routed = __ldg(item_start + E), total = __ldg(item_start + E + 1);
+  const int routed = ld_plain(item_start + E), total = ld_plain(item_start + E + 1);
   const int n_sh = total - routed;
   return it < n_sh ? routed + it : it - n_sh;
 }
@@ -154,7 +154,7 @@ __device__ inline int item_slot(int it, const int32_t *item_start, int E) {
 template <int MODE>
 __device__ inline Item decode_item(int it, const TcParams &p) {
   Item r;
-  const int4 d = __ldg(p.items + item_slot(it, p.item_start, p.E));
+  const int4 d = ld_plain(p.items + item_slot(it, p.item_start, p.E));
   r.seg = d.x;
   r.f = d.y;
   r.row0 = d.z;
@@ -327,7 +327,7 @@ tc_gemm_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
   griddep_wait();
-  const int total = __ldg(p.item_start + p.E + 1);
+  const int total = ld_plain(p.item_start + p.E + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -456,7 +456,7 @@ tc_gemm_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
           // Destination row of column c0 + lane, fetched before the accumulator loads.
           int dst = 0;
           if (c0 + lane < im.rows)
-            dst = (sh || p.y_sorted) ? (int)(im.row0 + c0 + lane) : __ldg(p.sorted_route + im.row0 + c0 + lane);
+            dst = (sh || p.y_sorted) ? (int)(im.row0 + c0 + lane) : ld_plain(p.sorted_route + im.row0 + c0 + lane);
           float vt[MT][32];
           if (MT == 2) tmem_ld32x2(tq + c0, tq + 256 + c0, vt[0], vt[MT - 1]);
           else tmem_ld32(tq + c0, vt[0]);
@@ -493,7 +493,7 @@ tc_gemm_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
       __syncwarp();
       if (lane < ni) {
         const int64_t row = im.row0 + 8 * lane + g;
-        tok[lane] = sh ? (int)row : __ldg(p.sorted_route + row) / p.k;
+        tok[lane] = sh ? (int)row : ld_plain(p.sorted_route + row) / p.k;
       }
       __syncwarp();
       for (int kb = 0; kb < im.nk; ++kb) {
@@ -615,7 +615,7 @@ tc_pair_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
   griddep_wait();
-  const int total = __ldg(p.item_start + p.E + 1);
+  const int total = ld_plain(p.item_start + p.E + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -742,7 +742,7 @@ tc_pair_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
         for (int c0 = cfirst; c0 < im.n; c0 += CSTEP) {
           int dst = 0;
           if (c0 + lane < im.rows)
-            dst = (sh || p.y_sorted) ? (int)(im.row0 + c0 + lane) : __ldg(p.sorted_route + im.row0 + c0 + lane);
+            dst = (sh || p.y_sorted) ? (int)(im.row0 + c0 + lane) : ld_plain(p.sorted_route + im.row0 + c0 + lane);
           float v[32];
           tmem_ld32(tq + c0, v);
           if (p.y_f32) down_epi_chunk_f32(v, mtile * 128 + q * 32, c0, dst, im, (float *)(void *)yout, p.H, lane);
@@ -790,7 +790,7 @@ tc_pair_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
           const int r = 4 * qd + j;
           if (r < hrows) {
             const int64_t row = im.row0 + hbase + r;
-            t4[j] = sh ? (int)row : __ldg(p.sorted_route + row) / p.k;
+            t4[j] = sh ? (int)row : ld_plain(p.sorted_route + row) / p.k;
           }
         }
       }
@@ -1014,7 +1014,7 @@ tc_router_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
       }
       if (!ok) break;
       const int e = im.f * 128 + q * 32 + lane;
-      const float bias = (p.bias && e < p.E) ? __ldg(p.bias + e) : 0.f;
+      const float bias = (p.bias && e < p.E) ? ld_plain(p.bias + e) : 0.f;
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
@@ -1239,7 +1239,7 @@ tc_router_pair_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
       if (!ok) break;
       const int e = im.f * 256 + (int)rank * 128 + q * 32 + lane;
       if (kparts == 1) {
-        const float bias = (p.bias && e < p.E) ? __ldg(p.bias + e) : 0.f;
+        const float bias = (p.bias && e < p.E) ? ld_plain(p.bias + e) : 0.f;
 #pragma unroll
         for (int cc = 0; cc < NCC; ++cc)
 #pragma unroll
@@ -1275,23 +1275,23 @@ tc_router_pair_kernel(const __grid_constant__ TcMaps maps, const TcParams p) {
 // chunks of an item itself, so a token's logits do not depend on which
 // form ran (that is, on T).  Four consecutive logits per thread (E % 256 == 0).
 __global__ void __launch_bounds__(256)
-router_chunk_sum_kernel(int64_t n, int E, const float *__restrict__ part, const float *__restrict__ bias,
-                        float *__restrict__ logits) {
+router_chunk_sum_kernel(int64_t n, int E, const float *part, const float *bias,
+                        float *logits) {
   griddep_launch();
   griddep_wait();
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (i >= n) return;
-  float4 a = __ldg((const float4 *)(part + i));
+  float4 a = ld_plain((const float4 *)(part + i));
 #pragma unroll
   for (int c = 1; c < RT_CHUNKS; ++c) {
-    const float4 b = __ldg((const float4 *)(part + c * n + i));
+    const float4 b = ld_plain((const float4 *)(part + c * n + i));
     a.x = a.x + b.x;
     a.y = a.y + b.y;
     a.z = a.z + b.z;
     a.w = a.w + b.w;
   }
   if (bias) {
-    const float4 g = __ldg((const float4 *)(bias + i % E));
+    const float4 g = ld_plain((const float4 *)(bias + i % E));
     a.x = a.x + g.x;
     a.y = a.y + g.y;
     a.z = a.z + g.z;
@@ -1306,14 +1306,14 @@ router_chunk_sum_kernel(int64_t n, int E, const float *__restrict__ part, const 
 // exact in FP32 and holds at most 16 then 8 significant bits, so W3 captures
 // the rest and W1 + W2 + W3 = w exactly.
 // ---------------------------------------------------------------------------
-__global__ void split_router_weight_kernel(int64_t n4, int H, const float4 *__restrict__ wr,
-                                           __nv_bfloat16 *__restrict__ wr3) {
+__global__ void split_router_weight_kernel(int64_t n4, int H, const float4 *wr,
+                                           __nv_bfloat16 *wr3) {
   griddep_launch();
   griddep_wait();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // four consecutive weights
   if (i >= n4) return;
   const int64_t e = (i * 4) / H, h = (i * 4) % H;  // H % 4 == 0: the four share a row
-  const float4 w4 = __ldg(wr + i);
+  const float4 w4 = ld_plain(wr + i);
   const float w[4] = {w4.x, w4.y, w4.z, w4.w};
   __nv_bfloat162 p1[2], p2[2], p3[2];
 #pragma unroll
@@ -1348,8 +1348,8 @@ __global__ void split_router_weight_kernel(int64_t n4, int H, const float4 *__re
 constexpr int IT_MAX_E = 1024;
 
 __global__ void __launch_bounds__(1024)
-item_tables_kernel(int E, int T, int nf_a_r, int nf_a_s, int nf_b_r, int nf_b_s, const int32_t *__restrict__ offsets,
-                   int32_t *__restrict__ start_a, int32_t *__restrict__ start_b, int e_begin, int e_end,
+item_tables_kernel(int E, int T, int nf_a_r, int nf_a_s, int nf_b_r, int nf_b_s, const int32_t *offsets,
+                   int32_t *start_a, int32_t *start_b, int e_begin, int e_end,
                    int with_shared, int tile) {
   griddep_launch();
   griddep_wait();
@@ -1395,22 +1395,22 @@ item_tables_kernel(int E, int T, int nf_a_r, int nf_a_s, int nf_b_r, int nf_b_s,
 
 // Expansion: one warp per segment writes that segment's items of both tables.
 __global__ void __launch_bounds__(256)
-item_expand_kernel(int E, int T, const int32_t *__restrict__ offsets, const int32_t *__restrict__ start_a,
-                   const int32_t *__restrict__ start_b, int4 *__restrict__ items_a, int4 *__restrict__ items_b,
+item_expand_kernel(int E, int T, const int32_t *offsets, const int32_t *start_a,
+                   const int32_t *start_b, int4 *items_a, int4 *items_b,
                    int max_a, int max_b, int tile) {
   griddep_launch();
   griddep_wait();
   const int sg = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
   if (sg > E) return;
-  if (__ldg(start_a + sg + 1) == __ldg(start_a + sg) && __ldg(start_b + sg + 1) == __ldg(start_b + sg))
+  if (ld_plain(start_a + sg + 1) == ld_plain(start_a + sg) && ld_plain(start_b + sg + 1) == ld_plain(start_b + sg))
     return;  // empty, or outside the expert range (its offsets are not read)
-  const int base = sg == E ? 0 : __ldg(offsets + sg);
-  const int n_s = sg == E ? T : __ldg(offsets + sg + 1) - base;
+  const int base = sg == E ? 0 : ld_plain(offsets + sg);
+  const int n_s = sg == E ? T : ld_plain(offsets + sg + 1) - base;
   if (n_s == 0) return;
   const int ntile = (n_s + tile - 1) / tile;
   const int rpt = ((n_s + ntile - 1) / ntile + 15) & ~15;
-  const int a0 = __ldg(start_a + sg), na = __ldg(start_a + sg + 1) - a0;
-  const int b0 = __ldg(start_b + sg), nb = __ldg(start_b + sg + 1) - b0;
+  const int a0 = ld_plain(start_a + sg), na = ld_plain(start_a + sg + 1) - a0;
+  const int b0 = ld_plain(start_b + sg), nb = ld_plain(start_b + sg + 1) - b0;
   for (int local = lane; local < max(na, nb); local += 32) {
     const int nt = local % ntile;
     const int4 v = make_int4(sg, local / ntile, base + nt * rpt, min(rpt, n_s - nt * rpt));

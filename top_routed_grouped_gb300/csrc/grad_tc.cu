@@ -106,9 +106,9 @@ struct DgItem {
 // The shared segment's items (last in the table, the largest row tiles) first.
 template <int MODE>
 __device__ inline DgItem dg_item(int it, const DgParams &p) {
-  const int routed = __ldg(p.item_start + p.E), total = __ldg(p.item_start + p.E + 1);
+  const int routed = ld_plain(p.item_start + p.E), total = ld_plain(p.item_start + p.E + 1);
   const int n_sh = total - routed;
-  const int4 d = __ldg(p.items + (it < n_sh ? routed + it : it - n_sh));
+  const int4 d = ld_plain(p.items + (it < n_sh ? routed + it : it - n_sh));
   DgItem r;
   r.seg = d.x;
   r.f = d.y;
@@ -160,7 +160,7 @@ tc_dgrad_kernel(const __grid_constant__ DgMaps maps, const DgParams p) {
   const uint32_t tmem = *tmem_slot;
   griddep_launch();
   griddep_wait();
-  const int total = __ldg(p.item_start + p.E + 1);
+  const int total = ld_plain(p.item_start + p.E + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -414,8 +414,8 @@ __device__ inline WgItem wg_item(int it, const WgParams &p) {
     local = (it - n_sh) % per;
     r.mt = local / p.tn_r;
     r.nt = local % p.tn_r;
-    r.r0 = __ldg(p.offsets + r.seg);
-    r.rows = __ldg(p.offsets + r.seg + 1) - (int)r.r0;
+    r.r0 = ld_plain(p.offsets + r.seg);
+    r.rows = ld_plain(p.offsets + r.seg + 1) - (int)r.r0;
   }
   r.nk = (int)ceil_div(r.rows, 64);
   return r;
@@ -656,10 +656,10 @@ gather_sorted_rows_kernel(int64_t R, int H, int k, const int32_t *sorted_route, 
   griddep_wait();
   const int64_t j = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (j >= R || j < __ldg(offsets + e_begin) || j >= __ldg(offsets + e_end)) return;
-  const uint4 *src = (const uint4 *)(x + (int64_t)(__ldg(sorted_route + j) / k) * H);
+  if (j >= R || j < ld_plain(offsets + e_begin) || j >= ld_plain(offsets + e_end)) return;
+  const uint4 *src = (const uint4 *)(x + (int64_t)(ld_plain(sorted_route + j) / k) * H);
   uint4 *dst = (uint4 *)(xs + j * H);
-  for (int c = lane; c < H / 8; c += 32) dst[c] = __ldg(src + c);
+  for (int c = lane; c < H / 8; c += 32) dst[c] = ld_plain(src + c);
 }
 
 // ===========================================================================

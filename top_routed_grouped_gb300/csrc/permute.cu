@@ -28,7 +28,7 @@ size_t permute_scratch_bytes(int64_t R, int E, int chunk) {
 
 template <int CH>
 __global__ void __launch_bounds__(32 * WARPS_PER_BLOCK)
-permute_count_kernel(int64_t R, int E, int n_chunks, const int32_t *__restrict__ ids, int32_t *__restrict__ counts,
+permute_count_kernel(int64_t R, int E, int n_chunks, const int32_t *ids, int32_t *counts,
                      int *status) {
   griddep_launch();
   griddep_wait();
@@ -43,7 +43,7 @@ permute_count_kernel(int64_t R, int E, int n_chunks, const int32_t *__restrict__
 #pragma unroll
   for (int step = 0; step < STEPS; ++step) {
     const int64_t r = (int64_t)c * CH + step * 32 + lane;
-    eid[step] = r < R ? __ldg(ids + r) : PAST_END;
+    eid[step] = r < R ? ld_plain(ids + r) : PAST_END;
   }
   __syncwarp();
 #pragma unroll
@@ -65,7 +65,7 @@ permute_count_kernel(int64_t R, int E, int n_chunks, const int32_t *__restrict__
 
 // grid: ceil(E/32) blocks of 32 warps; lane = expert, warp = range of chunks.
 __global__ void __launch_bounds__(1024)
-permute_scan_chunks_kernel(int E, int n_chunks, int32_t *__restrict__ counts, int32_t *__restrict__ totals) {
+permute_scan_chunks_kernel(int E, int n_chunks, int32_t *counts, int32_t *totals) {
   griddep_launch();
   griddep_wait();
   __shared__ int32_t part[32][33];
@@ -102,7 +102,7 @@ permute_scan_chunks_kernel(int E, int n_chunks, int32_t *__restrict__ counts, in
 
 // One block of 1024 threads: offsets[e] = sum_{e' < e} totals[e'], offsets[E] = total.
 __global__ void __launch_bounds__(1024)
-permute_scan_experts_kernel(int E, const int32_t *__restrict__ totals, int32_t *__restrict__ offsets) {
+permute_scan_experts_kernel(int E, const int32_t *totals, int32_t *offsets) {
   griddep_launch();
   griddep_wait();
   __shared__ int32_t buf[1024];
@@ -122,9 +122,9 @@ permute_scan_experts_kernel(int E, const int32_t *__restrict__ totals, int32_t *
 
 template <int CH>
 __global__ void __launch_bounds__(32 * WARPS_PER_BLOCK)
-permute_scatter_kernel(int64_t R, int E, int n_chunks, const int32_t *__restrict__ ids,
-                       const int32_t *__restrict__ chunk_prefix, const int32_t *__restrict__ offsets,
-                       int32_t *__restrict__ sorted_route, int32_t *__restrict__ route_pos) {
+permute_scatter_kernel(int64_t R, int E, int n_chunks, const int32_t *ids,
+                       const int32_t *chunk_prefix, const int32_t *offsets,
+                       int32_t *sorted_route, int32_t *route_pos) {
   griddep_launch();
   griddep_wait();
   extern __shared__ int32_t smem[];
@@ -141,7 +141,7 @@ permute_scatter_kernel(int64_t R, int E, int n_chunks, const int32_t *__restrict
 #pragma unroll
   for (int step = 0; step < STEPS; ++step) {
     const int64_t r = (int64_t)c * CH + step * 32 + lane;
-    eid[step] = r < R ? __ldg(ids + r) : -1;
+    eid[step] = r < R ? ld_plain(ids + r) : -1;
   }
 #pragma unroll
   for (int step = 0; step < STEPS; ++step) {
@@ -203,7 +203,7 @@ cudaError_t launch_permute(int64_t R, int E, const int32_t *ids, int32_t *offset
 // prefix, exact.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024)
-build_tiles_kernel(int E, int T, int bn, const int32_t *__restrict__ offsets, int32_t *__restrict__ tile_start,
+build_tiles_kernel(int E, int T, int bn, const int32_t *offsets, int32_t *tile_start,
                    int e_begin, int e_end, int with_shared) {
   griddep_launch();
   griddep_wait();

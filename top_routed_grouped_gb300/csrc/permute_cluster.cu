@@ -82,8 +82,8 @@ __device__ inline int32_t block_exclusive_scan(int32_t v, int32_t *buf, int32_t 
 }
 
 __global__ void __launch_bounds__(PC_THREADS, 1)
-permute_cluster_kernel(int64_t R, int E, const int32_t *__restrict__ ids, int32_t *__restrict__ offsets,
-                       int32_t *__restrict__ sorted_route, int32_t *__restrict__ route_pos, int *status,
+permute_cluster_kernel(int64_t R, int E, const int32_t *ids, int32_t *offsets,
+                       int32_t *sorted_route, int32_t *route_pos, int *status,
                        PermuteItems itab) {
   extern __shared__ int32_t sm[];
   int32_t *hist = sm;            // [PC_WARPS][E]: warp histograms, then their exclusive prefixes
@@ -110,7 +110,7 @@ permute_cluster_kernel(int64_t R, int E, const int32_t *__restrict__ ids, int32_
 #pragma unroll
     for (int u = 0; u < PC_UNROLL; ++u) {
       const int64_t r = b + 32 * u + lane;
-      eid[u] = r < r1 ? __ldg(ids + r) : PC_PAST_END;
+      eid[u] = r < r1 ? ld_plain(ids + r) : PC_PAST_END;
     }
 #pragma unroll
     for (int u = 0; u < PC_UNROLL; ++u) {
@@ -164,7 +164,7 @@ permute_cluster_kernel(int64_t R, int E, const int32_t *__restrict__ ids, int32_
 #pragma unroll
     for (int u = 0; u < PC_UNROLL; ++u) {
       const int64_t r = b + 32 * u + lane;
-      eid[u] = r < r1 ? __ldg(ids + r) : -1;
+      eid[u] = r < r1 ? ld_plain(ids + r) : -1;
     }
 #pragma unroll
     for (int u = 0; u < PC_UNROLL; ++u) {

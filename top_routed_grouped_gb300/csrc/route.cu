@@ -21,8 +21,8 @@ namespace moe {
 // ---------------------------------------------------------------------------
 template <typename TX>
 __global__ void __launch_bounds__(256)
-router_logits_simt_kernel(int T, int H, int E, const TX *__restrict__ x, const float *__restrict__ wr,
-                          const float *__restrict__ bias, float *__restrict__ logits) {
+router_logits_simt_kernel(int T, int H, int E, const TX *x, const float *wr,
+                          const float *bias, float *logits) {
   griddep_launch();
   griddep_wait();
   __shared__ float xs[32][68];
@@ -121,7 +121,7 @@ constexpr int GATE_BATCH = 4;  // 16-byte chunks of x / w_sg loaded together per
 // h = (lane + 32 m) VN, m ascending, summed in that order per lane, then a
 // fixed butterfly (every lane returns the same value).
 template <typename TX>
-__device__ inline float gate_dot(const TX *__restrict__ xr, const TX *__restrict__ wsg, int H, int lane) {
+__device__ inline float gate_dot(const TX *xr, const TX *wsg, int H, int lane) {
   constexpr int VN = Vec16<TX>::N;
   float part = 0.f;
   for (int h0 = lane * VN; h0 < H; h0 += 32 * VN * GATE_BATCH) {
@@ -130,8 +130,8 @@ __device__ inline float gate_dot(const TX *__restrict__ xr, const TX *__restrict
     for (int i = 0; i < GATE_BATCH; ++i) {
       const int h = h0 + 32 * VN * i;
       if (h < H) {
-        xa[i] = __ldg(reinterpret_cast<const uint4 *>(xr + h));
-        ga[i] = __ldg(reinterpret_cast<const uint4 *>(wsg + h));
+        xa[i] = ld_plain(reinterpret_cast<const uint4 *>(xr + h));
+        ga[i] = ld_plain(reinterpret_cast<const uint4 *>(wsg + h));
       }
     }
 #pragma unroll
@@ -152,9 +152,9 @@ __device__ inline float gate_dot(const TX *__restrict__ xr, const TX *__restrict
 
 template <typename TX, int EPL>
 __global__ void __launch_bounds__(256, 4)
-topk_gate_kernel(int T, int H, int E, int k, const float *__restrict__ logits, const TX *__restrict__ x,
-                 const TX *__restrict__ wsg, int32_t *__restrict__ ids, float *__restrict__ w,
-                 float *__restrict__ sig) {
+topk_gate_kernel(int T, int H, int E, int k, const float *logits, const TX *x,
+                 const TX *wsg, int32_t *ids, float *w,
+                 float *sig) {
   griddep_launch();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -166,7 +166,7 @@ topk_gate_kernel(int T, int H, int E, int k, const float *__restrict__ logits, c
   float lv[EPL];
   const float *lrow = logits + t * E;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) lv[i] = lane + 32 * i < E ? __ldg(lrow + lane + 32 * i) : 0.f;
+  for (int i = 0; i < EPL; ++i) lv[i] = lane + 32 * i < E ? ld_plain(lrow + lane + 32 * i) : 0.f;
 
   const float part = gate_dot<TX>(x + t * (int64_t)H, wsg, H, lane);
 
@@ -239,20 +239,20 @@ topk_gate_kernel(int T, int H, int E, int k, const float *__restrict__ logits, c
 // ---------------------------------------------------------------------------
 template <typename TX>
 __global__ void __launch_bounds__(256)
-replay_gate_kernel(int T, int H, int E, int k, const float *__restrict__ logits, const TX *__restrict__ x,
-                   const TX *__restrict__ wsg, const int32_t *__restrict__ ids, float *__restrict__ w,
-                   float *__restrict__ sig, int *status) {
+replay_gate_kernel(int T, int H, int E, int k, const float *logits, const TX *x,
+                   const TX *wsg, const int32_t *ids, float *w,
+                   float *sig, int *status) {
   griddep_launch();
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (t >= T) return;
-  const int e = lane < k ? __ldg(ids + t * k + lane) : -1;
+  const int e = lane < k ? ld_plain(ids + t * k + lane) : -1;
   const bool in_range = e >= 0 && e < E;
   const unsigned dup = __match_any_sync(FULL_MASK, e);
   const bool bad_range = __any_sync(FULL_MASK, lane < k && !in_range);
   const bool bad_dup = __any_sync(FULL_MASK, lane < k && __popc(dup) > 1);
-  const float l = lane < k && in_range ? __ldg(logits + t * E + e) : -INFINITY;
+  const float l = lane < k && in_range ? ld_plain(logits + t * E + e) : -INFINITY;
   const float part = gate_dot<TX>(x + t * (int64_t)H, wsg, H, lane);
   float m = l;
 #pragma unroll
