@@ -70,6 +70,14 @@ constexpr uint32_t CT_TMEM_COLS = 512;
 // chunks of 512 (1.1e-7 in 256; a rounded FP32 product of the kind that keeps
 // its logits: 4.6e-7).  512 takes 2 to 3 % more time than 1024, 256 six more.
 constexpr int CT_KCHUNK = 8;   // a multiple of SUB
+// An accumulator of the other products takes no more than this of a sum, in K
+// blocks (of dweight 8192 rows, as many as a chunk of dhidden has columns).  What
+// is left of a longer one goes into the other accumulator, and the epilogue
+// adds the sum so far onto it in FP32, rounded: the tensor cores cut off what
+// an addend has below 2^-23 of the sum, always towards zero (2^21 rows of one
+// sign in one chain: 1.1e-2 of dweight lost, in chains of 8192: 5e-7).
+template <int KIND>
+constexpr int CT_CHAIN = KIND == CE_STATS ? CT_KCHUNK : KIND == CE_LOGITS ? 1 << 16 : 128;
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
@@ -648,7 +656,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         const uint32_t idesc = idesc_bf16_f32(256, im.cols) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
         const uint32_t astep = a_mn ? 128 : 2, bstep = b_mn ? 128 : 2;  // K = 16: 2048 or 32 bytes
         for (int kb = 0; kb < im.nk; kb += SUB) {
-          const int kc = KIND == CE_STATS ? kb % CT_KCHUNK : kb;  // in this accumulator
+          const int kc = kb % CT_CHAIN<KIND>;  // in this accumulator
           const int sub = min(SUB, im.nk - kb);
           const int b = cnt & 1;
           if (kc == 0) {
@@ -669,7 +677,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
                 mma_bf16_pair(tmem + b * 256, ad + astep * kk, bd + bstep * kk, idesc, (kc | s | kk) != 0);
             }
           }
-          const bool last = kb + sub == im.nk || (KIND == CE_STATS && kc + sub == CT_KCHUNK);
+          const bool last = kb + sub == im.nk || kc + sub == CT_CHAIN<KIND>;
           if (elected) {
             mma_commit_pair(&empty[stage]);
             if (last) mma_commit_pair(&tfull[b]);
@@ -698,14 +706,25 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
       tc_fence_after();
       return true;
     };
-    auto release = [&] {  // the accumulator, to the MMA thread
+    auto release = [&](uint32_t b) {  // an accumulator, to the MMA thread
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (leader) mbar_arrive(&tempty[cnt & 1]);
-        else mbar_arrive_remote(tempty_leader0 + (uint32_t)((cnt & 1) * sizeof(uint64_t)));
+        if (leader) mbar_arrive(&tempty[b]);
+        else mbar_arrive_remote(tempty_leader0 + (uint32_t)(b * sizeof(uint64_t)));
       }
-      ++cnt;
+    };
+    // A sum that goes on: what it has come to, onto its next part (this warp's columns).
+    auto carry = [&](uint32_t from, uint32_t to) {
+#pragma unroll 1
+      for (int c = 0; c < im.cols; c += 32) {
+        if ((KIND == CE_LOGITS ? c / 64 & 1 : c >= im.cols / 2) != half) continue;
+        float a[32], b[32];
+        tmem_ld32x2(from + c, to + c, a, b);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) b[j] += a[j];
+        tmem_st32(to + c, b);
+      }
     };
     while (work.next(p, im)) {
       const int row0 = im.m * 256 + (int)rank * 128 + q * 32;
@@ -725,18 +744,31 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[c + j] += x[j];
           }
-          release();
+          release(cnt & 1);
+          ++cnt;
         }
         if (!ok) break;
         stats_epilogue(p, im, v, row0 + lane, half);
         continue;
       }
-      if (im.nk != 0 && !wait()) break;
+      bool ok = true;
+      for (int kb = 0; kb < im.nk; kb += CT_CHAIN<KIND>) {
+        if (!(ok = wait())) break;
+        if (kb != 0) {
+          carry(tq + (~cnt & 1) * 256, tq + (cnt & 1) * 256);
+          release(~cnt & 1);
+        }
+        if (kb + CT_CHAIN<KIND> < im.nk) ++cnt;
+      }
+      if (!ok) break;
       const uint32_t taddr = tq + (cnt & 1) * 256 + (KIND == CE_LOGITS ? 0 : half * (im.cols / 2));
       if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
       else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, work.count, half, stg, lane);
       else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane, out_policy);
-      if (im.nk != 0) release();
+      if (im.nk != 0) {
+        release(cnt & 1);
+        ++cnt;
+      }
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
