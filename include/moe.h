@@ -750,8 +750,9 @@ int moe_linear_ce(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void
  * run over chunks of the vocabulary whose bounds the type alone sets, in
  * order, so that its rows do not depend on the batch; dweight's over the rows
  * in order.  MOE_BF16: the tensor cores cut off what an addend has below 2^-23
- * of the sum, so no sum of theirs is longer than 8192 addends; parts are joined
- * in FP32, rounded.  One rounding of each output.  T = 0 (or no row left) zeroes
+ * of the sum, so no sum of theirs is longer than 8192 addends, a logit's 512
+ * (the forward's and the gradient's logits have the same bits); parts are
+ * joined in FP32, rounded.  One rounding of each output.  T = 0 (or no row left) zeroes
  * dweight unless `accumulate`.  Workspace: moe_linear_ce_workspace_size(a,
  * call) bytes, 256-byte aligned; it goes by T, D, V, the types, ld_weight and
  * weight's alignment to 16 bytes (NULL: aligned; the other buffers need not be

@@ -37,3 +37,31 @@ def test_dweight_of_many_rows_on_one_target(T):
         print(f"T = {T}: dweight {float(off):.2e} off, bound {tol:.2e}")
         assert float(off) <= tol
     assert torch.equal(acc, base + dw)
+
+
+@pytest.mark.parametrize("D", [512, 2048, 4096, 16384])
+def test_probabilities_of_a_row_add_up_to_one(D):
+    """The gradient's logits are those that the statistics were taken of, to the
+    last bit, so that the row of g adds up to 0 however far the logits' sums are
+    off, here of D addends of one sign that make 60.  Each entry but the target's
+    is rounded to bfloat16, by 2^-8 of it at most: six times the root of the sum
+    of those squares (by Hoeffding's bound exceeded once in 10^7), and 2^-18 for
+    the exponentials and their sum."""
+    V = 8192
+    g = torch.Generator(device="cuda").manual_seed(2)
+    h = (0.5 + 0.5 * torch.rand(1, D, generator=g, device="cuda")).to(B)
+    w = ((0.5 + 0.5 * torch.rand(V, D, generator=g, device="cuda")) * (60 / (0.5625 * D))).to(B)
+    t, d = torch.tensor([5], device="cuda"), torch.ones(1, device="cuda")
+    x = (w.double() @ h[0].double())
+    p = torch.softmax(x, 0)
+    assert 50 < float(x.mean()) < 70
+    _, lse = moe.linear_cross_entropy(h, w, t)
+    for dw in (moe.linear_cross_entropy_step(h, w, t, d, dweight_dtype=F)[2],
+               moe.linear_cross_entropy_backward(d, lse, h, w, t, dweight_dtype=F)[1]):
+        # dweight's rows are g_v times one and the same rounding of hidden.
+        row = dw[5].double()
+        gv = (dw.double() @ row) / (row @ row)   # in units of the target's entry
+        total = float(gv.sum())
+        bound = 6 * 2.0 ** -8 * float(p.square().sum().sqrt()) + 2.0 ** -18
+        print(f"D = {D}: a row of g adds up to {total:.2e}, bound {bound:.2e}")
+        assert abs(total) <= bound

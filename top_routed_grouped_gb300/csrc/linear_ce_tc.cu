@@ -43,18 +43,21 @@ using namespace umma;
 
 constexpr int CE_STATS = 0, CE_LOGITS = 1, CE_GRADS = 2;
 constexpr int CT_TILE = 16384;  // a K block of 64: 128 rows of A, or half of B's columns, of a CTA
-// Epilogue warps: eight, half of the columns each, with a staging tile of 4 KB;
-// for the statistics sixteen with a quarter each, so that a thread's sums over
-// the K chunks (64) stay in registers.  Stages of two K blocks: one handshake
+// Epilogue warps: eight for the gradients, half of the columns each, with a
+// staging tile of 4 KB; for the logits sixteen with a quarter each, so that a
+// thread's sums over the K chunks (64) stay in registers (and 2 KB each for g:
+// 16-byte stores past shared memory made a step of 8192 x 2048 x 131072 11.0 ms,
+// 32-byte ones 10.75, these 10.6).  Stages of two K blocks: one handshake
 // and one commit for eight MMAs (forward 4096 x 2048 x 50257: 527 us with one block,
 // 459 with two; the gradients' products 1620 and 1569; three blocks leave too
 // few stages: 1720).
 constexpr int CT_EPI_FIRST = 4, SUB = 2;
 template <int KIND>
 struct CtCfg {
-  static constexpr int EPI_WARPS = KIND == CE_STATS ? 16 : 8;
+  static constexpr int EPI_WARPS = KIND == CE_GRADS ? 8 : 16;
   static constexpr int THREADS = 32 * (CT_EPI_FIRST + EPI_WARPS);
-  static constexpr int STG_BYTES = KIND == CE_STATS ? 0 : EPI_WARPS * 4096;
+  static constexpr int STG_WARP = KIND == CE_STATS ? 0 : KIND == CE_LOGITS ? 2048 : 4096;  // staging tile of a warp
+  static constexpr int STG_BYTES = EPI_WARPS * STG_WARP;
   static constexpr int RING = 7 * 2 * CT_TILE - STG_BYTES;  // bytes of the stages
   static constexpr int SMEM = 1024 + RING + STG_BYTES + 512;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -63,21 +66,25 @@ constexpr int CT_PREFETCH = 8;  // K blocks (none: 33.3 us at 5 rows x 2048 x 32
 constexpr int CT_MAX_STAGES = 5;
 constexpr uint32_t CT_HINT = 100000;  // ns
 constexpr uint32_t CT_TMEM_COLS = 512;
-// The statistics' products are summed in chunks of 512 of K, each in an
+// The logits are summed in chunks of 512 of K, each in an
 // accumulator of its own, and the chunks in FP32 registers: the tensor cores
 // cut each of their sums off instead of rounding it, which leaves a loss
 // 1.0e-6 off at K = 2048 in one chain, 5e-7 in chunks of 1024 and 2.4e-7 in
 // chunks of 512 (1.1e-7 in 256; a rounded FP32 product of the kind that keeps
 // its logits: 4.6e-7).  512 takes 2 to 3 % more time than 1024, 256 six more.
+// The gradient's logits are summed the same way and have the same bits, so that
+// probabilities add up to 1 however far the sums are off: in one chain a row of
+// 16384 addends that make 60 was short by 4.2e-3 of that (a step of 8192 x 2048 x
+// 131072 takes 10.6 ms for 10.4 with one).
 constexpr int CT_KCHUNK = 8;   // a multiple of SUB
-// An accumulator of the other products takes no more than this of a sum, in K
+// An accumulator of the gradients' products takes no more than this of a sum, in K
 // blocks (of dweight 8192 rows, as many as a chunk of dhidden has columns).  What
 // is left of a longer one goes into the other accumulator, and the epilogue
 // adds the sum so far onto it in FP32, rounded: the tensor cores cut off what
 // an addend has below 2^-23 of the sum, always towards zero (2^21 rows of one
 // sign in one chain: 1.1e-2 of dweight lost, in chains of 8192: 5e-7).
 template <int KIND>
-constexpr int CT_CHAIN = KIND == CE_STATS ? CT_KCHUNK : KIND == CE_LOGITS ? 1 << 16 : 128;
+constexpr int CT_CHAIN = KIND == CE_GRADS ? 128 : CT_KCHUNK;
 constexpr float CE_LOG2E = 1.44269504088896340736f;
 
 struct CtMaps {
@@ -85,7 +92,7 @@ struct CtMaps {
   CUtensorMap h32, w32;    // the same rows, 32 at a time
   CUtensorMap ht, wt, gt;  // MN-major tiles: boxes of 64 rows x 64, two blocks of columns at once
   CUtensorMap ht1, wt1;    // one block of columns
-  CUtensorMap gout;        // 32 rows x 64: g's stores
+  CUtensorMap gout;        // 32 rows x 32: g's stores
   CUtensorMap dw;          // dweight: 32 rows x 128 bytes
 };
 
@@ -337,48 +344,42 @@ __device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, float
   p.part[(int64_t)(col0 / 64) * p.tpad + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
-__device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, uint32_t taddr, int row,
-                                       int half, uint8_t *stg, int lane) {
+// g of the same 64 columns from the same sums, 32 at a time through the
+// warp's buffer: rows of 64 bytes, the 16-byte units of two rows together
+// changed round as the 64-byte swizzle has them.
+__device__ inline void logits_epilogue(const CtMaps &maps, const CtParams &p, const CtItem &im, const float (&v)[64],
+                                       int row, int cq, uint8_t *stg, int lane) {
+  const int pc = im.n0 + cq * 64;  // column in the piece
+  if (cq * 64 >= im.cols || pc >= p.n) return;
   const CeRow R = p.rows[row];
   const bool zero = R.c == 0.f && R.b == 0.f;
-#pragma unroll 1
-  for (int c = half * 64; c < im.cols; c += 128) {
-    const int pc = im.n0 + c;  // column in the piece
-    if (pc >= p.n) break;
-    const int target = R.target - p.v0 - pc;
-    float v[2][32];
-    tmem_ld32x2(taddr + c, taddr + c + 32, v[0], v[1]);
-    const int left = p.V - p.v0 - pc;
-    uint32_t w[32];
+  const int target = R.target - p.v0 - pc, left = p.V - p.v0 - pc;
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[hh][j] = R.c * ex2(fmaf(v[hh][j], p.s2, -R.lse2));
-      const unsigned at = (unsigned)(target - hh * 32);
-      if (at < 32u) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[hh][j] = at == (unsigned)j ? R.b : v[hh][j];
-      }
-      if (zero || left < 64) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (zero || hh * 32 + j >= left) v[hh][j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[hh][2 * j], v[hh][2 * j + 1]);
-        w[hh * 16 + j] = *(const uint32_t *)&b;
-      }
-    }
+  for (int c = 0; c < 64; c += 32) {
     if (lane == 0) bulk_wait_read<0>();  // the last store has read the buffer
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *(uint4 *)(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    for (int u = 0; u < 4; ++u) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = c + 8 * u + 2 * i + k;
+          x[k] = R.c * ex2(fmaf(v[j], p.s2, -R.lse2));
+          if (j == target) x[k] = R.b;
+          if (zero || j >= left) x[k] = 0.f;
+        }
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[0], x[1]);
+        w[i] = *(const uint32_t *)&b;
+      }
+      *(uint4 *)(stg + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(&maps.gout, stg, pc, row);
+      tma_store_2d(&maps.gout, stg, pc + c, row);
       bulk_commit();
     }
   }
@@ -697,7 +698,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
   } else if (warp >= CT_EPI_FIRST) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - CT_EPI_FIRST) >> 2;  // TMEM lane quarter; which of the columns
-    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * 4096;
+    uint8_t *stg = epi + (warp - CT_EPI_FIRST) * CtCfg<KIND>::STG_WARP;
     const uint32_t tempty_leader0 = mapa_shared(&tempty[0], 0);
     const uint64_t out_policy = policy_evict_first();  // dweight is written once and not read again
     uint32_t cnt = 0;
@@ -717,8 +718,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     // A sum that goes on: what it has come to, onto its next part (this warp's columns).
     auto carry = [&](uint32_t from, uint32_t to) {
 #pragma unroll 1
-      for (int c = 0; c < im.cols; c += 32) {
-        if ((KIND == CE_LOGITS ? c / 64 & 1 : c >= im.cols / 2) != half) continue;
+      for (int c = half * (im.cols / 2); c < (half + 1) * (im.cols / 2); c += 32) {
         float a[32], b[32];
         tmem_ld32x2(from + c, to + c, a, b);
 #pragma unroll
@@ -729,7 +729,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
     while (work.next(p, im)) {
       const int row0 = im.m * 256 + (int)rank * 128 + q * 32;
       const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16);
-      if (KIND == CE_STATS) {
+      if (KIND != CE_GRADS) {
         float v[64];
 #pragma unroll
         for (int j = 0; j < 64; ++j) v[j] = 0.f;
@@ -748,7 +748,8 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
           ++cnt;
         }
         if (!ok) break;
-        stats_epilogue(p, im, v, row0 + lane, half);
+        if (KIND == CE_STATS) stats_epilogue(p, im, v, row0 + lane, half);
+        else logits_epilogue(maps, p, im, v, row0 + lane, half, stg, lane);
         continue;
       }
       bool ok = true;
@@ -761,9 +762,8 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
         if (kb + CT_CHAIN<KIND> < im.nk) ++cnt;
       }
       if (!ok) break;
-      const uint32_t taddr = tq + (cnt & 1) * 256 + (KIND == CE_LOGITS ? 0 : half * (im.cols / 2));
-      if (KIND == CE_LOGITS) logits_epilogue(maps, p, im, taddr, row0 + lane, half, stg, lane);
-      else if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, work.count, half, stg, lane);
+      const uint32_t taddr = tq + (cnt & 1) * 256 + half * (im.cols / 2);
+      if (im.kind == 1) dhidden_epilogue(p, im, taddr, row0, work.count, half, stg, lane);
       else dweight_epilogue(maps, p, im, taddr, p.v0 + row0, half, stg, lane, out_policy);
       if (im.nk != 0) {
         release(cnt & 1);
@@ -860,10 +860,12 @@ cudaError_t ce_tc_logits_grad(const CeMats &m, const CePiece &c, cudaStream_t st
   CtMaps maps = {};
   CtParams p = params(m);
   piece(p, c);
+  const uint64_t gdims[2] = {(uint64_t)m.ldg, (uint64_t)m.tpad}, gstride[1] = {(uint64_t)m.ldg * 2};
+  const uint32_t gbox[2] = {32, 32};
   if (!map_ld(&maps.h, m.h, m.tpad, m.ldh, m.ldh, 128) || !map_ld(&maps.h32, m.h, m.tpad, m.ldh, m.ldh, 32) ||
       !map_ld(&maps.w, m.w, m.V, m.D, m.ldw, 128) ||
       !map_ld(&maps.w32, m.w, m.V, m.D, m.ldw, 32) ||
-      !map_ld(&maps.gout, m.g, m.tpad, m.ldg, m.ldg, 32))
+      !encode_map(&maps.gout, m.g, 2, gdims, gstride, gbox, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   return launch<CE_LOGITS>(maps, p, (int64_t)(m.tpad / 256) * ceil_div(c.n, 64), stream);
 }

@@ -29,11 +29,12 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Tensor map with the 128-byte swizzle; out-of-range elements of a load read
+// Tensor map with the 128-byte swizzle unless another is asked for; out-of-range elements of a load read
 // as zero.  dims[0] is the contiguous dimension; strides_bytes[i] is the
 // stride of dimension i + 1.
 inline bool encode_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides_bytes,
-                       const uint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+                       const uint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t gd[5], gs[4];
@@ -45,7 +46,7 @@ inline bool encode_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t
     if (i + 1 < rank) gs[i] = strides_bytes[i];
   }
   return fn(m, type, (cuuint32_t)rank, const_cast<void *>(ptr), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
