@@ -723,12 +723,15 @@ enum moe_linear_ce_call { MOE_CE_LOSS = 1, MOE_CE_GRAD = 2, MOE_CE_STEP = 3 };
  *
  * The logits live in tensor memory (MOE_BF16) or registers only: a tile of
  * them leaves a maximum and a sum of exponentials for each row and 64 of its
- * columns.  Rows whose target is ignore_index (prompts, padding) are left out:
- * they are not read, their loss and lse are 0.  A target outside [0, V) that
- * is not ignore_index is left out the same way and recorded (code 7).  Logits
- * that are not finite give a loss that is not.  Products are exact, sums FP32,
- * in an order set by D, V and the type alone; a row's loss and lse do not
- * depend on T, on the other rows or on how many of them are left out.
+ * columns.  The target's logit joins the others' sum last, so that a small loss
+ * has FP32's relative precision.  Rows whose target is ignore_index (prompts,
+ * padding) are left out: they are not read, their loss and lse are 0.  A target
+ * outside [0, V) that is not ignore_index is left out the same way and recorded
+ * (code 7).  Logits that are not finite give a loss that is not, but for one of
+ * -infinity that is not the target's: its token cannot come.  Products are
+ * exact, sums FP32, in an order set by D, V and the type alone; a row's loss
+ * and lse do not depend on T, on the other rows or on how many of them are left
+ * out.
  * MOE_BF16 weights whose rows do not all start on 16-byte boundaries are first
  * copied to where they do.  Workspace: as for the gradient, below.
  */
@@ -763,8 +766,10 @@ int moe_linear_ce_backward(const moe_linear_ce_args_t *a, void *ws, size_t ws_by
 
 /* moe_linear_ce_step -- loss and gradients in one call, for a dloss that is
  * known beforehand: moe_linear_ce's loss and lse, and the gradients from the
- * statistics themselves (moe_linear_ce_backward has the target's probability
- * from lse and a dot product of its own; the two differ by that rounding). */
+ * statistics themselves.  There the target's probability is as far from 1 as
+ * the loss from 0, to FP32's relative precision however small (z_loss 0);
+ * moe_linear_ce_backward has it from lse and a dot product of its own, to
+ * about 2^-23 |lse| of 1. */
 int moe_linear_ce_step(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);
 
 typedef struct moe_grads_args {

@@ -98,8 +98,10 @@ ce_places_kernel(int T, int V, int64_t ignore, const Id *targets, int *count, in
 }
 
 // What the gradient needs of a row: d = scale * dloss, l its lse, nll = l -
-// x[target].  The target's entry is d (p - 1 + 2 z l p); p - 1 by expm1, exact
-// where the model is nearly sure.  Returns 1 / the row's factor.
+// x[target].  The target's entry is d (p - 1 + 2 z l p); p - 1 by expm1, which
+// keeps the bits that nll has: those of its size from the statistics (a step),
+// those of l's size where nll is a difference from l (the gradient alone).
+// Returns 1 / the row's factor.
 template <typename E>
 __device__ inline float grad_row(CeRow &r, float d, float l, float nll, float z) {
   const float zl = 2.f * z * l, p = expf(-nll);
@@ -270,7 +272,10 @@ ce_weight_copy_kernel(int64_t V, int D, int64_t ld, int64_t ldw, const __nv_bflo
 // ------------------------------------------------------------- the rows' statistics
 // A CTA joins 8 rows (64 bytes of each part): a row has 64 threads, which take
 // every 64th part each, first the maximum of eight parts at a time, then
-// their sums; the 64 results are joined in order of the threads.  In a step
+// their sums; the 64 results are joined in order of the threads.  The parts
+// are without the target's logit x_t, which comes in last: with o the sum of the others'
+// e^(x - x_t), lse - x_t = log(1 + o) keeps its bits where the model is
+// nearly sure, and a sum that had a 1 in it would have lost o.  In a step
 // also what the gradient needs of the rows, and the rows over their factors.
 constexpr int JOIN_ROWS = 8, JOIN_THREADS = 512;
 template <typename E>
@@ -334,9 +339,16 @@ ce_join_kernel(const int *count, int nparts, int tpad, const float2 *part, const
     if (part4 == 0) {
       float f = 1.f;
       if (r < n) {
-        // m and the target's logit are in units of log 2: their difference is exact
-        // where it is small, and 0 where the target has the largest logit.
-        const float ln = logf(s), l = fmaf(m, LN2, ln), nll = fmaf(m - xt[r], LN2, ln);
+        const float x = xt[r];  // (in units of log 2, as m)
+        float l, nll;
+        if (m <= x) {
+          nll = log1pf(s * exp2f(m - x));
+          l = fmaf(x, LN2, nll);
+        } else {  // the target's e^(x_t - m) beside the others' sum
+          const float ln = logf(s) + log1pf(exp2f(x - m) / s);
+          nll = fmaf(m - x, LN2, ln);
+          l = fmaf(m, LN2, ln);
+        }
         const int t = row_of[r];
         loss[t] = fmaf(z * l, l, nll);
         if (lse) lse[t] = l;

@@ -113,7 +113,7 @@ struct CePiece {
   bool first, last;
 };
 
-// The logits' (maximum, sum) of every 64 columns, and the targets' logits.
+// The logits' (maximum, sum) of every 64 columns without the targets', and the targets' logits.
 cudaError_t ce_tc_stats(const CeMats &m, cudaStream_t stream);
 cudaError_t ce_simt_stats(const CeMats &m, cudaStream_t stream);
 // g of a piece.

@@ -168,7 +168,7 @@ __device__ inline void simt_tile(const SimtParams &a, float (*sA)[SK][64 * S + 4
           const int c = colof(j);
           const float x = acc[i][j] * (m.scale * L2E);
           if (c == target) m.xt[row] = x;
-          acc[i][j] = c0 + c < m.V ? x : -INFINITY;
+          acc[i][j] = c0 + c < m.V && c != target ? x : -INFINITY;
           big = fmaxf(big, acc[i][j]);
         }
         for (int d = 8; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL_MASK, big, d));

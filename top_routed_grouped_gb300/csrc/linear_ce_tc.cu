@@ -6,7 +6,7 @@
 // its tensor memory receives 128 rows of the tile.
 //
 //   STATS   x[t, v] = sum_d h[t, d] w[v, d]     epilogue: for each row and 64 columns the
-//           maximum and the sum of exponentials, and the target's logit
+//           maximum and the sum of exponentials of all but the target, and the target's logit
 //   LOGITS  the same product for the columns of a piece; epilogue: g, one
 //           rounding to bf16, by TMA stores
 //   GRADS   dh[t, d] = sum_v g[t, v] w[v, d]    (A K-major, B MN-major)
@@ -320,14 +320,17 @@ __device__ inline void stats_epilogue(const CtParams &p, const CtItem &im, float
   const int col0 = im.n0 + cq * 64;
   const int target = p.rows[row].target - col0, left = p.V - col0;
   if (cq * 64 >= im.cols || left <= 0) return;
+#pragma unroll
+  for (int j = 0; j < 64; ++j) v[j] *= p.s2;
   if ((unsigned)target < 64u) {
     float x = 0.f;
 #pragma unroll
-    for (int j = 0; j < 64; ++j) x = target == j ? v[j] : x;
-    p.xt[row] = x * p.s2;
+    for (int j = 0; j < 64; ++j) {
+      x = target == j ? v[j] : x;
+      v[j] = target == j ? -INFINITY : v[j];
+    }
+    p.xt[row] = x;
   }
-#pragma unroll
-  for (int j = 0; j < 64; ++j) v[j] *= p.s2;
   if (left < 64) {
 #pragma unroll
     for (int j = 0; j < 64; ++j)
