@@ -790,8 +790,9 @@ typedef struct moe_grads_args {
  * FP32 squares would lose their bits (some |g| above about 1e13, or all of a
  * warp's below 1e-12) in FP64 from the start, so the norm is right wherever it
  * fits a float.  An infinite or NaN element makes it infinite or NaN.  The
- * order of the sums is fixed (set by the sizes, their order and the device's
- * number of SMs).  The host arrays are read before the call returns.
+ * order of the sums is fixed (set by the sizes, their order, each address
+ * modulo 16 and the device's number of SMs: the same gradients between other
+ * 16-byte boundaries may give another last bit).  The host arrays are read before the call returns.
  * Workspace: moe_grad_workspace_size(a) bytes, 256-byte aligned.
  */
 size_t moe_grad_workspace_size(const moe_grads_args_t *a);

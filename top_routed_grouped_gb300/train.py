@@ -173,7 +173,8 @@ def _listed(ts, name: str) -> list:
 
 def grad_norm(grads, ws=None, stream=None):
     """The 2-norm over all elements of ``grads`` (tensors of float32 or
-    bfloat16 on one device, in any gapless order), a float32 scalar there."""
+    bfloat16 on one device, in any gapless order), a float32 scalar there.  Its
+    last bit may depend on where the tensors lie between 16-byte boundaries."""
     grads = _listed(grads, "grads")
     if not grads:
         return torch.zeros((), dtype=torch.float32, device="cuda")
