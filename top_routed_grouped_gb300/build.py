@@ -3,7 +3,9 @@
 
 Each translation unit compiles in parallel into ``_build/``; the objects are
 linked into the shared library next to this file (in-tree).  Rebuilds only
-when a source or header is newer than the library.
+when a source or header is newer than the library, the module also where it is
+of another torch or Python.  The library needs neither: it is there when the
+module cannot be built, and without torch the module is left out.
 
     python -m top_routed_grouped_gb300.build [--force] [-v] [--ptxas]
 """
@@ -49,23 +51,39 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def build_bind(force: bool = False) -> str:
-    """The Python module that packs lists of tensors (against the torch that is installed)."""
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND_SRC) <= os.path.getmtime(BIND):
-        return BIND
+def bind_target() -> str:
+    """What the module is compiled against; it says so itself (``built_for``)."""
     import sysconfig
 
     import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def build_bind(force: bool = False) -> str | None:
+    """The Python module that packs lists of tensors (against the torch that is installed)."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        sys.stderr.write("no torch: _tensor_list.so is left out\n")
+        return None
+    target, stamp = bind_target(), os.path.join(BUILD, "tensor_list.target")
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND_SRC) <= os.path.getmtime(BIND) and \
+            os.path.exists(stamp) and open(stamp).read() == target:
+        return BIND
+    os.makedirs(BUILD, exist_ok=True)
     tmp = BIND + f".tmp{os.getpid()}"
     home = os.path.dirname(torch.__file__)
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DBUILT_FOR="{target}"',
            f"-I{home}/include", f"-I{home}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
            BIND_SRC, f"-L{home}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    with open(stamp, "w") as f:
+        f.write(target)
     return BIND
 
 
@@ -90,13 +108,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with ThreadPoolExecutor(max(1, min(9, os.cpu_count() or 1))) as ex:
         bind = ex.submit(build_bind, force)
         objs = list(ex.map(compile_one, sources()))
-        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    bind.result()  # (raises what its compiler said; the library is there)
     return LIB
 
 

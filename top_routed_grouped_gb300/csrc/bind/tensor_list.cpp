@@ -99,4 +99,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_list", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_list() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensor_list() {
+  PyObject *m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -135,13 +135,24 @@ def linear_cross_entropy_step(hidden, weight, targets, dloss, scale: float = 1.0
 
 
 # ---------------------------------------------------------------- gradients
+def _packer():
+    """``pack`` of the native module, which reads tensors as the torch has them that it was built for."""
+    from .build import bind_target
+    try:
+        from . import _tensor_list as m
+    except ImportError as e:
+        m, why = None, e
+    else:
+        why = None
+    if m is None or getattr(m, "built_for", None) != bind_target():
+        raise RuntimeError("_tensor_list.so is missing or of another torch: build it with "
+                           "`python -m top_routed_grouped_gb300.build`") from why
+    return m.pack
+
+
 def _pack(grads, out, dev):
     global _pack
-    try:
-        from ._tensor_list import pack as _pack
-    except ImportError as e:
-        raise RuntimeError("_tensor_list.so is missing or of another torch: build it with "
-                           "`python -m top_routed_grouped_gb300.build`") from e
+    _pack = _packer()
     return _pack(grads, out, dev)
 
 
