@@ -41,3 +41,18 @@ def test_bits_go_by_the_addresses_modulo_16(dtype):
         assert torch.equal(moe.grad_norm(moved(by + unit)), moe.grad_norm(first))
         assert torch.equal(moe.grad_norm(moved(by + 5 * unit)), moe.grad_norm(first))
         near(moe.grad_norm(first), norm64(at), NORM_TOL)
+
+
+def test_an_infinite_max_norm_reads_the_norm():
+    """As with the function of torch whose name it bears."""
+    ps = [torch.nn.Parameter(torch.zeros(n, device="cuda", dtype=t)) for n, t in ((300, F), (70, B), (5, F))]
+    ps[0].grad, ps[1].grad = make([300, 70], (F, B))
+    before = [p.grad.clone() for p in ps[:2]]
+    versions = [p.grad._version for p in ps[:2]]
+    assert torch.equal(moe.clip_grad_norm_(ps, float("inf")), moe.grad_norm(before))
+    assert all(torch.equal(p.grad, b) for p, b in zip(ps, before)) and versions == [p.grad._version for p in ps[:2]]
+    ps[0].grad[7] = float("nan")
+    assert torch.isnan(moe.clip_grad_norm_(iter(ps), float("inf"))) and torch.equal(ps[1].grad, before[1])
+    for bad in (float("-inf"), float("nan"), -1.0):
+        with pytest.raises(moe.MoEError):
+            moe.clip_grad_norm_(ps, bad)

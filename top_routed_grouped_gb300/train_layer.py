@@ -8,10 +8,12 @@ derivative: asking for one raises.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 from torch.autograd.function import once_differentiable
 
-from .train import clip_grads, linear_cross_entropy, linear_cross_entropy_backward
+from .train import clip_grads, grad_norm, linear_cross_entropy, linear_cross_entropy_backward
 
 
 class LinearCrossEntropyFunction(torch.autograd.Function):
@@ -64,6 +66,8 @@ class LMHead(torch.nn.Module):
 
 def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     """Clip the gradients of ``parameters`` (those that have one) in place to a
-    global norm of ``max_norm`` and return the norm that they had."""
+    global norm of ``max_norm`` and return the norm that they had.  An infinite
+    ``max_norm`` only reads it: the gradients stay as they are, whatever it is."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
-    return clip_grads([p.grad for p in parameters if p.grad is not None], max_norm, eps)
+    grads = [p.grad for p in parameters if p.grad is not None]
+    return grad_norm(grads) if max_norm == math.inf else clip_grads(grads, max_norm, eps)
