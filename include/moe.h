@@ -759,7 +759,13 @@ int moe_linear_ce(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void
  * dweight unless `accumulate`.  Workspace: moe_linear_ce_workspace_size(a,
  * call) bytes, 256-byte aligned; it goes by T, D, V, the types, ld_weight and
  * weight's alignment to 16 bytes (NULL: aligned; the other buffers need not be
- * set).
+ * set).  Most of it is T rows (rounded up to 256, whether they count or not)
+ * of: D copied units, twice for gradients in MOE_BF16; V / 8 bytes of statistics
+ * (forward, step); and for gradients g of min(V, 8192) columns (MOE_F32: 512),
+ * or of more chunks of as many while they stay below 256 MB in all, and D sums
+ * in FP32 for each of those chunks, where there are several.  At T = 2^24 g
+ * alone takes 2^25 bytes for each of up to 8192 columns: take such batches in
+ * parts (with `accumulate`).
  */
 size_t moe_linear_ce_workspace_size(const moe_linear_ce_args_t *a, int32_t call);
 int moe_linear_ce_backward(const moe_linear_ce_args_t *a, void *ws, size_t ws_bytes, void *stream);

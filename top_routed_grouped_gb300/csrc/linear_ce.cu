@@ -10,13 +10,13 @@
 // Then one product leaves a maximum and a sum of exponentials for each row and
 // 64 columns (8 bytes for 128 of logits), which are joined per row; the
 // gradient recomputes the logits a piece of the vocabulary at a time (2 TDV of
-// the 8 TDV operations, where keeping them would take 4 TV bytes) and takes
+// its 6, of a step's 8; keeping them would take 4 TV bytes) and takes
 // both products of the piece while it is near L2's size.
 //
 // The kernels here move little and are bound by latency, at large sizes by
 // memory: 5 rows x 2048 x 32000 spend 9 of their 31 us in them and in starts; 4096 x 2048
-// rows are copied in 13 us, their statistics over 24576 columns joined in 21
-// and the planes of three chunks added in 26 (under ncu, from a cold L2).
+// rows are copied in 13 us, their statistics over 24576 columns joined in 22
+// and the planes of three chunks added in 25 (under ncu, from a cold L2).
 #include <math.h>
 
 #include "linear_ce.h"

@@ -25,11 +25,11 @@
 // with five).  Every output is summed in K blocks of 64 in order; the tile it
 // falls in does not change that.
 //
-// What bounds them: the tensor cores.  At 4096 x 2048 x 50257 STATS runs at 1.93
-// PFLOP/s, as cuBLAS does in a burst; a step of 8192 x 2048 x 131072 at 1.72
-// over its four products, as cuBLAS does under the power cap.  Counters at
-// 4096 x 2048 x 24576: the tensor pipe is busy 88 % of STATS, 79 % of LOGITS, 86 % of
-// GRADS.  At few columns of K (1000) the SMs' reads of L2 (64 KB a K block and
+// What bounds them: the tensor cores.  A forward of 4096 x 2048 x 50257 takes 433
+// us in a burst (1.95 PFLOP/s; a large cuBLAS product: 1.90) and 487 in a long
+// run under the power cap (1.73; 1.71); a step of 8192 x 2048 x 131072 10.6 ms, 1.66
+// PFLOP/s over its four products.  Counters at 4096 x 2048 x 24576: the tensor pipe
+// is busy 89 % of STATS, 79 % of LOGITS, 84 % of GRADS.  At few columns of K (1000) the SMs' reads of L2 (64 KB a K block and
 // pair, 13 TB/s in all) share it with g's stores, and LOGITS takes a fifth longer than its MMAs.
 #include <cuda.h>
 

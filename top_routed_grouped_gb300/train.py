@@ -120,7 +120,9 @@ def linear_cross_entropy_backward(dloss, lse, hidden, weight, targets, scale: fl
     """(dhidden, dweight) of ``linear_cross_entropy`` for upstream gradients
     ``dloss`` [T] float32 and the forward's lse.  dhidden has hidden's type and
     zeros in the rows that are left out; dweight [V, D] has the weight's type
-    or ``dweight_dtype`` (float32), or is the float32 tensor ``dweight``, added to."""
+    or ``dweight_dtype`` (float32), or is the float32 tensor ``dweight``, added to.
+    Float32 sums of bfloat16 rows: what goes into their products, dx and the rows
+    of hidden, is bfloat16 all the same, rounded once each."""
     return _on(hidden, stream, _linear_ce, hidden, weight, targets, scale, z_loss, ignore_index, dloss, lse, dweight,
                dweight_dtype, ws, GRAD)
 

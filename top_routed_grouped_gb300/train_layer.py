@@ -38,7 +38,8 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
 def cross_entropy_loss(hidden, weight, targets, scale: float = 1.0, z_loss: float = 0.0, ignore_index: int = -100):
     """Loss [T] float32 of the next token from ``hidden`` [T, D] and the output
     embedding ``weight`` [V, D] (see ``linear_cross_entropy``), differentiable
-    in both.  Rows that are left out have loss 0: divide the sum by the number
+    in both (the backward computes both gradients, also where one of them is not
+    asked for).  Rows that are left out have loss 0: divide the sum by the number
     of the others for their mean."""
     return LinearCrossEntropyFunction.apply(hidden, weight, targets, scale, z_loss, ignore_index)[0]
 
