@@ -545,7 +545,7 @@ ce_pair_kernel(const __grid_constant__ CtMaps maps, const __grid_constant__ CtPa
       prefetch_tmap(p.w_blocks ? &maps.wt : &maps.wt1);
       prefetch_tmap(&maps.gt);
       prefetch_tmap(&maps.ht);
-      prefetch_tmap(&maps.dw);
+      if (p.dw_tma) prefetch_tmap(&maps.dw);
     } else {
       prefetch_tmap(&maps.h);
       prefetch_tmap(&maps.w);
